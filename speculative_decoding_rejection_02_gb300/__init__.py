@@ -1,7 +1,8 @@
 """GB300 speculative-sampling verifier: Python binding of the C ABI.
 
 Thin ``ctypes`` marshalling over ``libspecverify.so`` (declared in
-``include/spec_verify.h``). Every step of the verification runs in the
+``include/spec_verify.h``; the paged cache of ``include/spec_cache.h`` is
+bound in ``cache.py``). Every step of the verification runs in the
 library's CUDA kernels; PyTorch only supplies device memory and streams.
 There is no CPU fallback: if the library is missing or fails to load, every
 entry point raises.
@@ -50,6 +51,10 @@ ENTRY_POINTS = (
 )
 
 _SHARD_CALLS = ENTRY_POINTS[-5:]
+
+# The entry points declared in include/spec_cache.h.
+CACHE_ENTRY_POINTS = ("spec_cache_step", "spec_cache_append", "spec_cache_attend_workspace",
+                      "spec_cache_attend")
 
 
 class SpecVerifyError(RuntimeError):
@@ -116,6 +121,10 @@ def lib():
             for name in _SHARD_CALLS:
                 getattr(L, name).argtypes = [C.c_void_p, C.POINTER(Batch), C.POINTER(Shard),
                                              C.c_void_p]
+            for name in CACHE_ENTRY_POINTS:
+                getattr(L, name).argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
+            L.spec_cache_attend_workspace.argtypes = [C.c_void_p]
+            L.spec_cache_attend_workspace.restype = C.c_longlong
             for name in ENTRY_POINTS:
                 getattr(L, name)  # raises if the library lacks a declared symbol
             _lib = L
@@ -316,3 +325,8 @@ def check_batch(cfg: Config, b: Batch) -> int:
 
 def strerror(code: int) -> str:
     return lib().spec_verify_strerror(code).decode()
+
+
+from .cache import (  # noqa: E402  (needs the definitions above)
+    CACHE_BAD_LENGTHS, CACHE_BAD_PAGE, CACHE_BAD_SLOT, CACHE_NO_PAGES, AppendArgs, AttendArgs,
+    CacheStep, StepArgs, cache_append, cache_attend, cache_step)

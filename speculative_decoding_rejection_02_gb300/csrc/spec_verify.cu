@@ -737,7 +737,7 @@ const char* spec_verify_strerror(int code) {
   switch (code) {
     case SPEC_OK: return "ok";
     case SPEC_ERR_INVALID_ARG: return "invalid argument";
-    case SPEC_ERR_UNSUPPORTED: return "unsupported device (needs sm_103)";
+    case SPEC_ERR_UNSUPPORTED: return "unsupported form, or a device that is not sm_103";
     case SPEC_ERR_CUDA: return "CUDA runtime error";
     case SPEC_ERR_NOT_INIT: return "null handle";
     case SPEC_ERR_CAPACITY: return "batch exceeds the handle's maxima";
