@@ -1,9 +1,35 @@
 // Attention of a round's new tokens over the paged cache (spec_cache_attend).
 //
-// The plainest form: one block per new token and query head, whose warps take
-// the visible tokens in turn and keep a running maximum, sum and output each,
-// joined at the end.
+// The rows of one kv head are the new tokens times the G query heads that
+// share it: a tile of 128 rows is floor(128 / G) tokens (or as many as a
+// request is expected to have), so a round's few tokens still read each key
+// and value once for all their heads. Keys come in tiles of 128 tokens:
+//
+//   S = Q K^T       tcgen05, Q and K in shared memory, S (fp32) in TMEM
+//   P = 2^(c S - m) one thread per row: running maximum m and sum l in fp32,
+//                   P rounded to the cache's type and written over S
+//   O += P V        tcgen05, P from TMEM, V in shared memory, O (fp32) in TMEM
+//
+// with c = scale * log2(e). O is rescaled only when a row's maximum has grown by
+// more than 2^8 since the last time: until then P may exceed 1, which costs no
+// precision (bf16 and fp32 have the range; for fp16, P is kept 2^7 above 1 at
+// most 2^15 and reaches down to 2^-31 of the row's largest).
+//
+// Two streams of S and O run side by side in one block, so that one's products
+// cover the other's softmax: two tiles of rows over the same keys where a unit
+// has more than one tile of rows, else the even and the odd key tiles of the
+// one tile of rows, joined at the end.
+//
+// Work is one list of key tiles over (request, kv head, tiles of rows), cut
+// into equal parts, one for each block (one block per SM): ragged batches
+// balance without a plan on the host, and a unit that a cut crosses leaves
+// partial (m, l, O) in the workspace, which k_attend_join joins. Tiles that no
+// row of a unit sees are not in the list.
+//
+// Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 the loader (TMA, through
+// the block table), 9 the tensor cores' issuer, 10 the walk over the list.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -12,115 +38,845 @@
 
 #include "../../include/spec_cache.h"
 #include "pipe.cuh"
+#include "tcgen05.cuh"
 
 namespace sv {
 
-struct AttendParams {
-  spec_cache_attend_args a;
-  unsigned* status;
-  int page_shift;
+constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
+constexpr int kAttThreads = 352;  // 11 warps
+constexpr int kAttSegs = 4;       // list entries ahead of the slowest warp
+constexpr float kAttGrow = 8.f;   // log2 of how far a row's maximum may grow unscaled
+
+constexpr int kAttSharedBytes = 3072;  // barriers and the like, beside the tiles
+
+template <int DP>
+struct AttCfg {
+  static constexpr int kTileBytes = kAttTile * DP * 2;
+  static constexpr int kStages = DP == 128 ? 5 : 10;  // of one K or V tile each
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + kAttSharedBytes;
 };
 
-constexpr int kAttendWarps = 4;
+struct AttendParams {
+  CUtensorMap q_map, k_map, v_map;
+  int B, T, heads, kv_heads, G, dim;
+  int page_shift, width;
+  long long num_pages, table_stride;
+  const int* table;
+  const int* kv_lens;
+  const int* cu_q;
+  char* out;
+  long long out_token, out_head;  // bytes
+  float* lse;
+  float c;       // |scale| log2(e)
+  int negate;    // scale < 0
+  int window, sinks;
+  int tile_tokens;  // new tokens of a tile of rows
+  unsigned* status;
+  float4* part_o;   // [blocks][2][2 tiles][DP / 4][128] partial outputs
+  float2* part_ml;  // [blocks][2][2][128] their maxima and sums
+  struct AttJoin* join;  // [blocks]
+};
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f32(float x, __nv_bfloat16& y) { y = __float2bfloat16(x); }
-__device__ __forceinline__ void from_f32(float x, __half& y) { y = __float2half(x); }
+// A unit that starts in one block's part of the list and ends in another's.
+struct AttJoin {
+  int last;              // its last block; -1: none
+  int head, token, tokens;  // rows: new tokens token .. token + tokens - 1
+};
 
-// The new tokens of request b as rows [lo, hi) of q, and its length; a request
-// whose offsets or length cannot be has length 0.
+// One entry of a block's walk: key tiles i0 .. i1 - 1 of a unit.
+struct AttSeg {
+  int n;          // key tiles here; 0: the end of the walk
+  int i0;         // the first one's number within the unit
+  int b, head;
+  int token, tokens;  // rows of q
+  int pos;        // position of the first row's token
+  int lo, hi;     // tokens that some row sees: [lo, hi) and [0, min(sinks, lo))
+  int gap_at, gap;  // tile i of the unit is tile i, from gap_at on tile i + gap
+  int pair;       // 1: two tiles of rows; 0: even and odd key tiles
+  int q_at;       // Q tiles loaded before
+  unsigned ring;  // K and V tiles loaded before
+  int slot;       // partial result: 0 or 1; -1: the unit is whole
+};
+
+// sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0.
+__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// The units of one request: `count` of `step` new tokens each (the last may
+// have fewer), for each kv head.
+struct AttUnits {
+  long long p0;  // position of the first new token
+  int q, step, count, window;
+  long long sink_tiles;
+
+  __host__ __device__ AttUnits(int len, int q_, int step_, int window_, int sinks)
+      : p0((long long)len - q_), q(q_), step(step_), count((q_ + step_ - 1) / step_),
+        window(window_), sink_tiles(((long long)sinks + kAttTile - 1) / kAttTile) {}
+
+  __host__ __device__ long long hi(int u) const {
+    const long long end = (long long)(u + 1) * step;
+    return p0 + (end < q ? end : q);
+  }
+  __host__ __device__ long long lo(int u) const {
+    const long long x = window ? p0 + (long long)u * step - window + 1 : 0;
+    return x > 0 ? x : 0;
+  }
+  __host__ __device__ long long gap(int u) const {
+    const long long g = lo(u) / kAttTile - sink_tiles;
+    return g > 0 ? g : 0;
+  }
+  // Key tiles of unit u; one (in which no row sees anything) at least.
+  __host__ __device__ long long tiles(int u) const {
+    const long long h = hi(u);
+    return h <= 0 ? 1 : (h + kAttTile - 1) / kAttTile - gap(u);
+  }
+  // Key tiles of the units before k, in closed form.
+  __host__ __device__ long long before(int k) const {
+    long long sum = 0;
+    if (k == count && k > 0) sum += tiles(--k);  // the last one ends where the request does
+    if (k <= 0) return sum;
+    long long dead = p0 < 0 ? -p0 / step : 0;  // units before position 0
+    if (dead > k) dead = k;
+    sum += dead + floor_sum(k - dead, kAttTile, step, p0 + (dead + 1) * step + kAttTile - 1);
+    if (window) {
+      const long long from = (sink_tiles + 1) * kAttTile + window - 1 - p0;  // gap > 0
+      const long long u = from > 0 ? (from + step - 1) / step : 0;
+      if (u < k)
+        sum -= floor_sum(k - u, kAttTile, step, p0 + u * step - window + 1) -
+               (k - u) * sink_tiles;
+    }
+    return sum;
+  }
+};
+
+// The new tokens of request b as rows [lo, hi) of q, and its length. Offsets
+// that cannot be give no rows, a length that cannot be length 0.
 __device__ __forceinline__ int attend_request(const AttendParams& p, int b, int& lo, int& hi) {
-  const spec_cache_attend_args& a = p.a;
-  lo = a.cu_q[b];
-  hi = a.cu_q[b + 1];
-  int len = a.kv_lens[b];
-  const bool bad = lo < 0 || hi < lo || hi > a.num_tokens || len < 0 ||
-                   len > ((long long)a.width << p.page_shift);
-  if (bad) {
+  lo = p.cu_q[b];
+  hi = p.cu_q[b + 1];
+  int len = p.kv_lens[b];
+  const bool bad_rows = lo < 0 || hi < lo || hi > p.T;
+  const bool bad_len = len < 0 || len > ((long long)p.width << p.page_shift);
+  if (bad_rows || bad_len) {
     if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
-    lo = min(max(lo, 0), a.num_tokens);
-    hi = min(max(hi, lo), a.num_tokens);
+    if (bad_rows) lo = hi = 0;
     len = 0;
   }
   return len;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kAttendWarps * 32) k_cache_attend(const AttendParams p) {
-  const spec_cache_attend_args& a = p.a;
-  __shared__ float sm[kAttendWarps], sl[kAttendWarps], so[kAttendWarps][128];
-  pdl_trigger();
-  pdl_wait();
-  const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ int owner;
-  if (threadIdx.x == 0) owner = -1;
-  __syncthreads();
-  int lo = 0, hi = 0, len = 0;
-  for (int r = threadIdx.x; r < a.B; r += kAttendWarps * 32) {
-    attend_request(p, r, lo, hi);
-    if (lo <= t && t < hi) owner = r;
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+struct AttShared {
+  uint64_t kv_full[10], kv_empty[10];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_full, o_free, ml_full, drain;
+  uint64_t seg_full[kAttSegs], seg_empty[kAttSegs];
+  AttSeg seg[kAttSegs];
+  float2 ml[2][kAttTile];
+  long long scan[kAttThreads / 32];
+  int pad[kAttThreads / 32];
+  long long start_before;  // tiles before the run of requests where the part starts
+  int start_run;
+  uint32_t tmem;
+  int stop;
+};
+
+static_assert(sizeof(AttShared) <= kAttSharedBytes, "shared memory beside the tiles");
+
+// A bounded wait; once one has run out every later one returns at once.
+__device__ __forceinline__ bool att_wait(AttShared& sh, const AttendParams& p, uint64_t* bar,
+                                         uint32_t parity) {
+  for (uint32_t i = 0; i < kTryLimit; ++i) {
+    if (mbar_try(bar, parity & 1)) return true;
+    if (*(volatile int*)&sh.stop) return false;
   }
-  __syncthreads();
-  const int b = owner;
-  if (b >= 0) len = attend_request(p, b, lo, hi);
-  const int pos = len - (hi - lo) + (t - lo);
-  const int kvh = h / (a.heads / a.kv_heads);
-  const T* q = (const T*)a.q + t * a.q_token + h * a.q_head;
-  float qx[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) qx[i] = lane + 32 * i < a.dim ? to_f32(q[lane + 32 * i]) : 0.f;
-  float m = -INFINITY, l = 0.f;
-  if (b >= 0) {
-    const int from = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-    const int first = min(min(a.sinks, from), pos + 1);
-    const int n = first + max(0, pos + 1 - from);
-    for (int i = warp; i < n; i += kAttendWarps) {
-      const int j = i < first ? i : from + (i - first);
-      const long long page = a.block_table[b * a.table_stride + (j >> p.page_shift)];
-      if (page < 0 || page >= a.num_pages) {
-        if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_PAGE);
+  *(volatile int*)&sh.stop = 1;
+  if (p.status) atomicOr(p.status, SPEC_STATUS_TIMEOUT);
+  return false;
+}
+
+// The same for a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool att_wait_warp(AttShared& sh, const AttendParams& p, uint64_t* bar,
+                                              uint32_t parity) {
+  return __all_sync(~0u, att_wait(sh, p, bar, parity));
+}
+
+// Place of key tile i's K and V among the 2 n loads of a segment: in the order
+// in which the products use them.
+__device__ __forceinline__ int att_k_at(bool pair, int i) {
+  return pair ? 2 * i : i ? 2 * i - 1 : 0;
+}
+__device__ __forceinline__ int att_v_at(bool pair, int i, int n) {
+  return pair ? 2 * i + 1 : min(2 * i + 2, 2 * n - 1);
+}
+
+__device__ __forceinline__ int att_tile(const AttSeg& g, int i) {
+  const int u = g.i0 + i;
+  return u < g.gap_at ? u : u + g.gap;
+}
+
+// ---- warp 10: the walk over this block's part of the list
+
+__device__ __forceinline__ void att_walk(AttShared& sh, const AttendParams& p, long long begin,
+                                         long long end, long long total, int blocks, int run) {
+  int b = sh.start_run * run;
+  long long before = sh.start_before;  // tiles before request b
+  int lo = 0, hi = 0, len = 0, head = 0, u = 0;
+  long long skip = begin;  // tiles of the list already given out
+  bool fresh = true;
+  int q_at = 0, entry = 0;
+  unsigned ring = 0;
+  AttJoin join = {-1, 0, 0, 0};
+  p.join[blockIdx.x] = join;
+  const int step = 2 * p.tile_tokens;
+  long long rest = 0;  // tiles of the current unit already given out
+  while (skip < end) {
+    if (fresh) {  // request b
+      if (b >= p.B) break;  // not reached: the parts end with the list
+      len = attend_request(p, b, lo, hi);
+      const AttUnits units(len, hi - lo, step, p.window, p.sinks);
+      const long long per_head = units.before(units.count);
+      const long long all = per_head * p.kv_heads;
+      if (all == 0 || before + all <= skip) {
+        before += all;
+        ++b;
         continue;
       }
-      const int at = j & (a.page_size - 1);
-      const T* k = (const T*)a.k_pages + page * a.kp_page + at * a.kp_token + kvh * a.kp_head;
-      const T* v = (const T*)a.v_pages + page * a.vp_page + at * a.vp_token + kvh * a.vp_head;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (lane + 32 * e < a.dim) s += qx[e] * to_f32(k[lane + 32 * e]);
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      s *= a.scale;
-      const float top = fmaxf(m, s);
-      if (top == -INFINITY) continue;  // only scores of -inf so far
-      const float keep = __expf(m - top), w = __expf(s - top);
-      l = l * keep + w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (lane + 32 * e < a.dim) o[e] = o[e] * keep + w * to_f32(v[lane + 32 * e]);
-      m = top;
+      head = (int)((skip - before) / per_head);
+      const long long x = skip - before - head * per_head;
+      int u0 = 0, u1 = units.count - 1;  // the last unit that starts at or before x
+      while (u0 < u1) {
+        const int mid = (u0 + u1 + 1) >> 1;
+        if (units.before(mid) <= x) u0 = mid; else u1 = mid - 1;
+      }
+      u = u0;
+      rest = x - units.before(u);
+      before += all;
+      fresh = false;
+    }
+    const AttUnits units(len, hi - lo, step, p.window, p.sinks);
+    const long long n = units.tiles(u);
+    const long long take = min(n - rest, end - skip);
+    AttSeg g;
+    g.n = (int)take;
+    g.i0 = (int)rest;
+    g.b = b;
+    g.head = head;
+    g.token = lo + u * step;
+    g.tokens = min(step, hi - g.token);
+    g.pos = (int)(units.p0 + (long long)u * step);
+    g.lo = (int)units.lo(u);
+    g.hi = (int)max(units.hi(u), 0ll);
+    g.gap = (int)units.gap(u);
+    g.gap_at = g.gap ? (int)units.sink_tiles : 0x7fffffff;
+    g.pair = g.tokens > p.tile_tokens;
+    g.q_at = q_at;
+    g.ring = ring;
+    const bool starts = rest == 0, ends = rest + take == n;
+    g.slot = starts && ends ? -1 : starts ? 1 : 0;
+    if (starts && !ends) {
+      // the block that holds the unit's last tile
+      const long long last = skip + n - 1;
+      join.last = (int)(((last + 1) * blocks - 1) / total);
+      join.head = head;
+      join.token = g.token;
+      join.tokens = g.tokens;
+    }
+    const int at = entry % kAttSegs;
+    if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return;
+    sh.seg[at] = g;
+    mbar_arrive(&sh.seg_full[at]);
+    ++entry;
+    q_at += g.pair ? 2 : 1;
+    ring += 2 * g.n;
+    skip += take;
+    rest += take;
+    if (rest == n) {
+      rest = 0;
+      if (++u == units.count) {
+        u = 0;
+        if (++head == p.kv_heads) {
+          ++b;
+          fresh = true;
+        }
+      }
     }
   }
-  sm[warp] = m;
-  sl[warp] = l;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) so[warp][lane + 32 * e] = o[e];
-  __syncthreads();
-  if (warp) return;
-  float top = -INFINITY;
-  for (int w = 0; w < kAttendWarps; ++w) top = fmaxf(top, sm[w]);
-  float total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int w = 0; w < kAttendWarps && top > -INFINITY; ++w) {
-    const float keep = __expf(sm[w] - top);
-    total += sl[w] * keep;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] += so[w][lane + 32 * e] * keep;
+  p.join[blockIdx.x] = join;
+  const int at = entry % kAttSegs;
+  if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return;
+  sh.seg[at].n = 0;
+  mbar_arrive(&sh.seg_full[at]);
+}
+
+// ---- warp 8: Q, K and V tiles by TMA
+
+template <int DP>
+__device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, char* q_smem,
+                                         char* kv_smem, int lane) {
+  using Cfg = AttCfg<DP>;
+  constexpr int kBlocks = DP / 64, kBlockBytes = kAttTile * 128;
+  const int page = 1 << p.page_shift;
+  const int box = min(page, kAttTile);         // tokens of one load
+  const int boxes = kAttTile / box;            // of a tile
+  unsigned issued = 0;
+  for (int e = 0;; ++e) {
+    const int at = e % kAttSegs;
+    if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) break;
+    const AttSeg g = sh.seg[at];
+    if (g.n == 0) return;
+    bool ok = true;
+    for (int s = 0; s <= g.pair; ++s) {
+      const int x = g.q_at + s, slot = x & 1;
+      ok = ok && att_wait_warp(sh, p, &sh.q_empty[slot], (x / 2 + 1) & 1);
+      if (ok && lane == 0) {
+        mbar_arrive_expect_tx(&sh.q_full[slot], kBlocks * p.tile_tokens * p.G * 128);
+        for (int k = 0; k < kBlocks; ++k)
+          tma_load_4d(q_smem + slot * Cfg::kTileBytes + k * kBlockBytes, &p.q_map, 64 * k, 0,
+                      g.head, g.token + s * p.tile_tokens, &sh.q_full[slot]);
+      }
+      __syncwarp();
+    }
+    const int* table = p.table + g.b * p.table_stride;
+    for (int x = 0; ok && x < 2 * g.n; ++x) {
+      bool is_v;
+      int i;
+      if (g.pair) {
+        is_v = x & 1;
+        i = x >> 1;
+      } else if (x == 2 * g.n - 1) {
+        is_v = true;
+        i = g.n - 1;
+      } else {
+        is_v = x > 0 && !(x & 1);
+        i = is_v ? (x - 2) >> 1 : (x + 1) >> 1;
+      }
+      const int j = att_tile(g, i) * kAttTile + lane * box;  // the lane's first token
+      bool live = lane < boxes && j < g.hi && (j + box > g.lo || j < p.sinks);
+      int number = 0;
+      if (live) {
+        number = __ldg(table + (j >> p.page_shift));
+        if (number < 0 || number >= p.num_pages) {
+          if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_PAGE);
+          live = false;
+        }
+      }
+      const int count = __popc(__ballot_sync(~0u, live));
+      const unsigned r = g.ring + x, slot = r % Cfg::kStages;
+      ok = att_wait_warp(sh, p, &sh.kv_empty[slot], (r / Cfg::kStages + 1) & 1);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], count * kBlocks * box * 128);
+      __syncwarp();
+      if (live) {
+        char* dst = kv_smem + slot * Cfg::kTileBytes + lane * box * 128;
+        for (int k = 0; k < kBlocks; ++k)
+          tma_load_4d(dst + k * kBlockBytes, is_v ? &p.v_map : &p.k_map, 64 * k, j & (page - 1),
+                      g.head, number, &sh.kv_full[slot]);
+      }
+      issued = r + 1;
+    }
+    if (!ok) break;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.seg_empty[at]);
   }
-  T* out = (T*)a.out + t * a.out_token + h * a.out_head;
+  // A wait ran out: let the loads in flight land before the block's end.
+  for (unsigned r = issued > Cfg::kStages ? issued - Cfg::kStages : 0; r < issued; ++r)
+    for (int i = 0; i < 1024; ++i)
+      if (mbar_try(&sh.kv_full[r % Cfg::kStages], (r / Cfg::kStages) & 1)) break;
+}
+
+// ---- warp 9, one thread: the products
+
+template <int DP, bool BF16>
+__device__ __forceinline__ bool att_products(AttShared& sh, const AttendParams& p, char* q_smem,
+                                             char* kv_smem) {
+  using Cfg = AttCfg<DP>;
+  constexpr uint32_t kQK = mma_kind(BF16, false, kAttTile, kAttTile);
+  constexpr uint32_t kPV = mma_kind(BF16, true, kAttTile, DP);
+  const uint32_t tmem = sh.tmem;
+  unsigned p_count[2] = {0, 0};
+  auto qk = [&](int s, int q_slot, unsigned k_ring) {
+    const uint32_t q = smem_addr(q_smem) + q_slot * Cfg::kTileBytes;
+    const uint32_t k = smem_addr(kv_smem) + (k_ring % Cfg::kStages) * Cfg::kTileBytes;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < a.dim) from_f32(total > 0.f ? acc[e] / total : 0.f, out[lane + 32 * e]);
-  if (a.lse && lane == 0) a.lse[(long long)t * a.heads + h] = top + logf(total);
+    for (int x = 0; x < DP / 16; ++x) {
+      const uint32_t at = (x / 4) * (kAttTile * 128) + (x % 4) * 32;
+      mma_ss(tmem + s * 128, mma_desc(q + at, 16), mma_desc(k + at, 16), kQK, x > 0);
+    }
+    mma_commit(&sh.s_full[s]);
+  };
+  auto pv = [&](int s, unsigned v_ring, bool add) {
+    const uint32_t v = smem_addr(kv_smem) + (v_ring % Cfg::kStages) * Cfg::kTileBytes;
+#pragma unroll
+    for (int x = 0; x < kAttTile / 16; ++x)
+      mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * x,
+             mma_desc(v + x * 16 * 128, kAttTile * 128), kPV, add || x > 0);
+  };
+  auto loaded = [&](unsigned r) {
+    return att_wait(sh, p, &sh.kv_full[r % Cfg::kStages], r / Cfg::kStages);
+  };
+  auto release = [&](unsigned r) { mma_commit(&sh.kv_empty[r % Cfg::kStages]); };
+  // P of stream s written, and the V tile there.
+  // Before a segment's first PV the results of the segment before it have been read by all.
+  auto weights = [&](int s, unsigned v_ring, int e) {
+    if (!att_wait(sh, p, &sh.p_full[s], p_count[s]++) || !loaded(v_ring)) return false;
+    if (e >= 0 && !att_wait(sh, p, &sh.o_free, e + 1)) return false;
+    tmem_fence_after();
+    return true;
+  };
+  for (int e = 0;; ++e) {
+    const int at = e % kAttSegs;
+    if (!att_wait(sh, p, &sh.seg_full[at], e / kAttSegs)) return false;
+    const AttSeg g = sh.seg[at];
+    if (g.n == 0) return true;
+    for (int s = 0; s <= g.pair; ++s)
+      if (!att_wait(sh, p, &sh.q_full[(g.q_at + s) & 1], (g.q_at + s) / 2)) return false;
+    if (g.pair) {
+      for (int i = 0; i <= g.n; ++i) {
+        const unsigned k = g.ring + att_k_at(true, i);
+        const unsigned v = g.ring + att_v_at(true, i - 1, g.n);
+        for (int s = 0; s < 2; ++s) {
+          if (i > 0) {
+            if (!weights(s, v, i == 1 && s == 0 ? e : -1)) return false;
+            pv(s, v, i > 1);
+            if (s) release(v);
+          }
+          if (i < g.n) {
+            if (s == 0 && !loaded(k)) return false;
+            qk(s, (g.q_at + s) & 1, k);
+            if (s) release(k);
+          }
+        }
+      }
+    } else {
+      for (int i = 0; i < g.n + 2; ++i) {
+        const int s = i & 1;
+        const int x = i - 2;  // the tile whose weights are next
+        if (x >= 0 && x < g.n) {
+          const unsigned v = g.ring + att_v_at(false, x, g.n);
+          if (!weights(s, v, x == 0 ? e : -1)) return false;
+          pv(s, v, x >= 2);
+          release(v);
+        }
+        if (i < g.n) {
+          const unsigned k = g.ring + att_k_at(false, i);
+          if (!loaded(k)) return false;
+          qk(s, g.q_at & 1, k);
+          release(k);
+        }
+      }
+    }
+    for (int s = 0; s <= g.pair; ++s) mma_commit(&sh.q_empty[(g.q_at + s) & 1]);
+    mma_commit(&sh.o_full);
+    mbar_arrive(&sh.seg_empty[at]);
+  }
+}
+
+// ---- warps 0-7: softmax, rescaling, results
+
+// Rows of P V that no row of the unit sees may hold anything: zero them.
+template <int DP>
+__device__ __forceinline__ void att_clear_dead(char* v_tile, int row, bool dead) {
+  if (dead) {
+#pragma unroll
+    for (int k = 0; k < DP / 64; ++k)
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        *(uint4*)(v_tile + k * (kAttTile * 128) + row * 128 + 16 * x) = make_uint4(0, 0, 0, 0);
+  }
+  fence_async_shared();
+}
+
+// log2 of what every P and l carries beside 2^-m: fp16 has few exponents below 1.
+template <bool BF16>
+__device__ constexpr float att_bias() {
+  return BF16 ? 0.f : 7.f;
+}
+template <bool BF16>
+__device__ __forceinline__ float att_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l) - att_bias<BF16>()) * 0.69314718055994531f;
+}
+
+template <int DP, bool BF16>
+__device__ __forceinline__ void att_store_out(const AttendParams& p, char* out, int col,
+                                              const float* o, float scale) {
+  // 32 columns from col
+#pragma unroll
+  for (int x = 0; x < 32; x += 8) {
+    if (col + x >= p.dim) break;
+    uint4 v;
+    v.x = pack2<BF16>(o[x] * scale, o[x + 1] * scale);
+    v.y = pack2<BF16>(o[x + 2] * scale, o[x + 3] * scale);
+    v.z = pack2<BF16>(o[x + 4] * scale, o[x + 5] * scale);
+    v.w = pack2<BF16>(o[x + 6] * scale, o[x + 7] * scale);
+    *(uint4*)(out + (col + x) * 2) = v;
+  }
+}
+
+template <int DP, bool BF16>
+__device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p, char* kv_smem,
+                                            int warp, int lane) {
+  using Cfg = AttCfg<DP>;
+  constexpr float kBias = att_bias<BF16>();
+  const int s = warp >> 2, row = (warp & 3) * 32 + lane;
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t tmem_s = sh.tmem + lanes + s * 128;
+  const uint32_t tmem_o = sh.tmem + lanes + 256;
+  const int row_token = row / p.G, row_head = row - row_token * p.G;
+  unsigned s_count = 0, joins = 0;
+  for (int e = 0;; ++e) {
+    const int at = e % kAttSegs;
+    if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) return;
+    const AttSeg g = sh.seg[at];
+    if (g.n == 0) return;
+    // This thread's row: token and position; rows past the unit's tokens see nothing.
+    const int tile0 = g.pair ? s * p.tile_tokens : 0;  // the stream's first token
+    const int tokens = min(p.tile_tokens, g.tokens - tile0);
+    const bool mine = row_token < tokens;
+    const int pos = mine ? g.pos + tile0 + row_token : -1;
+    const bool busy = (warp & 3) * 32 < tokens * p.G;  // rows in this warp
+    const int first_pos = g.pos + tile0, last_pos = g.pos + tile0 + tokens - 1;
+    float m = -INFINITY, l = 0.f;
+    const int step = g.pair ? 1 : 2;
+    for (int i = g.pair ? 0 : s; i < g.n; i += step) {
+      const int j0 = att_tile(g, i) * kAttTile;
+      if (!att_wait_warp(sh, p, &sh.s_full[s], s_count)) return;
+      ++s_count;
+      if (busy) {
+        tmem_fence_after();
+        float f[128];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32(tmem_s + 32 * k, f + 32 * k);
+        tmem_wait_ld();
+        if (p.negate) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) f[k] = -f[k];
+        }
+        const bool all_seen =
+            j0 + kAttTile - 1 <= first_pos &&
+            (!p.window || j0 > last_pos - p.window || j0 + kAttTile <= p.sinks);
+        if (!all_seen) {
+          // tokens [0, sink_end) and [from, end) of the tile
+          const int end = min(pos - j0 + 1, kAttTile);
+          const int from = p.window && pos >= p.window ? pos - p.window + 1 - j0 : -j0;
+          const int sink_end = p.sinks - j0;
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k >= end || (k < from && k >= sink_end)) f[k] = -INFINITY;
+        }
+        float top[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+        for (int k = 4; k < 128; k += 8) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            top[y] = k + 4 + y < 128 ? fmaxf(fmaxf(top[y], f[k + y]), f[k + 4 + y])
+                                     : fmaxf(top[y], f[k + y]);
+        }
+        const float now =
+            fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c);
+        const bool grown = now > m + kAttGrow || (m == -INFINITY && now > m);
+        if (__any_sync(~0u, grown)) {
+          const float keep = grown ? ex2(m - now) : 1.f;
+          l *= keep;
+          if (grown) m = now;
+          if (i >= step) {  // O holds earlier tiles
+#pragma unroll
+            for (int k = 0; k < DP; k += 32) {
+              float o[32];
+              uint32_t u[32];
+              tmem_ld32(tmem_o + s * 128 + k, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(o[y] * keep);
+              tmem_st32(tmem_o + s * 128 + k, u);
+            }
+          }
+        }
+        const float shift = kBias - (m == -INFINITY ? 0.f : m);
+        const unsigned long long c2 = f2_pack(p.c, p.c), shift2 = f2_pack(shift, shift);
+        unsigned long long sum2[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w[32];
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {
+            float a, b;
+            f2_unpack(f2_fma(f2_pack(f[64 * k + 2 * y], f[64 * k + 2 * y + 1]), c2, shift2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum2[y & 1] = f2_add(sum2[y & 1], f2_pack(a, b));
+            w[y] = pack2<BF16>(a, b);
+          }
+          tmem_st32(tmem_s + 32 * k, w);
+        }
+        float a, b;
+        f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
+        l += a + b;
+        tmem_wait_st();
+        tmem_fence_before();
+      }
+      // V's rows that no row of the unit sees. Only now: S of tile i is there, so every load
+      // before K's of tile i has been used, and with it what V's slot held before (a wait for
+      // a barrier's phase is only sound once the phase before it is over).
+      const int sinks = min(p.sinks, g.lo);
+      if ((!g.pair || s == 0) && !(j0 >= g.lo && j0 + kAttTile <= g.hi) &&
+          j0 + kAttTile > sinks) {
+        const unsigned r = g.ring + att_v_at(g.pair, i, g.n);
+        if (!att_wait_warp(sh, p, &sh.kv_full[r % Cfg::kStages], r / Cfg::kStages)) return;
+        const int j = j0 + row;
+        att_clear_dead<DP>(kv_smem + (r % Cfg::kStages) * Cfg::kTileBytes, row,
+                           !(j < sinks || (j >= g.lo && j < g.hi)));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[s]);
+    }
+    // ---- results of the segment
+    float w[2] = {1.f, 1.f};  // of the two streams' O
+    if (!g.pair) {
+      // ml of the segment before has been read by all
+      if (!att_wait_warp(sh, p, &sh.o_free, e + 1)) return;
+      sh.ml[s][row] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.ml_full);
+      if (!att_wait_warp(sh, p, &sh.ml_full, joins)) return;
+      ++joins;
+      const float2 x = sh.ml[0][row], y = sh.ml[1][row];
+      m = fmaxf(x.x, y.x);
+      w[0] = x.x == -INFINITY ? 0.f : ex2(x.x - m);
+      w[1] = y.x == -INFINITY ? 0.f : ex2(y.x - m);
+      l = x.y * w[0] + y.y * w[1];
+    }
+    if (!att_wait_warp(sh, p, &sh.o_full, e)) return;
+    if (busy) {
+      tmem_fence_after();
+      const int half = g.pair ? DP : DP / 2;  // columns of this warp: stream s of a pair, or
+      const int col0 = g.pair ? 0 : s * half;  // half the columns of both streams
+      const uint32_t first = tmem_o + (g.pair ? s * 128 : 0);
+      const bool both = !g.pair && g.n > 1;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const long long token = g.token + tile0 + row_token;
+      const int head = g.head * p.G + row_head;
+      const int part = ((blockIdx.x * 2 + max(g.slot, 0)) * 2 + (g.pair ? s : 0));
+      char* out = p.out + token * p.out_token + head * p.out_head;
+      float4* part_o = p.part_o + (size_t)part * (DP / 4) * kAttTile + row;
+      for (int k = 0; k < half; k += 32) {
+        float o[32], y[32];
+        tmem_ld32(first + col0 + k, o);
+        if (both) tmem_ld32(first + 128 + col0 + k, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int z = 0; z < 32; ++z) o[z] *= w[0];
+        if (both) {
+#pragma unroll
+          for (int z = 0; z < 32; ++z) o[z] += y[z] * w[1];
+        }
+        if (mine && g.slot < 0) {
+          att_store_out<DP, BF16>(p, out, col0 + k, o, inv);
+        } else if (mine) {
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            part_o[((col0 + k) / 4 + z) * kAttTile] =
+                make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+        }
+        __syncwarp();
+      }
+      if (mine && (g.pair || s == 0)) {
+        if (g.slot >= 0)
+          p.part_ml[part * kAttTile + row] = make_float2(m, l);
+        else if (p.lse)
+          p.lse[token * p.heads + head] = att_lse<BF16>(m, l);
+      }
+    }
+    tmem_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sh.o_free);
+      mbar_arrive(&sh.seg_empty[at]);
+    }
+  }
+}
+
+// ---- the kernels
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kAttThreads, 1)
+    k_attend(const __grid_constant__ AttendParams p, const int run) {
+  using Cfg = AttCfg<DP>;
+  extern __shared__ __align__(1024) char smem[];
+  char* q_smem = smem;
+  char* kv_smem = smem + 2 * Cfg::kTileBytes;
+  AttShared& sh = *reinterpret_cast<AttShared*>(kv_smem + Cfg::kStages * Cfg::kTileBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < Cfg::kStages; ++i) {
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+    }
+    mbar_init(&sh.o_full, 1);
+    mbar_init(&sh.ml_full, 8);
+    mbar_init(&sh.o_free, 8);
+    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < kAttSegs; ++i) {
+      mbar_init(&sh.seg_full[i], 1);
+      mbar_init(&sh.seg_empty[i], 10);
+    }
+    fence_mbar_init();
+    sh.stop = 0;
+  }
+  if (warp == 9) tmem_alloc(&sh.tmem, 512);
+  pdl_trigger();
+  pdl_wait();
+  // Key tiles of each thread's run of requests, and of all.
+  const int step = 2 * p.tile_tokens;
+  const int r0 = (int)min((long long)tid * run, (long long)p.B), r1 = min(r0 + run, p.B);
+  long long mine = 0;
+  int pad = 0;  // rows from here on belong to no request
+  for (int r = r0; r < r1; ++r) {
+    int lo, hi;
+    const int len = attend_request(p, r, lo, hi);
+    const AttUnits units(len, hi - lo, step, p.window, p.sinks);
+    mine += units.before(units.count) * p.kv_heads;
+    pad = max(pad, hi);
+  }
+  long long upto = mine;
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += x;
+  }
+  pad = __reduce_max_sync(~0u, pad);
+  if (lane == 31) sh.scan[warp] = upto;
+  if (lane == 0) sh.pad[warp] = pad;
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  long long total = 0, before = upto - mine;
+  for (int w = 0; w < kAttThreads / 32; ++w) {
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
+    pad = max(pad, sh.pad[w]);
+  }
+  const int blocks = (int)min((long long)gridDim.x, total);
+  const bool works = (int)blockIdx.x < blocks;
+  const long long begin = works ? total * blockIdx.x / blocks : 0;
+  const long long end = works ? total * (blockIdx.x + 1) / blocks : 0;
+  if (works && before <= begin && begin < before + mine) {
+    sh.start_run = tid;
+    sh.start_before = before;
+  }
+  __syncthreads();
+  if (works) {
+    if (warp < 8) {
+      att_softmax<DP, BF16>(sh, p, kv_smem, warp, lane);
+    } else if (warp == 8) {
+      att_load<DP>(sh, p, q_smem, kv_smem, lane);
+    } else if (warp == 9) {
+      if (lane == 0 && !att_products<DP, BF16>(sh, p, q_smem, kv_smem)) {
+        mma_commit(&sh.drain);
+        for (int i = 0; i < 1024; ++i)
+          if (mbar_try(&sh.drain, 0)) break;
+      }
+      __syncwarp();
+    } else {
+      if (lane == 0) att_walk(sh, p, begin, end, total, blocks, run);
+      __syncwarp();
+    }
+  } else if (tid == 0) {
+    p.join[blockIdx.x].last = -1;
+  }
+  // Rows of q past the last request: zeros.
+  for (long long t = pad + blockIdx.x; t < p.T; t += gridDim.x) {
+    const int pieces = p.dim / 8;
+    for (int i = tid; i < p.heads * pieces; i += kAttThreads)
+      *(uint4*)(p.out + t * p.out_token + (i / pieces) * p.out_head + (i % pieces) * 16) =
+          make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int i = tid; i < p.heads; i += kAttThreads) p.lse[t * p.heads + i] = -INFINITY;
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tmem_fence_after();
+    tmem_free(sh.tmem, 512);
+  }
+}
+
+constexpr int kJoinThreads = 256, kJoinSplit = 4;
+
+// Join the partial results of the unit that starts in block blockIdx.x's part
+// of the list and ends in another's: parts of one row weigh 2^(m - max m).
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams p) {
+  pdl_trigger();
+  pdl_wait();
+  const AttJoin j = p.join[blockIdx.x];
+  if (j.last < 0) return;
+  const int parts = j.last - blockIdx.x + 1;
+  constexpr int kCols = DP / 4 / kJoinSplit;  // groups of four columns of this block
+  for (int tile = 0; tile < 2; ++tile) {
+    const int tokens = min(p.tile_tokens, j.tokens - tile * p.tile_tokens);
+    if (tokens <= 0) break;
+    const int rows = tokens * p.G;
+    for (int x = threadIdx.x; x < rows * kCols; x += kJoinThreads) {
+      const int col4 = x / rows, row = x - col4 * rows, c4 = blockIdx.y * kCols + col4;
+      auto at = [&](int i) { return ((blockIdx.x + i) * 2 + (i == 0)) * 2 + tile; };
+      float m = -INFINITY;
+      for (int i = 0; i < parts; ++i) m = fmaxf(m, p.part_ml[at(i) * kAttTile + row].x);
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int i = 0; i < parts; ++i) {
+        const float2 ml = p.part_ml[at(i) * kAttTile + row];
+        const float4 y = p.part_o[((size_t)at(i) * (DP / 4) + c4) * kAttTile + row];
+        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+        l += w * ml.y;
+        o.x += w * y.x;
+        o.y += w * y.y;
+        o.z += w * y.z;
+        o.w += w * y.w;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int row_token = row / p.G;
+      const long long token = j.token + tile * p.tile_tokens + row_token;
+      const int head = j.head * p.G + (row - row_token * p.G);
+      if (4 * c4 < p.dim) {
+        uint2 v;
+        v.x = pack2<BF16>(o.x * inv, o.y * inv);
+        v.y = pack2<BF16>(o.z * inv, o.w * inv);
+        *(uint2*)(p.out + token * p.out_token + head * p.out_head + 8 * c4) = v;
+      }
+      if (c4 == 0 && p.lse) p.lse[token * p.heads + head] = att_lse<BF16>(m, l);
+    }
+  }
 }
 
 }  // namespace sv

@@ -2,6 +2,7 @@
 // argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -31,8 +32,9 @@ int sm_count() {
 
 // Launch after the stream's earlier work, but with the launch itself prepared
 // while that work still runs (the kernels begin with pdl_wait).
-template <typename P>
-int launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
+template <typename... A, typename... B>
+int launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, void* stream,
+           const B&... args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = grid;
@@ -44,7 +46,7 @@ int launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return SPEC_OK;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return SPEC_OK;
   cudaGetLastError();
   return SPEC_ERR_CUDA;
 }
@@ -102,11 +104,85 @@ int check_attend(const spec_cache_attend_args* a, bool pointers) {
   const void* ptrs[] = {a->q, a->k_pages, a->v_pages, a->out};
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return SPEC_ERR_INVALID_ARG;
-  const long long strides[] = {a->q_token,  a->q_head,  a->kp_page,   a->kp_token, a->kp_head,
-                               a->vp_page, a->vp_token, a->vp_head, a->out_token, a->out_head};
-  for (long long s : strides)
-    if (s < 0 || s % 8) return SPEC_ERR_INVALID_ARG;
+  const struct {
+    long long extent, stride;
+  } axes[] = {{a->num_tokens, a->q_token},   {a->heads, a->q_head},
+              {a->num_pages, a->kp_page},    {a->page_size, a->kp_token},
+              {a->kv_heads, a->kp_head},     {a->num_pages, a->vp_page},
+              {a->page_size, a->vp_token},   {a->kv_heads, a->vp_head},
+              {a->num_tokens, a->out_token}, {a->heads, a->out_head}};
+  for (auto& x : axes)
+    if (x.extent > 1 && (x.stride <= 0 || x.stride % 8 || x.stride >= 1ll << 38))
+      return SPEC_ERR_INVALID_ARG;
   return SPEC_OK;
+}
+
+// Partial results of spec_cache_attend: offsets of their parts.
+struct Workspace {
+  size_t ml, join, bytes;
+};
+Workspace attend_workspace(int sms, int dim) {
+  const size_t tiles = (size_t)sms * 2 * 2;  // two partial units of two tiles for each block
+  Workspace w;
+  w.ml = tiles * (dim > 64 ? 128 : 64) * sv::kAttTile * sizeof(float);
+  w.join = w.ml + tiles * sv::kAttTile * sizeof(float2);
+  w.bytes = w.join + sms * sizeof(sv::AttJoin);
+  return w;
+}
+
+// A map of [x3][x2][x1][dim] 16-bit elements (strides in elements, not looked
+// at for an extent of 1) for boxes of 64 elements x box1 x 1 x box3 in rows of
+// 128 bytes, swizzled; elements past an extent read as zeros.
+bool tensor_map(CUtensorMap* map, int dtype, const void* base, int dim, long long x1,
+                long long s1, long long x2, long long s2, long long x3, long long s3,
+                unsigned box1, unsigned box3) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return (Encode)fn;
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)x1, (cuuint64_t)x2, (cuuint64_t)x3};
+  const cuuint64_t least = ((cuuint64_t)dim * 2 + 15) / 16 * 16;
+  const cuuint64_t strides[3] = {x1 > 1 ? (cuuint64_t)s1 * 2 : least,
+                                 x2 > 1 ? (cuuint64_t)s2 * 2 : least,
+                                 x3 > 1 ? (cuuint64_t)s3 * 2 : least};
+  const cuuint32_t box[4] = {64, box1, 1, box3}, ones[4] = {1, 1, 1, 1};
+  return encode(map, dtype == SPEC_CACHE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                4, const_cast<void*>(base), dims, strides, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, bool BF16>
+int attend(const sv::AttendParams& p, int sms, void* stream) {
+  constexpr int smem = sv::AttCfg<DP>::kSmem;
+  static std::atomic<unsigned long long> ready;  // devices whose kernel may use the memory
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (!(ready.load() >> dev & 1)) {
+    if (cudaFuncSetAttribute(sv::k_attend<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess) {
+      cudaGetLastError();
+      return SPEC_ERR_CUDA;
+    }
+    ready.fetch_or(1ull << dev);
+  }
+  const int run = p.B > sv::kAttThreads ? (p.B + sv::kAttThreads - 1) / sv::kAttThreads : 1;
+  const int rc = launch(sv::k_attend<DP, BF16>, dim3(sms), sv::kAttThreads, smem, stream, p, run);
+  if (rc != SPEC_OK) return rc;
+  return launch(sv::k_attend_join<DP, BF16>, dim3(sms, sv::kJoinSplit), sv::kJoinThreads, 0,
+                stream, p);
 }
 
 }  // namespace
@@ -160,7 +236,10 @@ int spec_cache_append(const spec_cache_append_args* a, void* stream, unsigned* d
 
 long long spec_cache_attend_workspace(const spec_cache_attend_args* a) {
   const int rc = check_attend(a, false);
-  return rc != SPEC_OK ? rc : 0;
+  if (rc != SPEC_OK) return rc;
+  const int sms = sm_count();
+  if (!sms) return SPEC_ERR_UNSUPPORTED;
+  return (long long)attend_workspace(sms, a->dim).bytes;
 }
 
 int spec_cache_attend(const spec_cache_attend_args* a, void* stream, unsigned* device_status) {
@@ -169,14 +248,54 @@ int spec_cache_attend(const spec_cache_attend_args* a, void* stream, unsigned* d
   const int sms = sm_count();
   if (!sms) return SPEC_ERR_UNSUPPORTED;
   if (a->num_tokens == 0) return SPEC_OK;
+  const Workspace ws = attend_workspace(sms, a->dim);
+  if (!a->workspace || a->workspace_bytes < ws.bytes) return SPEC_ERR_CAPACITY;
+  if (!aligned(a->workspace, 256)) return SPEC_ERR_INVALID_ARG;
   sv::AttendParams p;
-  p.a = *a;
-  p.status = device_status;
-  p.page_shift = 0;
+  std::memset(&p, 0, sizeof p);
+  p.B = a->B;
+  p.T = a->num_tokens;
+  p.heads = a->heads;
+  p.kv_heads = a->kv_heads;
+  p.G = a->heads / a->kv_heads;
+  p.dim = a->dim;
   while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
-  auto kernel = a->dtype == SPEC_CACHE_BF16 ? sv::k_cache_attend<__nv_bfloat16>
-                                            : sv::k_cache_attend<__half>;
-  return launch(kernel, dim3(a->num_tokens, a->heads), sv::kAttendWarps * 32, 0, stream, p);
+  p.width = a->width;
+  p.num_pages = a->num_pages;
+  p.table_stride = a->table_stride;
+  p.table = a->block_table;
+  p.kv_lens = a->kv_lens;
+  p.cu_q = a->cu_q;
+  p.out = (char*)a->out;
+  p.out_token = a->out_token * 2;
+  p.out_head = a->out_head * 2;
+  p.lse = a->lse;
+  // a scale of 0 still leaves masked scores at -inf
+  p.c = std::fmax(std::fabs(a->scale) * 1.4426950408889634f, 1.1754944e-38f);
+  p.negate = a->scale < 0;
+  p.window = a->window < (long long)a->width * a->page_size ? a->window : 0;
+  p.sinks = a->sinks;
+  p.tile_tokens = sv::kAttTile / p.G < a->max_q ? sv::kAttTile / p.G : a->max_q;
+  p.status = device_status;
+  char* w = (char*)a->workspace;
+  p.part_o = (float4*)w;
+  p.part_ml = (float2*)(w + ws.ml);
+  p.join = (sv::AttJoin*)(w + ws.join);
+  const unsigned box_page = a->page_size < sv::kAttTile ? a->page_size : sv::kAttTile;
+  const int dim = a->dim, kv = a->kv_heads;
+  if (!tensor_map(&p.q_map, a->dtype, a->q, dim, p.G, a->q_head, kv, a->q_head * p.G, p.T,
+                  a->q_token, p.G, p.tile_tokens))
+    return SPEC_ERR_CUDA;
+  if (a->B > 0 &&
+      (!tensor_map(&p.k_map, a->dtype, a->k_pages, dim, a->page_size, a->kp_token, kv,
+                   a->kp_head, a->num_pages, a->kp_page, box_page, 1) ||
+       !tensor_map(&p.v_map, a->dtype, a->v_pages, dim, a->page_size, a->vp_token, kv,
+                   a->vp_head, a->num_pages, a->vp_page, box_page, 1)))
+    return SPEC_ERR_CUDA;
+  const bool bf16 = a->dtype == SPEC_CACHE_BF16;
+  if (dim > 64)
+    return bf16 ? attend<128, true>(p, sms, stream) : attend<128, false>(p, sms, stream);
+  return bf16 ? attend<64, true>(p, sms, stream) : attend<64, false>(p, sms, stream);
 }
 
 }  // extern "C"

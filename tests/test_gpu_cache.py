@@ -337,11 +337,20 @@ def test_attend_long_context_and_split():
 
 
 def test_attend_is_reproducible():
-    gpu, _ = attend_case([3, 40, 1], [5000, 900, 20000], 16, 4, 128, 16, BF)
+    """Equal to the bit whatever ran on the SMs before and lies in the workspace, with
+    units of one and of two tiles of rows side by side in a block's part of the work."""
+    gpu, host = attend_case([3, 40, 1], [5000, 900, 20000], 16, 4, 128, 16, BF)
+    other, _ = attend_case([7, 50], [700, 3000], 16, 4, 128, 16, FP, seed=9, loud=3.0)
     a, al = sv.cache_attend(**gpu, return_lse=True)
-    for _ in range(3):
+    ref.assert_attend(a, al, ref.attend(*host))
+    for k in range(12):
+        if k % 3 == 0:
+            rubbish = torch.full((10 ** 7,), math.nan if k % 2 else 7.0, device=DEV)
+            del rubbish
+        elif k % 3 == 1:
+            sv.cache_attend(**other, max_q=5 + k)
         b, bl = sv.cache_attend(**gpu, return_lse=True)
-        assert torch.equal(a, b) and torch.equal(al, bl)
+        assert torch.equal(a, b) and torch.equal(al, bl), k
 
 
 def test_attend_offsets_past_32_bits():
