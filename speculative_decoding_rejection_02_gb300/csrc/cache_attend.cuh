@@ -27,7 +27,8 @@
 // row of a unit sees are not in the list.
 //
 // Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 the loader (TMA, through
-// the block table), 9 the tensor cores' issuer, 10 the walk over the list.
+// the block table), 9 the tensor cores' issuer, 10 the walk over the list;
+// 11 only fills their warpgroup, which gives registers to the softmax warps.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,7 +44,8 @@
 namespace sv {
 
 constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
-constexpr int kAttThreads = 352;  // 11 warps
+constexpr int kAttThreads = 384;  // 12 warps, at most 168 registers each at launch
+constexpr int kAttRegsMany = 216, kAttRegsFew = 72;  // 2 * 216 + 72 = 3 * 168
 constexpr int kAttSegs = 4;       // list entries ahead of the slowest warp
 constexpr float kAttGrow = 8.f;   // log2 of how far a row's maximum may grow unscaled
 
@@ -568,33 +570,40 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
       ++s_count;
       if (busy) {
         tmem_fence_after();
-        float f[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(tmem_s + 32 * k, f + 32 * k);
-        tmem_wait_ld();
-        if (p.negate) {
-#pragma unroll
-          for (int k = 0; k < 128; ++k) f[k] = -f[k];
-        }
         const bool all_seen =
             j0 + kAttTile - 1 <= first_pos &&
             (!p.window || j0 > last_pos - p.window || j0 + kAttTile <= p.sinks);
-        if (!all_seen) {
-          // tokens [0, sink_end) and [from, end) of the tile
-          const int end = min(pos - j0 + 1, kAttTile);
-          const int from = p.window && pos >= p.window ? pos - p.window + 1 - j0 : -j0;
-          const int sink_end = p.sinks - j0;
+        // otherwise tokens [0, sink_end) and [from, end) of the tile
+        const int end = min(pos - j0 + 1, kAttTile);
+        const int from = p.window && pos >= p.window ? pos - p.window + 1 - j0 : -j0;
+        const int sink_end = p.sinks - j0;
+        auto scores = [&](float* f, int at) {  // 32 columns, as loaded
+          if (p.negate) {
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k >= end || (k < from && k >= sink_end)) f[k] = -INFINITY;
-        }
-        float top[4] = {f[0], f[1], f[2], f[3]};
+            for (int k = 0; k < 32; ++k) f[k] = -f[k];
+          }
+          if (!all_seen) {
 #pragma unroll
-        for (int k = 4; k < 128; k += 8) {
+            for (int k = 0; k < 32; ++k)
+              if (at + k >= end || (at + k < from && at + k >= sink_end)) f[k] = -INFINITY;
+          }
+        };
+        // The scores are read twice, 32 columns ahead of their use, for their maximum and
+        // for the weights: 128 of them do not fit the registers beside everything else.
+        float f[2][32];
+        tmem_ld32(tmem_s, f[0]);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            top[y] = k + 4 + y < 128 ? fmaxf(fmaxf(top[y], f[k + y]), f[k + 4 + y])
-                                     : fmaxf(top[y], f[k + y]);
+        for (int k = 0; k < 4; ++k) {
+          float* x = f[k & 1];
+          tmem_wait_ld(x);
+          tmem_ld32(tmem_s + 32 * ((k + 1) & 3), f[(k + 1) & 1]);
+          scores(x, 32 * k);
+#pragma unroll
+          for (int y = 0; y < 32; y += 8) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) top[z] = fmaxf(fmaxf(top[z], x[y + z]), x[y + z + 4]);
+          }
         }
         const float now =
             fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c);
@@ -607,31 +616,35 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
 #pragma unroll
             for (int k = 0; k < DP; k += 32) {
               float o[32];
-              uint32_t u[32];
               tmem_ld32(tmem_o + s * 128 + k, o);
-              tmem_wait_ld();
+              tmem_wait_ld(o);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) u[y] = __float_as_uint(o[y] * keep);
-              tmem_st32(tmem_o + s * 128 + k, u);
+              for (int y = 0; y < 32; ++y) o[y] *= keep;
+              tmem_st32(tmem_o + s * 128 + k, o);
             }
           }
         }
         const float shift = kBias - (m == -INFINITY ? 0.f : m);
         const unsigned long long c2 = f2_pack(p.c, p.c), shift2 = f2_pack(shift, shift);
         unsigned long long sum2[2] = {0, 0};
+        uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t w[32];
+        for (int k = 0; k < 4; ++k) {
+          float* x = f[k & 1];
+          tmem_wait_ld(x);
+          if (k < 3) tmem_ld32(tmem_s + 32 * (k + 1), f[(k + 1) & 1]);
+          scores(x, 32 * k);
 #pragma unroll
-          for (int y = 0; y < 32; ++y) {
+          for (int y = 0; y < 16; ++y) {
             float a, b;
-            f2_unpack(f2_fma(f2_pack(f[64 * k + 2 * y], f[64 * k + 2 * y + 1]), c2, shift2), a, b);
+            f2_unpack(f2_fma(f2_pack(x[2 * y], x[2 * y + 1]), c2, shift2), a, b);
             a = ex2(a);
             b = ex2(b);
             sum2[y & 1] = f2_add(sum2[y & 1], f2_pack(a, b));
-            w[y] = pack2<BF16>(a, b);
+            w[16 * (k & 1) + y] = pack2<BF16>(a, b);
           }
-          tmem_st32(tmem_s + 32 * k, w);
+          // P over columns of S that have been read
+          if (k & 1) tmem_st32(tmem_s + 16 * (k - 1), w);
         }
         float a, b;
         f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
@@ -686,11 +699,12 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
       for (int k = 0; k < half; k += 32) {
         float o[32], y[32];
         tmem_ld32(first + col0 + k, o);
-        if (both) tmem_ld32(first + 128 + col0 + k, y);
-        tmem_wait_ld();
+        tmem_wait_ld(o);
 #pragma unroll
         for (int z = 0; z < 32; ++z) o[z] *= w[0];
         if (both) {
+          tmem_ld32(first + 128 + col0 + k, y);
+          tmem_wait_ld(y);
 #pragma unroll
           for (int z = 0; z < 32; ++z) o[z] += y[z] * w[1];
         }
@@ -796,18 +810,21 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   __syncthreads();
   if (works) {
     if (warp < 8) {
+      regs_take<kAttRegsMany>();
       att_softmax<DP, BF16>(sh, p, kv_smem, warp, lane);
-    } else if (warp == 8) {
-      att_load<DP>(sh, p, q_smem, kv_smem, lane);
-    } else if (warp == 9) {
-      if (lane == 0 && !att_products<DP, BF16>(sh, p, q_smem, kv_smem)) {
-        mma_commit(&sh.drain);
-        for (int i = 0; i < 1024; ++i)
-          if (mbar_try(&sh.drain, 0)) break;
-      }
-      __syncwarp();
     } else {
-      if (lane == 0) att_walk(sh, p, begin, end, total, blocks, run);
+      regs_give<kAttRegsFew>();
+      if (warp == 8) {
+        att_load<DP>(sh, p, q_smem, kv_smem, lane);
+      } else if (warp == 9) {
+        if (lane == 0 && !att_products<DP, BF16>(sh, p, q_smem, kv_smem)) {
+          mma_commit(&sh.drain);
+          for (int i = 0; i < 1024; ++i)
+            if (mbar_try(&sh.drain, 0)) break;
+        }
+      } else if (warp == 10) {
+        if (lane == 0) att_walk(sh, p, begin, end, total, blocks, run);
+      }
       __syncwarp();
     }
   } else if (tid == 0) {
