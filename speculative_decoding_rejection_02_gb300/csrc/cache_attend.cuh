@@ -69,8 +69,8 @@ struct AttendParams {
   char* out;
   long long out_token, out_head;  // bytes
   float* lse;
-  float c;       // |scale| log2(e)
-  int negate;    // scale < 0
+  float c;       // scale * log2(e)
+  float hidden;  // score that c takes to -inf
   int window, sinks;
   int tile_tokens;  // new tokens of a tile of rows
   unsigned* status;
@@ -577,36 +577,42 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
         const int end = min(pos - j0 + 1, kAttTile);
         const int from = p.window && pos >= p.window ? pos - p.window + 1 - j0 : -j0;
         const int sink_end = p.sinks - j0;
-        auto scores = [&](float* f, int at) {  // 32 columns, as loaded
-          if (p.negate) {
+        auto hide = [&](float* f, int at) {  // columns at .. at + 31 that the row does not see
 #pragma unroll
-            for (int k = 0; k < 32; ++k) f[k] = -f[k];
-          }
-          if (!all_seen) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (at + k >= end || (at + k < from && at + k >= sink_end)) f[k] = -INFINITY;
-          }
+          for (int k = 0; k < 32; ++k)
+            if (at + k >= end || (at + k < from && at + k >= sink_end)) f[k] = p.hidden;
         };
         // The scores are read twice, 32 columns ahead of their use, for their maximum and
-        // for the weights: 128 of them do not fit the registers beside everything else.
+        // for the weights: 128 of them do not fit the registers beside everything else. Both
+        // loops are kept rolled: straight-line code for one warp waits for its instructions.
         float f[2][32];
         tmem_ld32(tmem_s, f[0]);
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float top[4] = {p.hidden, p.hidden, p.hidden, p.hidden};
+        auto raise = [&](float* f, int at) {
+          if (!all_seen) hide(f, at);
+          if (p.c > 0.f) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float* x = f[k & 1];
-          tmem_wait_ld(x);
-          tmem_ld32(tmem_s + 32 * ((k + 1) & 3), f[(k + 1) & 1]);
-          scores(x, 32 * k);
+            for (int y = 0; y < 32; y += 8)
 #pragma unroll
-          for (int y = 0; y < 32; y += 8) {
+              for (int z = 0; z < 4; ++z) top[z] = fmaxf(fmaxf(top[z], f[y + z]), f[y + z + 4]);
+          } else {
 #pragma unroll
-            for (int z = 0; z < 4; ++z) top[z] = fmaxf(fmaxf(top[z], x[y + z]), x[y + z + 4]);
+            for (int y = 0; y < 32; y += 8)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) top[z] = fminf(fminf(top[z], f[y + z]), f[y + z + 4]);
           }
+        };
+#pragma unroll 1
+        for (int k = 0; k < 128; k += 64) {
+          tmem_wait_ld(f[0]);
+          tmem_ld32(tmem_s + k + 32, f[1]);
+          raise(f[0], k);
+          tmem_wait_ld(f[1]);
+          tmem_ld32(tmem_s + (k ^ 64), f[0]);
+          raise(f[1], k + 32);
         }
         const float now =
-            fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c);
+            fmaxf(m, fmaxf(fmaxf(top[0] * p.c, top[1] * p.c), fmaxf(top[2] * p.c, top[3] * p.c)));
         const bool grown = now > m + kAttGrow || (m == -INFINITY && now > m);
         if (__any_sync(~0u, grown)) {
           const float keep = grown ? ex2(m - now) : 1.f;
@@ -628,23 +634,27 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
         const unsigned long long c2 = f2_pack(p.c, p.c), shift2 = f2_pack(shift, shift);
         unsigned long long sum2[2] = {0, 0};
         uint32_t w[32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float* x = f[k & 1];
-          tmem_wait_ld(x);
-          if (k < 3) tmem_ld32(tmem_s + 32 * (k + 1), f[(k + 1) & 1]);
-          scores(x, 32 * k);
+        auto weigh = [&](float* f, int at, uint32_t* w) {
+          if (!all_seen) hide(f, at);
 #pragma unroll
           for (int y = 0; y < 16; ++y) {
             float a, b;
-            f2_unpack(f2_fma(f2_pack(x[2 * y], x[2 * y + 1]), c2, shift2), a, b);
+            f2_unpack(f2_fma(f2_pack(f[2 * y], f[2 * y + 1]), c2, shift2), a, b);
             a = ex2(a);
             b = ex2(b);
             sum2[y & 1] = f2_add(sum2[y & 1], f2_pack(a, b));
-            w[16 * (k & 1) + y] = pack2<BF16>(a, b);
+            w[y] = pack2<BF16>(a, b);
           }
-          // P over columns of S that have been read
-          if (k & 1) tmem_st32(tmem_s + 16 * (k - 1), w);
+        };
+#pragma unroll 1
+        for (int k = 0; k < 128; k += 64) {
+          tmem_wait_ld(f[0]);
+          tmem_ld32(tmem_s + k + 32, f[1]);
+          weigh(f[0], k, w);
+          tmem_wait_ld(f[1]);
+          if (k == 0) tmem_ld32(tmem_s + 64, f[0]);
+          weigh(f[1], k + 32, w + 16);
+          tmem_st32(tmem_s + k / 2, w);  // P over columns of S that have been read
         }
         float a, b;
         f2_unpack(f2_add(sum2[0], sum2[1]), a, b);

@@ -271,8 +271,9 @@ int spec_cache_attend(const spec_cache_attend_args* a, void* stream, unsigned* d
   p.out_head = a->out_head * 2;
   p.lse = a->lse;
   // a scale of 0 still leaves masked scores at -inf
-  p.c = std::fmax(std::fabs(a->scale) * 1.4426950408889634f, 1.1754944e-38f);
-  p.negate = a->scale < 0;
+  p.c = a->scale * 1.4426950408889634f;
+  if (std::fabs(p.c) < 1.1754944e-38f) p.c = 1.1754944e-38f;
+  p.hidden = p.c > 0.f ? -INFINITY : INFINITY;
   p.window = a->window < (long long)a->width * a->page_size ? a->window : 0;
   p.sinks = a->sinks;
   p.tile_tokens = sv::kAttTile / p.G < a->max_q ? sv::kAttTile / p.G : a->max_q;
