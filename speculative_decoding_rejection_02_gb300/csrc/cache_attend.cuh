@@ -26,9 +26,9 @@
 // partial (m, l, O) in the workspace, which k_attend_join joins. Tiles that no
 // row of a unit sees are not in the list.
 //
-// Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 the loader (TMA, through
-// the block table), 9 the tensor cores' issuer, 10 the walk over the list;
-// 11 only fills their warpgroup, which gives registers to the softmax warps.
+// Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 and 11 the loaders (TMA,
+// through the block table), 9 the tensor cores' issuer, 10 the walk over the
+// list; the last four give registers to the softmax warps.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -335,9 +335,10 @@ __device__ __forceinline__ void att_walk(AttShared& sh, const AttendParams& p, l
   mbar_arrive(&sh.seg_full[at]);
 }
 
-// ---- warp 8: Q, K and V tiles by TMA
+// ---- warps 8 and 11: Q and K, and V tiles by TMA (two warps: with small pages it is the
+// issue of the loads that takes the time)
 
-template <int DP>
+template <int DP, bool V>
 __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, char* q_smem,
                                          char* kv_smem, int lane) {
   using Cfg = AttCfg<DP>;
@@ -352,7 +353,7 @@ __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, c
     const AttSeg g = sh.seg[at];
     if (g.n == 0) return;
     bool ok = true;
-    for (int s = 0; s <= g.pair; ++s) {
+    for (int s = 0; !V && s <= g.pair; ++s) {
       const int x = g.q_at + s, slot = x & 1;
       ok = ok && att_wait_warp(sh, p, &sh.q_empty[slot], (x / 2 + 1) & 1);
       if (ok && lane == 0) {
@@ -364,19 +365,7 @@ __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, c
       __syncwarp();
     }
     const int* table = p.table + g.b * p.table_stride;
-    for (int x = 0; ok && x < 2 * g.n; ++x) {
-      bool is_v;
-      int i;
-      if (g.pair) {
-        is_v = x & 1;
-        i = x >> 1;
-      } else if (x == 2 * g.n - 1) {
-        is_v = true;
-        i = g.n - 1;
-      } else {
-        is_v = x > 0 && !(x & 1);
-        i = is_v ? (x - 2) >> 1 : (x + 1) >> 1;
-      }
+    for (int i = 0; ok && i < g.n; ++i) {
       const int j = att_tile(g, i) * kAttTile + lane * box;  // the lane's first token
       bool live = lane < boxes && j < g.hi && (j + box > g.lo || j < p.sinks);
       int number = 0;
@@ -388,7 +377,8 @@ __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, c
         }
       }
       const int count = __popc(__ballot_sync(~0u, live));
-      const unsigned r = g.ring + x, slot = r % Cfg::kStages;
+      const unsigned r = g.ring + (V ? att_v_at(g.pair, i, g.n) : att_k_at(g.pair, i));
+      const unsigned slot = r % Cfg::kStages;
       ok = att_wait_warp(sh, p, &sh.kv_empty[slot], (r / Cfg::kStages + 1) & 1);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], count * kBlocks * box * 128);
@@ -396,7 +386,7 @@ __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, c
       if (live) {
         char* dst = kv_smem + slot * Cfg::kTileBytes + lane * box * 128;
         for (int k = 0; k < kBlocks; ++k)
-          tma_load_4d(dst + k * kBlockBytes, is_v ? &p.v_map : &p.k_map, 64 * k, j & (page - 1),
+          tma_load_4d(dst + k * kBlockBytes, V ? &p.v_map : &p.k_map, 64 * k, j & (page - 1),
                       g.head, number, &sh.kv_full[slot]);
       }
       issued = r + 1;
@@ -405,7 +395,8 @@ __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, c
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.seg_empty[at]);
   }
-  // A wait ran out: let the loads in flight land before the block's end.
+  // A wait ran out: let the loads in flight land before the block's end (those of the other
+  // of the two warps among them: a wait too many only takes its limit).
   for (unsigned r = issued > Cfg::kStages ? issued - Cfg::kStages : 0; r < issued; ++r)
     for (int i = 0; i < 1024; ++i)
       if (mbar_try(&sh.kv_full[r % Cfg::kStages], (r / Cfg::kStages) & 1)) break;
@@ -772,7 +763,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < kAttSegs; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 10);
+      mbar_init(&sh.seg_empty[i], 11);
     }
     fence_mbar_init();
     sh.stop = 0;
@@ -825,7 +816,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     } else {
       regs_give<kAttRegsFew>();
       if (warp == 8) {
-        att_load<DP>(sh, p, q_smem, kv_smem, lane);
+        att_load<DP, false>(sh, p, q_smem, kv_smem, lane);
+      } else if (warp == 11) {
+        att_load<DP, true>(sh, p, q_smem, kv_smem, lane);
       } else if (warp == 9) {
         if (lane == 0 && !att_products<DP, BF16>(sh, p, q_smem, kv_smem)) {
           mma_commit(&sh.drain);
