@@ -402,7 +402,7 @@ __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, c
       if (mbar_try(&sh.kv_full[r % Cfg::kStages], (r / Cfg::kStages) & 1)) break;
 }
 
-// ---- warp 9, one thread: the products
+// ---- warp 9: the products, issued by one of its threads
 
 template <int DP, bool BF16>
 __device__ __forceinline__ bool att_products(AttShared& sh, const AttendParams& p, char* q_smem,
@@ -410,44 +410,56 @@ __device__ __forceinline__ bool att_products(AttShared& sh, const AttendParams& 
   using Cfg = AttCfg<DP>;
   constexpr uint32_t kQK = mma_kind(BF16, false, kAttTile, kAttTile);
   constexpr uint32_t kPV = mma_kind(BF16, true, kAttTile, DP);
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
+  const bool one = elect_one();
+  // descriptors of the first tiles; others by what is added to their addresses (in 16 bytes)
+  const uint64_t q0 = mma_desc(smem_addr(q_smem), 16), k0 = mma_desc(smem_addr(kv_smem), 16);
+  const uint64_t v0 = mma_desc(smem_addr(kv_smem), kAttTile * 128);
+  constexpr unsigned kTile = Cfg::kTileBytes / 16;
   unsigned p_count[2] = {0, 0};
   auto qk = [&](int s, int q_slot, unsigned k_ring) {
-    const uint32_t q = smem_addr(q_smem) + q_slot * Cfg::kTileBytes;
-    const uint32_t k = smem_addr(kv_smem) + (k_ring % Cfg::kStages) * Cfg::kTileBytes;
+    const uint64_t q = q0 + q_slot * kTile, k = k0 + (k_ring % Cfg::kStages) * kTile;
 #pragma unroll
     for (int x = 0; x < DP / 16; ++x) {
-      const uint32_t at = (x / 4) * (kAttTile * 128) + (x % 4) * 32;
-      mma_ss(tmem + s * 128, mma_desc(q + at, 16), mma_desc(k + at, 16), kQK, x > 0);
+      const unsigned at = ((x / 4) * (kAttTile * 128) + (x % 4) * 32) / 16;
+      mma_ss(tmem + s * 128, q + at, k + at, kQK, x > 0, one);
     }
-    mma_commit(&sh.s_full[s]);
+    mma_commit(&sh.s_full[s], one);
   };
   auto pv = [&](int s, unsigned v_ring, bool add) {
-    const uint32_t v = smem_addr(kv_smem) + (v_ring % Cfg::kStages) * Cfg::kTileBytes;
+    const uint64_t v = v0 + (v_ring % Cfg::kStages) * kTile;
 #pragma unroll
     for (int x = 0; x < kAttTile / 16; ++x)
-      mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * x,
-             mma_desc(v + x * 16 * 128, kAttTile * 128), kPV, add || x > 0);
+      mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * x, v + x * (16 * 128 / 16), kPV,
+             add || x > 0, one);
   };
   auto loaded = [&](unsigned r) {
-    return att_wait(sh, p, &sh.kv_full[r % Cfg::kStages], r / Cfg::kStages);
+    return att_wait_warp(sh, p, &sh.kv_full[r % Cfg::kStages], r / Cfg::kStages);
   };
-  auto release = [&](unsigned r) { mma_commit(&sh.kv_empty[r % Cfg::kStages]); };
+  auto release = [&](unsigned r) { mma_commit(&sh.kv_empty[r % Cfg::kStages], one); };
   // P of stream s written, and the V tile there.
   // Before a segment's first PV the results of the segment before it have been read by all.
   auto weights = [&](int s, unsigned v_ring, int e) {
-    if (!att_wait(sh, p, &sh.p_full[s], p_count[s]++) || !loaded(v_ring)) return false;
-    if (e >= 0 && !att_wait(sh, p, &sh.o_free, e + 1)) return false;
+    if (!loaded(v_ring)) return false;
+    if (e >= 0 && !att_wait_warp(sh, p, &sh.o_free, e + 1)) return false;
+    if (!att_wait_warp(sh, p, &sh.p_full[s], p_count[s]++)) return false;
     tmem_fence_after();
     return true;
   };
   for (int e = 0;; ++e) {
     const int at = e % kAttSegs;
-    if (!att_wait(sh, p, &sh.seg_full[at], e / kAttSegs)) return false;
-    const AttSeg g = sh.seg[at];
+    if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) return false;
+    struct {
+      int n, pair, q_at;
+      unsigned ring;
+    } g;
+    g.n = __shfl_sync(~0u, sh.seg[at].n, 0);
+    g.pair = __shfl_sync(~0u, sh.seg[at].pair, 0);
+    g.q_at = __shfl_sync(~0u, sh.seg[at].q_at, 0);
+    g.ring = __shfl_sync(~0u, sh.seg[at].ring, 0);
     if (g.n == 0) return true;
     for (int s = 0; s <= g.pair; ++s)
-      if (!att_wait(sh, p, &sh.q_full[(g.q_at + s) & 1], (g.q_at + s) / 2)) return false;
+      if (!att_wait_warp(sh, p, &sh.q_full[(g.q_at + s) & 1], (g.q_at + s) / 2)) return false;
     if (g.pair) {
       for (int i = 0; i <= g.n; ++i) {
         const unsigned k = g.ring + att_k_at(true, i);
@@ -483,9 +495,10 @@ __device__ __forceinline__ bool att_products(AttShared& sh, const AttendParams& 
         }
       }
     }
-    for (int s = 0; s <= g.pair; ++s) mma_commit(&sh.q_empty[(g.q_at + s) & 1]);
-    mma_commit(&sh.o_full);
-    mbar_arrive(&sh.seg_empty[at]);
+    for (int s = 0; s <= g.pair; ++s) mma_commit(&sh.q_empty[(g.q_at + s) & 1], one);
+    mma_commit(&sh.o_full, one);
+    if (one) mbar_arrive(&sh.seg_empty[at]);
+    __syncwarp();
   }
 }
 
@@ -568,39 +581,45 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
         const int end = min(pos - j0 + 1, kAttTile);
         const int from = p.window && pos >= p.window ? pos - p.window + 1 - j0 : -j0;
         const int sink_end = p.sinks - j0;
-        auto hide = [&](float* f, int at) {  // columns at .. at + 31 that the row does not see
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (at + k >= end || (at + k < from && at + k >= sink_end)) f[k] = p.hidden;
-        };
-        // The scores are read twice, 32 columns ahead of their use, for their maximum and
-        // for the weights: 128 of them do not fit the registers beside everything else. Both
-        // loops are kept rolled: straight-line code for one warp waits for its instructions.
-        float f[2][32];
-        tmem_ld32(tmem_s, f[0]);
-        float top[4] = {p.hidden, p.hidden, p.hidden, p.hidden};
-        auto raise = [&](float* f, int at) {
-          if (!all_seen) hide(f, at);
-          if (p.c > 0.f) {
-#pragma unroll
-            for (int y = 0; y < 32; y += 8)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) top[z] = fmaxf(fmaxf(top[z], f[y + z]), f[y + z + 4]);
-          } else {
-#pragma unroll
-            for (int y = 0; y < 32; y += 8)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) top[z] = fminf(fminf(top[z], f[y + z]), f[y + z + 4]);
-          }
-        };
+        if (!all_seen) {
+          // Edge tiles: what a row does not see is overwritten in S first, 32 columns at a
+          // time in a rolled loop, so that the code below has no second form for them.
 #pragma unroll 1
-        for (int k = 0; k < 128; k += 64) {
-          tmem_wait_ld(f[0]);
-          tmem_ld32(tmem_s + k + 32, f[1]);
-          raise(f[0], k);
-          tmem_wait_ld(f[1]);
-          tmem_ld32(tmem_s + (k ^ 64), f[0]);
-          raise(f[1], k + 32);
+          for (int k = 0; k < kAttTile; k += 32) {
+            // columns [0, sink_end) and [from, end) of these 32, as bits
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+            const uint32_t seen = below(end - k) & (~below(from - k) | below(sink_end - k));
+            if (__all_sync(~0u, seen == ~0u)) continue;
+            float x[32];
+            tmem_ld32(tmem_s + k, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!(seen >> y & 1)) x[y] = p.hidden;
+            tmem_st32(tmem_s + k, x);
+          }
+          tmem_wait_st();
+        }
+        float f[128];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32(tmem_s + 32 * k, f + 32 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_wait_ld(f + 32 * k);
+        float top[4];
+        if (p.c > 0.f) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            top[z] = fmaxf(f[z], f[z + 4]);
+#pragma unroll
+            for (int y = 8; y < 128; y += 8) top[z] = fmaxf(fmaxf(top[z], f[y + z]), f[y + z + 4]);
+          }
+        } else {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            top[z] = fminf(f[z], f[z + 4]);
+#pragma unroll
+            for (int y = 8; y < 128; y += 8) top[z] = fminf(fminf(top[z], f[y + z]), f[y + z + 4]);
+          }
         }
         const float now =
             fmaxf(m, fmaxf(fmaxf(top[0] * p.c, top[1] * p.c), fmaxf(top[2] * p.c, top[3] * p.c)));
@@ -610,42 +629,32 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
           l *= keep;
           if (grown) m = now;
           if (i >= step) {  // O holds earlier tiles
+#pragma unroll 1
+            for (int k = 0; k < DP; k += 16) {
+              float o[16];
+              tmem_ld16(tmem_o + s * 128 + k, o);
 #pragma unroll
-            for (int k = 0; k < DP; k += 32) {
-              float o[32];
-              tmem_ld32(tmem_o + s * 128 + k, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] *= keep;
-              tmem_st32(tmem_o + s * 128 + k, o);
+              for (int y = 0; y < 16; ++y) o[y] *= keep;
+              tmem_st16(tmem_o + s * 128 + k, o);
             }
           }
         }
         const float shift = kBias - (m == -INFINITY ? 0.f : m);
         const unsigned long long c2 = f2_pack(p.c, p.c), shift2 = f2_pack(shift, shift);
         unsigned long long sum2[2] = {0, 0};
-        uint32_t w[32];
-        auto weigh = [&](float* f, int at, uint32_t* w) {
-          if (!all_seen) hide(f, at);
 #pragma unroll
-          for (int y = 0; y < 16; ++y) {
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w[32];
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {
             float a, b;
-            f2_unpack(f2_fma(f2_pack(f[2 * y], f[2 * y + 1]), c2, shift2), a, b);
+            f2_unpack(f2_fma(f2_pack(f[64 * k + 2 * y], f[64 * k + 2 * y + 1]), c2, shift2), a, b);
             a = ex2(a);
             b = ex2(b);
             sum2[y & 1] = f2_add(sum2[y & 1], f2_pack(a, b));
             w[y] = pack2<BF16>(a, b);
           }
-        };
-#pragma unroll 1
-        for (int k = 0; k < 128; k += 64) {
-          tmem_wait_ld(f[0]);
-          tmem_ld32(tmem_s + k + 32, f[1]);
-          weigh(f[0], k, w);
-          tmem_wait_ld(f[1]);
-          if (k == 0) tmem_ld32(tmem_s + 64, f[0]);
-          weigh(f[1], k + 32, w + 16);
-          tmem_st32(tmem_s + k / 2, w);  // P over columns of S that have been read
+          tmem_st32(tmem_s + 32 * k, w);
         }
         float a, b;
         f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
@@ -820,8 +829,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       } else if (warp == 11) {
         att_load<DP, true>(sh, p, q_smem, kv_smem, lane);
       } else if (warp == 9) {
-        if (lane == 0 && !att_products<DP, BF16>(sh, p, q_smem, kv_smem)) {
-          mma_commit(&sh.drain);
+        if (!att_products<DP, BF16>(sh, p, q_smem, kv_smem)) {
+          mma_commit(&sh.drain, elect_one());
           for (int i = 0; i < 1024; ++i)
             if (mbar_try(&sh.drain, 0)) break;
         }
