@@ -10,10 +10,12 @@
 //                   P rounded to the cache's type and written over S
 //   O += P V        tcgen05, P from TMEM, V in shared memory, O (fp32) in TMEM
 //
-// with c = scale * log2(e). O is rescaled only when a row's maximum has grown by
-// more than 2^8 since the last time: until then P may exceed 1, which costs no
-// precision (bf16 and fp32 have the range; for fp16, P is kept 2^7 above 1 at
-// most 2^15 and reaches down to 2^-31 of the row's largest).
+// with c = scale * log2(e). m is the maximum of the row's first tile; it and O
+// follow a higher one only when that has passed it by 2^32 (fp16: 2^4), and one
+// tile late, so that no weight waits for its tile's maximum: P may then exceed 1,
+// which costs no precision (bf16 and fp32 have the range; fp16's P starts at 2^7,
+// may reach 2^15 and goes down to 2^-31 of it). A tile that would go further (2^64,
+// fp16: 2^8) has its maximum taken first after all.
 //
 // Two streams of S and O run side by side in one block, so that one's products
 // cover the other's softmax: two tiles of rows over the same keys where a unit
@@ -27,8 +29,8 @@
 // row of a unit sees are not in the list.
 //
 // Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 and 11 the loaders (TMA,
-// through the block table), 9 the tensor cores' issuer, 10 the walk over the
-// list; the last four give registers to the softmax warps.
+// through the block table; 11 also walks over the list), 9 and 10 the issuers of
+// the two streams' products; the last four give registers to the softmax warps.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -45,17 +47,17 @@ namespace sv {
 
 constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
 constexpr int kAttThreads = 384;  // 12 warps, at most 168 registers each at launch
-constexpr int kAttRegsMany = 216, kAttRegsFew = 72;  // 2 * 216 + 72 = 3 * 168
+constexpr int kAttRegsMany = 208, kAttRegsFew = 88;  // 2 * 208 + 88 = 3 * 168
 constexpr int kAttSegs = 4;       // list entries ahead of the slowest warp
-constexpr float kAttGrow = 8.f;   // log2 of how far a row's maximum may grow unscaled
-
-constexpr int kAttSharedBytes = 3072;  // barriers and the like, beside the tiles
 
 template <int DP>
 struct AttCfg {
   static constexpr int kTileBytes = kAttTile * DP * 2;
   static constexpr int kStages = DP == 128 ? 5 : 10;  // of one K or V tile each
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + kAttSharedBytes;
+  // Barriers go by a longer ring than the tiles: no warp is ever kRing loads behind another,
+  // so a phase's parity says which load is meant, whichever of them a warp waits for.
+  static constexpr int kRing = DP == 128 ? 16 : 32;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + (DP == 128 ? 3072 : 4096);
 };
 
 struct AttendParams {
@@ -191,11 +193,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-struct AttShared {
-  uint64_t kv_full[10], kv_empty[10];
-  uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2];
-  uint64_t o_full, o_free, ml_full, drain;
+struct AttBase {
+  uint64_t q_full[4], q_empty[2];
+  uint64_t s_full[2], p_half[2], p_full[2];
+  uint64_t turn[2];
+  uint64_t o_full, o_free, ml_full, edge_full, drain[2];
   uint64_t seg_full[kAttSegs], seg_empty[kAttSegs];
   AttSeg seg[kAttSegs];
   float2 ml[2][kAttTile];
@@ -206,12 +208,19 @@ struct AttShared {
   uint32_t tmem;
   int stop;
 };
+template <int DP>
+struct AttShared : AttBase {
+  uint64_t kv_full[AttCfg<DP>::kRing], kv_empty[AttCfg<DP>::kRing];
+};
+static_assert(sizeof(AttShared<128>) <= 3072 && sizeof(AttShared<64>) <= 4096,
+              "shared memory beside the tiles");
 
-static_assert(sizeof(AttShared) <= kAttSharedBytes, "shared memory beside the tiles");
-
-// A bounded wait; once one has run out every later one returns at once.
-__device__ __forceinline__ bool att_wait(AttShared& sh, const AttendParams& p, uint64_t* bar,
+// A bounded wait; once one has run out every later one returns at once. The first probes
+// carry no time limit of their own: one with a limit costs three times as much.
+__device__ __forceinline__ bool att_wait(AttBase& sh, const AttendParams& p, uint64_t* bar,
                                          uint32_t parity) {
+  for (int i = 0; i < 256; ++i)
+    if (mbar_poll(bar, parity & 1)) return true;
   for (uint32_t i = 0; i < kTryLimit; ++i) {
     if (mbar_try(bar, parity & 1)) return true;
     if (*(volatile int*)&sh.stop) return false;
@@ -222,7 +231,7 @@ __device__ __forceinline__ bool att_wait(AttShared& sh, const AttendParams& p, u
 }
 
 // The same for a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool att_wait_warp(AttShared& sh, const AttendParams& p, uint64_t* bar,
+__device__ __forceinline__ bool att_wait_warp(AttBase& sh, const AttendParams& p, uint64_t* bar,
                                               uint32_t parity) {
   return __all_sync(~0u, att_wait(sh, p, bar, parity));
 }
@@ -241,112 +250,119 @@ __device__ __forceinline__ int att_tile(const AttSeg& g, int i) {
   return u < g.gap_at ? u : u + g.gap;
 }
 
-// ---- warp 10: the walk over this block's part of the list
+// ---- the walk over this block's part of the list, by one thread, an entry at a time
 
-__device__ __forceinline__ void att_walk(AttShared& sh, const AttendParams& p, long long begin,
-                                         long long end, long long total, int blocks, int run) {
-  int b = sh.start_run * run;
-  long long before = sh.start_before;  // tiles before request b
-  int lo = 0, hi = 0, len = 0, head = 0, u = 0;
-  long long skip = begin;  // tiles of the list already given out
-  bool fresh = true;
-  int q_at = 0, entry = 0;
-  unsigned ring = 0;
-  AttJoin join = {-1, 0, 0, 0};
-  p.join[blockIdx.x] = join;
-  const int step = 2 * p.tile_tokens;
-  long long rest = 0;  // tiles of the current unit already given out
-  while (skip < end) {
-    if (fresh) {  // request b
-      if (b >= p.B) break;  // not reached: the parts end with the list
-      len = attend_request(p, b, lo, hi);
-      const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-      const long long per_head = units.before(units.count);
-      const long long all = per_head * p.kv_heads;
-      if (all == 0 || before + all <= skip) {
-        before += all;
-        ++b;
-        continue;
-      }
-      head = (int)((skip - before) / per_head);
-      const long long x = skip - before - head * per_head;
-      int u0 = 0, u1 = units.count - 1;  // the last unit that starts at or before x
-      while (u0 < u1) {
-        const int mid = (u0 + u1 + 1) >> 1;
-        if (units.before(mid) <= x) u0 = mid; else u1 = mid - 1;
-      }
-      u = u0;
-      rest = x - units.before(u);
-      before += all;
-      fresh = false;
-    }
-    const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-    const long long n = units.tiles(u);
-    const long long take = min(n - rest, end - skip);
+struct AttWalk {
+  long long skip, end;   // tiles of the list given out, and where the part ends
+  long long before;      // tiles before request b
+  long long rest;        // tiles of the current unit given out
+  long long total;
+  int blocks, b, lo, hi, len, head, u, q_at, entry;
+  unsigned ring;
+  bool fresh;
+  AttJoin join;
+
+  __device__ __forceinline__ AttWalk(const AttBase& sh, long long begin, long long end_,
+                                     long long total_, int blocks_, int run)
+      : skip(begin), end(end_), before(sh.start_before), rest(0), total(total_), blocks(blocks_),
+        b(sh.start_run * run), lo(0), hi(0), len(0), head(0), u(0), q_at(0), entry(0), ring(0),
+        fresh(true), join{-1, 0, 0, 0} {}
+
+  // Puts the next entry, or the end mark, into the ring; nothing once that is there.
+  __device__ __forceinline__ bool publish(AttBase& sh, const AttendParams& p) {
+    if (entry < 0) return true;
+    const int step = 2 * p.tile_tokens, at = entry % kAttSegs;
     AttSeg g;
-    g.n = (int)take;
-    g.i0 = (int)rest;
-    g.b = b;
-    g.head = head;
-    g.token = lo + u * step;
-    g.tokens = min(step, hi - g.token);
-    g.pos = (int)(units.p0 + (long long)u * step);
-    g.lo = (int)units.lo(u);
-    g.hi = (int)max(units.hi(u), 0ll);
-    g.gap = (int)units.gap(u);
-    g.gap_at = g.gap ? (int)units.sink_tiles : 0x7fffffff;
-    g.pair = g.tokens > p.tile_tokens;
-    g.q_at = q_at;
-    g.ring = ring;
-    const bool starts = rest == 0, ends = rest + take == n;
-    g.slot = starts && ends ? -1 : starts ? 1 : 0;
-    if (starts && !ends) {
-      // the block that holds the unit's last tile
-      const long long last = skip + n - 1;
-      join.last = (int)(((last + 1) * blocks - 1) / total);
-      join.head = head;
-      join.token = g.token;
-      join.tokens = g.tokens;
-    }
-    const int at = entry % kAttSegs;
-    if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return;
-    sh.seg[at] = g;
-    mbar_arrive(&sh.seg_full[at]);
-    ++entry;
-    q_at += g.pair ? 2 : 1;
-    ring += 2 * g.n;
-    skip += take;
-    rest += take;
-    if (rest == n) {
-      rest = 0;
-      if (++u == units.count) {
-        u = 0;
-        if (++head == p.kv_heads) {
+    g.n = 0;
+    while (skip < end && g.n == 0 && b < p.B) {
+      if (fresh) {  // request b
+        len = attend_request(p, b, lo, hi);
+        const AttUnits units(len, hi - lo, step, p.window, p.sinks);
+        const long long per_head = units.before(units.count);
+        const long long all = per_head * p.kv_heads;
+        if (all == 0 || before + all <= skip) {
+          before += all;
           ++b;
-          fresh = true;
+          continue;
+        }
+        const long long x = skip - before;
+        head = (int)(x / per_head);
+        rest = x - head * per_head;
+        int u0 = 0, u1 = units.count - 1;  // the last unit that starts at or before there
+        while (u0 < u1) {
+          const int mid = (u0 + u1 + 1) >> 1;
+          if (units.before(mid) <= rest) u0 = mid; else u1 = mid - 1;
+        }
+        u = u0;
+        rest -= units.before(u);
+        before += all;
+        fresh = false;
+      }
+      const AttUnits units(len, hi - lo, step, p.window, p.sinks);
+      const long long n = units.tiles(u);
+      const long long take = min(n - rest, end - skip);
+      g.n = (int)take;
+      g.i0 = (int)rest;
+      g.b = b;
+      g.head = head;
+      g.token = lo + u * step;
+      g.tokens = min(step, hi - g.token);
+      g.pos = (int)(units.p0 + (long long)u * step);
+      g.lo = (int)units.lo(u);
+      g.hi = (int)max(units.hi(u), 0ll);
+      g.gap = (int)units.gap(u);
+      g.gap_at = g.gap ? (int)units.sink_tiles : 0x7fffffff;
+      g.pair = g.tokens > p.tile_tokens;
+      g.q_at = q_at;
+      g.ring = ring;
+      const bool starts = rest == 0, ends = rest + take == n;
+      g.slot = starts && ends ? -1 : starts ? 1 : 0;
+      if (starts && !ends) {
+        // the block that holds the unit's last tile
+        join.last = (int)(((skip + n) * blocks - 1) / total);
+        join.head = head;
+        join.token = g.token;
+        join.tokens = g.tokens;
+      }
+      q_at += g.pair ? 2 : 1;
+      ring += 2 * g.n;
+      skip += take;
+      rest += take;
+      if (rest == n) {
+        rest = 0;
+        if (++u == units.count) {
+          u = 0;
+          if (++head == p.kv_heads) {
+            ++b;
+            fresh = true;
+          }
         }
       }
     }
+    if (g.n == 0) p.join[blockIdx.x] = join;
+    if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return false;
+    sh.seg[at] = g;
+    mbar_arrive(&sh.seg_full[at]);
+    entry = g.n ? entry + 1 : -1;
+    return true;
   }
-  p.join[blockIdx.x] = join;
-  const int at = entry % kAttSegs;
-  if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return;
-  sh.seg[at].n = 0;
-  mbar_arrive(&sh.seg_full[at]);
-}
+};
 
 // ---- warps 8 and 11: Q and K, and V tiles by TMA (two warps: with small pages it is the
-// issue of the loads that takes the time)
+// issue of the loads that takes the time). The one for V also does the walk, two entries
+// ahead of its loads.
 
 template <int DP, bool V>
-__device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, char* q_smem,
-                                         char* kv_smem, int lane) {
+__device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& p, char* q_smem,
+                                         char* kv_smem, int lane, AttWalk* walk) {
   using Cfg = AttCfg<DP>;
   constexpr int kBlocks = DP / 64, kBlockBytes = kAttTile * 128;
   const int page = 1 << p.page_shift;
   const int box = min(page, kAttTile);         // tokens of one load
   const int boxes = kAttTile / box;            // of a tile
-  unsigned issued = 0;
+  unsigned issued = 0, edges = 0;
+  if (V && lane == 0 && walk->publish(sh, p)) walk->publish(sh, p);
+  __syncwarp();
   for (int e = 0;; ++e) {
     const int at = e % kAttSegs;
     if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) break;
@@ -357,17 +373,18 @@ __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, c
       const int x = g.q_at + s, slot = x & 1;
       ok = ok && att_wait_warp(sh, p, &sh.q_empty[slot], (x / 2 + 1) & 1);
       if (ok && lane == 0) {
-        mbar_arrive_expect_tx(&sh.q_full[slot], kBlocks * p.tile_tokens * p.G * 128);
+        mbar_arrive_expect_tx(&sh.q_full[x & 3], kBlocks * p.tile_tokens * p.G * 128);
         for (int k = 0; k < kBlocks; ++k)
           tma_load_4d(q_smem + slot * Cfg::kTileBytes + k * kBlockBytes, &p.q_map, 64 * k, 0,
-                      g.head, g.token + s * p.tile_tokens, &sh.q_full[slot]);
+                      g.head, g.token + s * p.tile_tokens, &sh.q_full[x & 3]);
       }
       __syncwarp();
     }
     const int* table = p.table + g.b * p.table_stride;
+    const int sinks = min(p.sinks, g.lo);
     for (int i = 0; ok && i < g.n; ++i) {
-      const int j = att_tile(g, i) * kAttTile + lane * box;  // the lane's first token
-      bool live = lane < boxes && j < g.hi && (j + box > g.lo || j < p.sinks);
+      const int j0 = att_tile(g, i) * kAttTile, j = j0 + lane * box;  // the lane's first token
+      bool live = lane < boxes && j < g.hi && (j + box > g.lo || j < sinks);
       int number = 0;
       if (live) {
         number = __ldg(table + (j >> p.page_shift));
@@ -378,124 +395,129 @@ __device__ __forceinline__ void att_load(AttShared& sh, const AttendParams& p, c
       }
       const int count = __popc(__ballot_sync(~0u, live));
       const unsigned r = g.ring + (V ? att_v_at(g.pair, i, g.n) : att_k_at(g.pair, i));
-      const unsigned slot = r % Cfg::kStages;
-      ok = att_wait_warp(sh, p, &sh.kv_empty[slot], (r / Cfg::kStages + 1) & 1);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], count * kBlocks * box * 128);
+      char* tile = kv_smem + (r % Cfg::kStages) * Cfg::kTileBytes;
+      uint64_t* full = &sh.kv_full[r % Cfg::kRing];
+      if (r >= Cfg::kStages) {  // what the tile's place held has been used
+        const unsigned x = r - Cfg::kStages;
+        ok = att_wait_warp(sh, p, &sh.kv_empty[x % Cfg::kRing], x / Cfg::kRing);
+        if (!ok) break;
+      }
+      // V's rows that no row of the unit sees may hold anything, and P is 0 there: they are
+      // zeroed before the tile counts as loaded.
+      const bool clear = V && j0 + kAttTile > sinks && !(j0 >= g.lo && j0 + kAttTile <= g.hi);
+      uint64_t* landed = clear ? &sh.edge_full : full;
+      if (lane == 0) mbar_arrive_expect_tx(landed, count * kBlocks * box * 128);
       __syncwarp();
       if (live) {
-        char* dst = kv_smem + slot * Cfg::kTileBytes + lane * box * 128;
+        char* dst = tile + lane * box * 128;
         for (int k = 0; k < kBlocks; ++k)
           tma_load_4d(dst + k * kBlockBytes, V ? &p.v_map : &p.k_map, 64 * k, j & (page - 1),
-                      g.head, number, &sh.kv_full[slot]);
+                      g.head, number, landed);
       }
+      __syncwarp();
       issued = r + 1;
+      if (clear) {
+        ok = att_wait_warp(sh, p, &sh.edge_full, edges++);
+        if (!ok) break;
+        for (int y = lane; y < kAttTile; y += 32) {
+          if (j0 + y < sinks || (j0 + y >= g.lo && j0 + y < g.hi)) continue;
+#pragma unroll
+          for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *(uint4*)(tile + k * kBlockBytes + y * 128 + 16 * x) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+      }
     }
     if (!ok) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.seg_empty[at]);
+    if (V && lane == 0) walk->publish(sh, p);
+    __syncwarp();
   }
   // A wait ran out: let the loads in flight land before the block's end (those of the other
   // of the two warps among them: a wait too many only takes its limit).
   for (unsigned r = issued > Cfg::kStages ? issued - Cfg::kStages : 0; r < issued; ++r)
     for (int i = 0; i < 1024; ++i)
-      if (mbar_try(&sh.kv_full[r % Cfg::kStages], (r / Cfg::kStages) & 1)) break;
+      if (mbar_try(&sh.kv_full[r % Cfg::kRing], (r / Cfg::kRing) & 1)) break;
 }
 
-// ---- warp 9: the products, issued by one of its threads
+// ---- warps 9 and 10: the products of stream 0 and 1, issued by one thread of each.
+// A thread that issues is held until the tensor cores have all but caught up, so a warp for
+// each stream does its waiting for P, K and V while the other's products run. They take
+// turns (PV of a tile and QK of the stream's next), which keeps the streams half a period
+// apart: left to themselves they fall into step, and the tensor cores idle through both
+// softmaxes. A commit is dear, so there is one for each tile: S of tile i tells that K of
+// tile i and V of the stream's tile before have been used too, and the softmax warps, which
+// wait for it, hand those back.
 
 template <int DP, bool BF16>
-__device__ __forceinline__ bool att_products(AttShared& sh, const AttendParams& p, char* q_smem,
-                                             char* kv_smem) {
+__device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendParams& p,
+                                             char* q_smem, char* kv_smem, const int s) {
   using Cfg = AttCfg<DP>;
   constexpr uint32_t kQK = mma_kind(BF16, false, kAttTile, kAttTile);
   constexpr uint32_t kPV = mma_kind(BF16, true, kAttTile, DP);
-  const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
+  const uint32_t tmem_s = __shfl_sync(~0u, sh.tmem, 0) + s * 128, tmem_o = tmem_s + 256;
   const bool one = elect_one();
   // descriptors of the first tiles; others by what is added to their addresses (in 16 bytes)
   const uint64_t q0 = mma_desc(smem_addr(q_smem), 16), k0 = mma_desc(smem_addr(kv_smem), 16);
   const uint64_t v0 = mma_desc(smem_addr(kv_smem), kAttTile * 128);
   constexpr unsigned kTile = Cfg::kTileBytes / 16;
-  unsigned p_count[2] = {0, 0};
-  auto qk = [&](int s, int q_slot, unsigned k_ring) {
-    const uint64_t q = q0 + q_slot * kTile, k = k0 + (k_ring % Cfg::kStages) * kTile;
-#pragma unroll
-    for (int x = 0; x < DP / 16; ++x) {
-      const unsigned at = ((x / 4) * (kAttTile * 128) + (x % 4) * 32) / 16;
-      mma_ss(tmem + s * 128, q + at, k + at, kQK, x > 0, one);
-    }
-    mma_commit(&sh.s_full[s], one);
-  };
-  auto pv = [&](int s, unsigned v_ring, bool add) {
-    const uint64_t v = v0 + (v_ring % Cfg::kStages) * kTile;
-#pragma unroll
-    for (int x = 0; x < kAttTile / 16; ++x)
-      mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * x, v + x * (16 * 128 / 16), kPV,
-             add || x > 0, one);
-  };
+  unsigned p_count = 0, turn = 0;
   auto loaded = [&](unsigned r) {
-    return att_wait_warp(sh, p, &sh.kv_full[r % Cfg::kStages], r / Cfg::kStages);
-  };
-  auto release = [&](unsigned r) { mma_commit(&sh.kv_empty[r % Cfg::kStages], one); };
-  // P of stream s written, and the V tile there.
-  // Before a segment's first PV the results of the segment before it have been read by all.
-  auto weights = [&](int s, unsigned v_ring, int e) {
-    if (!loaded(v_ring)) return false;
-    if (e >= 0 && !att_wait_warp(sh, p, &sh.o_free, e + 1)) return false;
-    if (!att_wait_warp(sh, p, &sh.p_full[s], p_count[s]++)) return false;
-    tmem_fence_after();
-    return true;
+    return att_wait_warp(sh, p, &sh.kv_full[r % Cfg::kRing], r / Cfg::kRing);
   };
   for (int e = 0;; ++e) {
     const int at = e % kAttSegs;
     if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) return false;
-    struct {
-      int n, pair, q_at;
-      unsigned ring;
-    } g;
-    g.n = __shfl_sync(~0u, sh.seg[at].n, 0);
-    g.pair = __shfl_sync(~0u, sh.seg[at].pair, 0);
-    g.q_at = __shfl_sync(~0u, sh.seg[at].q_at, 0);
-    g.ring = __shfl_sync(~0u, sh.seg[at].ring, 0);
-    if (g.n == 0) return true;
-    for (int s = 0; s <= g.pair; ++s)
-      if (!att_wait_warp(sh, p, &sh.q_full[(g.q_at + s) & 1], (g.q_at + s) / 2)) return false;
-    if (g.pair) {
-      for (int i = 0; i <= g.n; ++i) {
-        const unsigned k = g.ring + att_k_at(true, i);
-        const unsigned v = g.ring + att_v_at(true, i - 1, g.n);
-        for (int s = 0; s < 2; ++s) {
-          if (i > 0) {
-            if (!weights(s, v, i == 1 && s == 0 ? e : -1)) return false;
-            pv(s, v, i > 1);
-            if (s) release(v);
+    const int n = __shfl_sync(~0u, sh.seg[at].n, 0);
+    if (n == 0) return true;
+    const bool pair = __shfl_sync(~0u, sh.seg[at].pair, 0);
+    const int q_at = __shfl_sync(~0u, sh.seg[at].q_at, 0) + (pair ? s : 0);
+    const unsigned ring = __shfl_sync(~0u, sh.seg[at].ring, 0);
+    if (!att_wait_warp(sh, p, &sh.q_full[q_at & 3], q_at / 4)) return false;
+    const int step = pair ? 1 : 2, first = pair ? 0 : s;
+    // The same number of turns for both streams, whether they have a tile for it or not.
+    const int turns = pair ? n + 1 : (n + 3) / 2;
+#pragma unroll 1
+    for (int t = 0; t < turns; ++t) {
+      const int next = first + t * step, last = next - step;  // QK of the one, PV of the other
+      const unsigned k = ring + att_k_at(pair, next), v = ring + att_v_at(pair, last, n);
+      const bool has_pv = t > 0 && last < n, has_qk = next < n;
+      // the results of the segment before (e > 0) have been read by all
+      if (t == 1 && !att_wait_warp(sh, p, &sh.o_free, e + 1)) return false;
+      if (has_qk && !loaded(k)) return false;
+      if (has_pv && (!loaded(v) || !att_wait_warp(sh, p, &sh.p_half[s], p_count))) return false;
+      if (!att_wait_warp(sh, p, &sh.turn[s], turn + 1 - s)) return false;
+      ++turn;
+      tmem_fence_after();
+      if (has_pv) {
+        const uint64_t vd = v0 + (v % Cfg::kStages) * kTile;
+#pragma unroll
+        for (int x = 0; x < kAttTile / 16; ++x) {
+          if (x == kAttTile / 32) {  // half of P at a time, as it comes
+            if (!att_wait_warp(sh, p, &sh.p_full[s], p_count)) return false;
+            tmem_fence_after();
           }
-          if (i < g.n) {
-            if (s == 0 && !loaded(k)) return false;
-            qk(s, (g.q_at + s) & 1, k);
-            if (s) release(k);
-          }
+          mma_ts(tmem_o, tmem_s + 8 * x, vd + x * (16 * 128 / 16), kPV, t > 1 || x > 0, one);
+        }
+        ++p_count;
+      }
+      if (has_qk) {
+        const uint64_t qd = q0 + (q_at & 1) * kTile, kd = k0 + (k % Cfg::kStages) * kTile;
+#pragma unroll
+        for (int x = 0; x < DP / 16; ++x) {
+          const unsigned y = ((x / 4) * (kAttTile * 128) + (x % 4) * 32) / 16;
+          mma_ss(tmem_s, qd + y, kd + y, kQK, x > 0, one);
         }
       }
-    } else {
-      for (int i = 0; i < g.n + 2; ++i) {
-        const int s = i & 1;
-        const int x = i - 2;  // the tile whose weights are next
-        if (x >= 0 && x < g.n) {
-          const unsigned v = g.ring + att_v_at(false, x, g.n);
-          if (!weights(s, v, x == 0 ? e : -1)) return false;
-          pv(s, v, x >= 2);
-          release(v);
-        }
-        if (i < g.n) {
-          const unsigned k = g.ring + att_k_at(false, i);
-          if (!loaded(k)) return false;
-          qk(s, g.q_at & 1, k);
-          release(k);
-        }
-      }
+      if (one) mbar_arrive(&sh.turn[s ^ 1]);
+      if (has_qk) mma_commit(&sh.s_full[s], one);
+      __syncwarp();
     }
-    for (int s = 0; s <= g.pair; ++s) mma_commit(&sh.q_empty[(g.q_at + s) & 1], one);
     mma_commit(&sh.o_full, one);
     if (one) mbar_arrive(&sh.seg_empty[at]);
     __syncwarp();
@@ -504,17 +526,65 @@ __device__ __forceinline__ bool att_products(AttShared& sh, const AttendParams& 
 
 // ---- warps 0-7: softmax, rescaling, results
 
-// Rows of P V that no row of the unit sees may hold anything: zero them.
-template <int DP>
-__device__ __forceinline__ void att_clear_dead(char* v_tile, int row, bool dead) {
-  if (dead) {
+// Overwrite the scores that the row at `pos` does not see, 32 columns at a time
+// in a rolled loop: edge tiles are few, and the code of the others stays short.
+__device__ __forceinline__ void att_hide(uint32_t tmem_s, int pos, int j0, int window, int sinks,
+                                      float hidden) {
+  const int end = min(pos - j0 + 1, kAttTile);
+  const int from = window && pos >= window ? pos - window + 1 - j0 : -j0;
+  const int sink_end = sinks - j0;
+#pragma unroll 1
+  for (int k = 0; k < kAttTile; k += 32) {
+    // columns [0, sink_end) and [from, end) of these 32, as bits
+    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+    const uint32_t seen = below(end - k) & (~below(from - k) | below(sink_end - k));
+    if (__all_sync(~0u, seen == ~0u)) continue;
+    float x[32];
+    tmem_ld32(tmem_s + k, x);
+    tmem_wait_ld(x);
 #pragma unroll
-    for (int k = 0; k < DP / 64; ++k)
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        *(uint4*)(v_tile + k * (kAttTile * 128) + row * 128 + 16 * x) = make_uint4(0, 0, 0, 0);
+    for (int y = 0; y < 32; ++y)
+      if (!(seen >> y & 1)) x[y] = hidden;
+    tmem_st32(tmem_s + k, x);
   }
-  fence_async_shared();
+  tmem_wait_st();
+}
+
+template <int DP>
+__device__ __forceinline__ void att_rescale(uint32_t tmem_o, float keep) {
+#pragma unroll 1
+  for (int k = 0; k < DP; k += 32) {
+    float o[32];
+    tmem_ld32(tmem_o + k, o);
+    tmem_wait_ld(o);
+#pragma unroll
+    for (int y = 0; y < 32; ++y) o[y] *= keep;
+    tmem_st32(tmem_o + k, o);
+  }
+}
+
+// Take the maximum of a tile's scores into m, and l and O (if it holds
+// anything) to it.
+template <int DP>
+__device__ __forceinline__ void att_settle(uint32_t tmem_s, uint32_t tmem_o, float c, bool filled,
+                                           float& m, float& l) {
+  float now = m;
+#pragma unroll 1
+  for (int k = 0; k < kAttTile; k += 64) {
+    float x[64];
+    tmem_ld32(tmem_s + k, x);
+    tmem_ld32(tmem_s + k + 32, x + 32);
+    tmem_wait_ld(x);
+    tmem_wait_ld(x + 32);
+    float top[4] = {now, now, now, now};
+#pragma unroll
+    for (int y = 0; y < 64; ++y) top[y & 3] = fmaxf(top[y & 3], x[y] * c);
+    now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  }
+  const float keep = now == -INFINITY ? 1.f : ex2(m - now);
+  m = now;
+  l *= keep;
+  if (filled) att_rescale<DP>(tmem_o, keep);
 }
 
 // log2 of what every P and l carries beside 2^-m: fp16 has few exponents below 1.
@@ -544,10 +614,10 @@ __device__ __forceinline__ void att_store_out(const AttendParams& p, char* out, 
 }
 
 template <int DP, bool BF16>
-__device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p, char* kv_smem,
-                                            int warp, int lane) {
-  using Cfg = AttCfg<DP>;
+__device__ __forceinline__ void att_softmax(AttShared<DP>& sh, const AttendParams& p, int warp, int lane) {
   constexpr float kBias = att_bias<BF16>();
+  // Weights may pass 2^kBias by 2^kGrow before m and O follow, one tile late; by 2^kFar never.
+  constexpr float kGrow = BF16 ? 32.f : 4.f, kFar = BF16 ? 64.f : 8.f;
   const int s = warp >> 2, row = (warp & 3) * 32 + lane;
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t tmem_s = sh.tmem + lanes + s * 128;
@@ -566,113 +636,107 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
     const int pos = mine ? g.pos + tile0 + row_token : -1;
     const bool busy = (warp & 3) * 32 < tokens * p.G;  // rows in this warp
     const int first_pos = g.pos + tile0, last_pos = g.pos + tile0 + tokens - 1;
+    // A tile's K and V are free after both streams' products, or twice after the one's.
+    auto release = [&](unsigned r) {
+      mbar_arrive(&sh.kv_empty[r % AttCfg<DP>::kRing]);
+      if (!g.pair) mbar_arrive(&sh.kv_empty[r % AttCfg<DP>::kRing]);
+    };
     float m = -INFINITY, l = 0.f;
+    float over = 0.f;  // log2 of how far some weight so far has passed 2^(kBias)
     const int step = g.pair ? 1 : 2;
     for (int i = g.pair ? 0 : s; i < g.n; i += step) {
+      // what can be known before S is there
       const int j0 = att_tile(g, i) * kAttTile;
+      const bool all_seen = j0 + kAttTile - 1 <= first_pos &&
+                            (!p.window || j0 > last_pos - p.window || j0 + kAttTile <= p.sinks);
+      const bool grown = __any_sync(~0u, mine && over > kGrow);
       if (!att_wait_warp(sh, p, &sh.s_full[s], s_count)) return;
       ++s_count;
+      if ((warp & 3) == 0 && lane == 0) {
+        release(g.ring + att_k_at(g.pair, i));
+        if (i >= step) release(g.ring + att_v_at(g.pair, i - step, g.n));
+      }
       if (busy) {
         tmem_fence_after();
-        const bool all_seen =
-            j0 + kAttTile - 1 <= first_pos &&
-            (!p.window || j0 > last_pos - p.window || j0 + kAttTile <= p.sinks);
-        // otherwise tokens [0, sink_end) and [from, end) of the tile
-        const int end = min(pos - j0 + 1, kAttTile);
-        const int from = p.window && pos >= p.window ? pos - p.window + 1 - j0 : -j0;
-        const int sink_end = p.sinks - j0;
-        if (!all_seen) {
-          // Edge tiles: what a row does not see is overwritten in S first, 32 columns at a
-          // time in a rolled loop, so that the code below has no second form for them.
-#pragma unroll 1
-          for (int k = 0; k < kAttTile; k += 32) {
-            // columns [0, sink_end) and [from, end) of these 32, as bits
-            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
-            const uint32_t seen = below(end - k) & (~below(from - k) | below(sink_end - k));
-            if (__all_sync(~0u, seen == ~0u)) continue;
-            float x[32];
-            tmem_ld32(tmem_s + k, x);
-            tmem_wait_ld(x);
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!(seen >> y & 1)) x[y] = p.hidden;
-            tmem_st32(tmem_s + k, x);
-          }
-          tmem_wait_st();
+        if (!all_seen) att_hide(tmem_s, pos, j0, p.window, p.sinks, p.hidden);
+        // The maximum: of the first tile before its weights, later one tile behind them.
+        if (i < step) {
+          att_settle<DP>(tmem_s, tmem_o + s * 128, p.c, false, m, l);
+        } else if (grown) {
+          const float keep = over > kGrow ? ex2(-over) : 1.f;
+          if (over > kGrow) m += over, over = 0.f;
+          l *= keep;
+          att_rescale<DP>(tmem_o + s * 128, keep);
         }
         float f[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(tmem_s + 32 * k, f + 32 * k);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_wait_ld(f + 32 * k);
-        float top[4];
-        if (p.c > 0.f) {
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            top[z] = fmaxf(f[z], f[z + 4]);
-#pragma unroll
-            for (int y = 8; y < 128; y += 8) top[z] = fmaxf(fmaxf(top[z], f[y + z]), f[y + z + 4]);
-          }
-        } else {
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            top[z] = fminf(f[z], f[z + 4]);
-#pragma unroll
-            for (int y = 8; y < 128; y += 8) top[z] = fminf(fminf(top[z], f[y + z]), f[y + z + 4]);
-          }
-        }
-        const float now =
-            fmaxf(m, fmaxf(fmaxf(top[0] * p.c, top[1] * p.c), fmaxf(top[2] * p.c, top[3] * p.c)));
-        const bool grown = now > m + kAttGrow || (m == -INFINITY && now > m);
-        if (__any_sync(~0u, grown)) {
-          const float keep = grown ? ex2(m - now) : 1.f;
-          l *= keep;
-          if (grown) m = now;
-          if (i >= step) {  // O holds earlier tiles
-#pragma unroll 1
-            for (int k = 0; k < DP; k += 16) {
-              float o[16];
-              tmem_ld16(tmem_o + s * 128 + k, o);
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] *= keep;
-              tmem_st16(tmem_o + s * 128 + k, o);
-            }
-          }
-        }
-        const float shift = kBias - (m == -INFINITY ? 0.f : m);
-        const unsigned long long c2 = f2_pack(p.c, p.c), shift2 = f2_pack(shift, shift);
-        unsigned long long sum2[2] = {0, 0};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t w[32];
+        uint32_t w[32];
+        unsigned long long sum2[2];
+        const unsigned long long c2 = f2_pack(p.c, p.c);
+        auto weigh = [&](const float* f) {  // 64 columns
 #pragma unroll
           for (int y = 0; y < 32; ++y) {
-            float a, b;
-            f2_unpack(f2_fma(f2_pack(f[64 * k + 2 * y], f[64 * k + 2 * y + 1]), c2, shift2), a, b);
-            a = ex2(a);
-            b = ex2(b);
+            const float a = ex2(f[2 * y]), b = ex2(f[2 * y + 1]);
             sum2[y & 1] = f2_add(sum2[y & 1], f2_pack(a, b));
             w[y] = pack2<BF16>(a, b);
           }
-          tmem_st32(tmem_s + 32 * k, w);
+        };
+#pragma unroll 1
+        for (;;) {
+          const float shift = kBias - (m == -INFINITY ? 0.f : m);
+          const unsigned long long shift2 = f2_pack(shift, shift);
+          float top[4];
+          auto scaled = [&](float* f, bool first) {  // 64 columns and their maximum
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              f2_unpack(f2_fma(f2_pack(f[2 * y], f[2 * y + 1]), c2, shift2), f[2 * y],
+                        f[2 * y + 1]);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              top[z] = first ? f[z] : fmaxf(top[z], f[z]);
+              top[z] = fmaxf(top[z], f[z + 4]);
+#pragma unroll
+              for (int y = 8; y < 64; y += 8)
+                top[z] = fmaxf(fmaxf(top[z], f[y + z]), f[y + z + 4]);
+            }
+          };
+          tmem_ld32(tmem_s, f);
+          tmem_ld32(tmem_s + 32, f + 32);
+          tmem_wait_ld(f);
+          tmem_wait_ld(f + 32);
+          tmem_ld32(tmem_s + 64, f + 64);
+          tmem_ld32(tmem_s + 96, f + 96);
+          sum2[0] = sum2[1] = 0;
+          scaled(f, true);
+          weigh(f);
+          tmem_wait_ld(f + 64);
+          tmem_wait_ld(f + 96);
+          scaled(f + 64, false);
+          const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) - kBias;
+          const bool far = now > kFar || (m == -INFINITY && now > m);
+          if (!__any_sync(~0u, mine && far)) {
+            over = fmaxf(over, now);
+            break;
+          }
+          // A weight would leave its type's range: S is still whole, take its maximum first.
+          att_settle<DP>(tmem_s, tmem_o + s * 128, p.c, i >= step, m, l);
+          over = 0.f;
         }
+        // P over S, each half as soon as it is there
+        tmem_st32(tmem_s, w);
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_half[s]);
+        weigh(f + 64);
+        tmem_st32(tmem_s + 32, w);
         float a, b;
         f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
         l += a + b;
         tmem_wait_st();
         tmem_fence_before();
-      }
-      // V's rows that no row of the unit sees. Only now: S of tile i is there, so every load
-      // before K's of tile i has been used, and with it what V's slot held before (a wait for
-      // a barrier's phase is only sound once the phase before it is over).
-      const int sinks = min(p.sinks, g.lo);
-      if ((!g.pair || s == 0) && !(j0 >= g.lo && j0 + kAttTile <= g.hi) &&
-          j0 + kAttTile > sinks) {
-        const unsigned r = g.ring + att_v_at(g.pair, i, g.n);
-        if (!att_wait_warp(sh, p, &sh.kv_full[r % Cfg::kStages], r / Cfg::kStages)) return;
-        const int j = j0 + row;
-        att_clear_dead<DP>(kv_smem + (r % Cfg::kStages) * Cfg::kTileBytes, row,
-                           !(j < sinks || (j >= g.lo && j < g.hi)));
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_half[s]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[s]);
@@ -694,6 +758,14 @@ __device__ __forceinline__ void att_softmax(AttShared& sh, const AttendParams& p
       l = x.y * w[0] + y.y * w[1];
     }
     if (!att_wait_warp(sh, p, &sh.o_full, e)) return;
+    if ((warp & 3) == 0 && lane == 0) {
+      const int last = g.pair ? g.n - 1 : (g.n - 1 - s) / 2 * 2 + s;  // the stream's last tile
+      if (g.pair || s < g.n) release(g.ring + att_v_at(g.pair, last, g.n));
+      // Q: read by both streams, or each stream's own
+      const int q = (g.q_at + (g.pair ? s : 0)) & 1;
+      mbar_arrive(&sh.q_empty[q]);
+      if (g.pair) mbar_arrive(&sh.q_empty[q]);
+    }
     if (busy) {
       tmem_fence_after();
       const int half = g.pair ? DP : DP / 2;  // columns of this warp: stream s of a pair, or
@@ -753,26 +825,33 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   extern __shared__ __align__(1024) char smem[];
   char* q_smem = smem;
   char* kv_smem = smem + 2 * Cfg::kTileBytes;
-  AttShared& sh = *reinterpret_cast<AttShared*>(kv_smem + Cfg::kStages * Cfg::kTileBytes);
+  AttShared<DP>& sh = *reinterpret_cast<AttShared<DP>*>(
+      kv_smem + Cfg::kStages * Cfg::kTileBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < Cfg::kStages; ++i) {
+    for (int i = 0; i < Cfg::kRing; ++i) {
       mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_empty[i], 1);
+      mbar_init(&sh.kv_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.q_full[i + 2], 1);
+      mbar_init(&sh.q_empty[i], 2);
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_half[i], 4);
       mbar_init(&sh.p_full[i], 4);
     }
-    mbar_init(&sh.o_full, 1);
+    mbar_init(&sh.o_full, 2);
     mbar_init(&sh.ml_full, 8);
     mbar_init(&sh.o_free, 8);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.edge_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.turn[i], 1);
+      mbar_init(&sh.drain[i], 1);
+    }
     for (int i = 0; i < kAttSegs; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 11);
+      mbar_init(&sh.seg_empty[i], 12);
     }
     fence_mbar_init();
     sh.stop = 0;
@@ -817,30 +896,29 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     sh.start_run = tid;
     sh.start_before = before;
   }
+  if (tid == 0) p.join[blockIdx.x].last = -1;
   __syncthreads();
   if (works) {
     if (warp < 8) {
       regs_take<kAttRegsMany>();
-      att_softmax<DP, BF16>(sh, p, kv_smem, warp, lane);
+      att_softmax<DP, BF16>(sh, p, warp, lane);
     } else {
       regs_give<kAttRegsFew>();
       if (warp == 8) {
-        att_load<DP, false>(sh, p, q_smem, kv_smem, lane);
+        att_load<DP, false>(sh, p, q_smem, kv_smem, lane, nullptr);
       } else if (warp == 11) {
-        att_load<DP, true>(sh, p, q_smem, kv_smem, lane);
-      } else if (warp == 9) {
-        if (!att_products<DP, BF16>(sh, p, q_smem, kv_smem)) {
-          mma_commit(&sh.drain, elect_one());
+        AttWalk walk(sh, begin, end, total, blocks, run);
+        att_load<DP, true>(sh, p, q_smem, kv_smem, lane, &walk);
+      } else {
+        const int s = warp - 9;
+        if (!att_products<DP, BF16>(sh, p, q_smem, kv_smem, s)) {
+          mma_commit(&sh.drain[s], elect_one());
           for (int i = 0; i < 1024; ++i)
-            if (mbar_try(&sh.drain, 0)) break;
+            if (mbar_try(&sh.drain[s], 0)) break;
         }
-      } else if (warp == 10) {
-        if (lane == 0) att_walk(sh, p, begin, end, total, blocks, run);
       }
       __syncwarp();
     }
-  } else if (tid == 0) {
-    p.join[blockIdx.x].last = -1;
   }
   // Rows of q past the last request: zeros.
   for (long long t = pad + blockIdx.x; t < p.T; t += gridDim.x) {
