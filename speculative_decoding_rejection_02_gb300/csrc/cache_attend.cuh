@@ -102,18 +102,24 @@ struct AttSeg {
   int slot;       // partial result: 0 or 1; -1: the unit is whole
 };
 
-// sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0.
-__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long sum = 0;
+// sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0, and a n + b and the sum
+// below 2^32.
+__host__ __device__ inline unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  unsigned sum = 0;
   while (n > 0) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long y = a * n + b;
+    if (a >= m) {
+      sum += (unsigned)((unsigned long long)(n - 1) * n / 2) * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const unsigned y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const long long t = m;
+    const unsigned t = m;
     m = a;
     a = t;
   }
@@ -121,51 +127,64 @@ __host__ __device__ inline long long floor_sum(long long n, long long m, long lo
 }
 
 // The units of one request: `count` of `step` new tokens each (the last may
-// have fewer), for each kv head.
+// have fewer), for each kv head. Positions, and the key tiles of one head's
+// units together, are below 2^31.
 struct AttUnits {
-  long long p0;  // position of the first new token
-  int q, step, count, window;
-  long long sink_tiles;
+  int p0;  // position of the first new token
+  int q, step, count, window, sink_tiles;
 
   __host__ __device__ AttUnits(int len, int q_, int step_, int window_, int sinks)
-      : p0((long long)len - q_), q(q_), step(step_), count((q_ + step_ - 1) / step_),
-        window(window_), sink_tiles(((long long)sinks + kAttTile - 1) / kAttTile) {}
+      : p0(len - q_), q(q_), step(step_), count(q_ <= step_ ? q_ > 0 : (q_ - 1) / step_ + 1),
+        window(window_), sink_tiles((int)(((unsigned)sinks + kAttTile - 1) / kAttTile)) {}
 
-  __host__ __device__ long long hi(int u) const {
-    const long long end = (long long)(u + 1) * step;
-    return p0 + (end < q ? end : q);
+  __host__ __device__ int hi(int u) const {
+    const int end = (u + 1) * step;
+    return p0 + (u + 1 < count && end < q ? end : q);
   }
-  __host__ __device__ long long lo(int u) const {
-    const long long x = window ? p0 + (long long)u * step - window + 1 : 0;
-    return x > 0 ? x : 0;
+  __host__ __device__ int lo(int u) const {
+    const int first = p0 + u * step + 1;
+    return window && first > window ? first - window : 0;
   }
-  __host__ __device__ long long gap(int u) const {
-    const long long g = lo(u) / kAttTile - sink_tiles;
+  __host__ __device__ int gap(int u) const {
+    const int g = lo(u) / kAttTile - sink_tiles;
     return g > 0 ? g : 0;
   }
   // Key tiles of unit u; one (in which no row sees anything) at least.
-  __host__ __device__ long long tiles(int u) const {
-    const long long h = hi(u);
-    return h <= 0 ? 1 : (h + kAttTile - 1) / kAttTile - gap(u);
+  __host__ __device__ int tiles(int u) const {
+    const int h = hi(u);
+    return h <= 0 ? 1 : (h - 1) / kAttTile + 1 - gap(u);
   }
   // Key tiles of the units before k, in closed form.
-  __host__ __device__ long long before(int k) const {
-    long long sum = 0;
+  __host__ __device__ int before(int k) const {
+    int sum = 0;
     if (k == count && k > 0) sum += tiles(--k);  // the last one ends where the request does
     if (k <= 0) return sum;
-    long long dead = p0 < 0 ? -p0 / step : 0;  // units before position 0
+    int dead = p0 < 0 ? -p0 / step : 0;  // units before position 0
     if (dead > k) dead = k;
-    sum += dead + floor_sum(k - dead, kAttTile, step, p0 + (dead + 1) * step + kAttTile - 1);
+    if (dead < k)
+      sum += floor_sum(k - dead, kAttTile, step, p0 + (dead + 1) * step + kAttTile - 1);
+    sum += dead;
     if (window) {
-      const long long from = (sink_tiles + 1) * kAttTile + window - 1 - p0;  // gap > 0
+      const long long from =
+          (long long)(sink_tiles + 1) * kAttTile + window - 1 - p0;  // gap > 0
       const long long u = from > 0 ? (from + step - 1) / step : 0;
       if (u < k)
-        sum -= floor_sum(k - u, kAttTile, step, p0 + u * step - window + 1) -
-               (k - u) * sink_tiles;
+        sum -= (int)floor_sum(k - (int)u, kAttTile, step, (unsigned)(p0 + u * step - window + 1)) -
+               (k - (int)u) * sink_tiles;
     }
     return sum;
   }
 };
+
+// The list's part of block c begins at tile att_begin(c): the first total % blocks parts are
+// a tile longer.
+__device__ __forceinline__ int att_begin(int c, int total, int blocks) {
+  return c * (total / blocks) + min(c, total % blocks);
+}
+__device__ __forceinline__ int att_block_of(int tile, int total, int blocks) {
+  const int part = total / blocks, more = total % blocks;
+  return tile < more * (part + 1) ? tile / (part + 1) : more + (tile - more * (part + 1)) / part;
+}
 
 // The new tokens of request b as rows [lo, hi) of q, and its length. Offsets
 // that cannot be give no rows, a length that cannot be length 0.
@@ -201,10 +220,9 @@ struct AttBase {
   uint64_t seg_full[kAttSegs], seg_empty[kAttSegs];
   AttSeg seg[kAttSegs];
   float2 ml[2][kAttTile];
-  long long scan[kAttThreads / 32];
+  unsigned long long scan[kAttThreads / 32];
   int pad[kAttThreads / 32];
-  long long start_before;  // tiles before the run of requests where the part starts
-  int start_run;
+  int start_request, start_before;  // where the part starts, and tiles before that request
   uint32_t tmem;
   int stop;
 };
@@ -253,20 +271,36 @@ __device__ __forceinline__ int att_tile(const AttSeg& g, int i) {
 // ---- the walk over this block's part of the list, by one thread, an entry at a time
 
 struct AttWalk {
-  long long skip, end;   // tiles of the list given out, and where the part ends
-  long long before;      // tiles before request b
-  long long rest;        // tiles of the current unit given out
-  long long total;
-  int blocks, b, lo, hi, len, head, u, q_at, entry;
+  int skip, end;   // tiles of the list given out, and where the part ends
+  int rest;        // tiles of the current unit given out
+  int total, blocks, b, lo, hi, len, head, u, q_at, entry;
+  int lo1, hi1, len1;  // request b + 1, read ahead
   unsigned ring;
-  bool fresh;
   AttJoin join;
 
-  __device__ __forceinline__ AttWalk(const AttBase& sh, long long begin, long long end_,
-                                     long long total_, int blocks_, int run)
-      : skip(begin), end(end_), before(sh.start_before), rest(0), total(total_), blocks(blocks_),
-        b(sh.start_run * run), lo(0), hi(0), len(0), head(0), u(0), q_at(0), entry(0), ring(0),
-        fresh(true), join{-1, 0, 0, 0} {}
+  // begin < end, in request sh.start_request before which there are sh.start_before tiles.
+  __device__ __forceinline__ AttWalk(const AttBase& sh, const AttendParams& p, int begin, int end_,
+                                     int total_, int blocks_)
+      : skip(begin), end(end_), rest(0), total(total_), blocks(blocks_), b(sh.start_request),
+        lo(0), hi(0), len(0), head(0), u(0), q_at(0), entry(0), ring(0), join{-1, 0, 0, 0} {
+    len1 = attend_request(p, b, lo1, hi1);
+    next_request(p);
+    const AttUnits units(len, hi - lo, 2 * p.tile_tokens, p.window, p.sinks);
+    const int per_head = units.before(units.count), x = begin - sh.start_before;
+    head = x / per_head;
+    rest = x - head * per_head;
+    int u1 = units.count - 1;  // the last unit that starts at or before there
+    while (u < u1) {
+      const int mid = (u + u1 + 1) >> 1;
+      if (units.before(mid) <= rest) u = mid; else u1 = mid - 1;
+    }
+    rest -= units.before(u);
+  }
+
+  __device__ __forceinline__ void next_request(const AttendParams& p) {
+    lo = lo1, hi = hi1, len = len1;
+    if (b + 1 < p.B) len1 = attend_request(p, b + 1, lo1, hi1);
+  }
 
   // Puts the next entry, or the end mark, into the ring; nothing once that is there.
   __device__ __forceinline__ bool publish(AttBase& sh, const AttendParams& p) {
@@ -274,58 +308,37 @@ struct AttWalk {
     const int step = 2 * p.tile_tokens, at = entry % kAttSegs;
     AttSeg g;
     g.n = 0;
-    while (skip < end && g.n == 0 && b < p.B) {
-      if (fresh) {  // request b
-        len = attend_request(p, b, lo, hi);
-        const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-        const long long per_head = units.before(units.count);
-        const long long all = per_head * p.kv_heads;
-        if (all == 0 || before + all <= skip) {
-          before += all;
-          ++b;
-          continue;
-        }
-        const long long x = skip - before;
-        head = (int)(x / per_head);
-        rest = x - head * per_head;
-        int u0 = 0, u1 = units.count - 1;  // the last unit that starts at or before there
-        while (u0 < u1) {
-          const int mid = (u0 + u1 + 1) >> 1;
-          if (units.before(mid) <= rest) u0 = mid; else u1 = mid - 1;
-        }
-        u = u0;
-        rest -= units.before(u);
-        before += all;
-        fresh = false;
+    if (skip < end) {
+      while (hi == lo && b + 1 < p.B) {  // requests without rows
+        ++b;
+        next_request(p);
       }
       const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-      const long long n = units.tiles(u);
-      const long long take = min(n - rest, end - skip);
-      g.n = (int)take;
-      g.i0 = (int)rest;
+      const int n = units.tiles(u), take = min(n - rest, end - skip);
+      g.n = take;
+      g.i0 = rest;
       g.b = b;
       g.head = head;
       g.token = lo + u * step;
       g.tokens = min(step, hi - g.token);
-      g.pos = (int)(units.p0 + (long long)u * step);
-      g.lo = (int)units.lo(u);
-      g.hi = (int)max(units.hi(u), 0ll);
-      g.gap = (int)units.gap(u);
-      g.gap_at = g.gap ? (int)units.sink_tiles : 0x7fffffff;
+      g.pos = units.p0 + u * step;
+      g.lo = units.lo(u);
+      g.hi = max(units.hi(u), 0);
+      g.gap = units.gap(u);
+      g.gap_at = g.gap ? units.sink_tiles : 0x7fffffff;
       g.pair = g.tokens > p.tile_tokens;
       g.q_at = q_at;
       g.ring = ring;
       const bool starts = rest == 0, ends = rest + take == n;
       g.slot = starts && ends ? -1 : starts ? 1 : 0;
       if (starts && !ends) {
-        // the block that holds the unit's last tile
-        join.last = (int)(((skip + n) * blocks - 1) / total);
+        join.last = att_block_of(skip + n - 1, total, blocks);
         join.head = head;
         join.token = g.token;
         join.tokens = g.tokens;
       }
       q_at += g.pair ? 2 : 1;
-      ring += 2 * g.n;
+      ring += 2 * take;
       skip += take;
       rest += take;
       if (rest == n) {
@@ -333,13 +346,15 @@ struct AttWalk {
         if (++u == units.count) {
           u = 0;
           if (++head == p.kv_heads) {
+            head = 0;
             ++b;
-            fresh = true;
+            next_request(p);
           }
         }
       }
+    } else {
+      p.join[blockIdx.x] = join;
     }
-    if (g.n == 0) p.join[blockIdx.x] = join;
     if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return false;
     sh.seg[at] = g;
     mbar_arrive(&sh.seg_full[at]);
@@ -416,6 +431,10 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
       }
       __syncwarp();
       issued = r + 1;
+      if (V && i == g.n - 1) {  // in the shadow of this load
+        if (lane == 0) walk->publish(sh, p);
+        __syncwarp();
+      }
       if (clear) {
         ok = att_wait_warp(sh, p, &sh.edge_full, edges++);
         if (!ok) break;
@@ -435,8 +454,6 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
     if (!ok) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.seg_empty[at]);
-    if (V && lane == 0) walk->publish(sh, p);
-    __syncwarp();
   }
   // A wait ran out: let the loads in flight land before the block's end (those of the other
   // of the two warps among them: a wait too many only takes its limit).
@@ -451,8 +468,14 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
 // turns (PV of a tile and QK of the stream's next), which keeps the streams half a period
 // apart: left to themselves they fall into step, and the tensor cores idle through both
 // softmaxes. A commit is dear, so there is one for each tile: S of tile i tells that K of
-// tile i and V of the stream's tile before have been used too, and the softmax warps, which
-// wait for it, hand those back.
+// tile i and V of the stream's tile before have been used too.
+
+// A tile of K or V is free after both streams' products, or twice after the one's.
+template <int DP>
+__device__ __forceinline__ void att_release(AttShared<DP>& sh, unsigned r, bool pair) {
+  mbar_arrive(&sh.kv_empty[r % AttCfg<DP>::kRing]);
+  if (!pair) mbar_arrive(&sh.kv_empty[r % AttCfg<DP>::kRing]);
+}
 
 template <int DP, bool BF16>
 __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendParams& p,
@@ -489,6 +512,16 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
       const bool has_pv = t > 0 && last < n, has_qk = next < n;
       // the results of the segment before (e > 0) have been read by all
       if (t == 1 && !att_wait_warp(sh, p, &sh.o_free, e + 1)) return false;
+      if (has_pv) {
+        // S of the turn before is there: what its products read is free (and the loads below
+        // may be waiting for that)
+        if (!att_wait_warp(sh, p, &sh.s_full[s], p_count)) return false;
+        if (one) {
+          att_release<DP>(sh, ring + att_k_at(pair, last), pair);
+          if (t > 1) att_release<DP>(sh, ring + att_v_at(pair, last - step, n), pair);
+        }
+        __syncwarp();
+      }
       if (has_qk && !loaded(k)) return false;
       if (has_pv && (!loaded(v) || !att_wait_warp(sh, p, &sh.p_half[s], p_count))) return false;
       if (!att_wait_warp(sh, p, &sh.turn[s], turn + 1 - s)) return false;
@@ -518,6 +551,13 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
       if (has_qk) mma_commit(&sh.s_full[s], one);
       __syncwarp();
     }
+    // The stream's last V, and Q: read by both streams, or each stream's own.
+    if (first < n) {
+      const int last = first + (n - 1 - first) / step * step;
+      const unsigned v = ring + att_v_at(pair, last, n);
+      for (int x = 0; x <= !pair; ++x) mma_commit(&sh.kv_empty[v % Cfg::kRing], one);
+    }
+    for (int x = 0; x <= pair; ++x) mma_commit(&sh.q_empty[q_at & 1], one);
     mma_commit(&sh.o_full, one);
     if (one) mbar_arrive(&sh.seg_empty[at]);
     __syncwarp();
@@ -614,7 +654,7 @@ __device__ __forceinline__ void att_store_out(const AttendParams& p, char* out, 
 }
 
 template <int DP, bool BF16>
-__device__ __forceinline__ void att_softmax(AttShared<DP>& sh, const AttendParams& p, int warp, int lane) {
+__device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, int warp, int lane) {
   constexpr float kBias = att_bias<BF16>();
   // Weights may pass 2^kBias by 2^kGrow before m and O follow, one tile late; by 2^kFar never.
   constexpr float kGrow = BF16 ? 32.f : 4.f, kFar = BF16 ? 64.f : 8.f;
@@ -636,11 +676,6 @@ __device__ __forceinline__ void att_softmax(AttShared<DP>& sh, const AttendParam
     const int pos = mine ? g.pos + tile0 + row_token : -1;
     const bool busy = (warp & 3) * 32 < tokens * p.G;  // rows in this warp
     const int first_pos = g.pos + tile0, last_pos = g.pos + tile0 + tokens - 1;
-    // A tile's K and V are free after both streams' products, or twice after the one's.
-    auto release = [&](unsigned r) {
-      mbar_arrive(&sh.kv_empty[r % AttCfg<DP>::kRing]);
-      if (!g.pair) mbar_arrive(&sh.kv_empty[r % AttCfg<DP>::kRing]);
-    };
     float m = -INFINITY, l = 0.f;
     float over = 0.f;  // log2 of how far some weight so far has passed 2^(kBias)
     const int step = g.pair ? 1 : 2;
@@ -652,10 +687,6 @@ __device__ __forceinline__ void att_softmax(AttShared<DP>& sh, const AttendParam
       const bool grown = __any_sync(~0u, mine && over > kGrow);
       if (!att_wait_warp(sh, p, &sh.s_full[s], s_count)) return;
       ++s_count;
-      if ((warp & 3) == 0 && lane == 0) {
-        release(g.ring + att_k_at(g.pair, i));
-        if (i >= step) release(g.ring + att_v_at(g.pair, i - step, g.n));
-      }
       if (busy) {
         tmem_fence_after();
         if (!all_seen) att_hide(tmem_s, pos, j0, p.window, p.sinks, p.hidden);
@@ -758,14 +789,6 @@ __device__ __forceinline__ void att_softmax(AttShared<DP>& sh, const AttendParam
       l = x.y * w[0] + y.y * w[1];
     }
     if (!att_wait_warp(sh, p, &sh.o_full, e)) return;
-    if ((warp & 3) == 0 && lane == 0) {
-      const int last = g.pair ? g.n - 1 : (g.n - 1 - s) / 2 * 2 + s;  // the stream's last tile
-      if (g.pair || s < g.n) release(g.ring + att_v_at(g.pair, last, g.n));
-      // Q: read by both streams, or each stream's own
-      const int q = (g.q_at + (g.pair ? s : 0)) & 1;
-      mbar_arrive(&sh.q_empty[q]);
-      if (g.pair) mbar_arrive(&sh.q_empty[q]);
-    }
     if (busy) {
       tmem_fence_after();
       const int half = g.pair ? DP : DP / 2;  // columns of this warp: stream s of a pair, or
@@ -862,18 +885,22 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   // Key tiles of each thread's run of requests, and of all.
   const int step = 2 * p.tile_tokens;
   const int r0 = (int)min((long long)tid * run, (long long)p.B), r1 = min(r0 + run, p.B);
-  long long mine = 0;
-  int pad = 0;  // rows from here on belong to no request
-  for (int r = r0; r < r1; ++r) {
-    int lo, hi;
+  auto tiles_of = [&](int r, int& hi) {
+    int lo;
     const int len = attend_request(p, r, lo, hi);
     const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-    mine += units.before(units.count) * p.kv_heads;
+    return (unsigned long long)units.before(units.count) * p.kv_heads;
+  };
+  unsigned long long mine = 0;
+  int pad = 0;  // rows from here on belong to no request
+  for (int r = r0; r < r1; ++r) {
+    int hi;
+    mine += tiles_of(r, hi);
     pad = max(pad, hi);
   }
-  long long upto = mine;
+  unsigned long long upto = mine;
   for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(~0u, upto, d);
+    const unsigned long long x = __shfl_up_sync(~0u, upto, d);
     if (lane >= d) upto += x;
   }
   pad = __reduce_max_sync(~0u, pad);
@@ -882,19 +909,29 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  long long total = 0, before = upto - mine;
+  unsigned long long all = 0, before64 = upto - mine;
   for (int w = 0; w < kAttThreads / 32; ++w) {
-    if (w < warp) before += sh.scan[w];
-    total += sh.scan[w];
+    if (w < warp) before64 += sh.scan[w];
+    all += sh.scan[w];
     pad = max(pad, sh.pad[w]);
   }
-  const int blocks = (int)min((long long)gridDim.x, total);
+  // 2^31 tiles are 2^38 tokens of a head: no list is that long
+  if (all > 0x7fffffffull && tid == 0 && blockIdx.x == 0 && p.status)
+    atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
+  const int total = all > 0x7fffffffull ? 0 : (int)all, before = (int)before64;
+  const int blocks = min((int)gridDim.x, total);
   const bool works = (int)blockIdx.x < blocks;
-  const long long begin = works ? total * blockIdx.x / blocks : 0;
-  const long long end = works ? total * (blockIdx.x + 1) / blocks : 0;
-  if (works && before <= begin && begin < before + mine) {
-    sh.start_run = tid;
-    sh.start_before = before;
+  const int begin = works ? att_begin(blockIdx.x, total, blocks) : 0;
+  const int end = works ? att_begin(blockIdx.x + 1, total, blocks) : 0;
+  if (works && before <= begin && begin < before + (int)mine) {
+    int at = before, r = r0, hi;
+    for (; r + 1 < r1; ++r) {
+      const int n = (int)tiles_of(r, hi);
+      if (begin < at + n) break;
+      at += n;
+    }
+    sh.start_request = r;
+    sh.start_before = at;
   }
   if (tid == 0) p.join[blockIdx.x].last = -1;
   __syncthreads();
@@ -907,7 +944,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       if (warp == 8) {
         att_load<DP, false>(sh, p, q_smem, kv_smem, lane, nullptr);
       } else if (warp == 11) {
-        AttWalk walk(sh, begin, end, total, blocks, run);
+        AttWalk walk(sh, p, begin, end, total, blocks);
         att_load<DP, true>(sh, p, q_smem, kv_smem, lane, &walk);
       } else {
         const int s = warp - 9;
