@@ -10,12 +10,10 @@
 //                   P rounded to the cache's type and written over S
 //   O += P V        tcgen05, P from TMEM, V in shared memory, O (fp32) in TMEM
 //
-// with c = scale * log2(e). m is the maximum of the row's first tile; it and O
-// follow a higher one only when that has passed it by 2^32 (fp16: 2^4), and one
-// tile late, so that no weight waits for its tile's maximum: P may then exceed 1,
-// which costs no precision (bf16 and fp32 have the range; fp16's P starts at 2^7,
-// may reach 2^15 and goes down to 2^-31 of it). A tile that would go further (2^64,
-// fp16: 2^8) has its maximum taken first after all.
+// with c = scale * log2(e). m and O follow a higher maximum only when it has
+// passed m by 2^8: until then P may exceed 1, which costs no precision (bf16 and
+// fp32 have the range; fp16's P starts at 2^7, may reach 2^15 and goes down to
+// 2^-31 of it).
 //
 // Two streams of S and O run side by side in one block, so that one's products
 // cover the other's softmax: two tiles of rows over the same keys where a unit
@@ -49,6 +47,7 @@ constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
 constexpr int kAttThreads = 384;  // 12 warps, at most 168 registers each at launch
 constexpr int kAttRegsMany = 208, kAttRegsFew = 88;  // 2 * 208 + 88 = 3 * 168
 constexpr int kAttSegs = 4;       // list entries ahead of the slowest warp
+constexpr float kAttGrow = 8.f;   // log2 of how far a row's maximum may grow unscaled
 
 template <int DP>
 struct AttCfg {
@@ -603,28 +602,23 @@ __device__ __forceinline__ void att_rescale(uint32_t tmem_o, float keep) {
   }
 }
 
-// Take the maximum of a tile's scores into m, and l and O (if it holds
-// anything) to it.
-template <int DP>
-__device__ __forceinline__ void att_settle(uint32_t tmem_s, uint32_t tmem_o, float c, bool filled,
-                                           float& m, float& l) {
-  float now = m;
-#pragma unroll 1
-  for (int k = 0; k < kAttTile; k += 64) {
-    float x[64];
-    tmem_ld32(tmem_s + k, x);
-    tmem_ld32(tmem_s + k + 32, x + 32);
-    tmem_wait_ld(x);
-    tmem_wait_ld(x + 32);
-    float top[4] = {now, now, now, now};
+// The largest of 64 values and x (the least, where the scores' factor is negative).
+__device__ __forceinline__ float att_max64(const float* f, bool largest, float x) {
+  float top[4] = {x, f[1], f[2], f[3]};
+  if (largest) {
+    top[0] = fmaxf(top[0], f[0]);
 #pragma unroll
-    for (int y = 0; y < 64; ++y) top[y & 3] = fmaxf(top[y & 3], x[y] * c);
-    now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    for (int y = 4; y < 60; y += 8)
+#pragma unroll
+      for (int z = 0; z < 4; ++z) top[z] = max3(top[z], f[y + z], f[y + z + 4]);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) top[z] = fmaxf(top[z], f[60 + z]);
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   }
-  const float keep = now == -INFINITY ? 1.f : ex2(m - now);
-  m = now;
-  l *= keep;
-  if (filled) att_rescale<DP>(tmem_o, keep);
+  top[0] = fminf(top[0], f[0]);
+#pragma unroll
+  for (int y = 4; y < 64; ++y) top[y & 3] = fminf(top[y & 3], f[y]);
+  return fminf(fminf(top[0], top[1]), fminf(top[2], top[3]));
 }
 
 // log2 of what every P and l carries beside 2^-m: fp16 has few exponents below 1.
@@ -656,8 +650,6 @@ __device__ __forceinline__ void att_store_out(const AttendParams& p, char* out, 
 template <int DP, bool BF16>
 __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, int warp, int lane) {
   constexpr float kBias = att_bias<BF16>();
-  // Weights may pass 2^kBias by 2^kGrow before m and O follow, one tile late; by 2^kFar never.
-  constexpr float kGrow = BF16 ? 32.f : 4.f, kFar = BF16 ? 64.f : 8.f;
   const int s = warp >> 2, row = (warp & 3) * 32 + lane;
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t tmem_s = sh.tmem + lanes + s * 128;
@@ -677,100 +669,75 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
     const bool busy = (warp & 3) * 32 < tokens * p.G;  // rows in this warp
     const int first_pos = g.pos + tile0, last_pos = g.pos + tile0 + tokens - 1;
     float m = -INFINITY, l = 0.f;
-    float over = 0.f;  // log2 of how far some weight so far has passed 2^(kBias)
     const int step = g.pair ? 1 : 2;
     for (int i = g.pair ? 0 : s; i < g.n; i += step) {
       // what can be known before S is there
       const int j0 = att_tile(g, i) * kAttTile;
       const bool all_seen = j0 + kAttTile - 1 <= first_pos &&
                             (!p.window || j0 > last_pos - p.window || j0 + kAttTile <= p.sinks);
-      const bool grown = __any_sync(~0u, mine && over > kGrow);
       if (!att_wait_warp(sh, p, &sh.s_full[s], s_count)) return;
       ++s_count;
       if (busy) {
         tmem_fence_after();
         if (!all_seen) att_hide(tmem_s, pos, j0, p.window, p.sinks, p.hidden);
-        // The maximum: of the first tile before its weights, later one tile behind them.
-        if (i < step) {
-          att_settle<DP>(tmem_s, tmem_o + s * 128, p.c, false, m, l);
-        } else if (grown) {
-          const float keep = over > kGrow ? ex2(-over) : 1.f;
-          if (over > kGrow) m += over, over = 0.f;
-          l *= keep;
-          att_rescale<DP>(tmem_o + s * 128, keep);
+        float f[64], top;
+        {
+          float x[64];
+          tmem_ld32(tmem_s + 64, x);
+          tmem_ld32(tmem_s + 96, x + 32);
+          tmem_wait_ld(x);
+          tmem_wait_ld(x + 32);
+          tmem_ld32(tmem_s, f);
+          tmem_ld32(tmem_s + 32, f + 32);
+          top = att_max64(x, p.c > 0.f, p.hidden);
         }
-        float f[128];
-        uint32_t w[32];
-        unsigned long long sum2[2];
-        const unsigned long long c2 = f2_pack(p.c, p.c);
-        auto weigh = [&](const float* f) {  // 64 columns
+        tmem_wait_ld(f);
+        tmem_wait_ld(f + 32);
+        top = att_max64(f, p.c > 0.f, top) * p.c;
+        const bool grown = mine && top > m + kAttGrow;
+        if (__any_sync(~0u, grown)) {
+          const float keep = grown ? ex2(m - top) : 1.f;
+          l *= keep;
+          if (grown) m = top;
+          if (i >= step) att_rescale<DP>(tmem_o + s * 128, keep);  // O holds earlier tiles
+        }
+        const float shift = kBias - (m == -INFINITY ? 0.f : m);
+        const unsigned long long c2 = f2_pack(p.c, p.c), shift2 = f2_pack(shift, shift);
+        unsigned long long sum2[2] = {0, 0};
+        // P over S, half a tile at a time in a rolled loop: the warps of a block run through
+        // more code than the SM's instruction cache holds, and every line less counts.
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w[32];
 #pragma unroll
           for (int y = 0; y < 32; ++y) {
-            const float a = ex2(f[2 * y]), b = ex2(f[2 * y + 1]);
+            float a, b;
+            f2_unpack(f2_fma(f2_pack(f[2 * y], f[2 * y + 1]), c2, shift2), a, b);
+            a = ex2(a);
+            b = ex2(b);
             sum2[y & 1] = f2_add(sum2[y & 1], f2_pack(a, b));
             w[y] = pack2<BF16>(a, b);
           }
-        };
-#pragma unroll 1
-        for (;;) {
-          const float shift = kBias - (m == -INFINITY ? 0.f : m);
-          const unsigned long long shift2 = f2_pack(shift, shift);
-          float top[4];
-          auto scaled = [&](float* f, bool first) {  // 64 columns and their maximum
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              f2_unpack(f2_fma(f2_pack(f[2 * y], f[2 * y + 1]), c2, shift2), f[2 * y],
-                        f[2 * y + 1]);
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              top[z] = first ? f[z] : fmaxf(top[z], f[z]);
-              top[z] = fmaxf(top[z], f[z + 4]);
-#pragma unroll
-              for (int y = 8; y < 64; y += 8)
-                top[z] = fmaxf(fmaxf(top[z], f[y + z]), f[y + z + 4]);
-            }
-          };
-          tmem_ld32(tmem_s, f);
-          tmem_ld32(tmem_s + 32, f + 32);
-          tmem_wait_ld(f);
-          tmem_wait_ld(f + 32);
-          tmem_ld32(tmem_s + 64, f + 64);
-          tmem_ld32(tmem_s + 96, f + 96);
-          sum2[0] = sum2[1] = 0;
-          scaled(f, true);
-          weigh(f);
-          tmem_wait_ld(f + 64);
-          tmem_wait_ld(f + 96);
-          scaled(f + 64, false);
-          const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) - kBias;
-          const bool far = now > kFar || (m == -INFINITY && now > m);
-          if (!__any_sync(~0u, mine && far)) {
-            over = fmaxf(over, now);
-            break;
+          tmem_st32(tmem_s + 32 * k, w);
+          tmem_wait_st();
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k ? &sh.p_full[s] : &sh.p_half[s]);
+          if (k == 0) {
+            tmem_ld32(tmem_s + 64, f);
+            tmem_ld32(tmem_s + 96, f + 32);
+            tmem_wait_ld(f);
+            tmem_wait_ld(f + 32);
           }
-          // A weight would leave its type's range: S is still whole, take its maximum first.
-          att_settle<DP>(tmem_s, tmem_o + s * 128, p.c, i >= step, m, l);
-          over = 0.f;
         }
-        // P over S, each half as soon as it is there
-        tmem_st32(tmem_s, w);
-        tmem_wait_st();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_half[s]);
-        weigh(f + 64);
-        tmem_st32(tmem_s + 32, w);
         float a, b;
         f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
         l += a + b;
-        tmem_wait_st();
-        tmem_fence_before();
-      } else {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_half[s]);
+      } else if (lane == 0) {
+        mbar_arrive(&sh.p_half[s]);
+        mbar_arrive(&sh.p_full[s]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[s]);
     }
     // ---- results of the segment
     float w[2] = {1.f, 1.f};  // of the two streams' O

@@ -99,6 +99,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The largest of three (one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // Packed fp32 pairs (Blackwell f32x2 FMA-pipe instructions).
 __device__ __forceinline__ unsigned long long f2_pack(float lo, float hi) {
   unsigned long long r;
