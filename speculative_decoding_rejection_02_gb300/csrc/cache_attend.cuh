@@ -211,6 +211,53 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+struct AttBase;
+
+// ---- the walk over this block's part of the list, an entry at a time: begun by the thread
+// whose run of requests the part starts in, carried on by one of the V loader's
+
+struct AttWalk {
+  int skip, end;   // tiles of the list given out, and where the part ends
+  int rest;        // tiles of the current unit given out
+  int total, blocks, b, lo, hi, len, head, u, q_at, entry;
+  int lo1, hi1, len1;  // request b + 1, read ahead
+  unsigned ring;
+  AttJoin join;
+
+  // The part [begin, end_), begin < end_, starts in request b_, before which there are
+  // `before` tiles.
+  __device__ __forceinline__ void start(const AttendParams& p, int begin, int end_, int total_,
+                                        int blocks_, int b_, int before) {
+    skip = begin, end = end_, total = total_, blocks = blocks_, b = b_;
+    u = q_at = entry = 0;
+    ring = 0;
+    join = {-1, 0, 0, 0};
+    len = attend_request(p, b, lo, hi);
+    read_ahead(p);
+    const AttUnits units(len, hi - lo, 2 * p.tile_tokens, p.window, p.sinks);
+    const int per_head = units.before(units.count), x = begin - before;
+    head = x / per_head;
+    rest = x - head * per_head;
+    int u1 = units.count - 1;  // the last unit that starts at or before there
+    while (u < u1) {
+      const int mid = (u + u1 + 1) >> 1;
+      if (units.before(mid) <= rest) u = mid; else u1 = mid - 1;
+    }
+    rest -= units.before(u);
+  }
+  __device__ __forceinline__ void read_ahead(const AttendParams& p) {
+    if (b + 1 < p.B) len1 = attend_request(p, b + 1, lo1, hi1);
+  }
+
+  __device__ __forceinline__ void next_request(const AttendParams& p) {
+    lo = lo1, hi = hi1, len = len1;
+    read_ahead(p);
+  }
+
+  // Puts the next entry, or the end mark, into the ring; nothing once that is there.
+  __device__ __forceinline__ bool publish(AttBase& sh, const AttendParams& p);
+};
+
 struct AttBase {
   uint64_t q_full[4], q_empty[2];
   uint64_t s_full[2], p_half[2], p_full[2];
@@ -221,7 +268,7 @@ struct AttBase {
   float2 ml[2][kAttTile];
   unsigned long long scan[kAttThreads / 32];
   int pad[kAttThreads / 32];
-  int start_request, start_before;  // where the part starts, and tiles before that request
+  AttWalk walk;
   uint32_t tmem;
   int stop;
 };
@@ -267,102 +314,66 @@ __device__ __forceinline__ int att_tile(const AttSeg& g, int i) {
   return u < g.gap_at ? u : u + g.gap;
 }
 
-// ---- the walk over this block's part of the list, by one thread, an entry at a time
-
-struct AttWalk {
-  int skip, end;   // tiles of the list given out, and where the part ends
-  int rest;        // tiles of the current unit given out
-  int total, blocks, b, lo, hi, len, head, u, q_at, entry;
-  int lo1, hi1, len1;  // request b + 1, read ahead
-  unsigned ring;
-  AttJoin join;
-
-  // begin < end, in request sh.start_request before which there are sh.start_before tiles.
-  __device__ __forceinline__ AttWalk(const AttBase& sh, const AttendParams& p, int begin, int end_,
-                                     int total_, int blocks_)
-      : skip(begin), end(end_), rest(0), total(total_), blocks(blocks_), b(sh.start_request),
-        lo(0), hi(0), len(0), head(0), u(0), q_at(0), entry(0), ring(0), join{-1, 0, 0, 0} {
-    len1 = attend_request(p, b, lo1, hi1);
-    next_request(p);
-    const AttUnits units(len, hi - lo, 2 * p.tile_tokens, p.window, p.sinks);
-    const int per_head = units.before(units.count), x = begin - sh.start_before;
-    head = x / per_head;
-    rest = x - head * per_head;
-    int u1 = units.count - 1;  // the last unit that starts at or before there
-    while (u < u1) {
-      const int mid = (u + u1 + 1) >> 1;
-      if (units.before(mid) <= rest) u = mid; else u1 = mid - 1;
+__device__ __forceinline__ bool AttWalk::publish(AttBase& sh, const AttendParams& p) {
+  if (entry < 0) return true;
+  const int step = 2 * p.tile_tokens, at = entry % kAttSegs;
+  AttSeg g;
+  g.n = 0;
+  if (skip < end) {
+    while (hi == lo && b + 1 < p.B) {  // requests without rows
+      ++b;
+      next_request(p);
     }
-    rest -= units.before(u);
-  }
-
-  __device__ __forceinline__ void next_request(const AttendParams& p) {
-    lo = lo1, hi = hi1, len = len1;
-    if (b + 1 < p.B) len1 = attend_request(p, b + 1, lo1, hi1);
-  }
-
-  // Puts the next entry, or the end mark, into the ring; nothing once that is there.
-  __device__ __forceinline__ bool publish(AttBase& sh, const AttendParams& p) {
-    if (entry < 0) return true;
-    const int step = 2 * p.tile_tokens, at = entry % kAttSegs;
-    AttSeg g;
-    g.n = 0;
-    if (skip < end) {
-      while (hi == lo && b + 1 < p.B) {  // requests without rows
-        ++b;
-        next_request(p);
-      }
-      const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-      const int n = units.tiles(u), take = min(n - rest, end - skip);
-      g.n = take;
-      g.i0 = rest;
-      g.b = b;
-      g.head = head;
-      g.token = lo + u * step;
-      g.tokens = min(step, hi - g.token);
-      g.pos = units.p0 + u * step;
-      g.lo = units.lo(u);
-      g.hi = max(units.hi(u), 0);
-      g.gap = units.gap(u);
-      g.gap_at = g.gap ? units.sink_tiles : 0x7fffffff;
-      g.pair = g.tokens > p.tile_tokens;
-      g.q_at = q_at;
-      g.ring = ring;
-      const bool starts = rest == 0, ends = rest + take == n;
-      g.slot = starts && ends ? -1 : starts ? 1 : 0;
-      if (starts && !ends) {
-        join.last = att_block_of(skip + n - 1, total, blocks);
-        join.head = head;
-        join.token = g.token;
-        join.tokens = g.tokens;
-      }
-      q_at += g.pair ? 2 : 1;
-      ring += 2 * take;
-      skip += take;
-      rest += take;
-      if (rest == n) {
-        rest = 0;
-        if (++u == units.count) {
-          u = 0;
-          if (++head == p.kv_heads) {
-            head = 0;
-            ++b;
-            next_request(p);
-          }
+    const AttUnits units(len, hi - lo, step, p.window, p.sinks);
+    const int n = units.tiles(u), take = min(n - rest, end - skip);
+    g.n = take;
+    g.i0 = rest;
+    g.b = b;
+    g.head = head;
+    g.token = lo + u * step;
+    g.tokens = min(step, hi - g.token);
+    g.pos = units.p0 + u * step;
+    g.lo = units.lo(u);
+    g.hi = max(units.hi(u), 0);
+    g.gap = units.gap(u);
+    g.gap_at = g.gap ? units.sink_tiles : 0x7fffffff;
+    g.pair = g.tokens > p.tile_tokens;
+    g.q_at = q_at;
+    g.ring = ring;
+    const bool starts = rest == 0, ends = rest + take == n;
+    g.slot = starts && ends ? -1 : starts ? 1 : 0;
+    if (starts && !ends) {
+      join.last = att_block_of(skip + n - 1, total, blocks);
+      join.head = head;
+      join.token = g.token;
+      join.tokens = g.tokens;
+    }
+    q_at += g.pair ? 2 : 1;
+    ring += 2 * take;
+    skip += take;
+    rest += take;
+    if (rest == n) {
+      rest = 0;
+      if (++u == units.count) {
+        u = 0;
+        if (++head == p.kv_heads) {
+          head = 0;
+          ++b;
+          next_request(p);
         }
       }
-    } else {
-      p.join[blockIdx.x] = join;
     }
-    if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return false;
-    sh.seg[at] = g;
-    mbar_arrive(&sh.seg_full[at]);
-    entry = g.n ? entry + 1 : -1;
-    return true;
+  } else {
+    p.join[blockIdx.x] = join;
   }
-};
+  if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return false;
+  sh.seg[at] = g;
+  mbar_arrive(&sh.seg_full[at]);
+  entry = g.n ? entry + 1 : -1;
+  return true;
+}
 
-// ---- warps 8 and 11: Q and K, and V tiles by TMA (two warps: with small pages it is the
+// ---- warps 8 and 11: K, and Q and V tiles by TMA (two warps: with small pages it is the
 // issue of the loads that takes the time). The one for V also does the walk, two entries
 // ahead of its loads.
 
@@ -375,15 +386,13 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
   const int box = min(page, kAttTile);         // tokens of one load
   const int boxes = kAttTile / box;            // of a tile
   unsigned issued = 0, edges = 0;
-  if (V && lane == 0 && walk->publish(sh, p)) walk->publish(sh, p);
-  __syncwarp();
   for (int e = 0;; ++e) {
     const int at = e % kAttSegs;
     if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) break;
     const AttSeg g = sh.seg[at];
     if (g.n == 0) return;
     bool ok = true;
-    for (int s = 0; !V && s <= g.pair; ++s) {
+    for (int s = 0; V && s <= g.pair; ++s) {
       const int x = g.q_at + s, slot = x & 1;
       ok = ok && att_wait_warp(sh, p, &sh.q_empty[slot], (x / 2 + 1) & 1);
       if (ok && lane == 0) {
@@ -430,8 +439,9 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
       }
       __syncwarp();
       issued = r + 1;
-      if (V && i == g.n - 1) {  // in the shadow of this load
-        if (lane == 0) walk->publish(sh, p);
+      if (V) {  // the next entry, in the shadow of this load; and the second one at the start
+        for (int x = (i == g.n - 1) + (e == 0 && i == 0); x > 0; --x)
+          if (lane == 0) walk->publish(sh, p);
         __syncwarp();
       }
       if (clear) {
@@ -818,33 +828,36 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   AttShared<DP>& sh = *reinterpret_cast<AttShared<DP>*>(
       kv_smem + Cfg::kStages * Cfg::kTileBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < Cfg::kRing; ++i) {
+  if (warp == 0) {
+    for (int i = lane; i < Cfg::kRing; i += 32) {
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 2);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_full[i + 2], 1);
-      mbar_init(&sh.q_empty[i], 2);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_half[i], 4);
-      mbar_init(&sh.p_full[i], 4);
+    if (lane < 4) {
+      mbar_init(&sh.q_full[lane], 1);
+      mbar_init(&sh.seg_full[lane], 1);
+      mbar_init(&sh.seg_empty[lane], 12);
     }
-    mbar_init(&sh.o_full, 2);
-    mbar_init(&sh.ml_full, 8);
-    mbar_init(&sh.o_free, 8);
-    mbar_init(&sh.edge_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.turn[i], 1);
-      mbar_init(&sh.drain[i], 1);
+    if (lane < 2) {
+      mbar_init(&sh.q_empty[lane], 2);
+      mbar_init(&sh.s_full[lane], 1);
+      mbar_init(&sh.p_half[lane], 4);
+      mbar_init(&sh.p_full[lane], 4);
+      mbar_init(&sh.turn[lane], 1);
+      mbar_init(&sh.drain[lane], 1);
     }
-    for (int i = 0; i < kAttSegs; ++i) {
-      mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 12);
+    if (lane == 0) {
+      mbar_init(&sh.o_full, 2);
+      mbar_init(&sh.o_free, 8);
+      mbar_init(&sh.ml_full, 8);
+      mbar_init(&sh.edge_full, 1);
+      sh.stop = 0;
     }
     fence_mbar_init();
-    sh.stop = 0;
+  } else if (tid == 32) {
+    prefetch_map(&p.q_map);
+    prefetch_map(&p.k_map);
+    prefetch_map(&p.v_map);
   }
   if (warp == 9) tmem_alloc(&sh.tmem, 512);
   pdl_trigger();
@@ -897,8 +910,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       if (begin < at + n) break;
       at += n;
     }
-    sh.start_request = r;
-    sh.start_before = at;
+    AttWalk walk;
+    walk.start(p, begin, end, total, blocks, r, at);
+    walk.publish(sh, p);
+    sh.walk = walk;
   }
   if (tid == 0) p.join[blockIdx.x].last = -1;
   __syncthreads();
@@ -911,7 +926,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       if (warp == 8) {
         att_load<DP, false>(sh, p, q_smem, kv_smem, lane, nullptr);
       } else if (warp == 11) {
-        AttWalk walk(sh, p, begin, end, total, blocks);
+        AttWalk walk = sh.walk;
         att_load<DP, true>(sh, p, q_smem, kv_smem, lane, &walk);
       } else {
         const int s = warp - 9;
@@ -941,10 +956,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   }
 }
 
-constexpr int kJoinThreads = 256, kJoinSplit = 4;
+constexpr int kJoinThreads = 256, kJoinSplit = 8;
 
 // Join the partial results of the unit that starts in block blockIdx.x's part
-// of the list and ends in another's: parts of one row weigh 2^(m - max m).
+// of the list and ends in another's: parts of one row weigh 2^(m - max m). An
+// item is four columns of a row; where the items are fewer than the threads,
+// up to 32 lanes take an item's parts in turn and add up.
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams p) {
   pdl_trigger();
@@ -953,40 +970,54 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams
   if (j.last < 0) return;
   const int parts = j.last - blockIdx.x + 1;
   constexpr int kCols = DP / 4 / kJoinSplit;  // groups of four columns of this block
-  for (int tile = 0; tile < 2; ++tile) {
-    const int tokens = min(p.tile_tokens, j.tokens - tile * p.tile_tokens);
-    if (tokens <= 0) break;
-    const int rows = tokens * p.G;
-    for (int x = threadIdx.x; x < rows * kCols; x += kJoinThreads) {
-      const int col4 = x / rows, row = x - col4 * rows, c4 = blockIdx.y * kCols + col4;
-      auto at = [&](int i) { return ((blockIdx.x + i) * 2 + (i == 0)) * 2 + tile; };
-      float m = -INFINITY;
-      for (int i = 0; i < parts; ++i) m = fmaxf(m, p.part_ml[at(i) * kAttTile + row].x);
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int rows0 = min(p.tile_tokens, j.tokens) * p.G, rows = j.tokens * p.G;
+  int lanes = 1;  // of an item
+  while (lanes < 32 && lanes < parts && rows * kCols * lanes * 2 <= kJoinThreads) lanes *= 2;
+  const int mine = threadIdx.x & (lanes - 1);
+  // whole warps go round together: the sums below take all their lanes
+  for (int x0 = 0; x0 < rows * kCols; x0 += kJoinThreads / lanes) {
+    const int x = x0 + threadIdx.x / lanes;
+    const bool real = x < rows * kCols;
+    const int col4 = real ? x / rows : 0, any_row = real ? x - col4 * rows : 0;
+    const int tile = any_row >= rows0, row = any_row - tile * rows0;
+    const int c4 = blockIdx.y * kCols + col4;
+    auto at = [&](int i) { return ((blockIdx.x + i) * 2 + (i == 0)) * 2 + tile; };
+    float m = -INFINITY;
 #pragma unroll 4
-      for (int i = 0; i < parts; ++i) {
-        const float2 ml = p.part_ml[at(i) * kAttTile + row];
-        const float4 y = p.part_o[((size_t)at(i) * (DP / 4) + c4) * kAttTile + row];
-        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-        l += w * ml.y;
-        o.x += w * y.x;
-        o.y += w * y.y;
-        o.z += w * y.z;
-        o.w += w * y.w;
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int row_token = row / p.G;
-      const long long token = j.token + tile * p.tile_tokens + row_token;
-      const int head = j.head * p.G + (row - row_token * p.G);
-      if (4 * c4 < p.dim) {
-        uint2 v;
-        v.x = pack2<BF16>(o.x * inv, o.y * inv);
-        v.y = pack2<BF16>(o.z * inv, o.w * inv);
-        *(uint2*)(p.out + token * p.out_token + head * p.out_head + 8 * c4) = v;
-      }
-      if (c4 == 0 && p.lse) p.lse[token * p.heads + head] = att_lse<BF16>(m, l);
+    for (int i = mine; i < parts; i += lanes) m = fmaxf(m, p.part_ml[at(i) * kAttTile + row].x);
+    for (int d = 1; d < lanes; d <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = mine; i < parts; i += lanes) {
+      const float2 ml = p.part_ml[at(i) * kAttTile + row];
+      const float4 y = p.part_o[((size_t)at(i) * (DP / 4) + c4) * kAttTile + row];
+      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+      l += w * ml.y;
+      o.x += w * y.x;
+      o.y += w * y.y;
+      o.z += w * y.z;
+      o.w += w * y.w;
     }
+    for (int d = 1; d < lanes; d <<= 1) {
+      l += __shfl_xor_sync(~0u, l, d);
+      o.x += __shfl_xor_sync(~0u, o.x, d);
+      o.y += __shfl_xor_sync(~0u, o.y, d);
+      o.z += __shfl_xor_sync(~0u, o.z, d);
+      o.w += __shfl_xor_sync(~0u, o.w, d);
+    }
+    if (!real || mine) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int row_token = any_row / p.G;
+    const long long token = j.token + row_token;
+    const int head = j.head * p.G + (any_row - row_token * p.G);
+    if (4 * c4 < p.dim) {
+      uint2 v;
+      v.x = pack2<BF16>(o.x * inv, o.y * inv);
+      v.y = pack2<BF16>(o.z * inv, o.w * inv);
+      *(uint2*)(p.out + token * p.out_token + head * p.out_head + 8 * c4) = v;
+    }
+    if (c4 == 0 && p.lse) p.lse[token * p.heads + head] = att_lse<BF16>(m, l);
   }
 }
 
