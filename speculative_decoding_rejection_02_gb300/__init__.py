@@ -327,6 +327,16 @@ def strerror(code: int) -> str:
     return lib().spec_verify_strerror(code).decode()
 
 
-from .cache import (  # noqa: E402  (needs the definitions above)
-    CACHE_BAD_LENGTHS, CACHE_BAD_PAGE, CACHE_BAD_SLOT, CACHE_NO_PAGES, AppendArgs, AttendArgs,
-    CacheStep, StepArgs, cache_append, cache_attend, cache_step)
+_CACHE_NAMES = ("CACHE_BAD_LENGTHS", "CACHE_BAD_PAGE", "CACHE_BAD_SLOT", "CACHE_NO_PAGES",
+                "AppendArgs", "AttendArgs", "CacheStep", "StepArgs", "cache_append",
+                "cache_attend", "cache_step")
+
+
+def __getattr__(name):
+    """The paged cache's names, from cache.py (which imports torch) when first asked for."""
+    if name not in _CACHE_NAMES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import cache
+    for n in _CACHE_NAMES:
+        globals()[n] = getattr(cache, n)
+    return globals()[name]
