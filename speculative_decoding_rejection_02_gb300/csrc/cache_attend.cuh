@@ -224,15 +224,16 @@ struct AttWalk {
   unsigned ring;
   AttJoin join;
 
-  // The part [begin, end_), begin < end_, starts in request b_, before which there are
-  // `before` tiles.
+  // The part [begin, end_), begin < end_, starts in request b_ (rows lo_ .. hi_ - 1, length
+  // len_), before which there are `before` tiles.
   __device__ __forceinline__ void start(const AttendParams& p, int begin, int end_, int total_,
-                                        int blocks_, int b_, int before) {
+                                        int blocks_, int b_, int before, int lo_, int hi_,
+                                        int len_) {
+    lo = lo_, hi = hi_, len = len_;
     skip = begin, end = end_, total = total_, blocks = blocks_, b = b_;
     u = q_at = entry = 0;
     ring = 0;
     join = {-1, 0, 0, 0};
-    len = attend_request(p, b, lo, hi);
     read_ahead(p);
     const AttUnits units(len, hi - lo, 2 * p.tile_tokens, p.window, p.sinks);
     const int per_head = units.before(units.count), x = begin - before;
@@ -373,7 +374,7 @@ __device__ __forceinline__ bool AttWalk::publish(AttBase& sh, const AttendParams
   return true;
 }
 
-// ---- warps 8 and 11: K, and Q and V tiles by TMA (two warps: with small pages it is the
+// ---- warps 8 and 11: Q and K, and V tiles by TMA (two warps: with small pages it is the
 // issue of the loads that takes the time). The one for V also does the walk, two entries
 // ahead of its loads.
 
@@ -386,23 +387,41 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
   const int box = min(page, kAttTile);         // tokens of one load
   const int boxes = kAttTile / box;            // of a tile
   unsigned issued = 0, edges = 0;
+  // V's rows that no row of the unit sees may hold anything, and P is 0 there: they are zeroed
+  // before the tile counts as loaded. That waits for the load, so it is done after the next
+  // tile's has been issued (whose place in the ring does not wait for this one).
+  struct {
+    char* tile;
+    uint64_t* full;
+    int j0, sinks, lo, hi;
+  } edge = {nullptr, nullptr, 0, 0, 0, 0};
+  auto settle_edge = [&]() {
+    if (!V || !edge.tile) return true;
+    if (!att_wait_warp(sh, p, &sh.edge_full, edges++)) return false;
+    for (int y = lane; y < kAttTile; y += 32) {
+      const int j = edge.j0 + y;
+      if (j < edge.sinks || (j >= edge.lo && j < edge.hi)) continue;
+#pragma unroll
+      for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          *(uint4*)(edge.tile + k * kBlockBytes + y * 128 + 16 * x) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(edge.full);
+    edge.tile = nullptr;
+    return true;
+  };
   for (int e = 0;; ++e) {
     const int at = e % kAttSegs;
     if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) break;
     const AttSeg g = sh.seg[at];
-    if (g.n == 0) return;
-    bool ok = true;
-    for (int s = 0; V && s <= g.pair; ++s) {
-      const int x = g.q_at + s, slot = x & 1;
-      ok = ok && att_wait_warp(sh, p, &sh.q_empty[slot], (x / 2 + 1) & 1);
-      if (ok && lane == 0) {
-        mbar_arrive_expect_tx(&sh.q_full[x & 3], kBlocks * p.tile_tokens * p.G * 128);
-        for (int k = 0; k < kBlocks; ++k)
-          tma_load_4d(q_smem + slot * Cfg::kTileBytes + k * kBlockBytes, &p.q_map, 64 * k, 0,
-                      g.head, g.token + s * p.tile_tokens, &sh.q_full[x & 3]);
-      }
-      __syncwarp();
+    if (g.n == 0) {
+      if (settle_edge()) return;
+      break;
     }
+    bool ok = true;
     const int* table = p.table + g.b * p.table_stride;
     const int sinks = min(p.sinks, g.lo);
     for (int i = 0; ok && i < g.n; ++i) {
@@ -425,9 +444,11 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
         ok = att_wait_warp(sh, p, &sh.kv_empty[x % Cfg::kRing], x / Cfg::kRing);
         if (!ok) break;
       }
-      // V's rows that no row of the unit sees may hold anything, and P is 0 there: they are
-      // zeroed before the tile counts as loaded.
       const bool clear = V && j0 + kAttTile > sinks && !(j0 >= g.lo && j0 + kAttTile <= g.hi);
+      if (clear && !settle_edge()) {
+        ok = false;
+        break;
+      }
       uint64_t* landed = clear ? &sh.edge_full : full;
       if (lane == 0) mbar_arrive_expect_tx(landed, count * kBlocks * box * 128);
       __syncwarp();
@@ -439,25 +460,26 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
       }
       __syncwarp();
       issued = r + 1;
-      if (V) {  // the next entry, in the shadow of this load; and the second one at the start
+      if (V) {
+        ok = settle_edge();
+        if (!ok) break;
+        if (clear) edge = {tile, full, j0, sinks, g.lo, g.hi};
+        // the list's next entry; and the second one at the start
         for (int x = (i == g.n - 1) + (e == 0 && i == 0); x > 0; --x)
           if (lane == 0) walk->publish(sh, p);
         __syncwarp();
-      }
-      if (clear) {
-        ok = att_wait_warp(sh, p, &sh.edge_full, edges++);
-        if (!ok) break;
-        for (int y = lane; y < kAttTile; y += 32) {
-          if (j0 + y < sinks || (j0 + y >= g.lo && j0 + y < g.hi)) continue;
-#pragma unroll
-          for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              *(uint4*)(tile + k * kBlockBytes + y * 128 + 16 * x) = make_uint4(0, 0, 0, 0);
+      } else if (i == 0) {
+        for (int s = 0; s <= g.pair; ++s) {
+          const int x = g.q_at + s, q_slot = x & 1;
+          ok = ok && att_wait_warp(sh, p, &sh.q_empty[q_slot], (x / 2 + 1) & 1);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&sh.q_full[x & 3], kBlocks * p.tile_tokens * p.G * 128);
+            for (int k = 0; k < kBlocks; ++k)
+              tma_load_4d(q_smem + q_slot * Cfg::kTileBytes + k * kBlockBytes, &p.q_map, 64 * k,
+                          0, g.head, g.token + s * p.tile_tokens, &sh.q_full[x & 3]);
+          }
+          __syncwarp();
         }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full);
       }
     }
     if (!ok) break;
@@ -865,17 +887,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   // Key tiles of each thread's run of requests, and of all.
   const int step = 2 * p.tile_tokens;
   const int r0 = (int)min((long long)tid * run, (long long)p.B), r1 = min(r0 + run, p.B);
-  auto tiles_of = [&](int r, int& hi) {
-    int lo;
-    const int len = attend_request(p, r, lo, hi);
+  int lo = 0, hi = 0, len = 0;  // of the request read last
+  auto tiles_of = [&](int r) {
+    len = attend_request(p, r, lo, hi);
     const AttUnits units(len, hi - lo, step, p.window, p.sinks);
     return (unsigned long long)units.before(units.count) * p.kv_heads;
   };
   unsigned long long mine = 0;
   int pad = 0;  // rows from here on belong to no request
   for (int r = r0; r < r1; ++r) {
-    int hi;
-    mine += tiles_of(r, hi);
+    mine += tiles_of(r);
     pad = max(pad, hi);
   }
   unsigned long long upto = mine;
@@ -904,14 +925,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   const int begin = works ? att_begin(blockIdx.x, total, blocks) : 0;
   const int end = works ? att_begin(blockIdx.x + 1, total, blocks) : 0;
   if (works && before <= begin && begin < before + (int)mine) {
-    int at = before, r = r0, hi;
-    for (; r + 1 < r1; ++r) {
-      const int n = (int)tiles_of(r, hi);
-      if (begin < at + n) break;
-      at += n;
+    int at = before, r = r0;
+    if (run > 1) {
+      for (;; ++r) {
+        const int n = (int)tiles_of(r);
+        if (begin < at + n || r + 1 >= r1) break;
+        at += n;
+      }
     }
     AttWalk walk;
-    walk.start(p, begin, end, total, blocks, r, at);
+    walk.start(p, begin, end, total, blocks, r, at, lo, hi, len);
     walk.publish(sh, p);
     sh.walk = walk;
   }
@@ -956,7 +979,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   }
 }
 
-constexpr int kJoinThreads = 256, kJoinSplit = 8;
+constexpr int kJoinThreads = 256, kJoinSplit = 16;
 
 // Join the partial results of the unit that starts in block blockIdx.x's part
 // of the list and ends in another's: parts of one row weigh 2^(m - max m). An
