@@ -387,40 +387,11 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
   const int box = min(page, kAttTile);         // tokens of one load
   const int boxes = kAttTile / box;            // of a tile
   unsigned issued = 0, edges = 0;
-  // V's rows that no row of the unit sees may hold anything, and P is 0 there: they are zeroed
-  // before the tile counts as loaded. That waits for the load, so it is done after the next
-  // tile's has been issued (whose place in the ring does not wait for this one).
-  struct {
-    char* tile;
-    uint64_t* full;
-    int j0, sinks, lo, hi;
-  } edge = {nullptr, nullptr, 0, 0, 0, 0};
-  auto settle_edge = [&]() {
-    if (!V || !edge.tile) return true;
-    if (!att_wait_warp(sh, p, &sh.edge_full, edges++)) return false;
-    for (int y = lane; y < kAttTile; y += 32) {
-      const int j = edge.j0 + y;
-      if (j < edge.sinks || (j >= edge.lo && j < edge.hi)) continue;
-#pragma unroll
-      for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          *(uint4*)(edge.tile + k * kBlockBytes + y * 128 + 16 * x) = make_uint4(0, 0, 0, 0);
-    }
-    fence_async_shared();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(edge.full);
-    edge.tile = nullptr;
-    return true;
-  };
   for (int e = 0;; ++e) {
     const int at = e % kAttSegs;
     if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) break;
     const AttSeg g = sh.seg[at];
-    if (g.n == 0) {
-      if (settle_edge()) return;
-      break;
-    }
+    if (g.n == 0) return;
     bool ok = true;
     const int* table = p.table + g.b * p.table_stride;
     const int sinks = min(p.sinks, g.lo);
@@ -445,10 +416,6 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
         if (!ok) break;
       }
       const bool clear = V && j0 + kAttTile > sinks && !(j0 >= g.lo && j0 + kAttTile <= g.hi);
-      if (clear && !settle_edge()) {
-        ok = false;
-        break;
-      }
       uint64_t* landed = clear ? &sh.edge_full : full;
       if (lane == 0) mbar_arrive_expect_tx(landed, count * kBlocks * box * 128);
       __syncwarp();
@@ -461,13 +428,27 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
       __syncwarp();
       issued = r + 1;
       if (V) {
-        ok = settle_edge();
-        if (!ok) break;
-        if (clear) edge = {tile, full, j0, sinks, g.lo, g.hi};
-        // the list's next entry; and the second one at the start
+        // the list's next entry, in the shadow of this load; and the second one at the start
         for (int x = (i == g.n - 1) + (e == 0 && i == 0); x > 0; --x)
           if (lane == 0) walk->publish(sh, p);
         __syncwarp();
+        if (clear) {
+          // V's rows that no row of the unit sees may hold anything, and P is 0 there: they are
+          // zeroed before the tile counts as loaded.
+          ok = att_wait_warp(sh, p, &sh.edge_full, edges++);
+          if (!ok) break;
+#pragma unroll 1
+          for (int y = lane; y < kAttTile * kBlocks; y += 32) {
+            const int j = j0 + (y & (kAttTile - 1));
+            if (j < sinks || (j >= g.lo && j < g.hi)) continue;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *(uint4*)(tile + y * 128 + 16 * x) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+        }
       } else if (i == 0) {
         for (int s = 0; s <= g.pair; ++s) {
           const int x = g.q_at + s, q_slot = x & 1;
