@@ -47,6 +47,7 @@ constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
 constexpr int kAttThreads = 384;  // 12 warps, at most 168 registers each at launch
 constexpr int kAttRegsMany = 208, kAttRegsFew = 88;  // 2 * 208 + 88 = 3 * 168
 constexpr int kAttSegs = 4;       // list entries ahead of the slowest warp
+constexpr long long kAttPatience = 2000000000;  // clocks that a wait may take
 constexpr float kAttGrow = 8.f;   // log2 of how far a row's maximum may grow unscaled
 
 template <int DP>
@@ -280,16 +281,15 @@ struct AttShared : AttBase {
 static_assert(sizeof(AttShared<128>) <= 3072 && sizeof(AttShared<64>) <= 4096,
               "shared memory beside the tiles");
 
-// A bounded wait; once one has run out every later one returns at once. The first probes
-// carry no time limit of their own: one with a limit costs three times as much.
+// A bounded wait (about a second); once one has run out every later one returns at once. The
+// probes carry no time limit of their own: one with a limit costs three times as much.
 __device__ __forceinline__ bool att_wait(AttBase& sh, const AttendParams& p, uint64_t* bar,
                                          uint32_t parity) {
-  for (int i = 0; i < 256; ++i)
+  if (__builtin_expect(mbar_poll(bar, parity & 1), 1)) return true;
+  const long long from = clock64();
+  do {
     if (mbar_poll(bar, parity & 1)) return true;
-  for (uint32_t i = 0; i < kTryLimit; ++i) {
-    if (mbar_try(bar, parity & 1)) return true;
-    if (*(volatile int*)&sh.stop) return false;
-  }
+  } while (!*(volatile int*)&sh.stop && clock64() - from < kAttPatience);
   *(volatile int*)&sh.stop = 1;
   if (p.status) atomicOr(p.status, SPEC_STATUS_TIMEOUT);
   return false;
@@ -401,7 +401,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
       int number = 0;
       if (live) {
         number = __ldg(table + (j >> p.page_shift));
-        if (number < 0 || number >= p.num_pages) {
+        if (__builtin_expect(number < 0 || number >= p.num_pages, 0)) {
           if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_PAGE);
           live = false;
         }
@@ -429,10 +429,12 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
       issued = r + 1;
       if (V) {
         // the list's next entry, in the shadow of this load; and the second one at the start
-        for (int x = (i == g.n - 1) + (e == 0 && i == 0); x > 0; --x)
-          if (lane == 0) walk->publish(sh, p);
-        __syncwarp();
-        if (clear) {
+        if (__builtin_expect(i == g.n - 1 || (e == 0 && i == 0), 0)) {
+          for (int x = (i == g.n - 1) + (e == 0 && i == 0); x > 0; --x)
+            if (lane == 0) walk->publish(sh, p);
+          __syncwarp();
+        }
+        if (__builtin_expect(clear, 0)) {
           // V's rows that no row of the unit sees may hold anything, and P is 0 there: they are
           // zeroed before the tile counts as loaded.
           ok = att_wait_warp(sh, p, &sh.edge_full, edges++);
@@ -449,7 +451,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
           __syncwarp();
           if (lane == 0) mbar_arrive(full);
         }
-      } else if (i == 0) {
+      } else if (__builtin_expect(i == 0, 0)) {
         for (int s = 0; s <= g.pair; ++s) {
           const int x = g.q_at + s, q_slot = x & 1;
           ok = ok && att_wait_warp(sh, p, &sh.q_empty[q_slot], (x / 2 + 1) & 1);
@@ -618,7 +620,7 @@ __device__ __forceinline__ void att_rescale(uint32_t tmem_o, float keep) {
 // The largest of 64 values and x (the least, where the scores' factor is negative).
 __device__ __forceinline__ float att_max64(const float* f, bool largest, float x) {
   float top[4] = {x, f[1], f[2], f[3]};
-  if (largest) {
+  if (__builtin_expect(largest, 1)) {
     top[0] = fmaxf(top[0], f[0]);
 #pragma unroll
     for (int y = 4; y < 60; y += 8)
@@ -692,7 +694,7 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
       ++s_count;
       if (busy) {
         tmem_fence_after();
-        if (!all_seen) att_hide(tmem_s, pos, j0, p.window, p.sinks, p.hidden);
+        if (__builtin_expect(!all_seen, 0)) att_hide(tmem_s, pos, j0, p.window, p.sinks, p.hidden);
         float f[64], top;
         {
           float x[64];
@@ -708,7 +710,7 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
         tmem_wait_ld(f + 32);
         top = att_max64(f, p.c > 0.f, top) * p.c;
         const bool grown = mine && top > m + kAttGrow;
-        if (__any_sync(~0u, grown)) {
+        if (__builtin_expect(__any_sync(~0u, grown), 0)) {
           const float keep = grown ? ex2(m - top) : 1.f;
           l *= keep;
           if (grown) m = top;
