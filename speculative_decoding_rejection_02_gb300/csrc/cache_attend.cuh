@@ -395,17 +395,20 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
     bool ok = true;
     const int* table = p.table + g.b * p.table_stride;
     const int sinks = min(p.sinks, g.lo);
+    // The lane's first token of tile i, and the number of its page (-1: no row sees it).
+    auto place = [&](int i) { return att_tile(g, i) * kAttTile + lane * box; };
+    auto page_of = [&](int j) {
+      const bool seen = lane < boxes && j < g.hi && (j + box > g.lo || j < sinks);
+      return seen ? __ldg(table + (j >> p.page_shift)) : -1;
+    };
+    int number = page_of(place(0));
     for (int i = 0; ok && i < g.n; ++i) {
-      const int j0 = att_tile(g, i) * kAttTile, j = j0 + lane * box;  // the lane's first token
-      bool live = lane < boxes && j < g.hi && (j + box > g.lo || j < sinks);
-      int number = 0;
-      if (live) {
-        number = __ldg(table + (j >> p.page_shift));
-        if (__builtin_expect(number < 0 || number >= p.num_pages, 0)) {
-          if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_PAGE);
-          live = false;
-        }
-      }
+      const int j = place(i), j0 = j - lane * box, this_page = number;
+      // the next tile's pages, read while this one is loaded
+      if (i + 1 < g.n) number = page_of(place(i + 1));
+      const bool live = this_page >= 0 && this_page < p.num_pages;
+      if (__builtin_expect(!live && lane < boxes && j < g.hi && (j + box > g.lo || j < sinks), 0))
+        if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_PAGE);
       const int count = __popc(__ballot_sync(~0u, live));
       const unsigned r = g.ring + (V ? att_v_at(g.pair, i, g.n) : att_k_at(g.pair, i));
       char* tile = kv_smem + (r % Cfg::kStages) * Cfg::kTileBytes;
@@ -423,7 +426,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
         char* dst = tile + lane * box * 128;
         for (int k = 0; k < kBlocks; ++k)
           tma_load_4d(dst + k * kBlockBytes, V ? &p.v_map : &p.k_map, 64 * k, j & (page - 1),
-                      g.head, number, landed);
+                      g.head, this_page, landed);
       }
       __syncwarp();
       issued = r + 1;
