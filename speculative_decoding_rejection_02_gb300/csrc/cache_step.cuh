@@ -10,9 +10,10 @@
 // on its own, no block waits for another, and one launch does the whole step.
 //
 // Each block reads all lengths (16 bytes per request, from L2) and scans
-// them: a run of E consecutive requests per thread, one block-wide scan of
-// the run totals. That is work repeated by every block, against a second
-// launch or a chain through global memory between blocks.
+// them: a run of consecutive requests per thread, one block-wide scan of the
+// run totals. That is work repeated by every block, against a second launch
+// or a chain through global memory between blocks. The sums saturate at
+// 2^32 - 1, which no valid call reaches.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -23,23 +24,28 @@
 
 namespace sv {
 
-constexpr int kStepThreads = 512;
-
 struct StepParams {
   spec_cache_step_args a;
   unsigned* status;
   int run;  // requests per thread of the scan
+  // n / page_size = n * page_mul >> page_shift for 0 <= n < 2^31
+  unsigned long long page_mul;
+  int page_shift;
 };
+
+__device__ __forceinline__ int step_pages(const StepParams& p, int n) {  // page of token n
+  return (int)((unsigned long long)n * p.page_mul >> p.page_shift);
+}
 
 // Lengths and pages of one request.
 struct StepRequest {
-  long long kept, lens;
-  long long have, need;  // pages before and after
-  int fresh;             // new tokens
+  int kept, lens, fresh;
+  int have, need;  // pages before and after
   bool ok;
 };
 
-__device__ __forceinline__ StepRequest step_request(const spec_cache_step_args& a, int r) {
+__device__ __forceinline__ StepRequest step_request(const StepParams& p, int r) {
+  const spec_cache_step_args& a = p.a;
   StepRequest q;
   const int held = a.held_lens[r];
   q.fresh = a.new_lens[r];
@@ -48,140 +54,157 @@ __device__ __forceinline__ StepRequest step_request(const spec_cache_step_args& 
   if (a.cu_num_draft) {
     const int drafts = a.cu_num_draft[r + 1] - a.cu_num_draft[r];
     const int accepted = a.num_accepted[r];
-    q.ok = q.ok && drafts >= 0 && accepted >= 0 && accepted <= drafts;
     gone = drafts - accepted;
+    q.ok = q.ok && accepted >= 0 && gone >= 0 && gone <= held && drafts >= 0;
   }
-  q.kept = (long long)held - gone;
-  q.lens = q.kept + q.fresh;
-  const unsigned page = (unsigned)a.page_size;
-  // lengths are below 2^31, so the rounded-up sums fit 32 unsigned bits
-  q.have = ((unsigned)max(held, 0) + (page - 1u)) / page;
-  q.ok = q.ok && q.kept >= 0 && q.have <= a.width && q.lens <= (long long)a.width * page &&
-         q.lens <= 0x7fffffffll;
-  q.need = q.ok ? ((unsigned)q.lens + (page - 1u)) / page : 0;
+  q.kept = held - gone;
+  const long long lens = (long long)q.kept + q.fresh;
+  q.ok = q.ok && lens <= 0x7fffffffll;
+  q.lens = q.ok ? (int)lens : 0;
+  q.have = q.ok && held > 0 ? step_pages(p, held - 1) + 1 : 0;
+  q.need = q.lens > 0 ? step_pages(p, q.lens - 1) + 1 : 0;
+  q.ok = q.ok && q.have <= a.width && q.need <= a.width;
   return q;
 }
 
 struct StepSums {
-  long long fresh, gone, more;
+  unsigned fresh, gone, more;
 };
 
+__device__ __forceinline__ unsigned sat_add(unsigned x, unsigned y) {
+  const unsigned z = x + y;
+  return z < x ? ~0u : z;
+}
 __device__ __forceinline__ StepSums step_add(StepSums x, StepSums y) {
-  return {x.fresh + y.fresh, x.gone + y.gone, x.more + y.more};
+  return {sat_add(x.fresh, y.fresh), sat_add(x.gone, y.gone), sat_add(x.more, y.more)};
 }
 __device__ __forceinline__ StepSums step_of(const StepRequest& q) {
-  return {q.fresh, q.have > q.need ? q.have - q.need : 0, q.need > q.have ? q.need - q.have : 0};
+  return {(unsigned)max(q.fresh, 0), (unsigned)max(q.have - q.need, 0),
+          (unsigned)max(q.need - q.have, 0)};
 }
 __device__ __forceinline__ StepSums step_up(StepSums x, int d) {
   return {__shfl_up_sync(~0u, x.fresh, d), __shfl_up_sync(~0u, x.gone, d),
           __shfl_up_sync(~0u, x.more, d)};
 }
 
+template <int THREADS>
+struct StepShared {
+  unsigned fresh[THREADS], gone[THREADS], more[THREADS];  // before each thread's run
+  StepSums warp_sum[THREADS / 32];
+};
+
 // The request that item x of prefix sum WHICH (0 new tokens, 1 pages given
 // up, 2 pages taken) belongs to, and the sums before that request.
-template <int WHICH>
-__device__ __forceinline__ int step_find(const StepParams& p, const StepSums* before, long long x,
-                                         StepRequest& q, StepSums& at) {
+template <int WHICH, int THREADS>
+__device__ __forceinline__ int step_find(const StepParams& p, const StepShared<THREADS>& sh,
+                                         unsigned x, StepRequest& q, StepSums& at) {
+  const unsigned* before = WHICH == 0 ? sh.fresh : WHICH == 1 ? sh.gone : sh.more;
   auto part = [](const StepSums& s) { return WHICH == 0 ? s.fresh : WHICH == 1 ? s.gone : s.more; };
-  int lo = 0, hi = kStepThreads - 1;  // the last run that starts at or before x
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (part(before[mid]) <= x) lo = mid; else hi = mid - 1;
-  }
-  at = before[lo];
+  int lo = 0;  // the last run that starts at or before x
+#pragma unroll
+  for (int d = THREADS / 2; d; d >>= 1)
+    if (before[lo + d] <= x) lo += d;
+  at = {sh.fresh[lo], sh.gone[lo], sh.more[lo]};
   int r = lo * p.run;
   for (;; ++r) {  // x is below the total, so a request of this run holds it
-    q = step_request(p.a, r);
+    q = step_request(p, r);
     const StepSums next = step_add(at, step_of(q));
     if (x < part(next) || r + 1 >= p.a.B) return r;
     at = next;
   }
 }
 
-__global__ void __launch_bounds__(kStepThreads) k_cache_step(const StepParams p) {
-  __shared__ StepSums before[kStepThreads];
-  __shared__ StepSums warp_sum[kStepThreads / 32];
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) k_cache_step(const StepParams p) {
+  __shared__ StepShared<THREADS> sh;
   const spec_cache_step_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
+  const int count = *a.free_count;
   // Totals of this thread's run of requests, then the scan over the block.
   StepSums sum = {0, 0, 0};
   int bad = 0;
-  const int r0 = min((long long)tid * p.run, (long long)a.B), r1 = min(r0 + p.run, a.B);
+  const int r0 = min(tid * p.run, a.B), r1 = min(r0 + p.run, a.B);
+#pragma unroll 4
   for (int r = r0; r < r1; ++r) {
-    const StepRequest q = step_request(a, r);
+    const StepRequest q = step_request(p, r);
     bad |= !q.ok;
     sum = step_add(sum, step_of(q));
   }
   StepSums scan = sum;
+#pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const StepSums y = step_up(scan, d);
     if (lane >= d) scan = step_add(scan, y);
   }
-  if (lane == 31) warp_sum[warp] = scan;
+  if (lane == 31) sh.warp_sum[warp] = scan;
   bad = __syncthreads_or(bad);
   StepSums base = {0, 0, 0}, total = {0, 0, 0};
-  for (int w = 0; w < kStepThreads / 32; ++w) {
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w == warp) base = total;
-    total = step_add(total, warp_sum[w]);
+    total = step_add(total, sh.warp_sum[w]);
   }
   base = step_add(base, {scan.fresh - sum.fresh, scan.gone - sum.gone, scan.more - sum.more});
-  before[tid] = base;
+  sh.fresh[tid] = base.fresh;
+  sh.gone[tid] = base.gone;
+  sh.more[tid] = base.more;
   __syncthreads();
 
-  const long long count = *a.free_count;
-  bad = bad || total.fresh > a.num_tokens || count < 0 || count + total.gone > a.num_pages;
-  const bool dry = !bad && total.more > count + total.gone;
+  bad = bad || total.fresh > (unsigned)a.num_tokens || count < 0 ||
+        total.gone > (unsigned)a.num_pages ||
+        (unsigned)count + total.gone > (unsigned)a.num_pages;
+  const bool dry = !bad && total.more > (unsigned)count + total.gone;
   const bool go = !bad && !dry;
-  const int first = blockIdx.x * kStepThreads + tid, step = gridDim.x * kStepThreads;
+  const unsigned first = blockIdx.x * THREADS + tid, step = gridDim.x * THREADS;
   if (first == 0) {
     if (!go && p.status) atomicOr(p.status, bad ? SPEC_CACHE_BAD_LENGTHS : SPEC_CACHE_NO_PAGES);
-    *a.free_count_out = (int)(go ? count + total.gone - total.more : count);
+    *a.free_count_out = go ? (int)(count + total.gone - total.more) : count;
     a.cu_new[0] = 0;
   }
   // Lengths and offsets: the runs are dealt to the blocks in turn.
   if (tid % gridDim.x == blockIdx.x) {
     StepSums at = base;
     for (int r = r0; r < r1; ++r) {
-      const StepRequest q = step_request(a, r);
+      const StepRequest q = step_request(p, r);
       at = step_add(at, step_of(q));
-      a.lens[r] = go ? (int)q.lens : a.held_lens[r];
+      a.lens[r] = go ? q.lens : a.held_lens[r];
       a.cu_new[r + 1] = go ? (int)at.fresh : 0;
     }
   }
   if (!go) {
-    for (long long t = first; t < a.num_tokens; t += step) {
+    for (unsigned t = first; t < (unsigned)a.num_tokens; t += step) {
       a.slots[t] = -1;
       if (a.positions) a.positions[t] = -1;
     }
     return;
   }
   // Entry i of the stack once the pages given up are on it.
-  auto entry = [&](long long i) -> int {
-    if (i < count) return a.free_pages[i];
+  auto entry = [&](unsigned i) -> int {
+    if (i < (unsigned)count) return a.free_pages[i];
     StepRequest q;
     StepSums at;
-    const int r = step_find<1>(p, before, i - count, q, at);
+    const int r = step_find<1, THREADS>(p, sh, i - count, q, at);
     return a.block_table[r * a.table_stride + q.need + (i - count - at.gone)];
   };
-  const long long top = count + total.gone - 1;
-  for (long long i = first; i < total.gone; i += step) a.free_pages[count + i] = entry(count + i);
-  for (long long i = first; i < total.more; i += step) {
+  const unsigned top = count + total.gone - 1;
+  for (unsigned i = first; i < total.gone; i += step) a.free_pages[count + i] = entry(count + i);
+  for (unsigned i = first; i < total.more; i += step) {
     StepRequest q;
     StepSums at;
-    const int r = step_find<2>(p, before, i, q, at);
+    const int r = step_find<2, THREADS>(p, sh, i, q, at);
     a.block_table[r * a.table_stride + q.have + (i - at.more)] = entry(top - i);
   }
-  for (long long t = first; t < a.num_tokens; t += step) {
+  for (unsigned t = first; t < (unsigned)a.num_tokens; t += step) {
     long long slot = -1;
     int pos = -1;
     if (t < total.fresh) {
       StepRequest q;
       StepSums at;
-      const int r = step_find<0>(p, before, t, q, at);
-      pos = (int)(q.kept + (t - at.fresh));
-      const int col = (int)((unsigned)pos / (unsigned)a.page_size);
+      const int r = step_find<0, THREADS>(p, sh, t, q, at);
+      pos = q.kept + (int)(t - at.fresh);
+      const int col = step_pages(p, pos);
       // a page taken in this call is looked up where it came from: another
       // block may not have written it to the table yet
       const int page = col < q.have ? a.block_table[r * a.table_stride + col]

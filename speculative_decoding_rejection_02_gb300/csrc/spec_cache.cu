@@ -197,12 +197,22 @@ int spec_cache_step(const spec_cache_step_args* a, void* stream, unsigned* devic
   sv::StepParams p;
   p.a = *a;
   p.status = device_status;
-  p.run = a->B > sv::kStepThreads ? (a->B + sv::kStepThreads - 1) / sv::kStepThreads : 1;
-  const long long items = a->num_tokens > a->B ? a->num_tokens : a->B;
-  long long blocks = (items + 2 * sv::kStepThreads - 1) / (2 * sv::kStepThreads);
-  if (blocks < 1) blocks = 1;
+  // for n < 2^31 and d < 2^31: floor(n / d) = n * (floor(2^(31 + s) / d) + 1) >> (31 + s),
+  // s the bits of d - 1
+  int bits = 0;
+  while ((1ll << bits) < a->page_size) ++bits;
+  p.page_shift = 31 + bits;
+  p.page_mul = (1ull << p.page_shift) / a->page_size + 1;
+  // A small call is one block of 256 threads (its latency is what counts), a larger one has a
+  // thread of 1024-thread blocks for each token and request, as far as the SMs go.
+  const int items = a->num_tokens > a->B ? a->num_tokens : a->B;
+  const bool small = items <= 512;
+  const int threads = small ? 256 : 1024;
+  p.run = a->B > threads ? (a->B + threads - 1) / threads : 1;
+  long long blocks = small ? 1 : ((long long)items + threads - 1) / threads;
   if (blocks > sms) blocks = sms;
-  return launch(sv::k_cache_step, dim3((unsigned)blocks), sv::kStepThreads, 0, stream, p);
+  return launch(small ? sv::k_cache_step<256> : sv::k_cache_step<1024>, dim3((unsigned)blocks),
+                threads, 0, stream, p);
 }
 
 int spec_cache_append(const spec_cache_append_args* a, void* stream, unsigned* device_status) {
