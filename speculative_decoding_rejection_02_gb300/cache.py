@@ -9,12 +9,15 @@ torch's allocator on the stream that the call runs on (``stream``, or the
 current one), and errors in device data set bits of ``status`` (an int32
 tensor of one element, OR-ed).
 
-A call costs the host about as much as its launch, so each check is one
-expression over plain attributes; what is wrong is worked out afterwards.
+The calls on tensors are ``csrc/cache_binding.cpp``; the structures of the C
+ABI are here for callers that come with addresses of their own.
 """
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
+import os
 from typing import NamedTuple
 
 import torch
@@ -27,11 +30,6 @@ CACHE_BAD_SLOT = 0x400
 CACHE_BAD_PAGE = 0x800
 
 _I, _L, _P = C.c_int, C.c_longlong, C.c_void_p
-_i32, _i64 = torch.int32, torch.int64
-_DTYPES = {torch.bfloat16: 1, torch.float16: 2}
-_empty = torch.empty
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class StepArgs(C.Structure):
@@ -70,43 +68,28 @@ class CacheStep(NamedTuple):
     free_count: torch.Tensor  # int32 [1]
 
 
-def _run(fn, name, args, dev, status):
-    """One call of the C ABI on the tensors' device and its current stream."""
-    if status is not None:
-        if status.numel() != 1 or status.element_size() != 4 or status.get_device() != dev:
-            raise ValueError("status must be one 32-bit integer beside the other tensors")
-        status = status.data_ptr()
-    if _device() == dev:
-        rc = fn(args, _raw_stream(dev), status)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(args, _raw_stream(dev), status)
-    if rc != 0:
-        raise _sv.SpecVerifyError(rc, name)
+class _Native:
+    """cache_binding.cpp, built and bound to the library at the first call (the package imports
+    without it)."""
+
+    def __getattr__(self, name):
+        lib = _sv.lib()
+        path = _sv._build.BINDING_PATH
+        if not os.path.exists(path):
+            raise ImportError(f"the cache binding is not built ({path}); "
+                              "run __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_cache_binding", path)
+        spec = importlib.util.spec_from_loader("_cache_binding", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.bind(*(C.cast(getattr(lib, "spec_cache_" + n), C.c_void_p).value
+                      for n in ("step", "append", "attend", "attend_workspace")))
+        for n in ("step", "append", "attend"):
+            setattr(self, n, getattr(module, n))
+        return object.__getattribute__(self, name)
 
 
-def _need(ok, what, *tensors):
-    if not ok:
-        raise ValueError(what + ", not " + ", ".join(
-            "none" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"
-            for t in tensors))
-
-
-def _one_device(dev, *tensors):
-    if dev < 0:
-        raise ValueError("the tensors must be on a CUDA device")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on cuda:{dev} and {t.device}")
-
-
-def _table(t, B):
-    """Stride of a block table's rows."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not _i32 or len(shape) != 2 or shape[0] != B or shape[1] < 1 or (
-            stride[1] != 1 and shape[1] > 1):
-        _need(False, f"block_table must be int32 [{B}, width] with adjacent columns", t)
-    return stride[0] if B > 1 else max(stride[0], shape[1])
+_native = _Native()
 
 
 def _on(stream, call, *args, **kw):
@@ -134,38 +117,11 @@ def cache_step(held_lens, new_lens, block_table, free_pages, free_count, *, page
         return _on(stream, cache_step, held_lens, new_lens, block_table, free_pages, free_count,
                    page_size=page_size, num_tokens=num_tokens, cu_num_draft=cu_num_draft,
                    num_accepted=num_accepted, status=status)
-    dev = held_lens.get_device()
-    _one_device(dev, new_lens, block_table, free_pages, free_count, cu_num_draft, num_accepted)
-    B = held_lens.numel()
-    if not (held_lens.dtype is _i32 and new_lens.dtype is _i32 and new_lens.numel() == B
-            and held_lens.is_contiguous() and new_lens.is_contiguous()):
-        _need(False, "held_lens and new_lens must be contiguous int32 [B]", held_lens, new_lens)
-    if not (free_pages.dtype is _i32 and free_pages.is_contiguous()
-            and free_count.dtype is _i32 and free_count.numel() == 1):
-        _need(False, "free_pages and free_count must be contiguous int32 [pages] and [1]",
-              free_pages, free_count)
-    drafts = accepted = None
-    if cu_num_draft is not None or num_accepted is not None:
-        if not (cu_num_draft is not None and num_accepted is not None
-                and cu_num_draft.dtype is _i32 and cu_num_draft.numel() == B + 1
-                and cu_num_draft.is_contiguous() and num_accepted.dtype is _i32
-                and num_accepted.numel() == B and num_accepted.is_contiguous()):
-            _need(False, "cu_num_draft and num_accepted must be contiguous int32 [B + 1] and [B]",
-                  cu_num_draft, num_accepted)
-        drafts, accepted = cu_num_draft.data_ptr(), num_accepted.data_ptr()
-    stride = _table(block_table, B)
-    place = held_lens.device
-    # one allocation for the 32-bit outputs
-    ints = _empty(2 * B + 2 + num_tokens, dtype=_i32, device=place)
-    at = ints.data_ptr()
-    lens, cu_new, count, positions = ints.split_with_sizes((B, B + 1, 1, num_tokens))
-    slots = _empty(num_tokens, dtype=_i64, device=place)
-    args = StepArgs(B, block_table.shape[1], stride, page_size, free_pages.numel(), num_tokens,
-                    held_lens.data_ptr(), new_lens.data_ptr(), drafts, accepted,
-                    block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), at,
-                    at + 4 * B, at + 4 * (2 * B + 2), slots.data_ptr(), at + 4 * (2 * B + 1))
-    _run(_lib.spec_cache_step, "spec_cache_step", args, dev, status)
-    return CacheStep(lens, cu_new, positions, slots, count)
+    r = _native.step(held_lens, new_lens, block_table, free_pages, free_count, page_size,
+                     num_tokens, cu_num_draft, num_accepted, status)
+    if type(r) is int:
+        raise _sv.SpecVerifyError(r, "spec_cache_step")
+    return CacheStep(*r)
 
 
 def cache_append(k, v, slots, k_pages, v_pages, *, status=None, stream=None) -> None:
@@ -174,29 +130,9 @@ def cache_append(k, v, slots, k_pages, v_pages, *, status=None, stream=None) -> 
     [pages, page_size, kv_heads, dim]. Any strides whose last one is 1."""
     if stream is not None:
         return _on(stream, cache_append, k, v, slots, k_pages, v_pages, status=status)
-    dev = k_pages.get_device()
-    _one_device(dev, k, v, slots, v_pages)
-    shape, dtype = k_pages.shape, k_pages.dtype
-    if dtype not in _DTYPES:
-        raise TypeError(f"the cache holds bfloat16 or float16, not {dtype}")
-    sk, sv, pk, pv = k.stride(), v.stride(), k_pages.stride(), v_pages.stride()
-    if not (len(shape) == 4 and v_pages.shape == shape and v_pages.dtype is dtype
-            and ((pk[3] == 1 and pv[3] == 1) or shape[3] == 1)):
-        _need(False, "k_pages and v_pages must be alike, [pages, page_size, kv_heads, dim] with "
-              "adjacent elements", k_pages, v_pages)
-    if not (len(sk) == 3 and k.shape[1:] == shape[2:] and v.shape == k.shape
-            and k.dtype is dtype and v.dtype is dtype
-            and ((sk[2] == 1 and sv[2] == 1) or shape[3] == 1)):
-        _need(False, f"k and v must be {dtype} [tokens, {shape[2]}, {shape[3]}] with adjacent "
-              "elements", k, v)
-    T = k.shape[0]
-    if not (slots.dtype is _i64 and slots.numel() == T and slots.is_contiguous()):
-        _need(False, f"slots must be contiguous int64 [{T}]", slots)
-    args = AppendArgs(T, shape[2], shape[3], shape[1], shape[0], _DTYPES[dtype], k.data_ptr(),
-                      sk[0], sk[1], v.data_ptr(), sv[0], sv[1], slots.data_ptr(),
-                      k_pages.data_ptr(), pk[0], pk[1], pk[2], v_pages.data_ptr(), pv[0], pv[1],
-                      pv[2])
-    _run(_lib.spec_cache_append, "spec_cache_append", args, dev, status)
+    r = _native.append(k, v, slots, k_pages, v_pages, status)
+    if r is not None:
+        raise _sv.SpecVerifyError(r, "spec_cache_append")
 
 
 def cache_attend(q, k_pages, v_pages, block_table, kv_lens, cu_q, *, max_q=None, scale=None,
@@ -217,63 +153,8 @@ def cache_attend(q, k_pages, v_pages, block_table, kv_lens, cu_q, *, max_q=None,
         return _on(stream, cache_attend, q, k_pages, v_pages, block_table, kv_lens, cu_q,
                    max_q=max_q, scale=scale, window=window, sinks=sinks, out=out,
                    return_lse=return_lse, status=status)
-    dev = q.get_device()
-    _one_device(dev, k_pages, v_pages, block_table, kv_lens, cu_q, out)
-    shape, dtype = k_pages.shape, q.dtype
-    if dtype not in _DTYPES:
-        raise TypeError(f"the cache holds bfloat16 or float16, not {dtype}")
-    sq, pk, pv = q.stride(), k_pages.stride(), v_pages.stride()
-    if not (len(shape) == 4 and v_pages.shape == shape and v_pages.dtype is dtype
-            and k_pages.dtype is dtype and ((pk[3] == 1 and pv[3] == 1) or shape[3] == 1)):
-        _need(False, f"k_pages and v_pages must be alike, {dtype} [pages, page_size, kv_heads, "
-              "dim] with adjacent elements", k_pages, v_pages)
-    n_pages, page_size, kv_heads, dim = shape
-    if not (len(sq) == 3 and q.shape[2] == dim and kv_heads > 0 and q.shape[1] % kv_heads == 0
-            and (sq[2] == 1 or dim == 1)):
-        _need(False, f"q must be [tokens, heads, {dim}] with adjacent elements and heads a "
-              f"multiple of {kv_heads}", q)
-    T, heads, _ = q.shape
-    B = kv_lens.numel()
-    if not (kv_lens.dtype is _i32 and cu_q.dtype is _i32 and cu_q.numel() == B + 1
-            and kv_lens.is_contiguous() and cu_q.is_contiguous()):
-        _need(False, "kv_lens and cu_q must be contiguous int32 [B] and [B + 1]", kv_lens, cu_q)
-    stride = _table(block_table, B)
-    if out is None:
-        out = _empty((T, heads, dim), dtype=dtype, device=q.device)
-        so = (heads * dim, dim)
-    else:
-        so = out.stride()
-        if not (out.shape == q.shape and out.dtype is dtype and (so[2] == 1 or dim == 1)):
-            _need(False, f"out must be {dtype} {tuple(q.shape)} with adjacent elements", out)
-    lse = _empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
-    args = AttendArgs(B, T, max_q or T or 1, heads, kv_heads, dim, page_size,
-                      block_table.shape[1], n_pages, _DTYPES[dtype], q.data_ptr(), sq[0], sq[1],
-                      k_pages.data_ptr(), pk[0], pk[1], pk[2], v_pages.data_ptr(), pv[0], pv[1],
-                      pv[2], block_table.data_ptr(), stride, kv_lens.data_ptr(), cu_q.data_ptr(),
-                      out.data_ptr(), so[0], so[1], lse.data_ptr() if return_lse else None,
-                      dim ** -0.5 if scale is None else scale, window, sinks, None, 0)
-    need = _lib.spec_cache_attend_workspace(args)
-    if need < 0:
-        raise _sv.SpecVerifyError(need, "spec_cache_attend")
-    workspace = _empty(need, dtype=torch.uint8, device=q.device)
-    args.workspace, args.workspace_bytes = workspace.data_ptr(), need
-    _run(_lib.spec_cache_attend, "spec_cache_attend", args, dev, status)
-    return (out, lse) if return_lse else out
-
-
-class _Lib:
-    """The library, loaded at the first call (the package imports without it)."""
-
-    def __getattr__(self, name):
-        lib = _sv.lib()
-        for n, kind in (("spec_cache_step", StepArgs), ("spec_cache_append", AppendArgs),
-                        ("spec_cache_attend", AttendArgs)):
-            # a prototype that takes the structure itself: no pointer object per call
-            fn = C.CFUNCTYPE(_I, C.POINTER(kind), _P, _P)((n, lib))
-            setattr(self, n, fn)
-        self.spec_cache_attend_workspace = C.CFUNCTYPE(_L, C.POINTER(AttendArgs))(
-            ("spec_cache_attend_workspace", lib))
-        return object.__getattribute__(self, name)
-
-
-_lib = _Lib()
+    r = _native.attend(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, scale, window,
+                       sinks, out, return_lse, status)
+    if type(r) is int:
+        raise _sv.SpecVerifyError(r, "spec_cache_attend")
+    return r
