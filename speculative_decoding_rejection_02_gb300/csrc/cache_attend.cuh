@@ -237,7 +237,10 @@ struct AttWalk {
     join = {-1, 0, 0, 0};
     read_ahead(p);
     const AttUnits units(len, hi - lo, 2 * p.tile_tokens, p.window, p.sinks);
-    const int per_head = units.before(units.count), x = begin - before;
+    const int x = begin - before;
+    head = rest = 0;
+    if (x == 0) return;
+    const int per_head = units.before(units.count);
     head = x / per_head;
     rest = x - head * per_head;
     int u1 = units.count - 1;  // the last unit that starts at or before there
@@ -387,6 +390,20 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
   const int box = min(page, kAttTile);         // tokens of one load
   const int boxes = kAttTile / box;            // of a tile
   unsigned issued = 0, edges = 0;
+  auto load_q = [&](const AttSeg& g) {
+    for (int s = 0; s <= g.pair; ++s) {
+      const int x = g.q_at + s, slot = x & 1;
+      if (!att_wait_warp(sh, p, &sh.q_empty[slot], (x / 2 + 1) & 1)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh.q_full[x & 3], kBlocks * p.tile_tokens * p.G * 128);
+        for (int k = 0; k < kBlocks; ++k)
+          tma_load_4d(q_smem + slot * Cfg::kTileBytes + k * kBlockBytes, &p.q_map, 64 * k, 0,
+                      g.head, g.token + s * p.tile_tokens, &sh.q_full[x & 3]);
+      }
+      __syncwarp();
+    }
+    return true;
+  };
   for (int e = 0;; ++e) {
     const int at = e % kAttSegs;
     if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) break;
@@ -402,6 +419,9 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
       return seen ? __ldg(table + (j >> p.page_shift)) : -1;
     };
     int number = page_of(place(0));
+    // Q of the first segment while that comes; later ones' after their first tile, which need
+    // not wait for Q's place
+    if (!V && e == 0) ok = load_q(g);
     for (int i = 0; ok && i < g.n; ++i) {
       const int j = place(i), j0 = j - lane * box, this_page = number;
       // the next tile's pages, read while this one is loaded
@@ -454,18 +474,8 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
           __syncwarp();
           if (lane == 0) mbar_arrive(full);
         }
-      } else if (__builtin_expect(i == 0, 0)) {
-        for (int s = 0; s <= g.pair; ++s) {
-          const int x = g.q_at + s, q_slot = x & 1;
-          ok = ok && att_wait_warp(sh, p, &sh.q_empty[q_slot], (x / 2 + 1) & 1);
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(&sh.q_full[x & 3], kBlocks * p.tile_tokens * p.G * 128);
-            for (int k = 0; k < kBlocks; ++k)
-              tma_load_4d(q_smem + q_slot * Cfg::kTileBytes + k * kBlockBytes, &p.q_map, 64 * k,
-                          0, g.head, g.token + s * p.tile_tokens, &sh.q_full[x & 3]);
-          }
-          __syncwarp();
-        }
+      } else if (__builtin_expect(i == 0 && e > 0, 0)) {
+        ok = load_q(g);
       }
     }
     if (!ok) break;
@@ -650,22 +660,6 @@ __device__ __forceinline__ float att_lse(float m, float l) {
 }
 
 template <int DP, bool BF16>
-__device__ __forceinline__ void att_store_out(const AttendParams& p, char* out, int col,
-                                              const float* o, float scale) {
-  // 32 columns from col
-#pragma unroll
-  for (int x = 0; x < 32; x += 8) {
-    if (col + x >= p.dim) break;
-    uint4 v;
-    v.x = pack2<BF16>(o[x] * scale, o[x + 1] * scale);
-    v.y = pack2<BF16>(o[x + 2] * scale, o[x + 3] * scale);
-    v.z = pack2<BF16>(o[x + 4] * scale, o[x + 5] * scale);
-    v.w = pack2<BF16>(o[x + 6] * scale, o[x + 7] * scale);
-    *(uint4*)(out + (col + x) * 2) = v;
-  }
-}
-
-template <int DP, bool BF16>
 __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, int warp, int lane) {
   constexpr float kBias = att_bias<BF16>();
   const int s = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -786,25 +780,34 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
       const int part = ((blockIdx.x * 2 + max(g.slot, 0)) * 2 + (g.pair ? s : 0));
       char* out = p.out + token * p.out_token + head * p.out_head;
       float4* part_o = p.part_o + (size_t)part * (DP / 4) * kAttTile + row;
-      for (int k = 0; k < half; k += 32) {
-        float o[32], y[32];
-        tmem_ld32(first + col0 + k, o);
-        tmem_wait_ld(o);
+#pragma unroll 1
+      for (int k = 0; k < half; k += 16) {  // short code: it is cold every time it runs
+        float o[16];
+        tmem_ld16(first + col0 + k, o);
 #pragma unroll
-        for (int z = 0; z < 32; ++z) o[z] *= w[0];
+        for (int z = 0; z < 16; ++z) o[z] *= w[0];
         if (both) {
-          tmem_ld32(first + 128 + col0 + k, y);
-          tmem_wait_ld(y);
+          float y[16];
+          tmem_ld16(first + 128 + col0 + k, y);
 #pragma unroll
-          for (int z = 0; z < 32; ++z) o[z] += y[z] * w[1];
+          for (int z = 0; z < 16; ++z) o[z] += y[z] * w[1];
         }
-        if (mine && g.slot < 0) {
-          att_store_out<DP, BF16>(p, out, col0 + k, o, inv);
-        } else if (mine) {
+        if (mine && g.slot >= 0) {
 #pragma unroll
-          for (int z = 0; z < 8; ++z)
+          for (int z = 0; z < 4; ++z)
             part_o[((col0 + k) / 4 + z) * kAttTile] =
                 make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+        } else if (mine) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            if (col0 + k + 8 * z >= p.dim) break;
+            uint4 v;
+            v.x = pack2<BF16>(o[8 * z] * inv, o[8 * z + 1] * inv);
+            v.y = pack2<BF16>(o[8 * z + 2] * inv, o[8 * z + 3] * inv);
+            v.z = pack2<BF16>(o[8 * z + 4] * inv, o[8 * z + 5] * inv);
+            v.w = pack2<BF16>(o[8 * z + 6] * inv, o[8 * z + 7] * inv);
+            *(uint4*)(out + (col0 + k + 8 * z) * 2) = v;
+          }
         }
         __syncwarp();
       }
@@ -965,7 +968,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   }
 }
 
-constexpr int kJoinThreads = 256, kJoinSplit = 16;
+constexpr int kJoinThreads = 512, kJoinSplit = 8;
 
 // Join the partial results of the unit that starts in block blockIdx.x's part
 // of the list and ends in another's: parts of one row weigh 2^(m - max m). An
