@@ -509,7 +509,9 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
                                              char* q_smem, char* kv_smem, const int s) {
   using Cfg = AttCfg<DP>;
   constexpr uint32_t kQK = mma_kind(BF16, false, kAttTile, kAttTile);
-  constexpr uint32_t kPV = mma_kind(BF16, true, kAttTile, DP);
+  // Head sizes between the tiles' have fewer steps in QK and fewer columns in PV.
+  const uint32_t kind_pv = mma_kind(BF16, true, kAttTile, (p.dim + 15) / 16 * 16);
+  const int steps = (p.dim + 15) / 16;
   const uint32_t tmem_s = __shfl_sync(~0u, sh.tmem, 0) + s * 128, tmem_o = tmem_s + 256;
   const bool one = elect_one();
   // descriptors of the first tiles; others by what is added to their addresses (in 16 bytes)
@@ -562,7 +564,8 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
             if (!att_wait_warp(sh, p, &sh.p_full[s], p_count)) return false;
             tmem_fence_after();
           }
-          mma_ts(tmem_o, tmem_s + 8 * x, vd + x * (16 * 128 / 16), kPV, t > 1 || x > 0, one);
+          mma_ts(tmem_o, tmem_s + 8 * x, vd + x * (16 * 128 / 16), kind_pv, t > 1 || x > 0,
+                 one);
         }
         ++p_count;
       }
@@ -571,7 +574,7 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
 #pragma unroll
         for (int x = 0; x < DP / 16; ++x) {
           const unsigned y = ((x / 4) * (kAttTile * 128) + (x % 4) * 32) / 16;
-          mma_ss(tmem_s, qd + y, kd + y, kQK, x > 0, one);
+          if (x < steps) mma_ss(tmem_s, qd + y, kd + y, kQK, x > 0, one);
         }
       }
       if (one) mbar_arrive(&sh.turn[s ^ 1]);
