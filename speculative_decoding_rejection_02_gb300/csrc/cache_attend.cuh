@@ -45,6 +45,7 @@ namespace sv {
 
 constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
 constexpr int kAttThreads = 384;  // 12 warps, at most 168 registers each at launch
+constexpr int kAttScan = 128;     // threads that scan the requests
 constexpr int kAttRegsMany = 208, kAttRegsFew = 88;  // 2 * 208 + 88 = 3 * 168
 constexpr int kAttSegs = 4;       // list entries ahead of the slowest warp
 constexpr long long kAttPatience = 2000000000;  // clocks that a wait may take
@@ -266,13 +267,13 @@ struct AttWalk {
 struct AttBase {
   uint64_t q_full[4], q_empty[2];
   uint64_t s_full[2], p_half[2], p_full[2];
-  uint64_t turn[2];
+  uint64_t turn[2], warm;
   uint64_t o_full, o_free, ml_full, edge_full, drain[2];
   uint64_t seg_full[kAttSegs], seg_empty[kAttSegs];
   AttSeg seg[kAttSegs];
   float2 ml[2][kAttTile];
-  unsigned long long scan[kAttThreads / 32];
-  int pad[kAttThreads / 32];
+  unsigned long long scan[kAttScan / 32];
+  int pad[kAttScan / 32], pad_all;
   AttWalk walk;
   uint32_t tmem;
   int stop;
@@ -519,6 +520,7 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
   const uint64_t v0 = mma_desc(smem_addr(kv_smem), kAttTile * 128);
   constexpr unsigned kTile = Cfg::kTileBytes / 16;
   unsigned p_count = 0, turn = 0;
+  if (!att_wait_warp(sh, p, &sh.warm, 0)) return false;  // the softmax warps' dry run
   auto loaded = [&](unsigned r) {
     return att_wait_warp(sh, p, &sh.kv_full[r % Cfg::kRing], r / Cfg::kRing);
   };
@@ -671,15 +673,22 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
   const uint32_t tmem_o = sh.tmem + lanes + 256;
   const int row_token = row / p.G, row_head = row - row_token * p.G;
   unsigned s_count = 0, joins = 0;
-  for (int e = 0;; ++e) {
-    const int at = e % kAttSegs;
-    if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) return;
-    const AttSeg g = sh.seg[at];
-    if (g.n == 0) return;
+  // The walk's entries, after one round that only brings the code near: its instructions come
+  // from L2 the first time, which takes as long as the list's head and the first loads do. It
+  // works on whatever TMEM holds, sees no row, and neither waits nor tells anyone.
+  for (int e = -1;; ++e) {
+    const bool dry = e < 0;
+    const int at = e & (kAttSegs - 1);
+    AttSeg g = {2, 0, 0, 0, 0, p.tile_tokens, 0, 0, 1, 0x7fffffff, 0, 0, 0, 0, -1};
+    if (!dry) {
+      if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) return;
+      g = sh.seg[at];
+      if (g.n == 0) return;
+    }
     // This thread's row: token and position; rows past the unit's tokens see nothing.
     const int tile0 = g.pair ? s * p.tile_tokens : 0;  // the stream's first token
     const int tokens = min(p.tile_tokens, g.tokens - tile0);
-    const bool mine = row_token < tokens;
+    const bool mine = row_token < tokens && !dry;
     const int pos = mine ? g.pos + tile0 + row_token : -1;
     const bool busy = (warp & 3) * 32 < tokens * p.G;  // rows in this warp
     const int first_pos = g.pos + tile0, last_pos = g.pos + tile0 + tokens - 1;
@@ -690,8 +699,7 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
       const int j0 = att_tile(g, i) * kAttTile;
       const bool all_seen = j0 + kAttTile - 1 <= first_pos &&
                             (!p.window || j0 > last_pos - p.window || j0 + kAttTile <= p.sinks);
-      if (!att_wait_warp(sh, p, &sh.s_full[s], s_count)) return;
-      ++s_count;
+      if (!dry && !att_wait_warp(sh, p, &sh.s_full[s], s_count++)) return;
       if (busy) {
         tmem_fence_after();
         if (__builtin_expect(!all_seen, 0)) att_hide(tmem_s, pos, j0, p.window, p.sinks, p.hidden);
@@ -737,7 +745,7 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
           tmem_wait_st();
           tmem_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(k ? &sh.p_full[s] : &sh.p_half[s]);
+          if (lane == 0 && !dry) mbar_arrive(k ? &sh.p_full[s] : &sh.p_half[s]);
           if (k == 0) {
             tmem_ld32(tmem_s + 64, f);
             tmem_ld32(tmem_s + 96, f + 32);
@@ -748,7 +756,7 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
         float a, b;
         f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
         l += a + b;
-      } else if (lane == 0) {
+      } else if (lane == 0 && !dry) {
         mbar_arrive(&sh.p_half[s]);
         mbar_arrive(&sh.p_full[s]);
       }
@@ -758,19 +766,18 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
     float w[2] = {1.f, 1.f};  // of the two streams' O
     if (!g.pair) {
       // ml of the segment before has been read by all
-      if (!att_wait_warp(sh, p, &sh.o_free, e + 1)) return;
+      if (!dry && !att_wait_warp(sh, p, &sh.o_free, e + 1)) return;
       sh.ml[s][row] = make_float2(m, l);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.ml_full);
-      if (!att_wait_warp(sh, p, &sh.ml_full, joins)) return;
-      ++joins;
+      if (lane == 0 && !dry) mbar_arrive(&sh.ml_full);
+      if (!dry && !att_wait_warp(sh, p, &sh.ml_full, joins++)) return;
       const float2 x = sh.ml[0][row], y = sh.ml[1][row];
       m = fmaxf(x.x, y.x);
       w[0] = x.x == -INFINITY ? 0.f : ex2(x.x - m);
       w[1] = y.x == -INFINITY ? 0.f : ex2(y.x - m);
       l = x.y * w[0] + y.y * w[1];
     }
-    if (!att_wait_warp(sh, p, &sh.o_full, e)) return;
+    if (!dry && !att_wait_warp(sh, p, &sh.o_full, e)) return;
     if (busy) {
       tmem_fence_after();
       const int half = g.pair ? DP : DP / 2;  // columns of this warp: stream s of a pair, or
@@ -823,10 +830,9 @@ __device__ __forceinline__ void att_softmax(AttBase& sh, const AttendParams& p, 
     }
     tmem_fence_before();
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&sh.o_free);
-      mbar_arrive(&sh.seg_empty[at]);
-    }
+    if (lane == 0) mbar_arrive(dry ? &sh.warm : &sh.o_free);
+    if (lane == 0 && !dry) mbar_arrive(&sh.seg_empty[at]);
+    if (dry) pdl_wait();
   }
 }
 
@@ -861,6 +867,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_init(&sh.drain[lane], 1);
     }
     if (lane == 0) {
+      mbar_init(&sh.warm, 8);
       mbar_init(&sh.o_full, 2);
       mbar_init(&sh.o_free, 8);
       mbar_init(&sh.ml_full, 8);
@@ -875,99 +882,107 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   }
   if (warp == 9) tmem_alloc(&sh.tmem, 512);
   pdl_trigger();
-  pdl_wait();
-  // Key tiles of each thread's run of requests, and of all.
-  const int step = 2 * p.tile_tokens;
-  const int r0 = (int)min((long long)tid * run, (long long)p.B), r1 = min(r0 + run, p.B);
-  int lo = 0, hi = 0, len = 0;  // of the request read last
-  auto tiles_of = [&](int r) {
-    len = attend_request(p, r, lo, hi);
-    const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-    return (unsigned long long)units.before(units.count) * p.kv_heads;
-  };
-  unsigned long long mine = 0;
-  int pad = 0;  // rows from here on belong to no request
-  for (int r = r0; r < r1; ++r) {
-    mine += tiles_of(r);
-    pad = max(pad, hi);
-  }
-  unsigned long long upto = mine;
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long x = __shfl_up_sync(~0u, upto, d);
-    if (lane >= d) upto += x;
-  }
-  pad = __reduce_max_sync(~0u, pad);
-  if (lane == 31) sh.scan[warp] = upto;
-  if (lane == 0) sh.pad[warp] = pad;
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  unsigned long long all = 0, before64 = upto - mine;
-  for (int w = 0; w < kAttThreads / 32; ++w) {
-    if (w < warp) before64 += sh.scan[w];
-    all += sh.scan[w];
-    pad = max(pad, sh.pad[w]);
-  }
-  // 2^31 tiles are 2^38 tokens of a head: no list is that long
-  if (all > 0x7fffffffull && tid == 0 && blockIdx.x == 0 && p.status)
-    atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
-  const int total = all > 0x7fffffffull ? 0 : (int)all, before = (int)before64;
-  const int blocks = min((int)gridDim.x, total);
-  const bool works = (int)blockIdx.x < blocks;
-  const int begin = works ? att_begin(blockIdx.x, total, blocks) : 0;
-  const int end = works ? att_begin(blockIdx.x + 1, total, blocks) : 0;
-  if (works && before <= begin && begin < before + (int)mine) {
-    int at = before, r = r0;
-    if (run > 1) {
-      for (;; ++r) {
-        const int n = (int)tiles_of(r);
-        if (begin < at + n || r + 1 >= r1) break;
-        at += n;
+  if (warp < 8) {
+    regs_take<kAttRegsMany>();
+    att_softmax<DP, BF16>(sh, p, warp, lane);
+  } else {
+    regs_give<kAttRegsFew>();
+    pdl_wait();
+    // Key tiles of each thread's run of requests, and of all.
+    const int t = tid - (kAttThreads - kAttScan), w0 = t >> 5, step = 2 * p.tile_tokens;
+    const int r0 = (int)min((long long)t * run, (long long)p.B), r1 = min(r0 + run, p.B);
+    int lo = 0, hi = 0, len = 0;  // of the request read last
+    auto tiles_of = [&](int r) {
+      len = attend_request(p, r, lo, hi);
+      const AttUnits units(len, hi - lo, step, p.window, p.sinks);
+      return (unsigned long long)units.before(units.count) * p.kv_heads;
+    };
+    unsigned long long mine = 0;
+    int pad = 0;  // rows from here on belong to no request
+    for (int r = r0; r < r1; ++r) {
+      mine += tiles_of(r);
+      pad = max(pad, hi);
+    }
+    unsigned long long upto = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned long long x = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += x;
+    }
+    pad = __reduce_max_sync(~0u, pad);
+    if (lane == 31) sh.scan[w0] = upto;
+    if (lane == 0) sh.pad[w0] = pad;
+    named_sync(1, kAttScan);
+    unsigned long long all = 0, before64 = upto - mine;
+    for (int w = 0; w < kAttScan / 32; ++w) {
+      if (w < w0) before64 += sh.scan[w];
+      all += sh.scan[w];
+      pad = max(pad, sh.pad[w]);
+    }
+    // 2^31 tiles are 2^38 tokens of a head: no list is that long
+    if (all > 0x7fffffffull && t == 0 && blockIdx.x == 0 && p.status)
+      atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
+    const int total = all > 0x7fffffffull ? 0 : (int)all, before = (int)before64;
+    const int blocks = min((int)gridDim.x, total);
+    const bool works = (int)blockIdx.x < blocks;
+    const int begin = works ? att_begin(blockIdx.x, total, blocks) : 0;
+    const int end = works ? att_begin(blockIdx.x + 1, total, blocks) : 0;
+    if (t == 0) {
+      p.join[blockIdx.x].last = -1;
+      sh.pad_all = pad;
+      if (!works) {
+        sh.seg[0].n = 0;
+        mbar_arrive(&sh.seg_full[0]);
       }
     }
-    AttWalk walk;
-    walk.start(p, begin, end, total, blocks, r, at, lo, hi, len);
-    walk.publish(sh, p);
-    sh.walk = walk;
-  }
-  if (tid == 0) p.join[blockIdx.x].last = -1;
-  __syncthreads();
-  if (works) {
-    if (warp < 8) {
-      regs_take<kAttRegsMany>();
-      att_softmax<DP, BF16>(sh, p, warp, lane);
-    } else {
-      regs_give<kAttRegsFew>();
-      if (warp == 8) {
-        att_load<DP, false>(sh, p, q_smem, kv_smem, lane, nullptr);
-      } else if (warp == 11) {
-        AttWalk walk = sh.walk;
-        att_load<DP, true>(sh, p, q_smem, kv_smem, lane, &walk);
-      } else {
-        const int s = warp - 9;
-        if (!att_products<DP, BF16>(sh, p, q_smem, kv_smem, s)) {
-          mma_commit(&sh.drain[s], elect_one());
-          for (int i = 0; i < 1024; ++i)
-            if (mbar_try(&sh.drain[s], 0)) break;
+    __syncwarp();
+    if (works && before <= begin && begin < before + (int)mine) {
+      int at = before, r = r0;
+      if (run > 1) {
+        for (;; ++r) {
+          const int n = (int)tiles_of(r);
+          if (begin < at + n || r + 1 >= r1) break;
+          at += n;
         }
       }
-      __syncwarp();
+      AttWalk walk;
+      walk.start(p, begin, end, total, blocks, r, at, lo, hi, len);
+      walk.publish(sh, p);
+      sh.walk = walk;
     }
-  }
-  // Rows of q past the last request: zeros.
-  for (long long t = pad + blockIdx.x; t < p.T; t += gridDim.x) {
-    const int pieces = p.dim / 8;
-    for (int i = tid; i < p.heads * pieces; i += kAttThreads)
-      *(uint4*)(p.out + t * p.out_token + (i / pieces) * p.out_head + (i % pieces) * 16) =
-          make_uint4(0, 0, 0, 0);
-    if (p.lse)
-      for (int i = tid; i < p.heads; i += kAttThreads) p.lse[t * p.heads + i] = -INFINITY;
+    named_sync(1, kAttScan);
+    if (!works) {
+    } else if (warp == 8) {
+      att_load<DP, false>(sh, p, q_smem, kv_smem, lane, nullptr);
+    } else if (warp == 11) {
+      AttWalk walk = sh.walk;
+      att_load<DP, true>(sh, p, q_smem, kv_smem, lane, &walk);
+    } else {
+      const int s = warp - 9;
+      if (!att_products<DP, BF16>(sh, p, q_smem, kv_smem, s)) {
+        mma_commit(&sh.drain[s], elect_one());
+        for (int i = 0; i < 1024; ++i)
+          if (mbar_try(&sh.drain[s], 0)) break;
+      }
+    }
+    __syncwarp();
   }
   tmem_fence_before();
   __syncthreads();
   if (warp == 9) {
     tmem_fence_after();
     tmem_free(sh.tmem, 512);
+  }
+  // Rows of q past the last request: zeros.
+  for (long long t = sh.pad_all + blockIdx.x; t < p.T; t += gridDim.x) {
+    const int pieces = p.dim / 8;
+    for (int i = tid; i < p.heads * pieces; i += kAttThreads)
+      *(uint4*)(p.out + t * p.out_token + (i / pieces) * p.out_head + (i % pieces) * 16) =
+          make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int i = tid; i < p.heads; i += kAttThreads) p.lse[t * p.heads + i] = -INFINITY;
   }
 }
 

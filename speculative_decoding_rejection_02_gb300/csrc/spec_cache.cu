@@ -178,7 +178,7 @@ int attend(const sv::AttendParams& p, int sms, void* stream) {
     }
     ready.fetch_or(1ull << dev);
   }
-  const int run = p.B > sv::kAttThreads ? (p.B + sv::kAttThreads - 1) / sv::kAttThreads : 1;
+  const int run = p.B > sv::kAttScan ? (p.B + sv::kAttScan - 1) / sv::kAttScan : 1;
   const int rc = launch(sv::k_attend<DP, BF16>, dim3(sms), sv::kAttThreads, smem, stream, p, run);
   if (rc != SPEC_OK) return rc;
   return launch(sv::k_attend_join<DP, BF16>, dim3(sms, sv::kJoinSplit), sv::kJoinThreads, 0,
