@@ -20,7 +20,8 @@
 // has more than one tile of rows, else the even and the odd key tiles of the
 // one tile of rows, joined at the end.
 //
-// Work is one list of key tiles over (request, kv head, tiles of rows), cut
+// Work is one list of key tiles over (request, kv head, tiles of rows), with a
+// unit's fixed cost in tiles beside them, cut
 // into equal parts, one for each block (one block per SM): ragged batches
 // balance without a plan on the host, and a unit that a cut crosses leaves
 // partial (m, l, O) in the workspace, which k_attend_join joins. Tiles that no
@@ -45,6 +46,8 @@ namespace sv {
 
 constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
 constexpr int kAttThreads = 384;  // 12 warps, at most 168 registers each at launch
+// What a unit costs beside its key tiles, in tiles: of one tile of rows, and of two.
+constexpr int kAttCost = 2, kAttPairCost = 4;
 constexpr int kAttScan = 128;     // threads that scan the requests
 constexpr int kAttRegsMany = 208, kAttRegsFew = 88;  // 2 * 208 + 88 = 3 * 168
 constexpr int kAttSegs = 4;       // list entries ahead of the slowest warp
@@ -132,11 +135,12 @@ __host__ __device__ inline unsigned floor_sum(unsigned n, unsigned m, unsigned a
 // units together, are below 2^31.
 struct AttUnits {
   int p0;  // position of the first new token
-  int q, step, count, window, sink_tiles;
+  int q, step, count, window, sink_tiles, cost;
 
   __host__ __device__ AttUnits(int len, int q_, int step_, int window_, int sinks)
       : p0(len - q_), q(q_), step(step_), count(q_ <= step_ ? q_ > 0 : (q_ - 1) / step_ + 1),
-        window(window_), sink_tiles((int)(((unsigned)sinks + kAttTile - 1) / kAttTile)) {}
+        window(window_), sink_tiles((int)(((unsigned)sinks + kAttTile - 1) / kAttTile)),
+        cost(q_ > step_ / 2 ? kAttPairCost : kAttCost) {}
 
   __host__ __device__ int hi(int u) const {
     const int end = (u + 1) * step;
@@ -155,9 +159,9 @@ struct AttUnits {
     const int h = hi(u);
     return h <= 0 ? 1 : (h - 1) / kAttTile + 1 - gap(u);
   }
-  // Key tiles of the units before k, in closed form.
+  // Length in the list of the units before k, in closed form.
   __host__ __device__ int before(int k) const {
-    int sum = 0;
+    int sum = k * cost;
     if (k == count && k > 0) sum += tiles(--k);  // the last one ends where the request does
     if (k <= 0) return sum;
     int dead = p0 < 0 ? -p0 / step : 0;  // units before position 0
@@ -219,8 +223,8 @@ struct AttBase;
 // whose run of requests the part starts in, carried on by one of the V loader's
 
 struct AttWalk {
-  int skip, end;   // tiles of the list given out, and where the part ends
-  int rest;        // tiles of the current unit given out
+  int skip, end;   // places of the list given out, and where the part ends
+  int rest;        // places of the current unit given out
   int total, blocks, b, lo, hi, len, head, u, q_at, entry;
   int lo1, hi1, len1;  // request b + 1, read ahead
   unsigned ring;
@@ -324,40 +328,45 @@ __device__ __forceinline__ bool AttWalk::publish(AttBase& sh, const AttendParams
   const int step = 2 * p.tile_tokens, at = entry % kAttSegs;
   AttSeg g;
   g.n = 0;
-  if (skip < end) {
+  // A unit takes its key tiles and `cost` places more in the list, which stand for what its
+  // start and its results cost.
+  while (skip < end) {
     while (hi == lo && b + 1 < p.B) {  // requests without rows
       ++b;
       next_request(p);
     }
     const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-    const int n = units.tiles(u), take = min(n - rest, end - skip);
-    g.n = take;
-    g.i0 = rest;
-    g.b = b;
-    g.head = head;
-    g.token = lo + u * step;
-    g.tokens = min(step, hi - g.token);
-    g.pos = units.p0 + u * step;
-    g.lo = units.lo(u);
-    g.hi = max(units.hi(u), 0);
-    g.gap = units.gap(u);
-    g.gap_at = g.gap ? units.sink_tiles : 0x7fffffff;
-    g.pair = g.tokens > p.tile_tokens;
-    g.q_at = q_at;
-    g.ring = ring;
-    const bool starts = rest == 0, ends = rest + take == n;
-    g.slot = starts && ends ? -1 : starts ? 1 : 0;
-    if (starts && !ends) {
-      join.last = att_block_of(skip + n - 1, total, blocks);
-      join.head = head;
-      join.token = g.token;
-      join.tokens = g.tokens;
+    const int n = units.tiles(u), here = min(n + units.cost - rest, end - skip);
+    const int take = min(n - rest, here);  // tiles among them
+    if (take > 0) {
+      g.n = take;
+      g.i0 = rest;
+      g.b = b;
+      g.head = head;
+      g.token = lo + u * step;
+      g.tokens = min(step, hi - g.token);
+      g.pos = units.p0 + u * step;
+      g.lo = units.lo(u);
+      g.hi = max(units.hi(u), 0);
+      g.gap = units.gap(u);
+      g.gap_at = g.gap ? units.sink_tiles : 0x7fffffff;
+      g.pair = g.tokens > p.tile_tokens;
+      g.q_at = q_at;
+      g.ring = ring;
+      const bool starts = rest == 0, ends = rest + take == n;
+      g.slot = starts && ends ? -1 : starts ? 1 : 0;
+      if (starts && !ends) {
+        join.last = att_block_of(skip + n - 1, total, blocks);
+        join.head = head;
+        join.token = g.token;
+        join.tokens = g.tokens;
+      }
+      q_at += g.pair ? 2 : 1;
+      ring += 2 * take;
     }
-    q_at += g.pair ? 2 : 1;
-    ring += 2 * take;
-    skip += take;
-    rest += take;
-    if (rest == n) {
+    skip += here;
+    rest += here;
+    if (rest == n + units.cost) {
       rest = 0;
       if (++u == units.count) {
         u = 0;
@@ -368,9 +377,9 @@ __device__ __forceinline__ bool AttWalk::publish(AttBase& sh, const AttendParams
         }
       }
     }
-  } else {
-    p.join[blockIdx.x] = join;
+    if (take > 0) break;
   }
+  if (g.n == 0) p.join[blockIdx.x] = join;
   if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return false;
   sh.seg[at] = g;
   mbar_arrive(&sh.seg_full[at]);
