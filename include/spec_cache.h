@@ -165,8 +165,11 @@ long long spec_cache_attend_workspace(const spec_cache_attend_args* a);
  * and lse = -inf. Scores, softmax statistics and sums are fp32; the softmax
  * weights are rounded to the cache's type before they meet the values.
  * Whatever the memory of slots that no row of a request sees holds, NaN and
- * infinities too, does not reach the outputs. Pages that lie wholly outside every
- * row's window are not read and may have been given to others.
+ * infinities too, does not reach the outputs (a value that some row sees and that
+ * is not finite may make other rows of its request not finite). Pages that lie
+ * wholly outside every row's window are not read and may have been given to others.
+ * The result is the same to the bit in every call with the same arguments on the
+ * same kind of GPU.
  * Addresses and strides (of more than one element) of q, pages and out:
  * multiples of 16 bytes (SPEC_ERR_INVALID_ARG).
  */

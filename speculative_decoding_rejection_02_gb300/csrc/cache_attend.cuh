@@ -10,18 +10,18 @@
 //                   P rounded to the cache's type and written over S
 //   O += P V        tcgen05, P from TMEM, V in shared memory, O (fp32) in TMEM
 //
-// with c = scale * log2(e). m and O follow a higher maximum only when it has
-// passed m by 2^8: until then P may exceed 1, which costs no precision (bf16 and
-// fp32 have the range; fp16's P starts at 2^7, may reach 2^15 and goes down to
-// 2^-31 of it).
+// with c = scale * log2(e). P's rounding is the one step below 32 bits before
+// the result's own: the tensor cores take 16-bit operands. l sums P unrounded.
+// m and O follow a higher maximum only when it has passed m by 2^8: until then P
+// may exceed 1, which costs no precision (bf16 and fp32 have the range; fp16's P
+// starts at 2^7, may reach 2^15 and goes down to 2^-31 of it).
 //
 // Two streams of S and O run side by side in one block, so that one's products
 // cover the other's softmax: two tiles of rows over the same keys where a unit
 // has more than one tile of rows, else the even and the odd key tiles of the
 // one tile of rows, joined at the end.
 //
-// Work is one list of key tiles over (request, kv head, tiles of rows), with a
-// unit's fixed cost in tiles beside them, cut
+// Work is one list of key tiles over (request, kv head, tiles of rows), cut
 // into equal parts, one for each block (one block per SM): ragged batches
 // balance without a plan on the host, and a unit that a cut crosses leaves
 // partial (m, l, O) in the workspace, which k_attend_join joins. Tiles that no
@@ -30,6 +30,20 @@
 // Warps: 0-3 and 4-7 the softmax of stream 0 and 1, 8 and 11 the loaders (TMA,
 // through the block table; 11 also walks over the list), 9 and 10 the issuers of
 // the two streams' products; the last four give registers to the softmax warps.
+//
+// What bounds it, on one GB300 (6792 GB/s, 1876 TFLOP/s bf16 measured):
+//  - long contexts and few rows: HBM. 64 requests of 2-8 tokens over 1000-30000
+//    (heads of 128): 0.348 ms, 6.43 TB/s; 128 single tokens over 150-9000: 0.190 ms,
+//    5.99 TB/s, the rest a unit's start and results (about 4000 clocks each, partly
+//    behind its successor's loads).
+//  - prompt chunks: the chain softmax -> PV -> QK of one stream against the other's.
+//    Two chunks of 2048 over 11000-14000: 0.58 ms (1560 TFLOP/s) in a short run, 0.66 ms
+//    (1370) when the clocks follow the power limit.
+//  - windows and small calls: the first tiles (about 11 us from launch to the first
+//    unit's result) and, in windows, the edge tiles.
+// Code size counts: the warps' loops together overflow the instruction cache, and
+// rolling the softmax's, shortening the waits' and moving rare paths out of the way
+// took the chunks from 1.13 ms to 0.58.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -198,7 +212,9 @@ __device__ __forceinline__ int attend_request(const AttendParams& p, int b, int&
   hi = p.cu_q[b + 1];
   int len = p.kv_lens[b];
   const bool bad_rows = lo < 0 || hi < lo || hi > p.T;
-  const bool bad_len = len < 0 || len > ((long long)p.width << p.page_shift);
+  // (the last key tiles' ends stay below 2^31)
+  const bool bad_len =
+      len < 0 || len > ((long long)p.width << p.page_shift) || len > 0x7fff0000;
   if (bad_rows || bad_len) {
     if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
     if (bad_rows) lo = hi = 0;
@@ -962,13 +978,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       sh.walk = walk;
     }
     named_sync(1, kAttScan);
-    if (!works) {
-    } else if (warp == 8) {
+    if (works && warp == 8) {
       att_load<DP, false>(sh, p, q_smem, kv_smem, lane, nullptr);
-    } else if (warp == 11) {
+    } else if (works && warp == 11) {
       AttWalk walk = sh.walk;
       att_load<DP, true>(sh, p, q_smem, kv_smem, lane, &walk);
-    } else {
+    } else if (works) {
       const int s = warp - 9;
       if (!att_products<DP, BF16>(sh, p, q_smem, kv_smem, s)) {
         mma_commit(&sh.drain[s], elect_one());

@@ -316,6 +316,32 @@ def test_attend_extreme_scores(dtype):
     ref.assert_attend(got, lse, ref.attend(*host, scale=0.5))
 
 
+@pytest.mark.parametrize("seed", range(16))
+def test_attend_random(seed):
+    """Ragged batches of any make-up: empty requests, single tokens and chunks side by side."""
+    g = torch.Generator().manual_seed(100 + seed)
+
+    def pick(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=g))
+    B = pick(1, 30)
+    kv_heads = pick(1, 3)
+    heads = kv_heads * pick(1, 9)
+    dim = 8 * pick(1, 16)
+    q_lens = [pick(0, 1) * pick(0, (3, 40, 200)[pick(0, 2)]) for _ in range(B)]
+    kv_lens = [max(0, n + pick(-3, (10, 300, 1500)[pick(0, 2)])) for n in q_lens]
+    window = pick(0, 1) * pick(1, 400)
+    check_attend(q_lens, kv_lens, heads, kv_heads, dim, 8 << pick(0, 5), (BF, FP)[seed % 2],
+                 layout=("token", "head")[pick(0, 1)], seed=seed, window=window,
+                 sinks=pick(0, 1) * pick(0, 200), max_q=pick(0, 1) * pick(1, 50) or None)
+
+
+def test_attend_more_requests_than_threads():
+    """The list's head is found in runs of requests; many of them have no rows."""
+    q_lens = [(r * 7) % 3 if r % 5 else 0 for r in range(700)]
+    check_attend(q_lens, [n + (r * 31) % 150 for r, n in enumerate(q_lens)], 4, 2, 64, 16, BF)
+    check_attend([0] * 400 + [3], [20] * 400 + [500], 4, 2, 64, 16, FP)
+
+
 def test_attend_scale_and_negative_scale():
     check_attend([3], [300], 8, 2, 128, 16, BF, scale=0.02)
     check_attend([3], [300], 8, 2, 128, 16, BF, scale=-0.11)
