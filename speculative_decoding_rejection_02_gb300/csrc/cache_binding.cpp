@@ -105,6 +105,16 @@ Tensor empty(at::IntArrayRef sizes, at::ScalarType dtype, int dev) {
   return Tensor(at::detail::empty_cuda(sizes, dtype, c10::Device(c10::kCUDA, dev), std::nullopt));
 }
 
+// n elements of a byte buffer from `at` on, as a tensor that shares its storage.
+Tensor part(const Tensor& bytes, int64_t at, int64_t n, at::ScalarType dtype) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(bytes.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+      c10::scalarTypeToTypeMeta(dtype));
+  t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)c10::elementSize(dtype));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 template <typename F, typename A>
 int call(F fn, const A& a, int dev, unsigned* status) {
   return fn(&a, c10::cuda::getCurrentCUDAStream(dev).stream(), status);
@@ -144,9 +154,12 @@ PyObject* step(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   unsigned* status = x.status();
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.dev);
-  const Tensor out[5] = {empty({B}, at::kInt, x.dev), empty({B + 1}, at::kInt, x.dev),
-                         empty({a.num_tokens}, at::kInt, x.dev),
-                         empty({a.num_tokens}, at::kLong, x.dev), empty({1}, at::kInt, x.dev)};
+  // one allocation for the five outputs
+  const int64_t T = a.num_tokens;
+  const Tensor all = empty({12 * T + 4 * (2 * B + 2)}, at::kByte, x.dev);
+  const Tensor out[5] = {part(all, 12 * T, B, at::kInt), part(all, 12 * T + 4 * B, B + 1, at::kInt),
+                         part(all, 8 * T, T, at::kInt), part(all, 0, T, at::kLong),
+                         part(all, 12 * T + 4 * (2 * B + 1), 1, at::kInt)};
   a.lens = (int*)out[0].data_ptr();
   a.cu_new = (int*)out[1].data_ptr();
   a.positions = (int*)out[2].data_ptr();
