@@ -1010,7 +1010,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   }
 }
 
-constexpr int kJoinThreads = 512, kJoinSplit = 8;
+constexpr int kJoinThreads = 512;
 
 // Join the partial results of the unit that starts in block blockIdx.x's part
 // of the list and ends in another's: parts of one row weigh 2^(m - max m). An
@@ -1023,18 +1023,18 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const AttendParams
   const AttJoin j = p.join[blockIdx.x];
   if (j.last < 0) return;
   const int parts = j.last - blockIdx.x + 1;
-  constexpr int kCols = DP / 4 / kJoinSplit;  // groups of four columns of this block
+  const int cols = DP / 4 / gridDim.y;  // groups of four columns of this block
   const int rows0 = min(p.tile_tokens, j.tokens) * p.G, rows = j.tokens * p.G;
   int lanes = 1;  // of an item
-  while (lanes < 32 && lanes < parts && rows * kCols * lanes * 2 <= kJoinThreads) lanes *= 2;
+  while (lanes < 32 && lanes < parts && rows * cols * lanes * 2 <= kJoinThreads) lanes *= 2;
   const int mine = threadIdx.x & (lanes - 1);
   // whole warps go round together: the sums below take all their lanes
-  for (int x0 = 0; x0 < rows * kCols; x0 += kJoinThreads / lanes) {
+  for (int x0 = 0; x0 < rows * cols; x0 += kJoinThreads / lanes) {
     const int x = x0 + threadIdx.x / lanes;
-    const bool real = x < rows * kCols;
+    const bool real = x < rows * cols;
     const int col4 = real ? x / rows : 0, any_row = real ? x - col4 * rows : 0;
     const int tile = any_row >= rows0, row = any_row - tile * rows0;
-    const int c4 = blockIdx.y * kCols + col4;
+    const int c4 = blockIdx.y * cols + col4;
     auto at = [&](int i) { return ((blockIdx.x + i) * 2 + (i == 0)) * 2 + tile; };
     float m = -INFINITY;
 #pragma unroll 4

@@ -181,7 +181,10 @@ int attend(const sv::AttendParams& p, int sms, void* stream) {
   const int run = p.B > sv::kAttScan ? (p.B + sv::kAttScan - 1) / sv::kAttScan : 1;
   const int rc = launch(sv::k_attend<DP, BF16>, dim3(sms), sv::kAttThreads, smem, stream, p, run);
   if (rc != SPEC_OK) return rc;
-  return launch(sv::k_attend_join<DP, BF16>, dim3(sms, sv::kJoinSplit), sv::kJoinThreads, 0,
+  // join's columns over 8 blocks a unit, over 4 where a unit has few rows (64 requests of 1-6
+  // tokens in a window: 66.2 us a call against 68.0 with 8, 66.7 with 2 and 70.0 with one)
+  const int split = p.tile_tokens * p.G <= 32 ? 4 : 8;
+  return launch(sv::k_attend_join<DP, BF16>, dim3(sms, split), sv::kJoinThreads, 0,
                 stream, p);
 }
 
