@@ -75,7 +75,7 @@ struct AttCfg {
   // Barriers go by a longer ring than the tiles: no warp is ever kRing loads behind another,
   // so a phase's parity says which load is meant, whichever of them a warp waits for.
   static constexpr int kRing = DP == 128 ? 16 : 32;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + (DP == 128 ? 3072 : 4096);
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + (DP == 128 ? 3 : 4) * 1024;
 };
 
 struct AttendParams {
@@ -302,7 +302,7 @@ template <int DP>
 struct AttShared : AttBase {
   uint64_t kv_full[AttCfg<DP>::kRing], kv_empty[AttCfg<DP>::kRing];
 };
-static_assert(sizeof(AttShared<128>) <= 3072 && sizeof(AttShared<64>) <= 4096,
+static_assert(sizeof(AttShared<128>) <= 3 * 1024 && sizeof(AttShared<64>) <= 4 * 1024,
               "shared memory beside the tiles");
 
 // A bounded wait (about a second); once one has run out every later one returns at once. The
