@@ -53,15 +53,13 @@
 #include <cstdint>
 
 #include "../../include/spec_cache.h"
+#include "attend_list.cuh"
 #include "pipe.cuh"
 #include "tcgen05.cuh"
 
 namespace sv {
 
-constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
 constexpr int kAttThreads = 384;  // 12 warps, at most 168 registers each at launch
-// What a unit costs beside its key tiles, in tiles: of one tile of rows, and of two.
-constexpr int kAttCost = 2, kAttPairCost = 4;
 constexpr int kAttScan = 128;     // threads that scan the requests
 constexpr int kAttRegsMany = 208, kAttRegsFew = 88;  // 2 * 208 + 88 = 3 * 168
 constexpr int kAttSegs = 4;       // list entries ahead of the slowest warp
@@ -96,132 +94,25 @@ struct AttendParams {
   unsigned* status;
   float4* part_o;   // [blocks][2][2 tiles][DP / 4][128] partial outputs
   float2* part_ml;  // [blocks][2][2][128] their maxima and sums
-  struct AttJoin* join;  // [blocks]
-};
+  AttJoin* join;  // [blocks]
 
-// A unit that starts in one block's part of the list and ends in another's.
-struct AttJoin {
-  int last;              // its last block; -1: none
-  int head, token, tokens;  // rows: new tokens token .. token + tokens - 1
-};
-
-// One entry of a block's walk: key tiles i0 .. i1 - 1 of a unit.
-struct AttSeg {
-  int n;          // key tiles here; 0: the end of the walk
-  int i0;         // the first one's number within the unit
-  int b, head;
-  int token, tokens;  // rows of q
-  int pos;        // position of the first row's token
-  int lo, hi;     // tokens that some row sees: [lo, hi) and [0, min(sinks, lo))
-  int gap_at, gap;  // tile i of the unit is tile i, from gap_at on tile i + gap
-  int pair;       // 1: two tiles of rows; 0: even and odd key tiles
-  int q_at;       // Q tiles loaded before
-  unsigned ring;  // K and V tiles loaded before
-  int slot;       // partial result: 0 or 1; -1: the unit is whole
-};
-
-// sum over 0 <= i < n of floor((a i + b) / m); a, b >= 0, m > 0, and a n + b and the sum
-// below 2^32.
-__host__ __device__ inline unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  unsigned sum = 0;
-  while (n > 0) {
-    if (a >= m) {
-      sum += (unsigned)((unsigned long long)(n - 1) * n / 2) * (a / m);
-      a %= m;
+  // The new tokens of request b as rows [lo, hi) of q, and its length. Offsets
+  // that cannot be give no rows, a length that cannot be length 0.
+  __device__ __forceinline__ int request(int b, int& lo, int& hi) const {
+    lo = cu_q[b];
+    hi = cu_q[b + 1];
+    int len = kv_lens[b];
+    const bool bad_rows = lo < 0 || hi < lo || hi > T;
+    // (the last key tiles' ends stay below 2^31)
+    const bool bad_len = len < 0 || len > ((long long)width << page_shift) || len > 0x7fff0000;
+    if (bad_rows || bad_len) {
+      if (status) atomicOr(status, SPEC_CACHE_BAD_LENGTHS);
+      if (bad_rows) lo = hi = 0;
+      len = 0;
     }
-    if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
-    }
-    const unsigned y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const unsigned t = m;
-    m = a;
-    a = t;
-  }
-  return sum;
-}
-
-// The units of one request: `count` of `step` new tokens each (the last may
-// have fewer), for each kv head. Positions, and the key tiles of one head's
-// units together, are below 2^31.
-struct AttUnits {
-  int p0;  // position of the first new token
-  int q, step, count, window, sink_tiles, cost;
-
-  __host__ __device__ AttUnits(int len, int q_, int step_, int window_, int sinks)
-      : p0(len - q_), q(q_), step(step_), count(q_ <= step_ ? q_ > 0 : (q_ - 1) / step_ + 1),
-        window(window_), sink_tiles((int)(((unsigned)sinks + kAttTile - 1) / kAttTile)),
-        cost(q_ > step_ / 2 ? kAttPairCost : kAttCost) {}
-
-  __host__ __device__ int hi(int u) const {
-    const int end = (u + 1) * step;
-    return p0 + (u + 1 < count && end < q ? end : q);
-  }
-  __host__ __device__ int lo(int u) const {
-    const int first = p0 + u * step + 1;
-    return window && first > window ? first - window : 0;
-  }
-  __host__ __device__ int gap(int u) const {
-    const int g = lo(u) / kAttTile - sink_tiles;
-    return g > 0 ? g : 0;
-  }
-  // Key tiles of unit u; one (in which no row sees anything) at least.
-  __host__ __device__ int tiles(int u) const {
-    const int h = hi(u);
-    return h <= 0 ? 1 : (h - 1) / kAttTile + 1 - gap(u);
-  }
-  // Length in the list of the units before k, in closed form.
-  __host__ __device__ int before(int k) const {
-    int sum = k * cost;
-    if (k == count && k > 0) sum += tiles(--k);  // the last one ends where the request does
-    if (k <= 0) return sum;
-    int dead = p0 < 0 ? -p0 / step : 0;  // units before position 0
-    if (dead > k) dead = k;
-    if (dead < k)
-      sum += floor_sum(k - dead, kAttTile, step, p0 + (dead + 1) * step + kAttTile - 1);
-    sum += dead;
-    if (window) {
-      const long long from =
-          (long long)(sink_tiles + 1) * kAttTile + window - 1 - p0;  // gap > 0
-      const long long u = from > 0 ? (from + step - 1) / step : 0;
-      if (u < k)
-        sum -= (int)floor_sum(k - (int)u, kAttTile, step, (unsigned)(p0 + u * step - window + 1)) -
-               (k - (int)u) * sink_tiles;
-    }
-    return sum;
+    return len;
   }
 };
-
-// The list's part of block c begins at tile att_begin(c): the first total % blocks parts are
-// a tile longer.
-__device__ __forceinline__ int att_begin(int c, int total, int blocks) {
-  return c * (total / blocks) + min(c, total % blocks);
-}
-__device__ __forceinline__ int att_block_of(int tile, int total, int blocks) {
-  const int part = total / blocks, more = total % blocks;
-  return tile < more * (part + 1) ? tile / (part + 1) : more + (tile - more * (part + 1)) / part;
-}
-
-// The new tokens of request b as rows [lo, hi) of q, and its length. Offsets
-// that cannot be give no rows, a length that cannot be length 0.
-__device__ __forceinline__ int attend_request(const AttendParams& p, int b, int& lo, int& hi) {
-  lo = p.cu_q[b];
-  hi = p.cu_q[b + 1];
-  int len = p.kv_lens[b];
-  const bool bad_rows = lo < 0 || hi < lo || hi > p.T;
-  // (the last key tiles' ends stay below 2^31)
-  const bool bad_len =
-      len < 0 || len > ((long long)p.width << p.page_shift) || len > 0x7fff0000;
-  if (bad_rows || bad_len) {
-    if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
-    if (bad_rows) lo = hi = 0;
-    len = 0;
-  }
-  return len;
-}
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -232,57 +123,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-
-struct AttBase;
-
-// ---- the walk over this block's part of the list, an entry at a time: begun by the thread
-// whose run of requests the part starts in, carried on by one of the V loader's
-
-struct AttWalk {
-  int skip, end;   // places of the list given out, and where the part ends
-  int rest;        // places of the current unit given out
-  int total, blocks, b, lo, hi, len, head, u, q_at, entry;
-  int lo1, hi1, len1;  // request b + 1, read ahead
-  unsigned ring;
-  AttJoin join;
-
-  // The part [begin, end_), begin < end_, starts in request b_ (rows lo_ .. hi_ - 1, length
-  // len_), before which there are `before` tiles.
-  __device__ __forceinline__ void start(const AttendParams& p, int begin, int end_, int total_,
-                                        int blocks_, int b_, int before, int lo_, int hi_,
-                                        int len_) {
-    lo = lo_, hi = hi_, len = len_;
-    skip = begin, end = end_, total = total_, blocks = blocks_, b = b_;
-    u = q_at = entry = 0;
-    ring = 0;
-    join = {-1, 0, 0, 0};
-    read_ahead(p);
-    const AttUnits units(len, hi - lo, 2 * p.tile_tokens, p.window, p.sinks);
-    const int x = begin - before;
-    head = rest = 0;
-    if (x == 0) return;
-    const int per_head = units.before(units.count);
-    head = x / per_head;
-    rest = x - head * per_head;
-    int u1 = units.count - 1;  // the last unit that starts at or before there
-    while (u < u1) {
-      const int mid = (u + u1 + 1) >> 1;
-      if (units.before(mid) <= rest) u = mid; else u1 = mid - 1;
-    }
-    rest -= units.before(u);
-  }
-  __device__ __forceinline__ void read_ahead(const AttendParams& p) {
-    if (b + 1 < p.B) len1 = attend_request(p, b + 1, lo1, hi1);
-  }
-
-  __device__ __forceinline__ void next_request(const AttendParams& p) {
-    lo = lo1, hi = hi1, len = len1;
-    read_ahead(p);
-  }
-
-  // Puts the next entry, or the end mark, into the ring; nothing once that is there.
-  __device__ __forceinline__ bool publish(AttBase& sh, const AttendParams& p);
-};
 
 struct AttBase {
   uint64_t q_full[4], q_empty[2];
@@ -295,6 +135,7 @@ struct AttBase {
   unsigned long long scan[kAttScan / 32];
   int pad[kAttScan / 32], pad_all;
   AttWalk walk;
+  int entry;  // the walk's next
   uint32_t tmem;
   int stop;
 };
@@ -334,68 +175,17 @@ __device__ __forceinline__ int att_v_at(bool pair, int i, int n) {
   return pair ? 2 * i + 1 : min(2 * i + 2, 2 * n - 1);
 }
 
-__device__ __forceinline__ int att_tile(const AttSeg& g, int i) {
-  const int u = g.i0 + i;
-  return u < g.gap_at ? u : u + g.gap;
-}
+// ---- the walk over this block's part of the list: begun by the thread whose run of requests
+// the part starts in, carried on by one of the V loader's
 
-__device__ __forceinline__ bool AttWalk::publish(AttBase& sh, const AttendParams& p) {
+// Puts the walk's next entry, or the end mark, into the ring; nothing once that is there.
+__device__ __forceinline__ bool att_publish(AttWalk& walk, int& entry, AttBase& sh,
+                                            const AttendParams& p) {
   if (entry < 0) return true;
-  const int step = 2 * p.tile_tokens, at = entry % kAttSegs;
+  const int at = entry % kAttSegs;
   AttSeg g;
-  g.n = 0;
-  // A unit takes its key tiles and `cost` places more in the list, which stand for what its
-  // start and its results cost.
-  while (skip < end) {
-    while (hi == lo && b + 1 < p.B) {  // requests without rows
-      ++b;
-      next_request(p);
-    }
-    const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-    const int n = units.tiles(u), here = min(n + units.cost - rest, end - skip);
-    const int take = min(n - rest, here);  // tiles among them
-    if (take > 0) {
-      g.n = take;
-      g.i0 = rest;
-      g.b = b;
-      g.head = head;
-      g.token = lo + u * step;
-      g.tokens = min(step, hi - g.token);
-      g.pos = units.p0 + u * step;
-      g.lo = units.lo(u);
-      g.hi = max(units.hi(u), 0);
-      g.gap = units.gap(u);
-      g.gap_at = g.gap ? units.sink_tiles : 0x7fffffff;
-      g.pair = g.tokens > p.tile_tokens;
-      g.q_at = q_at;
-      g.ring = ring;
-      const bool starts = rest == 0, ends = rest + take == n;
-      g.slot = starts && ends ? -1 : starts ? 1 : 0;
-      if (starts && !ends) {
-        join.last = att_block_of(skip + n - 1, total, blocks);
-        join.head = head;
-        join.token = g.token;
-        join.tokens = g.tokens;
-      }
-      q_at += g.pair ? 2 : 1;
-      ring += 2 * take;
-    }
-    skip += here;
-    rest += here;
-    if (rest == n + units.cost) {
-      rest = 0;
-      if (++u == units.count) {
-        u = 0;
-        if (++head == p.kv_heads) {
-          head = 0;
-          ++b;
-          next_request(p);
-        }
-      }
-    }
-    if (take > 0) break;
-  }
-  if (g.n == 0) p.join[blockIdx.x] = join;
+  walk.next(p, g);
+  if (g.n == 0) p.join[blockIdx.x] = walk.join;
   if (!att_wait(sh, p, &sh.seg_empty[at], (entry / kAttSegs + 1) & 1)) return false;
   sh.seg[at] = g;
   mbar_arrive(&sh.seg_full[at]);
@@ -416,6 +206,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
   const int box = min(page, kAttTile);         // tokens of one load
   const int boxes = kAttTile / box;            // of a tile
   unsigned issued = 0, edges = 0;
+  int entry = V ? sh.entry : 0;
   auto load_q = [&](const AttSeg& g) {
     for (int s = 0; s <= g.pair; ++s) {
       const int x = g.q_at + s, slot = x & 1;
@@ -480,7 +271,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
         // the list's next entry, in the shadow of this load; and the second one at the start
         if (__builtin_expect(i == g.n - 1 || (e == 0 && i == 0), 0)) {
           for (int x = (i == g.n - 1) + (e == 0 && i == 0); x > 0; --x)
-            if (lane == 0) walk->publish(sh, p);
+            if (lane == 0) att_publish(*walk, entry, sh, p);
           __syncwarp();
         }
         if (__builtin_expect(clear, 0)) {
@@ -921,7 +712,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const int r0 = (int)min((long long)t * run, (long long)p.B), r1 = min(r0 + run, p.B);
     int lo = 0, hi = 0, len = 0;  // of the request read last
     auto tiles_of = [&](int r) {
-      len = attend_request(p, r, lo, hi);
+      len = p.request(r, lo, hi);
       const AttUnits units(len, hi - lo, step, p.window, p.sinks);
       return (unsigned long long)units.before(units.count) * p.kv_heads;
     };
@@ -974,8 +765,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       }
       AttWalk walk;
       walk.start(p, begin, end, total, blocks, r, at, lo, hi, len);
-      walk.publish(sh, p);
+      int entry = 0;
+      att_publish(walk, entry, sh, p);
       sh.walk = walk;
+      sh.entry = entry;
     }
     named_sync(1, kAttScan);
     if (works && warp == 8) {
