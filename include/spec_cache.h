@@ -45,9 +45,12 @@ extern "C" {
 /* Device status bits; they do not overlap SPEC_STATUS_*, and a wait that gave
  * up sets SPEC_STATUS_TIMEOUT. */
 #define SPEC_CACHE_NO_PAGES 0x100u    /* step: too few free pages; nothing was changed */
-#define SPEC_CACHE_BAD_LENGTHS 0x200u /* step: lengths or counts that cannot be; nothing
-                                         was changed. attend: a request whose offsets or
-                                         length cannot be; it sees nothing */
+#define SPEC_CACHE_BAD_LENGTHS 0x200u /* step: lengths or counts that cannot be; nothing was
+                                         changed. attend: a request whose offsets or length
+                                         cannot be; it sees nothing. Or a call of more than
+                                         2^30 steps (128 keys against some rows) for each
+                                         multiprocessor, about ten minutes of work: all its
+                                         rows see nothing */
 #define SPEC_CACHE_BAD_SLOT 0x400u    /* append: a slot past the pool; it was skipped */
 #define SPEC_CACHE_BAD_PAGE 0x800u    /* attend: a page number outside the pool; the
                                          request's outputs are not meaningful */
@@ -137,7 +140,8 @@ typedef struct {
   long long vp_page, vp_token, vp_head;
   const int* block_table;    /* [B x width] */
   long long table_stride;
-  const int* kv_lens;        /* [B] tokens of each request, the new ones among them */
+  const int* kv_lens;        /* [B] tokens of each request, the new ones among them; at most
+                                width pages and 2^31 - 2^16 */
   const int* cu_q;           /* [B+1] offsets of the new tokens in q: 0 .. <= T */
   void* out;                 /* [T, heads, dim] out */
   long long out_token, out_head;

@@ -5,7 +5,9 @@
 // A unit is up to two tiles of rows of one request and kv head. It takes its key
 // tiles and a fixed number of places more, which stand for what its start and its
 // results cost. The list is all units in order of request, kv head and rows, and
-// is never written down: a block finds its part from the requests' lengths.
+// is never written down: a block finds its part from the requests' lengths. A list
+// may be longer than 2^32 places (a chunk of 1.6 million tokens in units of two has
+// 5e9), a block's part of it may not (kAttMostPart).
 #pragma once
 #ifdef __CUDACC__
 #define SV_LIST __device__ __forceinline__
@@ -24,6 +26,9 @@ using std::min;
 constexpr int kAttTile = 128;     // rows of a tile, and tokens of a key tile
 // What a unit costs beside its key tiles, in tiles: of one tile of rows, and of two.
 constexpr int kAttCost = 2, kAttPairCost = 4;
+// The most places of a block's part: its loads are counted in 32 bits, two for each place.
+// (That many take a block about ten minutes.)
+constexpr long long kAttMostPart = 1ll << 30;
 
 // A unit that starts in one block's part of the list and ends in another's.
 struct AttJoin {
@@ -72,9 +77,23 @@ SV_LIST unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   return sum;
 }
 
+// sum over 0 <= u < n of floor((a u + b) / kAttTile), a <= 2 kAttTile, b <= 2^31: n may be so
+// large that the sum needs 64 bits. A term is a more than the one kAttTile before it, and the
+// kAttTile terms of one such period together need only 32.
+SV_LIST long long tile_sum(unsigned n, unsigned a, unsigned b) {
+  const unsigned periods = n / kAttTile, rest = n % kAttTile;
+  const long long rise = (long long)a * periods;  // of a term over all periods
+  long long sum = rise * rest + rise * (kAttTile / 2) * (periods - (periods > 0));
+#ifdef __CUDACC__
+#pragma unroll 1
+#endif
+  for (int whole = 0; whole <= (periods > 0); ++whole)
+    sum += (long long)floor_sum(whole ? kAttTile : rest, kAttTile, a, b) * (whole ? periods : 1);
+  return sum;
+}
+
 // The units of one request: `count` of `step` new tokens each (the last may
-// have fewer), for each kv head. Positions, and the key tiles of one head's
-// units together, are below 2^31.
+// have fewer), for each kv head. Positions are below 2^31.
 struct AttUnits {
   int p0;  // position of the first new token
   int q, step, count, window, sink_tiles, cost;
@@ -85,8 +104,7 @@ struct AttUnits {
         cost(q_ > step_ / 2 ? kAttPairCost : kAttCost) {}
 
   SV_LIST int hi(int u) const {
-    const int end = (u + 1) * step;
-    return p0 + (u + 1 < count && end < q ? end : q);
+    return p0 + (u + 1 < count ? (u + 1) * step : q);
   }
   SV_LIST int lo(int u) const {
     const int first = p0 + u * step + 1;
@@ -102,36 +120,50 @@ struct AttUnits {
     return h <= 0 ? 1 : (h - 1) / kAttTile + 1 - gap(u);
   }
   // Length in the list of the units before k, in closed form.
-  SV_LIST int before(int k) const {
-    int sum = k * cost;
+  SV_LIST long long before(int k) const {
+    long long sum = (long long)k * cost;
     if (k == count && k > 0) sum += tiles(--k);  // the last one ends where the request does
     if (k <= 0) return sum;
     int dead = p0 < 0 ? -p0 / step : 0;  // units before position 0
     if (dead > k) dead = k;
     if (dead < k)
-      sum += floor_sum(k - dead, kAttTile, step, p0 + (dead + 1) * step + kAttTile - 1);
+      sum += tile_sum(k - dead, step, (unsigned)p0 + (dead + 1) * step + kAttTile - 1);
     sum += dead;
     if (window) {
       const long long from =
           (long long)(sink_tiles + 1) * kAttTile + window - 1 - p0;  // gap > 0
       const long long u = from > 0 ? (from + step - 1) / step : 0;
       if (u < k)
-        sum -= (int)floor_sum(k - (int)u, kAttTile, step, (unsigned)(p0 + u * step - window + 1)) -
-               (k - (int)u) * sink_tiles;
+        sum -= tile_sum(k - (int)u, step, (unsigned)(p0 + u * step - window + 1)) -
+               (k - u) * sink_tiles;
     }
     return sum;
   }
 };
 
-// The list's part of block c begins at tile att_begin(c): the first total % blocks parts are
-// a tile longer.
-SV_LIST int att_begin(int c, int total, int blocks) {
-  return c * (total / blocks) + min(c, total % blocks);
-}
-SV_LIST int att_block_of(int tile, int total, int blocks) {
-  const int part = total / blocks, more = total % blocks;
-  return tile < more * (part + 1) ? tile / (part + 1) : more + (tile - more * (part + 1)) / part;
-}
+// One block's part of the list: the first total % blocks parts are a place longer.
+struct AttPart {
+  long long begin;
+  int places;
+  int part, longer;  // places of the later parts, of which the first `longer` have one more
+
+  // Of block c of blocks <= 2^16 with 0 < total <= kAttMostPart * blocks.
+  SV_LIST AttPart(int c, long long total, unsigned blocks) {
+    // total / blocks in two steps of 32 bits (a division of 64 is a long call)
+    const unsigned high = (unsigned)(total >> 16);
+    const unsigned low = (high % blocks) << 16 | ((unsigned)total & 0xffff);
+    const unsigned more = low % blocks;
+    part = (int)((high / blocks << 16) + low / blocks);
+    begin = (long long)c * part + min((unsigned)c, more);
+    places = part + ((unsigned)c < more);
+    longer = max((int)more - c - 1, 0);
+  }
+  // How many blocks later the place lies that is `x` places past the part's end.
+  SV_LIST int blocks_to(int x) const {
+    if (x < (long long)longer * (part + 1)) return 1 + x / (part + 1);
+    return 1 + longer + (x - longer * (part + 1)) / part;
+  }
+};
 
 // Number of the entry's key tile i.
 SV_LIST int att_tile(const AttSeg& g, int i) {
@@ -143,37 +175,44 @@ SV_LIST int att_tile(const AttSeg& g, int i) {
 // kv_heads, tile_tokens, window, sinks) and gives the new tokens [lo, hi) and the length of
 // request b by request(b, lo, hi).
 struct AttWalk {
-  int skip, end;   // places of the list given out, and where the part ends
+  AttPart part;
+  int left;        // places of the part not given out
   int rest;        // places of the current unit given out
-  int total, blocks, b, lo, hi, len, head, u, q_at;
+  int block, b, lo, hi, len, head, u, q_at;
   int lo1, hi1, len1;  // request b + 1, read ahead
   unsigned ring;
   AttJoin join;
 
-  // The part [begin, end_), begin < end_, starts in request b_ (rows lo_ .. hi_ - 1, length
-  // len_), before which there are `before` tiles.
+  // The part of block block_ starts in request b_ (rows lo_ .. hi_ - 1, length len_), before
+  // which there are `before` places.
   template <typename P>
-  SV_LIST void start(const P& p, int begin, int end_, int total_, int blocks_, int b_, int before,
-                     int lo_, int hi_, int len_) {
-    lo = lo_, hi = hi_, len = len_;
-    skip = begin, end = end_, total = total_, blocks = blocks_, b = b_;
-    u = q_at = 0;
-    ring = 0;
-    join = {-1, 0, 0, 0};
+  SV_LIST AttWalk(const P& p, const AttPart& part_, int block_, int b_, long long before, int lo_,
+                  int hi_, int len_)
+      : part(part_), left(part_.places), rest(0), block(block_), b(b_), lo(lo_), hi(hi_),
+        len(len_), head(0), u(0), q_at(0), ring(0), join{-1, 0, 0, 0} {
     read_ahead(p);
     const AttUnits units(len, hi - lo, 2 * p.tile_tokens, p.window, p.sinks);
-    const int x = begin - before;
-    head = rest = 0;
+    const long long x = part.begin - before;
     if (x == 0) return;
-    const int per_head = units.before(units.count);
-    head = x / per_head;
-    rest = x - head * per_head;
-    int u1 = units.count - 1;  // the last unit that starts at or before there
-    while (u < u1) {
-      const int mid = (u + u1 + 1) >> 1;
-      if (units.before(mid) <= rest) u = mid; else u1 = mid - 1;
+    // The head, from the length of a whole one; then the last unit of it that starts at or
+    // before the part. (One loop, so that before()'s code is there once.)
+    long long in_head = 0, from = 0;
+    int u1 = units.count - 1;
+    for (int k = units.count;;) {
+      const long long at = units.before(k);
+      if (k == units.count) {
+        head = (int)(x / at);
+        in_head = x - head * at;
+      } else if (at <= in_head) {
+        u = k;
+        from = at;
+      } else {
+        u1 = k - 1;
+      }
+      if (u >= u1) break;
+      k = (u + u1 + 1) >> 1;
     }
-    rest -= units.before(u);
+    rest = (int)(in_head - from);
   }
   template <typename P>
   SV_LIST void read_ahead(const P& p) {
@@ -193,13 +232,13 @@ struct AttWalk {
     g.n = 0;
     // A unit takes its key tiles and `cost` places more in the list, which stand for what its
     // start and its results cost.
-    while (skip < end) {
+    while (left > 0) {
       while (hi == lo && b + 1 < p.B) {  // requests without rows
         ++b;
         next_request(p);
       }
       const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-      const int n = units.tiles(u), here = min(n + units.cost - rest, end - skip);
+      const int n = units.tiles(u), here = min(n + units.cost - rest, left);
       const int take = min(n - rest, here);  // tiles among them
       if (take > 0) {
         g.n = take;
@@ -219,7 +258,7 @@ struct AttWalk {
         const bool starts = rest == 0, ends = rest + take == n;
         g.slot = starts && ends ? -1 : starts ? 1 : 0;
         if (starts && !ends) {
-          join.last = att_block_of(skip + n - 1, total, blocks);
+          join.last = block + part.blocks_to(n - here - 1);
           join.head = head;
           join.token = g.token;
           join.tokens = g.tokens;
@@ -227,7 +266,7 @@ struct AttWalk {
         q_at += g.pair ? 2 : 1;
         ring += 2 * take;
       }
-      skip += here;
+      left -= here;
       rest += here;
       if (rest == n + units.cost) {
         rest = 0;

@@ -132,7 +132,7 @@ struct AttBase {
   uint64_t seg_full[kAttSegs], seg_empty[kAttSegs];
   AttSeg seg[kAttSegs];
   float2 ml[2][kAttTile];
-  unsigned long long scan[kAttScan / 32];
+  long long scan[kAttScan / 32];
   int pad[kAttScan / 32], pad_all;
   AttWalk walk;
   int entry;  // the walk's next
@@ -714,37 +714,37 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     auto tiles_of = [&](int r) {
       len = p.request(r, lo, hi);
       const AttUnits units(len, hi - lo, step, p.window, p.sinks);
-      return (unsigned long long)units.before(units.count) * p.kv_heads;
+      return units.before(units.count) * p.kv_heads;
     };
-    unsigned long long mine = 0;
+    long long mine = 0;
     int pad = 0;  // rows from here on belong to no request
     for (int r = r0; r < r1; ++r) {
       mine += tiles_of(r);
       pad = max(pad, hi);
     }
-    unsigned long long upto = mine;
+    long long upto = mine;
     for (int d = 1; d < 32; d <<= 1) {
-      const unsigned long long x = __shfl_up_sync(~0u, upto, d);
+      const long long x = __shfl_up_sync(~0u, upto, d);
       if (lane >= d) upto += x;
     }
     pad = __reduce_max_sync(~0u, pad);
     if (lane == 31) sh.scan[w0] = upto;
     if (lane == 0) sh.pad[w0] = pad;
     named_sync(1, kAttScan);
-    unsigned long long all = 0, before64 = upto - mine;
+    long long all = 0, before = upto - mine;
     for (int w = 0; w < kAttScan / 32; ++w) {
-      if (w < w0) before64 += sh.scan[w];
+      if (w < w0) before += sh.scan[w];
       all += sh.scan[w];
       pad = max(pad, sh.pad[w]);
     }
-    // 2^31 tiles are 2^38 tokens of a head: no list is that long
-    if (all > 0x7fffffffull && t == 0 && blockIdx.x == 0 && p.status)
-      atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
-    const int total = all > 0x7fffffffull ? 0 : (int)all, before = (int)before64;
-    const int blocks = min((int)gridDim.x, total);
+    long long total = all;
+    if (total > kAttMostPart * gridDim.x) {  // too much for one call: all rows see nothing
+      if (t == 0 && blockIdx.x == 0 && p.status) atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
+      total = pad = 0;
+    }
+    const int blocks = (int)min((long long)gridDim.x, total);
     const bool works = (int)blockIdx.x < blocks;
-    const int begin = works ? att_begin(blockIdx.x, total, blocks) : 0;
-    const int end = works ? att_begin(blockIdx.x + 1, total, blocks) : 0;
+    const AttPart part(blockIdx.x, total, max(blocks, 1));
     if (t == 0) {
       p.join[blockIdx.x].last = -1;
       sh.pad_all = pad;
@@ -754,17 +754,17 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       }
     }
     __syncwarp();
-    if (works && before <= begin && begin < before + (int)mine) {
-      int at = before, r = r0;
+    if (works && before <= part.begin && part.begin < before + mine) {
+      long long at = before;
+      int r = r0;
       if (run > 1) {
         for (;; ++r) {
-          const int n = (int)tiles_of(r);
-          if (begin < at + n || r + 1 >= r1) break;
+          const long long n = tiles_of(r);
+          if (part.begin < at + n || r + 1 >= r1) break;
           at += n;
         }
       }
-      AttWalk walk;
-      walk.start(p, begin, end, total, blocks, r, at, lo, hi, len);
+      AttWalk walk(p, part, blockIdx.x, r, at, lo, hi, len);
       int entry = 0;
       att_publish(walk, entry, sh, p);
       sh.walk = walk;

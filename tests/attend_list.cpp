@@ -3,6 +3,7 @@
 #include "../speculative_decoding_rejection_02_gb300/csrc/attend_list.cuh"
 
 #include <cstring>
+#include <new>
 #include <vector>
 
 namespace {
@@ -42,12 +43,12 @@ int list_walk(const int* cu_q, const int* kv_lens, int B, int kv_heads, int tile
   int b = 0;
   first[0] = 0;
   for (int c = 0; c < blocks; ++c) {
-    const long long begin = sv::att_begin(c, total, blocks);
-    const long long end = sv::att_begin(c + 1, total, blocks);
-    while (before[b + 1] <= begin) ++b;
-    sv::AttWalk walk;
-    std::memset((void*)&walk, 0xcd, sizeof walk);  // start() has to set all that next() reads
-    walk.start(p, begin, end, total, blocks, b, before[b], cu_q[b], cu_q[b + 1], kv_lens[b]);
+    const sv::AttPart part(c, total, blocks);
+    while (before[b + 1] <= part.begin) ++b;
+    alignas(sv::AttWalk) unsigned char memory[sizeof(sv::AttWalk)];
+    std::memset(memory, 0xcd, sizeof memory);  // the walk has to set all that next() reads
+    sv::AttWalk& walk = *new (memory)
+        sv::AttWalk(p, part, c, b, before[b], cu_q[b], cu_q[b + 1], kv_lens[b]);
     for (;; ++at) {
       if (at == most) return -1;
       walk.next(p, segs[at]);

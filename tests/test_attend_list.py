@@ -140,3 +140,25 @@ def test_units_before_in_closed_form(L, window, sinks):
         want = np.concatenate([[0], np.cumsum(x["tiles"] + x["cost"])])
         for k in {0, len(x), int(r.integers(0, len(x) + 1))}:
             assert L.list_before(length, q, step, window, sinks, k) == want[k]
+
+
+LONG = [
+    # new tokens, length, kv heads, new tokens of a tile of rows, window, sinks
+    (1600000, 1600000, 1, 1, 0, 0),   # 5.0e9 places
+    (1 << 20, 1 << 20, 8, 8, 0, 0),   # 2.1e9
+    (400000, 400000, 8, 1, 0, 0),     # 2.5e9
+    (1500000, 1400000, 1, 1, 0, 0),   # rows before position 0
+    (3000000, 3000000, 2, 1, 2000000, 300),
+    (300000, 0x7fff0000, 1, 128, 0, 0),
+    (5, 0x7fff0000, 64, 5, 0, 0),
+]
+
+
+@pytest.mark.parametrize("q,length,kv_heads,tile_tokens,window,sinks", LONG)
+def test_lists_past_32_bits(L, q, length, kv_heads, tile_tokens, window, sinks):
+    x = units_of([0, q], [length], 1, tile_tokens, window, sinks)
+    want = np.concatenate([[0], np.cumsum(x["tiles"] + x["cost"])])
+    for k in (0, 1, len(x) // 3, len(x) - 1, len(x)):
+        if k >= 0:
+            assert L.list_before(length, q, 2 * tile_tokens, window, sinks, k) == want[k]
+    check_walk(L, [3, q, 7], [2000, length, 9], kv_heads, tile_tokens, window, sinks)
