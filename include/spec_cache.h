@@ -47,7 +47,7 @@ extern "C" {
 #define SPEC_CACHE_NO_PAGES 0x100u    /* step: too few free pages; nothing was changed */
 #define SPEC_CACHE_BAD_LENGTHS 0x200u /* step: lengths or counts that cannot be; nothing was
                                          changed. attend: a request whose offsets or length
-                                         cannot be; it sees nothing. Or a call of more than
+                                         cannot be; its rows see nothing. Or a call of more than
                                          2^30 steps (128 keys against some rows) for each
                                          multiprocessor, about ten minutes of work: all its
                                          rows see nothing */
@@ -165,8 +165,8 @@ long long spec_cache_attend_workspace(const spec_cache_attend_args* a);
  * window only those with p - j < window or j < sinks; query head h reads the
  * keys and values of head h / G:
  *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j e^(scale q . k_j).
- * A token that sees nothing (p < 0), and the rows past cu_q[B], give out = 0
- * and lse = -inf. Scores, softmax statistics and sums are fp32; the softmax
+ * A token that sees nothing (p < 0), and the rows that belong to no request
+ * (past cu_q[B], before cu_q[0]), give out = 0 and lse = -inf. Scores, softmax statistics and sums are fp32; the softmax
  * weights are rounded to the cache's type before they meet the values.
  * Whatever the memory of slots that no row of a request sees holds, NaN and
  * infinities too, does not reach the outputs (a value that some row sees and that

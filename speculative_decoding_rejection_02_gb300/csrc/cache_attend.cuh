@@ -97,7 +97,7 @@ struct AttendParams {
   AttJoin* join;  // [blocks]
 
   // The new tokens of request b as rows [lo, hi) of q, and its length. Offsets
-  // that cannot be give no rows, a length that cannot be length 0.
+  // that cannot be give no rows (lo = hi = -1), a length that cannot be length 0.
   __device__ __forceinline__ int request(int b, int& lo, int& hi) const {
     lo = cu_q[b];
     hi = cu_q[b + 1];
@@ -107,7 +107,7 @@ struct AttendParams {
     const bool bad_len = len < 0 || len > ((long long)width << page_shift) || len > 0x7fff0000;
     if (bad_rows || bad_len) {
       if (status) atomicOr(status, SPEC_CACHE_BAD_LENGTHS);
-      if (bad_rows) lo = hi = 0;
+      if (bad_rows) lo = hi = -1;
       len = 0;
     }
     return len;
@@ -134,6 +134,7 @@ struct AttBase {
   float2 ml[2][kAttTile];
   long long scan[kAttScan / 32];
   int pad[kAttScan / 32], pad_all;
+  int gaps;  // some rows before pad_all may belong to no request
   AttWalk walk;
   int entry;  // the walk's next
   uint32_t tmem;
@@ -688,7 +689,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_init(&sh.o_free, 8);
       mbar_init(&sh.ml_full, 8);
       mbar_init(&sh.edge_full, 1);
-      sh.stop = 0;
+      sh.stop = sh.gaps = 0;
     }
     fence_mbar_init();
   } else if (tid == 32) {
@@ -721,6 +722,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     for (int r = r0; r < r1; ++r) {
       mine += tiles_of(r);
       pad = max(pad, hi);
+      if (lo < 0 || (r == 0 && lo > 0)) sh.gaps = 1;
     }
     long long upto = mine;
     for (int d = 1; d < 32; d <<= 1) {
@@ -792,8 +794,21 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     tmem_fence_after();
     tmem_free(sh.tmem, 512);
   }
-  // Rows of q past the last request: zeros.
-  for (long long t = sh.pad_all + blockIdx.x; t < p.T; t += gridDim.x) {
+  // Rows of q that belong to no request: zeros. Those past the last one as a rule; where the
+  // offsets do not start at 0 or cannot be, a row is looked for in all requests.
+  const int pad_all = sh.pad_all;
+  const bool gaps = sh.gaps;
+#pragma unroll 1
+  for (long long t = (gaps ? 0 : pad_all) + blockIdx.x; t < p.T; t += gridDim.x) {
+    if (t < pad_all) {
+      bool mine = false;
+#pragma unroll 1
+      for (int b = tid; b < p.B; b += kAttThreads) {
+        const int lo = p.cu_q[b], hi = p.cu_q[b + 1];
+        mine |= lo >= 0 && lo <= t && t < hi && hi <= p.T;
+      }
+      if (__syncthreads_or(mine)) continue;
+    }
     const int pieces = p.dim / 8;
     for (int i = tid; i < p.heads * pieces; i += kAttThreads)
       *(uint4*)(p.out + t * p.out_token + (i / pieces) * p.out_head + (i % pieces) * 16) =
