@@ -234,7 +234,9 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
     auto place = [&](int i) { return att_tile(g, i) * kAttTile + lane * box; };
     auto page_of = [&](int j) {
       const bool seen = lane < boxes && j < g.hi && (j + box > g.lo || j < sinks);
-      return seen ? __ldg(table + (j >> p.page_shift)) : -1;
+      // (an ordinary load: the kernel before this one may still be writing the table when this
+      // one starts, which loads through the read-only path do not allow)
+      return seen ? table[j >> p.page_shift] : -1;
     };
     int number = page_of(place(0));
     // Q of the first segment while that comes; later ones' after their first tile, which need
