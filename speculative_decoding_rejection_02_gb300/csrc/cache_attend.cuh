@@ -161,7 +161,15 @@ __device__ __forceinline__ bool att_wait(AttBase& sh, const AttendParams& p, uin
   return false;
 }
 
-// The same for a whole warp, with one answer for all its lanes.
+// The wait for what a warp has in flight when it ends: 20 ms at most (one for what was never
+// issued takes its limit).
+__device__ __forceinline__ void att_land(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 1024; ++i)
+    if (mbar_try(bar, parity & 1)) break;
+}
+
+// att_wait for a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool att_wait_warp(AttBase& sh, const AttendParams& p, uint64_t* bar,
                                               uint32_t parity) {
   return __all_sync(~0u, att_wait(sh, p, bar, parity));
@@ -194,6 +202,18 @@ __device__ __forceinline__ bool att_publish(AttWalk& walk, int& entry, AttBase& 
   return true;
 }
 
+// Lets the last tiles' loads land: none outlives the block, whether all went well or a wait ran
+// out. (A call: inlined, this code moves the tile loops, and two chunks of 2048 take 667 us
+// instead of 648.)
+template <int DP>
+__device__ __noinline__ void att_drain(AttShared<DP>& sh, unsigned issued, unsigned q_issued) {
+  using Cfg = AttCfg<DP>;
+  for (unsigned r = issued > Cfg::kStages ? issued - Cfg::kStages : 0; r < issued; ++r)
+    att_land(&sh.kv_full[r % Cfg::kRing], r / Cfg::kRing);
+  for (unsigned x = q_issued > 2 ? q_issued - 2 : 0; x < q_issued; ++x)
+    att_land(&sh.q_full[x & 3], x / 4);
+}
+
 // ---- warps 8 and 11: Q and K, and V tiles by TMA (two warps: with small pages it is the
 // issue of the loads that takes the time). The one for V also does the walk, two entries
 // ahead of its loads.
@@ -206,7 +226,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
   const int page = 1 << p.page_shift;
   const int box = min(page, kAttTile);         // tokens of one load
   const int boxes = kAttTile / box;            // of a tile
-  unsigned issued = 0, edges = 0;
+  unsigned issued = 0, q_issued = 0, edges = 0;
   int entry = V ? sh.entry : 0;
   auto load_q = [&](const AttSeg& g) {
     for (int s = 0; s <= g.pair; ++s) {
@@ -219,6 +239,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
                       g.head, g.token + s * p.tile_tokens, &sh.q_full[x & 3]);
       }
       __syncwarp();
+      q_issued = x + 1;
     }
     return true;
   };
@@ -226,7 +247,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
     const int at = e % kAttSegs;
     if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) break;
     const AttSeg g = sh.seg[at];
-    if (g.n == 0) return;
+    if (g.n == 0) break;
     bool ok = true;
     const int* table = p.table + g.b * p.table_stride;
     const int sinks = min(p.sinks, g.lo);
@@ -280,8 +301,12 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
         if (__builtin_expect(clear, 0)) {
           // V's rows that no row of the unit sees may hold anything, and P is 0 there: they are
           // zeroed before the tile counts as loaded.
-          ok = att_wait_warp(sh, p, &sh.edge_full, edges++);
-          if (!ok) break;
+          ok = att_wait_warp(sh, p, &sh.edge_full, edges);
+          if (!ok) {
+            att_land(&sh.edge_full, edges);
+            break;
+          }
+          ++edges;
 #pragma unroll 1
           for (int y = lane; y < kAttTile * kBlocks; y += 32) {
             const int j = j0 + (y & (kAttTile - 1));
@@ -302,11 +327,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.seg_empty[at]);
   }
-  // A wait ran out: let the loads in flight land before the block's end (those of the other
-  // of the two warps among them: a wait too many only takes its limit).
-  for (unsigned r = issued > Cfg::kStages ? issued - Cfg::kStages : 0; r < issued; ++r)
-    for (int i = 0; i < 1024; ++i)
-      if (mbar_try(&sh.kv_full[r % Cfg::kRing], (r / Cfg::kRing) & 1)) break;
+  att_drain<DP>(sh, issued, q_issued);
 }
 
 // ---- warps 9 and 10: the products of stream 0 and 1, issued by one thread of each.
@@ -325,7 +346,7 @@ __device__ __forceinline__ void att_release(AttShared<DP>& sh, unsigned r, bool 
 }
 
 template <int DP, bool BF16>
-__device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendParams& p,
+__device__ __forceinline__ void att_products(AttShared<DP>& sh, const AttendParams& p,
                                              char* q_smem, char* kv_smem, const int s) {
   using Cfg = AttCfg<DP>;
   constexpr uint32_t kQK = mma_kind(BF16, false, kAttTile, kAttTile);
@@ -339,19 +360,19 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
   const uint64_t v0 = mma_desc(smem_addr(kv_smem), kAttTile * 128);
   constexpr unsigned kTile = Cfg::kTileBytes / 16;
   unsigned p_count = 0, turn = 0;
-  if (!att_wait_warp(sh, p, &sh.warm, 0)) return false;  // the softmax warps' dry run
+  if (!att_wait_warp(sh, p, &sh.warm, 0)) return;  // the softmax warps' dry run
   auto loaded = [&](unsigned r) {
     return att_wait_warp(sh, p, &sh.kv_full[r % Cfg::kRing], r / Cfg::kRing);
   };
   for (int e = 0;; ++e) {
     const int at = e % kAttSegs;
-    if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) return false;
+    if (!att_wait_warp(sh, p, &sh.seg_full[at], e / kAttSegs)) return;
     const int n = __shfl_sync(~0u, sh.seg[at].n, 0);
-    if (n == 0) return true;
+    if (n == 0) return;
     const bool pair = __shfl_sync(~0u, sh.seg[at].pair, 0);
     const int q_at = __shfl_sync(~0u, sh.seg[at].q_at, 0) + (pair ? s : 0);
     const unsigned ring = __shfl_sync(~0u, sh.seg[at].ring, 0);
-    if (!att_wait_warp(sh, p, &sh.q_full[q_at & 3], q_at / 4)) return false;
+    if (!att_wait_warp(sh, p, &sh.q_full[q_at & 3], q_at / 4)) return;
     const int step = pair ? 1 : 2, first = pair ? 0 : s;
     // The same number of turns for both streams, whether they have a tile for it or not.
     const int turns = pair ? n + 1 : (n + 3) / 2;
@@ -361,20 +382,20 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
       const unsigned k = ring + att_k_at(pair, next), v = ring + att_v_at(pair, last, n);
       const bool has_pv = t > 0 && last < n, has_qk = next < n;
       // the results of the segment before (e > 0) have been read by all
-      if (t == 1 && !att_wait_warp(sh, p, &sh.o_free, e + 1)) return false;
+      if (t == 1 && !att_wait_warp(sh, p, &sh.o_free, e + 1)) return;
       if (has_pv) {
         // S of the turn before is there: what its products read is free (and the loads below
         // may be waiting for that)
-        if (!att_wait_warp(sh, p, &sh.s_full[s], p_count)) return false;
+        if (!att_wait_warp(sh, p, &sh.s_full[s], p_count)) return;
         if (one) {
           att_release<DP>(sh, ring + att_k_at(pair, last), pair);
           if (t > 1) att_release<DP>(sh, ring + att_v_at(pair, last - step, n), pair);
         }
         __syncwarp();
       }
-      if (has_qk && !loaded(k)) return false;
-      if (has_pv && (!loaded(v) || !att_wait_warp(sh, p, &sh.p_half[s], p_count))) return false;
-      if (!att_wait_warp(sh, p, &sh.turn[s], turn + 1 - s)) return false;
+      if (has_qk && !loaded(k)) return;
+      if (has_pv && (!loaded(v) || !att_wait_warp(sh, p, &sh.p_half[s], p_count))) return;
+      if (!att_wait_warp(sh, p, &sh.turn[s], turn + 1 - s)) return;
       ++turn;
       tmem_fence_after();
       if (has_pv) {
@@ -382,7 +403,7 @@ __device__ __forceinline__ bool att_products(AttShared<DP>& sh, const AttendPara
 #pragma unroll
         for (int x = 0; x < kAttTile / 16; ++x) {
           if (x == kAttTile / 32) {  // half of P at a time, as it comes
-            if (!att_wait_warp(sh, p, &sh.p_full[s], p_count)) return false;
+            if (!att_wait_warp(sh, p, &sh.p_full[s], p_count)) return;
             tmem_fence_after();
           }
           mma_ts(tmem_o, tmem_s + 8 * x, vd + x * (16 * 128 / 16), kind_pv, t > 1 || x > 0,
@@ -782,11 +803,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       att_load<DP, true>(sh, p, q_smem, kv_smem, lane, &walk);
     } else if (works) {
       const int s = warp - 9;
-      if (!att_products<DP, BF16>(sh, p, q_smem, kv_smem, s)) {
-        mma_commit(&sh.drain[s], elect_one());
-        for (int i = 0; i < 1024; ++i)
-          if (mbar_try(&sh.drain[s], 0)) break;
-      }
+      att_products<DP, BF16>(sh, p, q_smem, kv_smem, s);
+      mma_commit(&sh.drain[s], elect_one());  // no product outlives the block either
+      att_land(&sh.drain[s], 0);
     }
     __syncwarp();
   }
