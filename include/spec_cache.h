@@ -94,9 +94,10 @@ typedef struct {
  * pages, or the new tokens exceed num_tokens, a status bit is set, tables and
  * stack stay as they are, lens = held_lens, cu_new = 0, positions = slots =
  * -1 and free_count_out = free_count.
- * lens and free_count_out must not be held_lens and free_count themselves; the
- * call leaves its inputs but for the pages' owners as they are, so it may be
- * repeated with the same inputs and gives the same result.
+ * What the call writes (the outputs, block_table, free_pages) overlaps no other
+ * argument: SPEC_ERR_INVALID_ARG. It leaves its inputs but for the pages' owners
+ * as they are, so it may be repeated with the same inputs and gives the same
+ * result.
  */
 int spec_cache_step(const spec_cache_step_args* a, void* stream, unsigned* device_status);
 

@@ -53,19 +53,46 @@ int launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, void* stre
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// Whether what the call writes overlaps anything else of its arguments.
+bool step_overlaps(const spec_cache_step_args* a) {
+  const long long B = a->B, T = a->num_tokens;
+  const struct {
+    const void* at;
+    long long bytes;
+  } x[] = {{a->lens, 4 * B},
+           {a->cu_new, 4 * (B + 1)},
+           {a->positions, 4 * T},
+           {a->slots, 8 * T},
+           {a->free_count_out, 4},
+           {a->block_table, B > 0 ? 4 * ((B - 1) * a->table_stride + a->width) : 0},
+           {a->free_pages, 4ll * a->num_pages},
+           {a->held_lens, 4 * B},  // from here on read only
+           {a->new_lens, 4 * B},
+           {a->cu_num_draft, 4 * (B + 1)},
+           {a->num_accepted, 4 * B},
+           {a->free_count, 4}};
+  const int written = 7, all = sizeof x / sizeof *x;
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < all; ++j) {
+      const unsigned long long p = (uintptr_t)x[i].at, q = (uintptr_t)x[j].at;
+      if (p && q && x[i].bytes > 0 && x[j].bytes > 0 && p < q + x[j].bytes && q < p + x[i].bytes)
+        return true;
+    }
+  return false;
+}
+
 int check_step(const spec_cache_step_args* a) {
   if (!a || a->B < 0 || a->width < 1 || a->table_stride < a->width || a->page_size < 1 ||
       a->num_pages < 1 || a->num_tokens < 0)
     return SPEC_ERR_INVALID_ARG;
-  if (!a->free_count || !a->cu_new || !a->free_count_out || a->free_count == a->free_count_out)
-    return SPEC_ERR_INVALID_ARG;
+  if (!a->free_count || !a->cu_new || !a->free_count_out) return SPEC_ERR_INVALID_ARG;
   if (a->B > 0 && (a->cu_num_draft == nullptr) != (a->num_accepted == nullptr))
     return SPEC_ERR_INVALID_ARG;
   if (a->num_tokens > 0 && !a->slots) return SPEC_ERR_INVALID_ARG;
   if (a->B > 0 && (!a->held_lens || !a->new_lens || !a->block_table || !a->free_pages ||
-                   !a->lens || a->lens == a->held_lens || a->lens == a->new_lens))
+                   !a->lens))
     return SPEC_ERR_INVALID_ARG;
-  return SPEC_OK;
+  return step_overlaps(a) ? SPEC_ERR_INVALID_ARG : SPEC_OK;
 }
 
 int check_append(const spec_cache_append_args* a) {
