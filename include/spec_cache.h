@@ -147,7 +147,7 @@ typedef struct {
   void* out;                 /* [T, heads, dim] out */
   long long out_token, out_head;
   float* lse;                /* [T, heads] out: ln of the sum of exp(score), or NULL */
-  float scale;               /* of the scores; 1 / sqrt(dim) as a rule */
+  float scale;               /* of the scores; 1 / sqrt(dim) as a rule. scale / ln 2 is finite */
   int window;                /* tokens that a row sees, itself among them; 0: all */
   int sinks;                 /* first tokens that a window leaves visible, >= 0 */
   void* workspace;           /* spec_cache_attend_workspace bytes, 256-byte aligned; its

@@ -113,6 +113,9 @@ int check_append(const spec_cache_append_args* a) {
   return SPEC_OK;
 }
 
+// The scores' factor: 2^x in place of e^x.
+float exponent_scale(const spec_cache_attend_args* a) { return a->scale * 1.4426950408889634f; }
+
 int check_attend(const spec_cache_attend_args* a, bool pointers) {
   if (!a || a->B < 0 || a->num_tokens < 0 || a->max_q < 1 || a->heads < 1 || a->kv_heads < 1 ||
       a->dim < 1 || a->page_size < 1 || a->width < 1 || a->num_pages < 1 || a->window < 0 ||
@@ -127,7 +130,7 @@ int check_attend(const spec_cache_attend_args* a, bool pointers) {
   if (a->B > 0 && (!a->k_pages || !a->v_pages || !a->block_table || !a->kv_lens ||
                    a->table_stride < a->width))
     return SPEC_ERR_INVALID_ARG;
-  if (!std::isfinite(a->scale)) return SPEC_ERR_INVALID_ARG;
+  if (!std::isfinite(exponent_scale(a))) return SPEC_ERR_INVALID_ARG;
   const void* ptrs[] = {a->q, a->k_pages, a->v_pages, a->out};
   for (const void* p : ptrs)
     if (!aligned(p, 16)) return SPEC_ERR_INVALID_ARG;
@@ -316,7 +319,7 @@ int spec_cache_attend(const spec_cache_attend_args* a, void* stream, unsigned* d
   p.out_head = a->out_head * 2;
   p.lse = a->lse;
   // a scale of 0 still leaves masked scores at -inf
-  p.c = a->scale * 1.4426950408889634f;
+  p.c = exponent_scale(a);
   if (std::fabs(p.c) < 1.1754944e-38f) p.c = 1.1754944e-38f;
   p.hidden = p.c > 0.f ? -INFINITY : INFINITY;
   p.window = a->window < (long long)a->width * a->page_size ? a->window : 0;
