@@ -275,9 +275,9 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   const bool return_lse = PyObject_IsTrue(*x.x++) == 1;
   unsigned* status = x.status();
-  const long long need = g_workspace(&a);
-  if (need < 0) return PyLong_FromLongLong(need);
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.dev);
+  const long long need = g_workspace(&a);  // of the current device, now the tensors'
+  if (need < 0) return PyLong_FromLongLong(need);
   if (!out.defined()) out = empty({T, heads, dim}, q.scalar_type(), x.dev);
   if (return_lse) lse = empty({T, heads}, at::kFloat, x.dev);
   workspace = empty({need}, at::kByte, x.dev);
