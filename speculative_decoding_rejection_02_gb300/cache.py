@@ -7,7 +7,8 @@ is one call of the C ABI on torch tensors: argument checks here and in the
 library raise before anything is enqueued, outputs and workspace come from
 torch's allocator on the stream that the call runs on (``stream``, or the
 current one), and errors in device data set bits of ``status`` (an int32
-tensor of one element, OR-ed).
+tensor of one element, OR-ed). There is no backward pass: a tensor that
+requires a gradient is refused while gradients are enabled.
 
 The calls on tensors are ``csrc/cache_binding.cpp``; the structures of the C
 ABI are here for callers that come with addresses of their own.

@@ -5,6 +5,7 @@
 // code of a call that was refused.
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -35,6 +36,9 @@ struct Args {
     PyObject* o = *x++;
     TORCH_CHECK_TYPE(THPVariable_Check(o), name, " must be a tensor");
     const Tensor& t = THPVariable_Unpack(o);
+    TORCH_CHECK_VALUE(!t.requires_grad() || !c10::GradMode::is_enabled(), name,
+                      " requires a gradient, and the call has no backward pass: detach it, or "
+                      "call under torch.no_grad()");
     TORCH_CHECK_VALUE(t.is_cuda(), name, " must be on a CUDA device, not ", t.device());
     if (dev < 0) dev = t.get_device();
     TORCH_CHECK_VALUE(t.get_device() == dev, name, " is on ", t.device(),
