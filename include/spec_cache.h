@@ -23,8 +23,9 @@
  *    synchronise the host, so they can be captured into a CUDA graph;
  *  - argument errors are found on the host before anything is enqueued;
  *    errors in device data (lengths, slots, page numbers) set bits of
- *    *device_status (OR-ed in: clear it first; NULL drops them) and lead to
- *    no access out of bounds;
+ *    *device_status (OR-ed in: clear it first), or with NULL of a word that the
+ *    library has on each device (spec_cache_status reads it), and lead to no
+ *    access out of bounds;
  *  - returns SPEC_OK or a SPEC_ERR_* code of spec_verify.h:
  *    SPEC_ERR_INVALID_ARG (null pointer, size, alignment),
  *    SPEC_ERR_UNSUPPORTED (a form the call does not have, or a device that is
@@ -43,7 +44,7 @@ extern "C" {
 #endif
 
 /* Device status bits; they do not overlap SPEC_STATUS_*, and a wait that gave
- * up sets SPEC_STATUS_TIMEOUT. */
+ * up sets SPEC_STATUS_TIMEOUT (the call's outputs are not meaningful then). */
 #define SPEC_CACHE_NO_PAGES 0x100u    /* step: too few free pages; nothing was changed */
 #define SPEC_CACHE_BAD_LENGTHS 0x200u /* step: lengths or counts that cannot be; nothing was
                                          changed. attend: a request whose offsets or length
@@ -179,6 +180,13 @@ long long spec_cache_attend_workspace(const spec_cache_attend_args* a);
  * multiples of 16 bytes (SPEC_ERR_INVALID_ARG).
  */
 int spec_cache_attend(const spec_cache_attend_args* a, void* stream, unsigned* device_status);
+
+/*
+ * spec_cache_status — wait for the current device's work, read the status bits of
+ * the calls that had device_status = NULL on it, and clear them. Returns SPEC_OK,
+ * or SPEC_ERR_DEVICE_STATUS where a bit is set.
+ */
+int spec_cache_status(unsigned* bits);
 
 #ifdef __cplusplus
 }

@@ -54,7 +54,7 @@ _SHARD_CALLS = ENTRY_POINTS[-5:]
 
 # The entry points declared in include/spec_cache.h.
 CACHE_ENTRY_POINTS = ("spec_cache_step", "spec_cache_append", "spec_cache_attend_workspace",
-                      "spec_cache_attend")
+                      "spec_cache_attend", "spec_cache_status")
 
 
 class SpecVerifyError(RuntimeError):
@@ -125,6 +125,7 @@ def lib():
                 getattr(L, name).argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
             L.spec_cache_attend_workspace.argtypes = [C.c_void_p]
             L.spec_cache_attend_workspace.restype = C.c_longlong
+            L.spec_cache_status.argtypes = [C.POINTER(C.c_uint)]
             for name in ENTRY_POINTS:
                 getattr(L, name)  # raises if the library lacks a declared symbol
             _lib = L
@@ -329,7 +330,7 @@ def strerror(code: int) -> str:
 
 _CACHE_NAMES = ("CACHE_BAD_LENGTHS", "CACHE_BAD_PAGE", "CACHE_BAD_SLOT", "CACHE_NO_PAGES",
                 "AppendArgs", "AttendArgs", "CacheStep", "StepArgs", "cache_append",
-                "cache_attend", "cache_step")
+                "cache_attend", "cache_status", "cache_step")
 
 
 def __getattr__(name):

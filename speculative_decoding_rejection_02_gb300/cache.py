@@ -7,7 +7,7 @@ is one call of the C ABI on torch tensors: argument checks here and in the
 library raise before anything is enqueued, outputs and workspace come from
 torch's allocator on the stream that the call runs on (``stream``, or the
 current one), and errors in device data set bits of ``status`` (an int32
-tensor of one element, OR-ed). There is no backward pass: a tensor that
+tensor of one element, OR-ed), or without one are kept for ``cache_status``. There is no backward pass: a tensor that
 requires a gradient is refused while gradients are enabled.
 
 The calls on tensors are ``csrc/cache_binding.cpp``; the structures of the C
@@ -159,3 +159,14 @@ def cache_attend(q, k_pages, v_pages, block_table, kv_lens, cu_q, *, max_q=None,
     if type(r) is int:
         raise _sv.SpecVerifyError(r, "spec_cache_attend")
     return r
+
+
+def cache_status(device=None) -> int:
+    """Wait for the device's work (the current device's) and return the status bits of the
+    cache's calls that came without ``status``, which are cleared."""
+    bits = C.c_uint(0)
+    with torch.cuda.device(device):
+        rc = _sv.lib().spec_cache_status(C.byref(bits))
+    if rc not in (_sv.SPEC_OK, -6):
+        raise _sv.SpecVerifyError(rc, "spec_cache_status")
+    return int(bits.value)

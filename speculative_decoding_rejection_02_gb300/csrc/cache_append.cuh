@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_cache_append(const AppendPar
     const long long t = t0 + threadIdx.x;
     long long slot = t < a.num_tokens ? a.slots[t] : -1;
     if (slot >= 0 && slot / a.page_size >= a.num_pages) {
-      if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_SLOT);
+      atomicOr(p.status, SPEC_CACHE_BAD_SLOT);
       slot = -1;
     }
     const long long page = slot / a.page_size, at = slot - page * a.page_size;

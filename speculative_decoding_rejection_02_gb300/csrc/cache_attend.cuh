@@ -106,7 +106,7 @@ struct AttendParams {
     // (the last key tiles' ends stay below 2^31)
     const bool bad_len = len < 0 || len > ((long long)width << page_shift) || len > 0x7fff0000;
     if (bad_rows || bad_len) {
-      if (status) atomicOr(status, SPEC_CACHE_BAD_LENGTHS);
+      atomicOr(status, SPEC_CACHE_BAD_LENGTHS);
       if (bad_rows) lo = hi = -1;
       len = 0;
     }
@@ -157,7 +157,7 @@ __device__ __forceinline__ bool att_wait(AttBase& sh, const AttendParams& p, uin
     if (mbar_poll(bar, parity & 1)) return true;
   } while (!*(volatile int*)&sh.stop && clock64() - from < kAttPatience);
   *(volatile int*)&sh.stop = 1;
-  if (p.status) atomicOr(p.status, SPEC_STATUS_TIMEOUT);
+  atomicOr(p.status, SPEC_STATUS_TIMEOUT);
   return false;
 }
 
@@ -269,7 +269,7 @@ __device__ __forceinline__ void att_load(AttShared<DP>& sh, const AttendParams& 
       if (i + 1 < g.n) number = page_of(place(i + 1));
       const bool live = this_page >= 0 && this_page < p.num_pages;
       if (__builtin_expect(!live && lane < boxes && j < g.hi && (j + box > g.lo || j < sinks), 0))
-        if (p.status) atomicOr(p.status, SPEC_CACHE_BAD_PAGE);
+        atomicOr(p.status, SPEC_CACHE_BAD_PAGE);
       const int count = __popc(__ballot_sync(~0u, live));
       const unsigned r = g.ring + (V ? att_v_at(g.pair, i, g.n) : att_k_at(g.pair, i));
       char* tile = kv_smem + (r % Cfg::kStages) * Cfg::kTileBytes;
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
     long long total = all;
     if (total > kAttMostPart * gridDim.x) {  // too much for one call: all rows see nothing
-      if (t == 0 && blockIdx.x == 0 && p.status) atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
+      if (t == 0 && blockIdx.x == 0) atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
       total = pad = 0;
     }
     const int blocks = (int)min((long long)gridDim.x, total);

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(THREADS) k_cache_step(const StepParams p) {
   const bool go = !bad && !dry;
   const unsigned first = blockIdx.x * THREADS + tid, step = gridDim.x * THREADS;
   if (first == 0) {
-    if (!go && p.status) atomicOr(p.status, bad ? SPEC_CACHE_BAD_LENGTHS : SPEC_CACHE_NO_PAGES);
+    if (!go) atomicOr(p.status, bad ? SPEC_CACHE_BAD_LENGTHS : SPEC_CACHE_NO_PAGES);
     *a.free_count_out = go ? (int)(count + total.gone - total.more) : count;
     a.cu_new[0] = 0;
   }

@@ -30,6 +30,28 @@ int sm_count() {
   return known[dev] > 0 ? known[dev] : 0;
 }
 
+// Status bits of calls that come without a word for them.
+__device__ unsigned g_status;
+
+// Where a call's status bits go on the current device; NULL: no such place.
+unsigned* status_word(unsigned* given) {
+  if (given) return given;
+  static std::atomic<unsigned*> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  unsigned* word = known[dev].load();
+  if (!word) {
+    if (cudaGetSymbolAddress((void**)&word, g_status) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    known[dev].store(word);
+  }
+  return word;
+}
+
+__global__ void k_clear_status(unsigned bits) { atomicAnd(&g_status, ~bits); }
+
 // Launch after the stream's earlier work, but with the launch itself prepared
 // while that work still runs (the kernels begin with pdl_wait).
 template <typename... A, typename... B>
@@ -229,7 +251,8 @@ int spec_cache_step(const spec_cache_step_args* a, void* stream, unsigned* devic
   if (!sms) return SPEC_ERR_UNSUPPORTED;
   sv::StepParams p;
   p.a = *a;
-  p.status = device_status;
+  p.status = status_word(device_status);
+  if (!p.status) return SPEC_ERR_CUDA;
   // for n < 2^31 and d < 2^31: floor(n / d) = n * (floor(2^(31 + s) / d) + 1) >> (31 + s),
   // s the bits of d - 1
   int bits = 0;
@@ -258,7 +281,8 @@ int spec_cache_append(const spec_cache_append_args* a, void* stream, unsigned* d
   if (a->num_tokens == 0) return SPEC_OK;
   sv::AppendParams p;
   p.a = *a;
-  p.status = device_status;
+  p.status = status_word(device_status);
+  if (!p.status) return SPEC_ERR_CUDA;
   long long* strides[] = {&p.a.k_token,  &p.a.k_head,  &p.a.v_token, &p.a.v_head,   &p.a.kp_page,
                           &p.a.kp_token, &p.a.kp_head, &p.a.vp_page, &p.a.vp_token, &p.a.vp_head};
   bool wide = a->dim % 8 == 0 && aligned(a->k, 16) && aligned(a->v, 16) &&
@@ -325,7 +349,8 @@ int spec_cache_attend(const spec_cache_attend_args* a, void* stream, unsigned* d
   p.window = a->window < (long long)a->width * a->page_size ? a->window : 0;
   p.sinks = a->sinks;
   p.tile_tokens = sv::kAttTile / p.G < a->max_q ? sv::kAttTile / p.G : a->max_q;
-  p.status = device_status;
+  p.status = status_word(device_status);
+  if (!p.status) return SPEC_ERR_CUDA;
   char* w = (char*)a->workspace;
   p.part_o = (float4*)w;
   p.part_ml = (float2*)(w + ws.ml);
@@ -345,6 +370,22 @@ int spec_cache_attend(const spec_cache_attend_args* a, void* stream, unsigned* d
   if (dim > 64)
     return bf16 ? attend<128, true>(p, sms, stream) : attend<128, false>(p, sms, stream);
   return bf16 ? attend<64, true>(p, sms, stream) : attend<64, false>(p, sms, stream);
+}
+
+int spec_cache_status(unsigned* bits) {
+  if (!bits) return SPEC_ERR_INVALID_ARG;
+  if (!sm_count()) return SPEC_ERR_UNSUPPORTED;
+  const unsigned* word = status_word(nullptr);
+  unsigned v = 0;
+  if (!word || cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (v) {  // (bits that another thread's call sets meanwhile stay)
+    k_clear_status<<<1, 1>>>(v);
+    if (cudaDeviceSynchronize() != cudaSuccess) return SPEC_ERR_CUDA;
+  }
+  *bits = v;
+  return v ? SPEC_ERR_DEVICE_STATUS : SPEC_OK;
 }
 
 }  // extern "C"
