@@ -11,8 +11,10 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -29,9 +31,13 @@ NVCC_FLAGS = [
 ]
 
 
-def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + glob.glob(os.path.join(CSRC, "*.cpp")) + HEADERS)
+def _newest(*patterns):
+    files = [f for p in patterns for f in glob.glob(os.path.join(CSRC, p))]
+    return max(os.path.getmtime(f) for f in files + HEADERS)
+
+
+def _stale(path, *patterns):
+    return not os.path.exists(path) or os.path.getmtime(path) < _newest(*patterns)
 
 
 def _nvcc():
@@ -41,9 +47,27 @@ def _nvcc():
     return "nvcc"
 
 
+def _torch_dir():
+    """Where torch is installed, without importing it; None where it is not."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def _binding_lacks():
+    """What the Python module cannot be built without, or None where all is there."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(torch_dir, "include", "ATen", "ATen.h")):
+        return "torch's headers are not installed"
+    if shutil.which("g++") is None:
+        return "there is no g++"
+    return None
+
+
 def _binding_command(out):
     """The host compiler's command for the Python module (torch's headers, no torch import)."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = _torch_dir()
     nvcc = _nvcc()
     cuda = os.path.dirname(os.path.dirname(nvcc)) if os.path.sep in nvcc else "/usr/local/cuda"
     dirs = [os.path.join(torch_dir, "include"),
@@ -56,29 +80,38 @@ def _binding_command(out):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile what is missing or older than its sources. The library needs nvcc alone: where
+    the Python module cannot be built (a warning says why) the cache's calls on tensors raise,
+    and all else works."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH):
-        newest = max(os.path.getmtime(s) for s in _sources())
-        if min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH)) >= newest:
-            return LIB_PATH
     tag = f".tmp{os.getpid()}"
-    objs = [os.path.join(LIB_DIR, u + tag + ".o") for u in UNITS]
     extra = ["-Xptxas=-v"] if verbose else []
-    units = [subprocess.Popen([_nvcc(), *NVCC_FLAGS, *extra, "-c", "-o", o,
-                               os.path.join(CSRC, u + ".cu")]) for u, o in zip(UNITS, objs)]
-    names = [u + ".cu" for u in UNITS] + ["cache_binding.cpp"]
-    units.append(subprocess.Popen(_binding_command(BINDING_PATH + tag)))
-    failed = [n for n, p in zip(names, units) if p.wait() != 0]  # every compiler is waited for
+    objs, jobs, binding = [], {}, None  # jobs: every compiler that was started, by source
+    if force or _stale(LIB_PATH, "*.cu", "*.cuh"):
+        objs = [os.path.join(LIB_DIR, u + tag + ".o") for u in UNITS]
+        for u, o in zip(UNITS, objs):
+            jobs[u + ".cu"] = subprocess.Popen([_nvcc(), *NVCC_FLAGS, *extra, "-c", "-o", o,
+                                                os.path.join(CSRC, u + ".cu")])
+    lacks = _binding_lacks()
+    if lacks:
+        warnings.warn(f"the paged cache's Python module is not built: {lacks}")
+    elif force or _stale(BINDING_PATH, "*.cpp"):
+        binding = BINDING_PATH + tag
+        jobs["cache_binding.cpp"] = subprocess.Popen(_binding_command(binding))
+    failed = [n for n, p in jobs.items() if p.wait() != 0]
     try:
-        if failed:
-            raise RuntimeError("the compiler failed on " + ", ".join(failed))
-        subprocess.run([_nvcc(), *NVCC_FLAGS, "-shared", "-o", LIB_PATH + tag, *objs], check=True)
+        if objs and not any(n.endswith(".cu") for n in failed):
+            subprocess.run([_nvcc(), *NVCC_FLAGS, "-shared", "-o", LIB_PATH + tag, *objs],
+                           check=True)
+            os.replace(LIB_PATH + tag, LIB_PATH)
+        if binding and "cache_binding.cpp" not in failed:
+            os.replace(binding, BINDING_PATH)
     finally:
-        for o in objs:
-            if os.path.exists(o):
-                os.remove(o)
-    os.replace(LIB_PATH + tag, LIB_PATH)
-    os.replace(BINDING_PATH + tag, BINDING_PATH)
+        for x in [*objs, binding, LIB_PATH + tag]:
+            if x and os.path.exists(x):
+                os.remove(x)
+    if failed:
+        raise RuntimeError("the compiler failed on " + ", ".join(failed))
     return LIB_PATH
 
 
