@@ -11,6 +11,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -51,6 +52,27 @@ def _torch_dir():
     """Where torch is installed, without importing it; None where it is not."""
     spec = importlib.util.find_spec("torch")
     return spec.submodule_search_locations[0] if spec else None
+
+
+def torch_version():
+    """Of the torch that is installed, without importing it where its version.py tells."""
+    path = os.path.join(_torch_dir(), "version.py")
+    if os.path.exists(path):
+        with open(path) as f:
+            found = re.search(r"""^__version__\s*=\s*['"](.+?)['"]""", f.read(), re.M)
+        if found:
+            return found.group(1)
+    import torch
+    return str(torch.__version__)
+
+
+def binding_torch():
+    """The torch version that the Python module was built for; None without a note of it."""
+    try:
+        with open(BINDING_PATH + ".torch") as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
 
 
 def _binding_lacks():
@@ -95,7 +117,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     lacks = _binding_lacks()
     if lacks:
         warnings.warn(f"the paged cache's Python module is not built: {lacks}")
-    elif force or _stale(BINDING_PATH, "*.cpp"):
+    elif force or _stale(BINDING_PATH, "*.cpp") or binding_torch() != torch_version():
         binding = BINDING_PATH + tag
         jobs["cache_binding.cpp"] = subprocess.Popen(_binding_command(binding))
     failed = [n for n, p in jobs.items() if p.wait() != 0]
@@ -106,6 +128,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             os.replace(LIB_PATH + tag, LIB_PATH)
         if binding and "cache_binding.cpp" not in failed:
             os.replace(binding, BINDING_PATH)
+            with open(binding, "w") as f:
+                f.write(torch_version())
+            os.replace(binding, BINDING_PATH + ".torch")
     finally:
         for x in [*objs, binding, LIB_PATH + tag]:
             if x and os.path.exists(x):

@@ -79,6 +79,10 @@ class _Native:
         if not os.path.exists(path):
             raise ImportError(f"the cache binding is not built ({path}); "
                               "run __graft_entry__.build()")
+        if _sv._build.binding_torch() != torch.__version__:  # its C++ interface differs
+            raise ImportError(f"the cache binding was built for torch "
+                              f"{_sv._build.binding_torch()}, not {torch.__version__}; "
+                              "run __graft_entry__.build()")
         loader = importlib.machinery.ExtensionFileLoader("_cache_binding", path)
         spec = importlib.util.spec_from_loader("_cache_binding", loader)
         module = importlib.util.module_from_spec(spec)

@@ -76,3 +76,33 @@ def test_failing_nvcc(place, monkeypatch):
         _build.build()
     assert not both()[0]
     assert not [f for f in os.listdir(_build.LIB_DIR) if ".tmp" in f]
+
+
+def rebuilt(path):
+    with open(path, "w") as f:
+        f.write("kept")
+    _build.build()
+    return open(path).read() == "built"
+
+
+def test_another_torch_rebuilds_the_module(place, monkeypatch):
+    _build.build()
+    assert not rebuilt(_build.BINDING_PATH)
+    monkeypatch.setattr(_build, "torch_version", lambda: "1.0+other")
+    assert rebuilt(_build.BINDING_PATH)
+    _build.build()
+    assert open(_build.LIB_PATH).read() == "built"
+
+
+def test_a_module_for_another_torch_is_not_loaded(place, monkeypatch):
+    import torch
+
+    import speculative_decoding_rejection_02_gb300 as sv
+    from speculative_decoding_rejection_02_gb300 import cache
+    assert _build.torch_version() == str(torch.__version__)
+    _build.build()
+    _build.build(force=True)
+    monkeypatch.setattr(torch, "__version__", "1.0+other")
+    monkeypatch.setattr(sv, "lib", lambda: None)
+    with pytest.raises(ImportError, match="1.0.other"):
+        cache._Native().step
