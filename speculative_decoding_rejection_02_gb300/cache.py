@@ -61,7 +61,8 @@ class AttendArgs(C.Structure):
 
 
 class CacheStep(NamedTuple):
-    """What ``cache_step`` computes, besides the block table and the stack."""
+    """What ``cache_step`` computes, besides the block table and the stack. ``positions`` and
+    ``slots`` share one storage, the other three another: clone what is to be saved alone."""
     lens: torch.Tensor        # int32 [B] tokens of each request
     cu_new: torch.Tensor      # int32 [B + 1] offsets of the new tokens
     positions: torch.Tensor   # int32 [num_tokens], -1 past the last new token
@@ -126,7 +127,7 @@ def cache_step(held_lens, new_lens, block_table, free_pages, free_count, *, page
                      num_tokens, cu_num_draft, num_accepted, status)
     if type(r) is int:
         raise _sv.SpecVerifyError(r, "spec_cache_step")
-    return CacheStep(*r)
+    return tuple.__new__(CacheStep, r)  # (as CacheStep(*r), without its Python)
 
 
 def cache_append(k, v, slots, k_pages, v_pages, *, status=None, stream=None) -> None:
