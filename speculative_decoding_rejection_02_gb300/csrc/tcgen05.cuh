@@ -31,11 +31,8 @@ __device__ __forceinline__ void tmem_fence_before() {
 __device__ __forceinline__ void tmem_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// The same, as the point where these registers get their values (the compiler
-// may move their uses up to the load otherwise).
+// Wait for this thread's TMEM loads, as the point where these 32 registers get
+// their values (the compiler may move their uses up to the load otherwise).
 __device__ __forceinline__ void tmem_wait_ld(float* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
@@ -92,7 +89,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const float* r) {
       "f"(r[29]), "f"(r[30]), "f"(r[31])
       : "memory");
 }
-// 16 columns, for O.
+// 16 columns, loaded and waited for.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -104,16 +101,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float* r) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const float* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
-      "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]),
-      "f"(r[15])
-      : "memory");
-}
-
 // Descriptor of an operand in shared memory in rows of 128 bytes with the
 // 128-byte swizzle (what a TMA load with that swizzle writes), 8 rows = 1024
 // bytes. Rows along the operand's M or N (K adjacent): groups of 8 rows are
