@@ -366,6 +366,7 @@ int spec_cache_attend(const spec_cache_attend_args* a, void* stream, unsigned* d
        !tensor_map(&p.v_map, a->dtype, a->v_pages, dim, a->page_size, a->vp_token, kv,
                    a->vp_head, a->num_pages, a->vp_page, box_page, 1)))
     return SPEC_ERR_CUDA;
+  if (a->B == 0) p.k_map = p.v_map = p.q_map;  // prefetched all the same, so they have to be maps
   const bool bf16 = a->dtype == SPEC_CACHE_BF16;
   if (dim > 64)
     return bf16 ? attend<128, true>(p, sms, stream) : attend<128, false>(p, sms, stream);
