@@ -15,8 +15,8 @@
 // or a chain through global memory between blocks. The sums saturate at
 // 2^32 - 1, which no valid call reaches.
 //
-// Latency bounds it: 3.0 us for 8 requests (one block), 6.8 us for 1024 with
-// 8192 token slots, 13.8 us for 6000 with 240000 (the search for each token's
+// Latency bounds it: 3.2 us for 8 requests (one block), 6.8 us for 1024 with
+// 8192 token slots, 15 us for 6000 with 240000 (the search for each token's
 // request, in the scan's prefix sums and then along a run of six).
 #pragma once
 #include <cuda_runtime.h>

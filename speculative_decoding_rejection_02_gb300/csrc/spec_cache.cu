@@ -233,8 +233,10 @@ int attend(const sv::AttendParams& p, int sms, void* stream) {
   const int run = p.B > sv::kAttScan ? (p.B + sv::kAttScan - 1) / sv::kAttScan : 1;
   const int rc = launch(sv::k_attend<DP, BF16>, dim3(sms), sv::kAttThreads, smem, stream, p, run);
   if (rc != SPEC_OK) return rc;
-  // join's columns over 8 blocks a unit, over 4 where a unit has few rows (64 requests of 1-6
-  // tokens in a window: 66.2 us a call against 68.0 with 8, 66.7 with 2 and 70.0 with one)
+  // join's columns over 8 blocks a unit, over 4 where units have up to 32 rows. Microseconds a
+  // call with 8 and with 4: 64 requests of 1-6 tokens in a window 68.2 and 66.5, 128 of one
+  // token 86.4 and 84.4, one of one token over 4097 15.3 and 15.6; and above 32 rows, 2 of 5
+  // tokens (35 rows) over 200000 76.8 and 79.0, 4 of 32 tokens (128 rows) 21.7 and 26.2.
   const int split = p.tile_tokens * p.G <= 32 ? 4 : 8;
   return launch(sv::k_attend_join<DP, BF16>, dim3(sms, split), sv::kJoinThreads, 0,
                 stream, p);
@@ -259,11 +261,12 @@ int spec_cache_step(const spec_cache_step_args* a, void* stream, unsigned* devic
   while ((1ll << bits) < a->page_size) ++bits;
   p.page_shift = 31 + bits;
   p.page_mul = (1ull << p.page_shift) / a->page_size + 1;
-  // Up to 1024 requests 256 threads scan them in runs of four at most and start sooner than
-  // 1024 (8 requests: 3.0 us against 5.7; 1024 with 8192 tokens: 5.2 against 7.0); with more
-  // the runs, which every search walks, get long (6000: 25.8 against 13.8).
+  // Up to 1792 requests 256 threads scan them, in runs of seven at most, and start sooner than
+  // 1024; with more the runs, which every search walks, get long. Microseconds with 256 and
+  // with 1024, eight tokens a request: 8 requests 3.2 and 5.9, 1024 6.8 and 8.0, 1536 8.9 and
+  // 9.6, 2000 11.2 and 10.3, 6000 25.9 and 17.5.
   const int items = a->num_tokens > a->B ? a->num_tokens : a->B;
-  const bool small = a->B <= 1024;
+  const bool small = a->B <= 1792;
   const int threads = small ? 256 : 1024;
   p.run = a->B > threads ? (a->B + threads - 1) / threads : 1;
   long long blocks = ((long long)items + threads - 1) / threads;

@@ -133,7 +133,7 @@ def test_round_in_a_graph(window, sinks):
     assert int(status) == 0
 
 
-@pytest.mark.parametrize("B,new_hi,page", [(300, 1400, 16), (1500, 260, 5)])
+@pytest.mark.parametrize("B,new_hi,page", [(300, 1400, 16), (1500, 260, 5), (2000, 200, 16)])
 def test_step_past_one_pass_of_its_grid(B, new_hi, page):
     """More token slots than the grid's threads (up to 152 x 1024), with pages taken and given
     back in numbers past them too."""
