@@ -279,7 +279,8 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
     out = x.tensor("out");
     check_rows("out", out, T, heads, dim, q.scalar_type());
   }
-  const bool return_lse = PyObject_IsTrue(*x.x++) == 1;
+  const int return_lse = PyObject_IsTrue(*x.x++);
+  if (return_lse < 0) throw python_error();
   unsigned* status = x.status();
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.dev);
   const long long need = g_workspace(&a);  // of the current device, now the tensors'
