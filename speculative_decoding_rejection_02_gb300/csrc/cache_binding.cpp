@@ -76,7 +76,9 @@ struct Args {
   unsigned* status() {
     if (none()) return ++x, nullptr;
     const Tensor& t = tensor("status");
-    TORCH_CHECK_VALUE(t.numel() == 1 && t.element_size() == 4, "status must be one 32-bit integer");
+    TORCH_CHECK_VALUE(t.numel() == 1 && (t.scalar_type() == at::kInt ||
+                                         t.scalar_type() == at::ScalarType::UInt32),
+                      "status must be one 32-bit integer, not ", t.scalar_type(), " ", t.sizes());
     return (unsigned*)t.data_ptr();
   }
 };
