@@ -33,14 +33,16 @@
 //
 // What bounds it, on one GB300 (6792 GB/s, 1876 TFLOP/s bf16 measured):
 //  - long contexts and few rows: HBM. 64 requests of 2-8 tokens over 1000-30000
-//    (heads of 128): 0.348 ms, 6.43 TB/s; 128 single tokens over 150-9000: 0.190 ms,
-//    5.99 TB/s, the rest a unit's start and results (about 4000 clocks each, partly
+//    (heads of 128): 0.346 ms, 6.48 TB/s; 128 single tokens over 150-9000: 0.188 ms,
+//    6.04 TB/s, the rest a unit's start and results (about 4000 clocks each, partly
 //    behind its successor's loads).
 //  - prompt chunks: the chain softmax -> PV -> QK of one stream against the other's.
 //    Two chunks of 2048 over 11000-14000: 0.58 ms (1560 TFLOP/s) in a short run, 0.66 ms
 //    (1370) when the clocks follow the power limit.
-//  - windows and small calls: the first tiles (about 11 us from launch to the first
-//    unit's result) and, in windows, the edge tiles.
+//  - small calls: the chain from launch to the first result and the join (one token over
+//    one cached token 12.1 us, over 4097 15.3).
+//  - windows: many short units, each with its start and its results (64 requests of 1-6
+//    tokens in a window of 1024: 66.5 us; over 1024 tokens without a window 61.5).
 // Code size counts: the warps' loops together overflow the instruction cache, and
 // rolling the softmax's, shortening the waits' and moving rare paths out of the way
 // took the chunks from 1.13 ms to 0.58.
