@@ -162,3 +162,21 @@ def test_lists_past_32_bits(L, q, length, kv_heads, tile_tokens, window, sinks):
         if k >= 0:
             assert L.list_before(length, q, 2 * tile_tokens, window, sinks, k) == want[k]
     check_walk(L, [3, q, 7], [2000, length, 9], kv_heads, tile_tokens, window, sinks)
+
+
+def test_longest_request(L):
+    """The most places that one request's lengths give: far from 64 bits."""
+    length, q, step = 2 ** 31 - 2 ** 16, 2 ** 22, 2
+    first = length - q + np.arange(q // step, dtype=np.int64) * step
+    tiles = (first + step - 1) // TILE + 1
+    want = int(tiles.sum()) + PAIR_COST * (q // step)
+    assert L.list_before(length, q, step, 0, 0, q // step) == want > 2 ** 45 - 2 ** 43
+    # units of two, as many as q can have: the formula stays exact
+    q = 2 ** 31 - 2 ** 17
+    n = q // step
+    at = length - q + step - 1  # of unit 0's last row; tiles (at + 2 u) / 128 + 1
+    total = sum((at % TILE + step * v) // TILE for v in range(TILE))
+    h = n // TILE
+    want = n * (at // TILE) + h * total + step * TILE * (h * (h - 1) // 2) + n * (1 + PAIR_COST)
+    assert n % TILE == 0
+    assert L.list_before(length, q, step, 0, 0, n) == want

@@ -43,3 +43,17 @@ def test_rows_of_no_request(offsets, spread):
             owned |= set(range(lo, hi))
     nobody = [t for t in range(T) if t not in owned]
     assert (got[nobody] == 0).all() and (lse[nobody] == -math.inf).all()
+
+
+def test_more_work_than_one_call_takes():
+    """2^22 tokens in units of two over 2^31 are 2^45 steps: no row sees anything, and the status
+    says so. (The pages are one page of 2^24 tokens over and over; none is read.)"""
+    T, page = 2 ** 22, 2 ** 24
+    pages = torch.zeros((1, page, 1, 8), dtype=BF, device=DEV)
+    q = torch.ones((T, 1, 8), dtype=BF, device=DEV)
+    out, status = torch.full_like(q, math.nan), status_word()
+    table = torch.zeros((1, 128), dtype=torch.int32, device=DEV)
+    got, lse = sv.cache_attend(q, pages, pages, table, ints([2 ** 31 - 2 ** 16]), ints([0, T]),
+                               max_q=1, out=out, return_lse=True, status=status)
+    assert int(status) == sv.CACHE_BAD_LENGTHS
+    assert (got == 0).all() and (lse == -math.inf).all()
