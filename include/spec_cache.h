@@ -167,9 +167,10 @@ long long spec_cache_attend_workspace(const spec_cache_attend_args* a);
  * window only those with p - j < window or j < sinks; query head h reads the
  * keys and values of head h / G:
  *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j e^(scale q . k_j).
- * A token that sees nothing (p < 0), and the rows that belong to no request
- * (past cu_q[B], before cu_q[0]), give out = 0 and lse = -inf. Scores, softmax statistics and sums are fp32; the softmax
- * weights are rounded to the cache's type before they meet the values.
+ * A token that sees nothing (p < 0), and the rows that belong to no request (past
+ * cu_q[B], before cu_q[0]), give out = 0 and lse = -inf. Scores, softmax
+ * statistics and sums are fp32; the softmax weights are rounded to the cache's
+ * type before they meet the values. out, lse and workspace overlap nothing else.
  * Whatever the memory of slots that no row of a request sees holds, NaN and
  * infinities too, does not reach the outputs (a value that some row sees and that
  * is not finite may make other rows of its request not finite). Pages that lie

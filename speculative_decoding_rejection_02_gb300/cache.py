@@ -4,12 +4,13 @@
 ``cache_step`` keeps block tables, free pages and slots between two rounds,
 ``cache_append`` writes new keys and values, ``cache_attend`` reads them. Each
 is one call of the C ABI on torch tensors: argument checks here and in the
-library raise before anything is enqueued, outputs and workspace come from
+library raise before anything is enqueued, and outputs and workspace come from
 torch's allocator on the stream that the call runs on (``stream``, or the
 current one; with ``stream`` the caller orders it after the inputs' stream and
-keeps the inputs until it is done, as for any work on another stream), and errors in device data set bits of ``status`` (an int32
-tensor of one element, OR-ed), or without one are kept for ``cache_status``. There is no backward pass: a tensor that
-requires a gradient is refused while gradients are enabled.
+keeps the inputs until it is done, as for any work on another stream). Errors
+in device data set bits of ``status`` (an int32 tensor of one element, OR-ed),
+or without one are kept for ``cache_status``. There is no backward pass: a
+tensor that requires a gradient is refused while gradients are enabled.
 
 The calls on tensors are ``csrc/cache_binding.cpp``; the structures of the C
 ABI are here for callers that come with addresses of their own.
