@@ -2,7 +2,8 @@
 
 Thin ``ctypes`` marshalling over ``libspecverify.so`` (declared in
 ``include/spec_verify.h``; the paged cache of ``include/spec_cache.h`` is
-bound in ``cache.py``). Every step of the verification runs in the
+bound in ``cache.py``, its sparse attention and eviction of
+``include/spec_sparse.h`` in ``sparse.py``). Every step of the verification runs in the
 library's CUDA kernels; PyTorch only supplies device memory and streams.
 There is no CPU fallback: if the library is missing or fails to load, every
 entry point raises.
@@ -55,6 +56,11 @@ _SHARD_CALLS = ENTRY_POINTS[-5:]
 # The entry points declared in include/spec_cache.h.
 CACHE_ENTRY_POINTS = ("spec_cache_step", "spec_cache_append", "spec_cache_attend_workspace",
                       "spec_cache_attend", "spec_cache_status")
+
+# The entry points declared in include/spec_sparse.h.
+SPARSE_ENTRY_POINTS = ("spec_cache_bounds", "spec_cache_score", "spec_cache_select",
+                       "spec_cache_attend_selected", "spec_cache_weigh",
+                       "spec_cache_evict_workspace", "spec_cache_evict")
 
 
 class SpecVerifyError(RuntimeError):
@@ -121,10 +127,11 @@ def lib():
             for name in _SHARD_CALLS:
                 getattr(L, name).argtypes = [C.c_void_p, C.POINTER(Batch), C.POINTER(Shard),
                                              C.c_void_p]
-            for name in CACHE_ENTRY_POINTS:
+            for name in CACHE_ENTRY_POINTS + SPARSE_ENTRY_POINTS:
                 getattr(L, name).argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
-            L.spec_cache_attend_workspace.argtypes = [C.c_void_p]
-            L.spec_cache_attend_workspace.restype = C.c_longlong
+            for name in ("spec_cache_attend_workspace", "spec_cache_evict_workspace"):
+                getattr(L, name).argtypes = [C.c_void_p]
+                getattr(L, name).restype = C.c_longlong
             L.spec_cache_status.argtypes = [C.POINTER(C.c_uint)]
             for name in ENTRY_POINTS:
                 getattr(L, name)  # raises if the library lacks a declared symbol
@@ -333,11 +340,22 @@ _CACHE_NAMES = ("CACHE_BAD_LENGTHS", "CACHE_BAD_PAGE", "CACHE_BAD_SLOT", "CACHE_
                 "cache_attend", "cache_status", "cache_step")
 
 
+_SPARSE_NAMES = ("AttendSelectedArgs", "BoundsArgs", "CACHE_BAD_SELECTION", "CacheEvict",
+                 "EvictArgs", "ScoreArgs", "SelectArgs", "WeighArgs", "cache_attend_selected",
+                 "cache_bounds", "cache_evict", "cache_score", "cache_select", "cache_weigh")
+
+
 def __getattr__(name):
-    """The paged cache's names, from cache.py (which imports torch) when first asked for."""
-    if name not in _CACHE_NAMES:
+    """The paged cache's names, from cache.py and sparse.py (which import torch) when first asked
+    for."""
+    if name in _CACHE_NAMES:
+        from . import cache as module
+        names = _CACHE_NAMES
+    elif name in _SPARSE_NAMES:
+        from . import sparse as module
+        names = _SPARSE_NAMES
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import cache
-    for n in _CACHE_NAMES:
-        globals()[n] = getattr(cache, n)
+    for n in names:
+        globals()[n] = getattr(module, n)
     return globals()[name]

@@ -1,8 +1,8 @@
 """Build of the verifier's CUDA library (nvcc, sm_103a only).
 
-``build()`` compiles ``csrc/spec_verify.cu`` (the verifier) and
-``csrc/spec_cache.cu`` (the paged cache), one translation unit each that
-includes its kernels, into ``_lib/libspecverify.so`` inside the package, and
+``build()`` compiles ``csrc/spec_verify.cu`` (the verifier),
+``csrc/spec_cache.cu`` (the paged cache) and ``csrc/spec_sparse.cu`` (its sparse
+attention and eviction), one translation unit each that includes its kernels, into ``_lib/libspecverify.so`` inside the package, and
 ``csrc/cache_binding.cpp`` (the paged cache's calls on torch tensors) into the
 Python module ``_lib/_cache_binding.so``.
 """
@@ -23,8 +23,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libspecverify.so")
 BINDING_PATH = os.path.join(LIB_DIR, "_cache_binding.so")
-HEADERS = [os.path.join(ROOT, "include", h) for h in ("spec_verify.h", "spec_cache.h")]
-UNITS = ("spec_verify", "spec_cache")
+HEADERS = [os.path.join(ROOT, "include", h)
+           for h in ("spec_verify.h", "spec_cache.h", "spec_sparse.h")]
+UNITS = ("spec_verify", "spec_cache", "spec_sparse")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -91,8 +91,11 @@ class _Native:
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
         module.bind(*(C.cast(getattr(lib, "spec_cache_" + n), C.c_void_p).value
-                      for n in ("step", "append", "attend", "attend_workspace")))
-        for n in ("step", "append", "attend"):
+                      for n in ("step", "append", "attend", "attend_workspace", "bounds", "score",
+                                "select", "attend_selected", "weigh", "evict",
+                                "evict_workspace")))
+        for n in ("step", "append", "attend", "bounds", "score", "select", "attend_selected",
+                  "weigh", "evict"):
             setattr(self, n, getattr(module, n))
         return object.__getattribute__(self, name)
 

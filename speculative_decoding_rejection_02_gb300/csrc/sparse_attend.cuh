@@ -1,0 +1,471 @@
+// Attention of new tokens over selected pages (spec_cache_attend_selected).
+//
+// The columns of a product are up to 8 tokens of one request times the query heads of one kv head
+// (32 at most), the keys of the pages that any of the tokens selected are gone through once, and a
+// byte for each page says which tokens see it:
+//
+//   S^T = K Q^T      16 keys x columns, on the warp's tensor cores, fp32
+//   P = 2^(c S - m)  running maximum m and sum l of each column in fp32, P rounded to the cache's
+//                    type: the products take 16-bit operands. l sums P unrounded. m follows a
+//                    higher maximum only when it has passed m by 2^8, as fp32 and the type allow
+//                    (fp16's P starts at 2^7)
+//   O^T += V^T P     dim x columns, fp32
+//
+// With c = scale * log2(e). Keys as the rows leave no tensor-core row empty however few columns
+// there are; P^T gets from a product's layout of sums to that of an operand by a transposition of
+// 8 x 8 values in registers.
+//
+// Each warp has its own ring of tiles of 16 keys and values, filled by 16-byte asynchronous
+// copies, and its own softmax statistics, and waits for no other warp until the end: a block's
+// warps, then a cluster's blocks through each other's shared memory, join their parts. Slots that
+// no token sees are not loaded; zeros stand in their place.
+//
+// Bound by HBM where the selections of a request's tokens agree, by the latency of the chain
+// (requests, list, pages, keys, join) in small calls.
+#pragma once
+#include "sparse_common.cuh"
+
+namespace sv {
+
+constexpr int kSelWarps = 4, kSelThreads = 32 * kSelWarps;
+constexpr int kSelStages = 3;
+constexpr int kSelList = 768;    // pages that a block lists at a time
+constexpr int kSelTokens = 8;    // bits of a page's byte
+
+struct SelectedParams {
+  Requests rq;
+  int heads, kv_heads, G, dim;
+  const char* q;
+  long long q_token, q_head;  // bytes
+  const char* k;
+  long long k_page, k_token, k_head;
+  const char* v;
+  long long v_page, v_token, v_head;
+  const int* selected;
+  int count;
+  char* out;
+  long long out_token, out_head;
+  float* lse;
+  float c;        // scale * log2(e)
+  int per;        // tokens of a unit
+  int unit_heads, splits;  // query heads of a unit, and units that share a kv head's
+  int cluster;    // blocks of a unit
+};
+
+template <int DP, int N8>
+struct SelCfg {
+  static constexpr int kTile = 16 * DP * 2;                       // bytes of 16 keys
+  static constexpr int kRing = kSelWarps * kSelStages * 2 * kTile;
+  static constexpr int kQ = N8 * (DP / 16) * 256;                 // [n8][step][lane] 8 bytes
+  static constexpr int kCols = 8 * N8;
+  static constexpr int kPitch = DP + 4;                           // floats of a column's partial O
+  static constexpr int kSmem = kRing + kQ + kSelList * 9;
+  static_assert((kSelWarps + 1) * kCols * (kPitch + 2) * 4 <= kRing, "partial results in the ring");
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <bool TRANS>
+__device__ __forceinline__ void load_matrix4(uint32_t* r, uint32_t at) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// 2^(a - b) for maxima a <= b, of which a may be -inf.
+__device__ __forceinline__ float weight_of(float a, float b) {
+  return a == -INFINITY ? 0.f : ex2(a - b);
+}
+
+template <bool BF16>
+__device__ constexpr float sel_bias() {  // log2 of what P and l carry beside 2^-m
+  return BF16 ? 0.f : 7.f;
+}
+
+struct SelList {
+  int* page;
+  int* col;
+  unsigned char* mask;
+};
+
+template <int DP, int N8, bool BF16>
+__global__ void __launch_bounds__(kSelThreads, 2)
+    k_attend_selected(const __grid_constant__ SelectedParams p) {
+  using Cfg = SelCfg<DP, N8>;
+  constexpr float kBias = sel_bias<BF16>();
+  constexpr int kLanes = DP / 8;        // lanes that copy a row's 16-byte pieces
+  constexpr int kRows = 32 / kLanes;    // rows of one copy instruction
+  extern __shared__ __align__(128) char smem[];
+  __shared__ GroupShared<kSelThreads> sh;
+  __shared__ int sums[kSelWarps], listed;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, x = lane >> 2, c = lane & 3;
+  const int rank = p.cluster > 1 ? blockIdx.x % p.cluster : 0;
+  long long unit = blockIdx.x / p.cluster;
+  const int split = (int)(unit % p.splits);
+  unit /= p.splits;
+  const int kv_head = (int)(unit % p.kv_heads);
+  unit /= p.kv_heads;
+  const TokenGroup g = find_group<kSelThreads>(p.rq, unit, p.per, sh);
+  if (g.b >= 0) {
+    char* ring = smem + warp * kSelStages * 2 * Cfg::kTile;
+    const uint32_t ring_at = smem_addr(ring);
+    uint2* q_frag = (uint2*)(smem + Cfg::kRing);
+    SelList list;
+    list.page = (int*)(smem + Cfg::kRing + Cfg::kQ);
+    list.col = list.page + kSelList;
+    list.mask = (unsigned char*)(list.col + kSelList);
+    const int shift = p.rq.page_shift, page_size = 1 << shift;
+    const int head0 = kv_head * p.G + split * p.unit_heads;
+    const int heads = min(p.unit_heads, p.G - split * p.unit_heads);
+    const int columns = g.tokens * heads;
+    const int steps = (p.dim + 15) / 16, pieces = p.dim / 8;
+    // Q as operands, from memory: two channels of one column at a time
+    for (int i = tid; i < N8 * (DP / 16) * 32; i += kSelThreads) {
+      const int n8 = i / ((DP / 16) * 32), step = i / 32 % (DP / 16);
+      const int column = n8 * 8 + (i >> 2 & 7), ch = step * 16 + 2 * (i & 3);
+      uint2 v = make_uint2(0, 0);
+      if (column < columns) {
+        const int tok = column / heads;
+        const char* src = p.q + (long long)(g.token + tok) * p.q_token +
+                          (long long)(head0 + column - tok * heads) * p.q_head + ch * 2;
+        if (ch < p.dim) v.x = *(const uint32_t*)src;
+        if (ch + 8 < p.dim) v.y = *(const uint32_t*)(src + 16);
+      }
+      q_frag[i] = v;
+    }
+    // the token of each of the lane's columns, 8 for none, four bits each
+    uint32_t token_of = 0;
+#pragma unroll
+    for (int y = 0; y < 2 * N8; ++y) {
+      const int column = (y >> 1) * 8 + 2 * c + (y & 1);
+      token_of |= (column < columns ? (uint32_t)(column / heads) : 8u) << (4 * y);
+    }
+    const uint32_t everyone = (1u << g.tokens) - 1;
+    const int last = g.pos + g.tokens - 1;                       // the last token's position
+    const int visible = last < 0 ? 0 : (last >> shift) + 1;      // columns it sees
+    const int* lists = p.selected + ((long long)g.token * p.kv_heads + kv_head) * p.count;
+    const long long next_list = (long long)p.kv_heads * p.count;
+
+    float m[N8][2], l[N8][2], o[DP / 16][N8][4];
+#pragma unroll
+    for (int n = 0; n < N8; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int y = 0; y < DP / 16; ++y) o[y][n][0] = o[y][n][1] = o[y][n][2] = o[y][n][3] = 0.f;
+    }
+    // Entry i of token k's list as a visible column, or -1. (Broken lists are told of once.)
+    auto entry = [&](int k, int i) {
+      const int* row = lists + k * next_list;
+      const int col = row[i], before = i > 0 ? row[i - 1] : -1;
+      if (col < 0) return -1;
+      if ((i > 0 && (before < 0 || before >= col)) ||
+          ((long long)col << shift) >= g.len) {
+        atomicOr(p.rq.status, SPEC_CACHE_BAD_SELECTION);
+        return -1;
+      }
+      return col < visible && ((long long)col << shift) <= g.pos + k ? col : -1;
+    };
+    const bool one = g.tokens == 1;
+    // One token's list is taken in parts of what the block lists at a time; of several tokens
+    // the host made sure that all their pages fit.
+    for (int part = 0; part < (one ? p.count : 1); part += kSelList) {
+      __syncthreads();  // (the list before has been used)
+      if (tid == 0) listed = 0;
+      __syncthreads();
+      if (one) {
+        int top = 0;
+        for (int i = tid; i < kSelList && part + i < p.count; i += kSelThreads) {
+          const int col = entry(0, part + i);
+          list.col[i] = col;
+          list.page[i] = col >= 0 ? p.rq.page(g.b, col) : -1;
+          list.mask[i] = col >= 0;
+          if (col >= 0) top = i + 1;
+        }
+        top = __reduce_max_sync(~0u, top);
+        if (lane == 0) atomicMax(&listed, top);
+      } else {
+        // a byte for each visible column, over the ring; then the bytes that are not 0 in order
+        uint32_t* bytes = (uint32_t*)smem;
+        const int words = (visible + 3) / 4, run = (words + kSelThreads - 1) / kSelThreads;
+        for (int i = tid; i < words; i += kSelThreads) bytes[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < g.tokens * p.count; i += kSelThreads) {
+          const int k = i / p.count, col = entry(k, i - k * p.count);
+          if (col >= 0) atomicOr(&bytes[col >> 2], 1u << (8 * (col & 3) + k));
+        }
+        __syncthreads();
+        const int w0 = min(tid * run, words), w1 = min(w0 + run, words);
+        int n = 0;
+        for (int i = w0; i < w1; ++i) n += __popc(__vcmpgtu4(bytes[i], 0)) / 8;
+        int all;
+        int at = block_before<kSelThreads>(n, sums, all);
+        for (int i = w0; i < w1; ++i)
+          for (uint32_t w = bytes[i], y = 0; w; w >>= 8, ++y)
+            if (w & 255) {
+              list.col[at] = 4 * i + y;
+              list.mask[at] = w & 255;
+              ++at;
+            }
+        __syncthreads();
+        for (int i = tid; i < all; i += kSelThreads) list.page[i] = p.rq.page(g.b, list.col[i]);
+        if (tid == 0) listed = all;
+      }
+      __syncthreads();
+      const int n = listed;
+      if (p.dim % 16) {  // channels that the products take beside those that there are
+        for (int i = lane; i < 2 * kSelStages * Cfg::kTile / 16; i += 32)
+          *(uint4*)(ring + 16 * i) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+      }
+      const int tiles = (int)(((long long)n * page_size + 15) / 16);
+      const int from = rank * kSelWarps + warp, step = p.cluster * kSelWarps;
+      uint32_t seen_by = 0;  // of key lane % 16 of the tiles in flight: bits of tokens, the
+                             // youngest tile's lowest
+      auto issue = [&](int tile, int stage) {
+        uint32_t mine = 0;
+        if (tile < tiles) {
+          const uint32_t dst = ring_at + stage * 2 * Cfg::kTile;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // 8 keys of one page
+            const long long key = 16ll * tile + 8 * half;
+            const int e = (int)(key >> shift), off = (int)key & (page_size - 1);
+            int page = -1, col = 0;
+            uint32_t mask = 0;
+            if (e < n) page = list.page[e], col = list.col[e], mask = list.mask[e];
+            if (page < 0) mask = 0;
+            const int ahead = (int)(((long long)col << shift) + off - g.pos);
+            // the tokens that see key r of the 8
+            auto see = [&](int r) {
+              const int z = ahead + r;
+              return z <= 0 ? mask : z >= kSelTokens ? 0u : mask & (everyone << z);
+            };
+            if ((lane >> 3 & 1) == half) mine = see(lane & 7);
+            const char* ks = p.k + page * p.k_page + off * p.k_token + kv_head * p.k_head;
+            const char* vs = p.v + page * p.v_page + off * p.v_token + kv_head * p.v_head;
+            const int piece = lane & (kLanes - 1);
+            if (piece < pieces) {
+#pragma unroll
+              for (int y = 0; y < 8 / kRows; ++y) {
+                const int r = y * kRows + lane / kLanes;
+                const bool there = see(r) != 0;
+                const uint32_t to = dst + (8 * half + r) * (DP * 2) + ((piece ^ r) & 7) * 16 +
+                                    (piece & 8) * 16;
+                copy16(to, there ? ks + r * p.k_token + piece * 16 : p.k, there);
+                copy16(to + Cfg::kTile, there ? vs + r * p.v_token + piece * 16 : p.v, there);
+              }
+            }
+          }
+        }
+        seen_by = seen_by << 8 | mine;
+        copy_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < kSelStages - 1; ++i) issue(from + i * step, i);
+      int stage = 0;
+#pragma unroll 1
+      for (int tile = from; tile < tiles; tile += step) {
+        copy_wait<kSelStages - 2>();
+        __syncwarp();
+        issue(tile + (kSelStages - 1) * step, stage == 0 ? kSelStages - 1 : stage - 1);
+        const uint32_t seen = seen_by >> (8 * (kSelStages - 1)) & 255;
+        const uint32_t k_at = ring_at + stage * 2 * Cfg::kTile, v_at = k_at + Cfg::kTile;
+        stage = stage == kSelStages - 1 ? 0 : stage + 1;
+        float s[N8][4];
+#pragma unroll
+        for (int n8 = 0; n8 < N8; ++n8) s[n8][0] = s[n8][1] = s[n8][2] = s[n8][3] = 0.f;
+#pragma unroll
+        for (int y = 0; y < DP / 16; ++y) {
+          if (y >= steps) break;
+          uint32_t a[4];
+          const int r = lane & 15, piece = 2 * y + (lane >> 4);
+          load_matrix4<false>(a, k_at + r * (DP * 2) + ((piece ^ r) & 7) * 16 + (piece & 8) * 16);
+#pragma unroll
+          for (int n8 = 0; n8 < N8; ++n8) {
+            const uint2 b = q_frag[(n8 * (DP / 16) + y) * 32 + lane];
+            mma_16816<BF16>(s[n8], a[0], a[1], a[2], a[3], b.x, b.y);
+          }
+        }
+#pragma unroll
+        for (int n8 = 0; n8 < N8; ++n8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[n8][y] *= p.c;
+        if (!__all_sync(~0u, seen == everyone)) {
+          const uint32_t k0 = __shfl_sync(~0u, seen, x), k1 = __shfl_sync(~0u, seen, x + 8);
+#pragma unroll
+          for (int n8 = 0; n8 < N8; ++n8)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t bit = token_of >> (4 * (2 * n8 + y)) & 15;
+              if (!(k0 >> bit & 1)) s[n8][y] = -INFINITY;
+              if (!(k1 >> bit & 1)) s[n8][y + 2] = -INFINITY;
+            }
+        }
+        bool grown = false;
+#pragma unroll
+        for (int n8 = 0; n8 < N8; ++n8)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) grown |= fmaxf(s[n8][y], s[n8][y + 2]) > m[n8][y] + 8.f;
+        if (__any_sync(~0u, grown)) {
+#pragma unroll
+          for (int n8 = 0; n8 < N8; ++n8)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float top = fmaxf(s[n8][y], s[n8][y + 2]);
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+              top = fmaxf(top, m[n8][y]);
+              const float keep = m[n8][y] == -INFINITY ? 0.f : ex2(m[n8][y] - top);
+              m[n8][y] = top;
+              l[n8][y] *= keep;
+#pragma unroll
+              for (int z = 0; z < DP / 16; ++z) o[z][n8][y] *= keep, o[z][n8][y + 2] *= keep;
+            }
+        }
+        uint32_t b[N8][2];
+#pragma unroll
+        for (int n8 = 0; n8 < N8; ++n8) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float base = kBias - (m[n8][y] == -INFINITY ? 0.f : m[n8][y]);
+            s[n8][y] = ex2(s[n8][y] + base);
+            s[n8][y + 2] = ex2(s[n8][y + 2] + base);
+            l[n8][y] += s[n8][y] + s[n8][y + 2];
+          }
+          b[n8][0] = transposed(pack_pair<BF16>(s[n8][0], s[n8][1]));
+          b[n8][1] = transposed(pack_pair<BF16>(s[n8][2], s[n8][3]));
+        }
+#pragma unroll
+        for (int y = 0; y < DP / 16; ++y) {
+          if (y >= steps) break;
+          uint32_t a[4];
+          const int r = (lane & 7) + (lane >> 4) * 8, piece = 2 * y + (lane >> 3 & 1);
+          load_matrix4<true>(a, v_at + r * (DP * 2) + ((piece ^ r) & 7) * 16 + (piece & 8) * 16);
+#pragma unroll
+          for (int n8 = 0; n8 < N8; ++n8)
+            mma_16816<BF16>(o[y][n8], a[0], a[1], a[2], a[3], b[n8][0], b[n8][1]);
+        }
+      }
+      copy_wait<0>();
+    }
+    // ---- join: the block's warps
+    __syncthreads();
+    float* part_o = (float*)smem;                                     // [warp][column][pitch]
+    float* all_o = part_o + kSelWarps * Cfg::kCols * Cfg::kPitch;     // the block's
+    float* part_m = all_o + Cfg::kCols * Cfg::kPitch;                 // [warp + 1][column]
+    float* part_l = part_m + (kSelWarps + 1) * Cfg::kCols;
+    float* all_m = part_m + kSelWarps * Cfg::kCols;
+    float* all_l = part_l + kSelWarps * Cfg::kCols;
+#pragma unroll
+    for (int n8 = 0; n8 < N8; ++n8)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float sum = l[n8][y];
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        const int column = n8 * 8 + 2 * c + y;
+        if (x == 0) {
+          part_m[warp * Cfg::kCols + column] = m[n8][y];
+          part_l[warp * Cfg::kCols + column] = sum;
+        }
+        float* to = part_o + (warp * Cfg::kCols + column) * Cfg::kPitch + x;
+#pragma unroll
+        for (int z = 0; z < DP / 16; ++z) {
+          to[16 * z] = o[z][n8][y];
+          to[16 * z + 8] = o[z][n8][y + 2];
+        }
+      }
+    __syncthreads();
+    const int pairs = p.dim / 2;
+    auto put = [&](int column, int d, float a, float b, float top, float sum) {
+      const int tok = column / heads;
+      const long long t = g.token + tok;
+      const int head = head0 + column - tok * heads;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      *(uint32_t*)(p.out + t * p.out_token + head * p.out_head + 4 * d) =
+          pack_pair<BF16>(a * inv, b * inv);
+      if (d == 0 && p.lse)
+        p.lse[t * p.heads + head] =
+            sum == 0.f ? -INFINITY : (top + log2f(sum) - kBias) * 0.69314718055994531f;
+    };
+    for (int i = tid; i < columns * pairs; i += kSelThreads) {
+      const int column = i / pairs, d = i - column * pairs;
+      float top = -INFINITY, sum = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSelWarps; ++w) top = fmaxf(top, part_m[w * Cfg::kCols + column]);
+#pragma unroll
+      for (int w = 0; w < kSelWarps; ++w) {
+        const float f = weight_of(part_m[w * Cfg::kCols + column], top);
+        const float2 y =
+            *(const float2*)(part_o + (w * Cfg::kCols + column) * Cfg::kPitch + 2 * d);
+        sum += f * part_l[w * Cfg::kCols + column];
+        a += f * y.x;
+        b += f * y.y;
+      }
+      if (p.cluster == 1) {
+        put(column, d, a, b, top, sum);
+      } else {
+        *(float2*)(all_o + column * Cfg::kPitch + 2 * d) = make_float2(a, b);
+        if (d == 0) all_m[column] = top, all_l[column] = sum;
+      }
+    }
+    // ---- the cluster's blocks, each a part of the results
+    if (p.cluster > 1) {
+      cluster_sync();
+      for (int i = tid + rank * kSelThreads; i < columns * pairs; i += p.cluster * kSelThreads) {
+        const int column = i / pairs, d = i - column * pairs;
+        float top = -INFINITY, sum = 0.f, a = 0.f, b = 0.f;
+        for (int w = 0; w < p.cluster; ++w) top = fmaxf(top, cluster_load(all_m + column, w));
+        for (int w = 0; w < p.cluster; ++w) {
+          const float f = weight_of(cluster_load(all_m + column, w), top);
+          sum += f * cluster_load(all_l + column, w);
+          a += f * cluster_load(all_o + column * Cfg::kPitch + 2 * d, w);
+          b += f * cluster_load(all_o + column * Cfg::kPitch + 2 * d + 1, w);
+        }
+        put(column, d, a, b, top, sum);
+      }
+      cluster_sync();
+    }
+  }
+  for_idle_rows<kSelThreads>(p.rq, g, [&](int t) {
+    const int pieces = p.dim / 8;
+    for (int i = tid; i < p.heads * pieces; i += kSelThreads)
+      *(uint4*)(p.out + t * p.out_token + (i / pieces) * p.out_head + (i % pieces) * 16) =
+          make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int i = tid; i < p.heads; i += kSelThreads) p.lse[(long long)t * p.heads + i] = -INFINITY;
+  });
+}
+
+}  // namespace sv

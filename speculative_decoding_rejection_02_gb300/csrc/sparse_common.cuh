@@ -1,0 +1,288 @@
+// What the kernels of sparse attention and eviction share: requests and groups of new
+// tokens, 16-bit products on the warp's tensor cores, the choice of the k largest values.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/spec_sparse.h"
+#include "pipe.cuh"
+
+namespace sv {
+
+struct Requests {
+  int B, T, width, page_shift;
+  long long table_stride, num_pages;
+  const int* table;
+  const int* kv_lens;
+  const int* cu_q;
+  unsigned* status;
+
+  // The length of request b; 0 with a status bit if it cannot be.
+  __device__ __forceinline__ int length(int b) const {
+    const int len = kv_lens[b];
+    if (len >= 0 && len <= ((long long)width << page_shift) && len <= 0x7fff0000) return len;
+    atomicOr(status, SPEC_CACHE_BAD_LENGTHS);
+    return 0;
+  }
+  // The new tokens of request b as rows [lo, hi), and its length. Offsets that cannot be give
+  // no rows (lo = hi = -1).
+  __device__ __forceinline__ int request(int b, int& lo, int& hi) const {
+    lo = cu_q[b];
+    hi = cu_q[b + 1];
+    if (lo < 0 || hi < lo || hi > T) {
+      atomicOr(status, SPEC_CACHE_BAD_LENGTHS);
+      lo = hi = -1;
+    }
+    return length(b);
+  }
+  // The page number in column c of request b; -1 with a status bit if it is none.
+  __device__ __forceinline__ int page(int b, int c) const {
+    const int x = table[b * table_stride + c];
+    if (x >= 0 && x < num_pages) return x;
+    atomicOr(status, SPEC_CACHE_BAD_PAGE);
+    return -1;
+  }
+};
+
+// Up to `per` new tokens of one request, in order: rows token .. token + tokens - 1, the first
+// at position pos. b < 0: none. `pad`: rows from there on belong to no request, nor do some
+// before it if `gaps`.
+struct TokenGroup {
+  int b, token, tokens, pos, len;
+  int pad, gaps;
+};
+
+template <int NT>
+struct GroupShared {
+  TokenGroup group;
+  long long sums[NT / 32];
+  int pad[NT / 32], gaps[NT / 32];
+};
+
+// Group number `unit` of all requests' groups of `per` tokens. By the whole block.
+template <int NT>
+__device__ __forceinline__ TokenGroup find_group(const Requests& p, long long unit, int per,
+                                                 GroupShared<NT>& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (p.B + NT - 1) / NT, r0 = min((long long)tid * run, (long long)p.B);
+  const int r1 = min(r0 + run, p.B);
+  long long mine = 0;
+  int pad = 0, gaps = 0, lo = 0, hi = 0;
+  auto groups_of = [&](int r) {
+    lo = p.cu_q[r];
+    hi = p.cu_q[r + 1];
+    if (lo < 0 || hi < lo || hi > p.T) {
+      atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
+      lo = hi = -1;
+    }
+    return (hi - lo + per - 1) / per;
+  };
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    mine += groups_of(r);
+    pad = max(pad, hi);
+    gaps |= lo < 0 || (r == 0 && lo > 0);
+  }
+  long long upto = mine;
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += x;
+  }
+  pad = __reduce_max_sync(~0u, pad);
+  gaps = __any_sync(~0u, gaps);
+  if (lane == 31) sh.sums[warp] = upto;
+  if (lane == 0) sh.pad[warp] = pad, sh.gaps[warp] = gaps;
+  if (tid == 0) sh.group.b = -1;
+  __syncthreads();
+  long long before = upto - mine;
+  for (int w = 0; w < warp; ++w) before += sh.sums[w];
+  if (before <= unit && unit < before + mine) {
+    long long at = before;
+    int r = r0;
+    if (run > 1)
+      for (;; ++r) {
+        const int n = groups_of(r);
+        if (unit < at + n || r + 1 >= r1) break;
+        at += n;
+      }
+    const int skip = (int)(unit - at) * per, len = p.length(r);
+    TokenGroup g;
+    g.b = r;
+    g.token = lo + skip;
+    g.tokens = min(per, hi - lo - skip);
+    g.pos = len - (hi - lo) + skip;
+    g.len = len;
+    if (len == 0) g.pos = -(1 << 30);  // sees nothing
+    sh.group = g;
+  }
+  __syncthreads();
+  TokenGroup g = sh.group;
+  g.pad = 0;
+  g.gaps = 0;
+  for (int w = 0; w < NT / 32; ++w) g.pad = max(g.pad, sh.pad[w]), g.gaps |= sh.gaps[w];
+  __syncthreads();
+  return g;
+}
+
+// f(t) for every row t that belongs to no request, spread over the blocks. By whole blocks.
+template <int NT, typename F>
+__device__ __forceinline__ void for_idle_rows(const Requests& p, const TokenGroup& g, F f) {
+#pragma unroll 1
+  for (long long t = (g.gaps ? 0 : g.pad) + blockIdx.x; t < p.T; t += gridDim.x) {
+    if (t < g.pad) {
+      bool mine = false;
+#pragma unroll 1
+      for (int b = threadIdx.x; b < p.B; b += NT) {
+        const int lo = p.cu_q[b], hi = p.cu_q[b + 1];
+        mine |= lo >= 0 && lo <= t && t < hi && hi <= p.T;
+      }
+      if (__syncthreads_or(mine)) continue;
+    }
+    f((int)t);
+  }
+}
+
+// D += A B on 16 x 8 x 16 of 16-bit values with fp32 sums. Lane 4 x + c of the warp holds rows x
+// and x + 8 of A and D and column x of B: of A the columns 2c, 2c + 1 (a0, a1) and 2c + 8, 2c + 9
+// (a2, a3), of B those rows (b0 and b1), of D columns 2c and 2c + 1 of row x, then of row x + 8.
+// These tensor-core instructions of the warp have a fraction of tcgen05's rate, but need neither
+// 64 rows nor TMEM: the calls here have 8 to 32 rows against keys that come once from memory,
+// and wait for those.
+template <bool BF16>
+__device__ __forceinline__ void mma_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack_pair(uint32_t v) {
+  if (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// ---- the k largest of many values, of equal ones the first
+
+// Whole numbers in the order of the values: NaN as +inf, -0 as 0.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) v = INFINITY;
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
+}
+
+template <int NT>
+struct PickShared {
+  int hist[2048];
+  int sums[NT / 32], sums2[NT / 32];
+  int bin, rest;
+};
+
+// Sum of v over the threads before this one, and over all.
+template <int NT>
+__device__ __forceinline__ int block_before(int v, int* sums, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int upto = v;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += x;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int before = upto - v;
+  all = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  __syncthreads();
+  return before;
+}
+
+// With keys key(0) .. key(m - 1) and 0 < k < m: the key `cut` of which fewer than k keys are
+// greater and at least k greater or equal; returns how many of those equal to it are among the
+// k largest. Three histograms of 11, 11 and 10 bits. By the whole block.
+template <int NT, typename F>
+__device__ __forceinline__ int pick_cut(F key, int m, int k, PickShared<NT>& sh, uint32_t& cut) {
+  constexpr int kRun = 2048 / NT;  // bins of a thread, from the top
+  uint32_t prefix = 0, mask = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    for (int i = threadIdx.x; i < 2048; i += NT) sh.hist[i] = 0;
+    __syncthreads();
+    for (int j = threadIdx.x; j < m; j += NT) {
+      const uint32_t x = key(j);
+      if ((x & mask) == prefix) atomicAdd(&sh.hist[x >> shift & (bins - 1)], 1);
+    }
+    __syncthreads();
+    int mine = 0, all;
+    const int top = 2047 - threadIdx.x * kRun;
+    for (int i = 0; i < kRun; ++i) mine += sh.hist[top - i];
+    const int before = block_before<NT>(mine, sh.sums, all);
+    if (before < k && k <= before + mine) {
+      int left = k - before, i = 0;
+      while (left > sh.hist[top - i]) left -= sh.hist[top - i++];
+      sh.bin = top - i;
+      sh.rest = left;
+    }
+    __syncthreads();
+    prefix |= (uint32_t)sh.bin << shift;
+    mask |= (uint32_t)(bins - 1) << shift;
+    k = sh.rest;
+    __syncthreads();
+  }
+  cut = prefix;
+  return k;
+}
+
+// Goes over items 0 .. n - 1 in words of 32: kind(j) says whether item j is taken (2), one of
+// equals (1), of which the first `equals` are taken, or not (0). put(w, taken, before) gets word
+// w's bits of taken items and the number of items taken before it. By the whole block.
+template <int NT, typename K, typename P>
+__device__ __forceinline__ void pick_words(K kind, int n, int equals, PickShared<NT>& sh, P put) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int ties_before = 0, taken_before = 0;
+#pragma unroll 1
+  for (int base = 0; base < n; base += NT * 32) {
+    uint32_t sure = 0, ties = 0;
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) {
+      const int j0 = base + (warp * 32 + i) * 32;
+      if (j0 >= n) break;
+      const int x = j0 + lane < n ? kind(j0 + lane) : 0;
+      const uint32_t a = __ballot_sync(~0u, x == 2), b = __ballot_sync(~0u, x == 1);
+      if (lane == i) sure = a, ties = b;
+    }
+    int all;
+    const int before = ties_before + block_before<NT>(__popc(ties), sh.sums, all);
+    ties_before += all;
+    for (int x = __popc(ties); x > 0 && before + x > equals; --x)
+      ties &= ~(1u << (31 - __clz(ties)));
+    const uint32_t taken = sure | ties;
+    const int at = taken_before + block_before<NT>(__popc(taken), sh.sums2, all);
+    taken_before += all;
+    put(base / 32 + (int)threadIdx.x, taken, at);
+  }
+}
+
+}  // namespace sv

@@ -10,28 +10,18 @@
 #include "../../include/spec_cache.h"
 #include "cache_append.cuh"
 #include "cache_attend.cuh"
+#include "cache_host.cuh"
 #include "cache_step.cuh"
 
+namespace sv {
 namespace {
-
-// The multiprocessors of the current device; 0 if it is not an sm_103.
-int sm_count() {
-  static int known[64];  // 0: not asked yet, -1: not an sm_103
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (known[dev] == 0) {
-    int major = 0, minor = 0, sms = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return 0;
-    known[dev] = major == 10 && minor == 3 ? sms : -1;
-  }
-  return known[dev] > 0 ? known[dev] : 0;
-}
 
 // Status bits of calls that come without a word for them.
 __device__ unsigned g_status;
+
+__global__ void k_clear_status(unsigned bits) { atomicAnd(&g_status, ~bits); }
+
+}  // namespace
 
 // Where a call's status bits go on the current device; NULL: no such place.
 unsigned* status_word(unsigned* given) {
@@ -50,30 +40,15 @@ unsigned* status_word(unsigned* given) {
   return word;
 }
 
-__global__ void k_clear_status(unsigned bits) { atomicAnd(&g_status, ~bits); }
+}  // namespace sv
 
-// Launch after the stream's earlier work, but with the launch itself prepared
-// while that work still runs (the kernels begin with pdl_wait).
-template <typename... A, typename... B>
-int launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, void* stream,
-           const B&... args) {
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return SPEC_OK;
-  cudaGetLastError();
-  return SPEC_ERR_CUDA;
-}
+namespace {
 
-bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+using sv::aligned;
+using sv::k_clear_status;
+using sv::launch;
+using sv::sm_count;
+using sv::status_word;
 
 // Whether what the call writes overlaps anything else of its arguments.
 bool step_overlaps(const spec_cache_step_args* a) {

@@ -1,0 +1,551 @@
+// C ABI of sparse attention and eviction on the paged cache (declared in
+// include/spec_sparse.h): host-side argument checks and launches.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/spec_sparse.h"
+#include "cache_host.cuh"
+#include "evict_drop.cuh"
+#include "evict_weigh.cuh"
+#include "sparse_attend.cuh"
+#include "sparse_bounds.cuh"
+#include "sparse_score.cuh"
+#include "sparse_select.cuh"
+
+namespace {
+
+using sv::aligned;
+using sv::launch;
+using sv::launch_cluster;
+using sv::sm_count;
+using sv::status_word;
+
+struct Axis {
+  long long extent, stride;  // elements
+};
+
+// What an array of `element` bytes takes up; stride 1 inside.
+struct Span {
+  const void* at;
+  long long bytes;
+};
+template <int N>
+Span span(const void* at, int element, long long inner, const Axis (&axes)[N]) {
+  long long last = inner - 1;
+  for (auto& x : axes) {
+    if (x.extent < 1) return {at, 0};
+    last += (x.extent - 1) * x.stride;
+  }
+  return {at, (last + 1) * element};
+}
+Span span(const void* at, long long bytes) { return {at, bytes}; }
+bool meet(const Span& a, const Span& b) {
+  const unsigned long long p = (uintptr_t)a.at, q = (uintptr_t)b.at;
+  return p && q && a.bytes > 0 && b.bytes > 0 && p < q + b.bytes && q < p + a.bytes;
+}
+// Whether one of the first `written` spans overlaps another one.
+template <int N>
+bool overlap(const Span (&x)[N], int written) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < N; ++j)
+      if (meet(x[i], x[j])) return true;
+  return false;
+}
+
+// Strides that 16-byte accesses of 16-bit elements can take, where they are used at all.
+template <int N>
+bool wide(const void* base, const Axis (&axes)[N]) {
+  if (!base || !aligned(base, 16)) return false;
+  for (auto& x : axes)
+    if (x.extent > 1 && (x.stride <= 0 || x.stride % 8 || x.stride >= 1ll << 38)) return false;
+  return true;
+}
+template <int N>
+bool words(const void* base, const Axis (&axes)[N]) {
+  if (!base || !aligned(base, 4)) return false;
+  for (auto& x : axes)
+    if (x.extent > 1 && (x.stride <= 0 || x.stride >= 1ll << 38)) return false;
+  return true;
+}
+
+// The sizes that all calls on pages have.
+int check_sizes(int B, int width, int kv_heads, int dim, int page_size, long long num_pages,
+                int dtype) {
+  if (B < 0 || width < 1 || kv_heads < 1 || dim < 1 || page_size < 1 || num_pages < 1)
+    return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_CACHE_BF16 && dtype != SPEC_CACHE_F16) return SPEC_ERR_INVALID_ARG;
+  if (dim % 8 || dim > 128 || page_size < 8 || (page_size & (page_size - 1)) ||
+      page_size > 1 << 24 || num_pages > 0x7fffffffll || kv_heads > 1 << 16)
+    return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+int check_heads(int heads, int kv_heads, int T, int max_q) {
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads || T < 0 || max_q < 1)
+    return SPEC_ERR_INVALID_ARG;
+  return heads / kv_heads > 128 ? SPEC_ERR_UNSUPPORTED : SPEC_OK;
+}
+
+int page_shift(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
+sv::Requests requests(int B, int T, int width, int page_size, long long table_stride,
+                      long long num_pages, const int* table, const int* lens, const int* cu_q,
+                      unsigned* status) {
+  sv::Requests r;
+  r.B = B;
+  r.T = T;
+  r.width = width;
+  r.page_shift = page_shift(page_size);
+  r.table_stride = table_stride;
+  r.num_pages = num_pages;
+  r.table = table;
+  r.kv_lens = lens;
+  r.cu_q = cu_q;
+  r.status = status;
+  return r;
+}
+
+// The blocks of a grid as the launch takes them, or 0.
+unsigned blocks(long long n) { return n > 0 && n <= 0x7fffffffll ? (unsigned)n : 0; }
+
+// Groups of `per` tokens that the requests may have.
+long long groups(int T, int B, int per) {
+  const long long n = (long long)T / per + B;
+  return n < T ? n : T;
+}
+
+// Lets a kernel have more than 48 KB of shared memory, once for each device.
+template <typename K>
+int allow(K kernel, int smem, std::atomic<unsigned long long>& ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return SPEC_ERR_CUDA;
+  if (ready.load() >> dev & 1) return SPEC_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return SPEC_ERR_CUDA;
+  }
+  ready.fetch_or(1ull << dev);
+  return SPEC_OK;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+int check_bounds(const spec_cache_bounds_args* a) {
+  if (!a || a->max_q < 1) return SPEC_ERR_INVALID_ARG;
+  const int rc = check_sizes(a->B, a->width, a->kv_heads, a->dim, a->page_size, a->num_pages,
+                             a->dtype);
+  if (rc != SPEC_OK || a->B == 0) return rc;
+  if (!a->block_table || !a->kv_lens || a->table_stride < a->width) return SPEC_ERR_INVALID_ARG;
+  const Axis k[] = {{a->num_pages, a->kp_page}, {a->page_size, a->kp_token},
+                    {a->kv_heads, a->kp_head}};
+  const Axis b[] = {{a->num_pages, a->b_page}, {a->kv_heads, a->b_head}, {2, a->b_side}};
+  if (!wide(a->k_pages, k) || !wide(a->bounds, b)) return SPEC_ERR_INVALID_ARG;
+  const Span x[] = {span(a->bounds, 2, a->dim, b), span(a->k_pages, 2, a->dim, k),
+                    span(a->block_table, 4 * ((a->B - 1) * a->table_stride + a->width)),
+                    span(a->kv_lens, 4ll * a->B), span(a->cu_q, 4ll * (a->B + 1))};
+  return overlap(x, 1) ? SPEC_ERR_INVALID_ARG : SPEC_OK;
+}
+
+int check_score(const spec_cache_score_args* a) {
+  if (!a) return SPEC_ERR_INVALID_ARG;
+  int rc = check_sizes(a->B, a->width, a->kv_heads, a->dim, a->page_size, a->num_pages, a->dtype);
+  if (rc == SPEC_OK) rc = check_heads(a->heads, a->kv_heads, a->num_tokens, a->max_q);
+  if (rc != SPEC_OK || a->num_tokens == 0) return rc;
+  const Axis q[] = {{a->num_tokens, a->q_token}, {a->heads, a->q_head}};
+  const Axis b[] = {{a->num_pages, a->b_page}, {a->kv_heads, a->b_head}, {2, a->b_side}};
+  const Axis s[] = {{a->num_tokens, a->s_token}, {a->kv_heads, a->s_head}};
+  if (!wide(a->q, q) || !words(a->scores, s) || !a->cu_q) return SPEC_ERR_INVALID_ARG;
+  if (a->B > 0 && (!wide(a->bounds, b) || !a->block_table || !a->kv_lens ||
+                   a->table_stride < a->width))
+    return SPEC_ERR_INVALID_ARG;
+  const Span x[] = {span(a->scores, 4, a->width, s), span(a->q, 2, a->dim, q),
+                    span(a->bounds, 2, a->dim, b),
+                    span(a->block_table, 4 * ((a->B - 1) * a->table_stride + a->width)),
+                    span(a->kv_lens, 4ll * a->B), span(a->cu_q, 4ll * (a->B + 1))};
+  return overlap(x, 1) ? SPEC_ERR_INVALID_ARG : SPEC_OK;
+}
+
+int check_select(const spec_cache_select_args* a) {
+  if (!a || a->count < 1 || a->first < 0 || a->recent < 0 ||
+      (long long)a->first + a->recent > a->count)
+    return SPEC_ERR_INVALID_ARG;
+  int rc = check_sizes(a->B, a->width, a->kv_heads, 8, a->page_size, 1, SPEC_CACHE_BF16);
+  if (rc == SPEC_OK) rc = check_heads(a->kv_heads, a->kv_heads, a->num_tokens, 1);
+  if (rc != SPEC_OK || a->num_tokens == 0) return rc;
+  const Axis s[] = {{a->num_tokens, a->s_token}, {a->kv_heads, a->s_head}};
+  if (!words(a->scores, s) || !a->selected || !a->cu_q || (a->B > 0 && !a->kv_lens))
+    return SPEC_ERR_INVALID_ARG;
+  const Span x[] = {span(a->selected, 4ll * a->num_tokens * a->kv_heads * a->count),
+                    span(a->scores, 4, a->width, s), span(a->kv_lens, 4ll * a->B),
+                    span(a->cu_q, 4ll * (a->B + 1))};
+  return overlap(x, 1) ? SPEC_ERR_INVALID_ARG : SPEC_OK;
+}
+
+int check_selected(const spec_cache_attend_selected_args* a) {
+  if (!a || a->count < 1) return SPEC_ERR_INVALID_ARG;
+  int rc = check_sizes(a->B, a->width, a->kv_heads, a->dim, a->page_size, a->num_pages, a->dtype);
+  if (rc == SPEC_OK) rc = check_heads(a->heads, a->kv_heads, a->num_tokens, 1);
+  if (rc != SPEC_OK || a->num_tokens == 0) return rc;
+  if (!std::isfinite(a->scale * kLog2e)) return SPEC_ERR_INVALID_ARG;
+  const Axis q[] = {{a->num_tokens, a->q_token}, {a->heads, a->q_head}};
+  const Axis o[] = {{a->num_tokens, a->out_token}, {a->heads, a->out_head}};
+  const Axis k[] = {{a->num_pages, a->kp_page}, {a->page_size, a->kp_token},
+                    {a->kv_heads, a->kp_head}};
+  const Axis v[] = {{a->num_pages, a->vp_page}, {a->page_size, a->vp_token},
+                    {a->kv_heads, a->vp_head}};
+  if (!wide(a->q, q) || !wide(a->out, o) || !a->cu_q) return SPEC_ERR_INVALID_ARG;
+  if (a->B > 0 && (!wide(a->k_pages, k) || !wide(a->v_pages, v) || !a->block_table ||
+                   !a->kv_lens || !a->selected || a->table_stride < a->width))
+    return SPEC_ERR_INVALID_ARG;
+  const Span x[] = {span(a->out, 2, a->dim, o),
+                    span(a->lse, 4ll * a->num_tokens * a->heads),
+                    span(a->q, 2, a->dim, q),
+                    span(a->k_pages, 2, a->dim, k),
+                    span(a->v_pages, 2, a->dim, v),
+                    span(a->block_table, 4 * ((a->B - 1) * a->table_stride + a->width)),
+                    span(a->selected, 4ll * a->num_tokens * a->kv_heads * a->count),
+                    span(a->kv_lens, 4ll * a->B),
+                    span(a->cu_q, 4ll * (a->B + 1))};
+  return overlap(x, 2) ? SPEC_ERR_INVALID_ARG : SPEC_OK;
+}
+
+int check_weigh(const spec_cache_weigh_args* a) {
+  if (!a) return SPEC_ERR_INVALID_ARG;
+  int rc = check_sizes(a->B, a->width, a->kv_heads, a->dim, a->page_size, a->num_pages, a->dtype);
+  if (rc == SPEC_OK) rc = check_heads(a->heads, a->kv_heads, a->num_tokens, a->max_q);
+  if (rc != SPEC_OK || a->num_tokens == 0 || a->B == 0) return rc;
+  if (!std::isfinite(a->scale * kLog2e) || !std::isfinite(a->decay)) return SPEC_ERR_INVALID_ARG;
+  if ((long long)a->num_tokens * a->heads > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+  const Axis q[] = {{a->num_tokens, a->q_token}, {a->heads, a->q_head}};
+  const Axis k[] = {{a->num_pages, a->kp_page}, {a->page_size, a->kp_token},
+                    {a->kv_heads, a->kp_head}};
+  const Axis w[] = {{a->num_pages, a->w_page}, {a->kv_heads, a->w_head}};
+  if (!wide(a->q, q) || !wide(a->k_pages, k) || !words(a->weights, w) || !a->lse ||
+      !aligned(a->lse, 4) || !a->block_table || !a->kv_lens || !a->cu_q ||
+      a->table_stride < a->width)
+    return SPEC_ERR_INVALID_ARG;
+  const Span x[] = {span(a->weights, 4, a->page_size, w),
+                    span(a->q, 2, a->dim, q),
+                    span(a->k_pages, 2, a->dim, k),
+                    span(a->lse, 4ll * a->num_tokens * a->heads),
+                    span(a->block_table, 4 * ((a->B - 1) * a->table_stride + a->width)),
+                    span(a->kv_lens, 4ll * a->B),
+                    span(a->cu_q, 4ll * (a->B + 1))};
+  return overlap(x, 1) ? SPEC_ERR_INVALID_ARG : SPEC_OK;
+}
+
+int check_evict(const spec_cache_evict_args* a, bool pointers) {
+  if (!a || a->first < 0 || a->recent < 0) return SPEC_ERR_INVALID_ARG;
+  const int rc = check_sizes(a->B, a->width, a->kv_heads, a->dim, a->page_size, a->num_pages,
+                             a->dtype);
+  if (rc != SPEC_OK || !pointers) return rc;
+  if (!a->free_count || !a->free_count_out) return SPEC_ERR_INVALID_ARG;
+  if (a->B == 0)
+    return a->free_count == a->free_count_out ? SPEC_ERR_INVALID_ARG : SPEC_OK;
+  const Axis k[] = {{a->num_pages, a->kp_page}, {a->page_size, a->kp_token},
+                    {a->kv_heads, a->kp_head}};
+  const Axis v[] = {{a->num_pages, a->vp_page}, {a->page_size, a->vp_token},
+                    {a->kv_heads, a->vp_head}};
+  const Axis w[] = {{a->num_pages, a->w_page}, {a->kv_heads, a->w_head}};
+  if (!wide(a->k_pages, k) || !wide(a->v_pages, v) || !words(a->weights, w) || !a->block_table ||
+      !a->lens || !a->budget || !a->free_pages || !a->lens_out || a->table_stride < a->width)
+    return SPEC_ERR_INVALID_ARG;
+  if (a->k_pages == a->v_pages) return SPEC_ERR_INVALID_ARG;
+  // (keys and values may be laid out between one another, so only the others are held apart)
+  const Span ks = span(a->k_pages, 2, a->dim, k), vs = span(a->v_pages, 2, a->dim, v);
+  const Span x[] = {span(a->weights, 4, a->page_size, w),
+                    span(a->free_pages, 4ll * a->num_pages),
+                    span(a->lens_out, 4ll * a->B),
+                    span(a->free_count_out, 4),
+                    span(a->workspace, (long long)a->workspace_bytes),
+                    span(a->block_table, 4 * ((a->B - 1) * a->table_stride + a->width)),
+                    span(a->lens, 4ll * a->B),
+                    span(a->budget, 4ll * a->B),
+                    span(a->free_count, 4)};
+  if (overlap(x, 5)) return SPEC_ERR_INVALID_ARG;
+  for (auto& y : x)
+    if (meet(y, ks) || meet(y, vs)) return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+// Workspace of spec_cache_evict: where each request's and head's moves begin, then where the
+// moved tokens come from, for all pages of the pool or all columns of the table.
+struct EvictSpace {
+  bool by_page;
+  size_t from, bytes;
+};
+EvictSpace evict_space(const spec_cache_evict_args* a) {
+  EvictSpace s;
+  const long long columns = (long long)a->B * a->width;
+  s.by_page = a->num_pages < columns;
+  s.from = ((size_t)a->B * a->kv_heads * 4 + 255) / 256 * 256;
+  s.bytes = s.from + (size_t)(s.by_page ? a->num_pages : columns) * a->kv_heads * a->page_size * 4;
+  return s;
+}
+
+template <int DP, bool BF16>
+int score(const sv::ScoreParams& p, unsigned grid, void* stream) {
+  static std::atomic<unsigned long long> ready;
+  using Cfg = sv::ScoreCfg<DP>;
+  const int rc = allow(sv::k_cache_score<DP, BF16>, sv::kScoreGroups * Cfg::kGroupBytes, ready);
+  if (rc != SPEC_OK) return rc;
+  const int groups = (p.per + sv::kScoreGroup - 1) / sv::kScoreGroup;
+  return launch(sv::k_cache_score<DP, BF16>, dim3(grid), sv::kScoreThreads,
+                groups * Cfg::kGroupBytes, stream, p);
+}
+
+template <int DP, int N8, bool BF16>
+int selected(const sv::SelectedParams& p, unsigned grid, void* stream) {
+  static std::atomic<unsigned long long> ready;
+  constexpr int smem = sv::SelCfg<DP, N8>::kSmem;
+  const int rc = allow(sv::k_attend_selected<DP, N8, BF16>, smem, ready);
+  if (rc != SPEC_OK) return rc;
+  return launch_cluster(sv::k_attend_selected<DP, N8, BF16>, p.cluster, dim3(grid),
+                        sv::kSelThreads, smem, stream, p);
+}
+template <int DP, bool BF16>
+int selected(const sv::SelectedParams& p, int columns, unsigned grid, void* stream) {
+  if (columns <= 8) return selected<DP, 1, BF16>(p, grid, stream);
+  if (columns <= 16) return selected<DP, 2, BF16>(p, grid, stream);
+  return selected<DP, 4, BF16>(p, grid, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int spec_cache_bounds(const spec_cache_bounds_args* a, void* stream, unsigned* device_status) {
+  const int rc = check_bounds(a);
+  if (rc != SPEC_OK) return rc;
+  const int sms = sm_count();
+  if (!sms) return SPEC_ERR_UNSUPPORTED;
+  if (a->B == 0) return SPEC_OK;
+  unsigned* status = status_word(device_status);
+  if (!status) return SPEC_ERR_CUDA;
+  sv::BoundsParams p;
+  p.rq = requests(a->B, 0x7fffffff, a->width, a->page_size, a->table_stride, a->num_pages,
+                  a->block_table, a->kv_lens, a->cu_q, status);
+  p.k = (const char*)a->k_pages;
+  p.k_page = a->kp_page * 2, p.k_token = a->kp_token * 2, p.k_head = a->kp_head * 2;
+  p.out = (char*)a->bounds;
+  p.o_page = a->b_page * 2, p.o_head = a->b_head * 2, p.o_side = a->b_side * 2;
+  p.pieces = a->dim / 8;
+  p.row_pieces = p.pieces * a->kv_heads;
+  // a block for each page that there may be, up to some waves of blocks
+  long long spread = a->cu_q ? ((long long)a->max_q + a->page_size - 2) / a->page_size + 1
+                             : a->width;
+  if (spread > a->width) spread = a->width;
+  const long long most = 64ll * sms / a->B + 1;
+  p.spread = (int)(spread < most ? spread : most);
+  const unsigned grid = blocks((long long)a->B * p.spread);
+  if (!grid) return SPEC_ERR_UNSUPPORTED;
+  return launch(a->dtype == SPEC_CACHE_BF16 ? sv::k_cache_bounds<true> : sv::k_cache_bounds<false>,
+                dim3(grid), sv::kBoundsThreads, 0, stream, p);
+}
+
+int spec_cache_score(const spec_cache_score_args* a, void* stream, unsigned* device_status) {
+  const int rc = check_score(a);
+  if (rc != SPEC_OK) return rc;
+  const int sms = sm_count();
+  if (!sms) return SPEC_ERR_UNSUPPORTED;
+  if (a->num_tokens == 0) return SPEC_OK;
+  unsigned* status = status_word(device_status);
+  if (!status) return SPEC_ERR_CUDA;
+  sv::ScoreParams p;
+  p.rq = requests(a->B, a->num_tokens, a->width, a->page_size, a->table_stride, a->num_pages,
+                  a->block_table, a->kv_lens, a->cu_q, status);
+  p.heads = a->heads, p.kv_heads = a->kv_heads, p.G = a->heads / a->kv_heads, p.dim = a->dim;
+  p.q = (const char*)a->q;
+  p.q_token = a->q_token * 2, p.q_head = a->q_head * 2;
+  p.bounds = (const char*)a->bounds;
+  p.b_page = a->b_page * 2, p.b_head = a->b_head * 2, p.b_side = a->b_side * 2;
+  p.scores = a->scores;
+  p.s_token = a->s_token, p.s_head = a->s_head;
+  const int most = sv::kScoreGroup * sv::kScoreGroups;
+  p.per = a->max_q < most ? a->max_q : most;
+  long long units = groups(a->num_tokens, a->B, p.per) * a->kv_heads;
+  if (units < 1) units = 1;  // (no requests: rows are filled all the same)
+  // some waves of blocks, for ragged batches, of no fewer than 64 columns each
+  const long long columns = ((long long)a->width + 63) / 64, waves = 16ll * sms / units + 1;
+  p.spread = (int)(columns < waves ? columns : waves);
+  const unsigned grid = blocks(units * p.spread);
+  if (!grid) return SPEC_ERR_UNSUPPORTED;
+  const bool bf16 = a->dtype == SPEC_CACHE_BF16;
+  if (a->dim > 64)
+    return bf16 ? score<128, true>(p, grid, stream) : score<128, false>(p, grid, stream);
+  return bf16 ? score<64, true>(p, grid, stream) : score<64, false>(p, grid, stream);
+}
+
+int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* device_status) {
+  const int rc = check_select(a);
+  if (rc != SPEC_OK) return rc;
+  if (!sm_count()) return SPEC_ERR_UNSUPPORTED;
+  if (a->num_tokens == 0) return SPEC_OK;
+  unsigned* status = status_word(device_status);
+  if (!status) return SPEC_ERR_CUDA;
+  sv::SelectParams p;
+  p.rq = requests(a->B, a->num_tokens, a->width, a->page_size, 0, 1, nullptr, a->kv_lens, a->cu_q,
+                  status);
+  p.kv_heads = a->kv_heads, p.count = a->count, p.first = a->first, p.recent = a->recent;
+  p.scores = a->scores;
+  p.s_token = a->s_token, p.s_head = a->s_head;
+  p.out = a->selected;
+  // up to 9216 scores (36 KB) in shared memory, which leaves an SM six blocks
+  p.held = a->width < 9216 ? a->width : 9216;
+  const unsigned grid = blocks((long long)a->num_tokens * a->kv_heads);
+  if (!grid) return SPEC_ERR_UNSUPPORTED;
+  return launch(sv::k_cache_select, dim3(grid), sv::kSelectThreads, p.held * 4, stream, p);
+}
+
+int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* stream,
+                               unsigned* device_status) {
+  const int rc = check_selected(a);
+  if (rc != SPEC_OK) return rc;
+  const int sms = sm_count();
+  if (!sms) return SPEC_ERR_UNSUPPORTED;
+  if (a->num_tokens == 0) return SPEC_OK;
+  unsigned* status = status_word(device_status);
+  if (!status) return SPEC_ERR_CUDA;
+  sv::SelectedParams p;
+  std::memset(&p, 0, sizeof p);
+  p.rq = requests(a->B, a->num_tokens, a->width, a->page_size, a->table_stride, a->num_pages,
+                  a->block_table, a->kv_lens, a->cu_q, status);
+  p.heads = a->heads, p.kv_heads = a->kv_heads, p.G = a->heads / a->kv_heads, p.dim = a->dim;
+  p.q = (const char*)a->q;
+  p.q_token = a->q_token * 2, p.q_head = a->q_head * 2;
+  p.k = (const char*)a->k_pages;
+  p.k_page = a->kp_page * 2, p.k_token = a->kp_token * 2, p.k_head = a->kp_head * 2;
+  p.v = (const char*)a->v_pages;
+  p.v_page = a->vp_page * 2, p.v_token = a->vp_token * 2, p.v_head = a->vp_head * 2;
+  p.selected = a->selected;
+  p.count = a->count;
+  p.out = (char*)a->out;
+  p.out_token = a->out_token * 2, p.out_head = a->out_head * 2;
+  p.lse = a->lse;
+  p.c = a->scale * kLog2e;
+  // a kv head's query heads in units of 32 at most, and as many tokens of a request (if there may
+  // be several) as 32 columns, the block's list and the bytes over its ring take
+  p.unit_heads = p.G < 32 ? p.G : 32;
+  p.splits = (p.G + p.unit_heads - 1) / p.unit_heads;
+  p.per = 1;
+  const int ring = a->dim > 64 ? sv::SelCfg<128, 1>::kRing : sv::SelCfg<64, 1>::kRing;
+  if (a->num_tokens > a->B && a->width <= ring) {
+    p.per = 32 / p.unit_heads;
+    if (p.per > sv::kSelTokens) p.per = sv::kSelTokens;
+    if (p.per > sv::kSelList / a->count) p.per = sv::kSelList / a->count;
+    if (p.per < 1) p.per = 1;
+  }
+  long long units = groups(a->num_tokens, a->B, p.per) * a->kv_heads * p.splits;
+  if (units < 1) units = 1;
+  // clusters of blocks where the units leave SMs idle, as long as each warp keeps two tiles
+  const long long tiles = (long long)a->count * a->page_size / 16;
+  p.cluster = 1;
+  while (p.cluster < 8 && units * p.cluster < 2ll * sms &&
+         tiles >= 4ll * p.cluster * sv::kSelWarps)
+    p.cluster *= 2;
+  const unsigned grid = blocks(units * p.cluster);
+  if (!grid) return SPEC_ERR_UNSUPPORTED;
+  const int columns = p.per * p.unit_heads;
+  const bool bf16 = a->dtype == SPEC_CACHE_BF16;
+  if (a->dim > 64)
+    return bf16 ? selected<128, true>(p, columns, grid, stream)
+                : selected<128, false>(p, columns, grid, stream);
+  return bf16 ? selected<64, true>(p, columns, grid, stream)
+              : selected<64, false>(p, columns, grid, stream);
+}
+
+int spec_cache_weigh(const spec_cache_weigh_args* a, void* stream, unsigned* device_status) {
+  const int rc = check_weigh(a);
+  if (rc != SPEC_OK) return rc;
+  const int sms = sm_count();
+  if (!sms) return SPEC_ERR_UNSUPPORTED;
+  if (a->num_tokens == 0 || a->B == 0) return SPEC_OK;
+  unsigned* status = status_word(device_status);
+  if (!status) return SPEC_ERR_CUDA;
+  sv::WeighParams p;
+  p.rq = requests(a->B, a->num_tokens, a->width, a->page_size, a->table_stride, a->num_pages,
+                  a->block_table, a->kv_lens, a->cu_q, status);
+  p.heads = a->heads, p.kv_heads = a->kv_heads, p.G = a->heads / a->kv_heads, p.dim = a->dim;
+  p.q = (const char*)a->q;
+  p.q_token = a->q_token * 2, p.q_head = a->q_head * 2;
+  p.k = (const char*)a->k_pages;
+  p.k_page = a->kp_page * 2, p.k_token = a->kp_token * 2, p.k_head = a->kp_head * 2;
+  p.lse = a->lse;
+  p.weights = a->weights;
+  p.w_page = a->w_page, p.w_head = a->w_head;
+  p.c = a->scale * kLog2e;
+  p.decay = a->decay;
+  const long long units = (long long)a->B * a->kv_heads;
+  const long long tiles = ((long long)a->width * a->page_size + 63) / 64;
+  const long long waves = 32ll * sms / units + 1;
+  p.spread = (int)(tiles < waves ? tiles : waves);
+  const unsigned grid = blocks(units * p.spread);
+  if (!grid) return SPEC_ERR_UNSUPPORTED;
+  const bool bf16 = a->dtype == SPEC_CACHE_BF16;
+  auto kernel = a->dim > 64
+                    ? (bf16 ? sv::k_cache_weigh<128, true> : sv::k_cache_weigh<128, false>)
+                    : (bf16 ? sv::k_cache_weigh<64, true> : sv::k_cache_weigh<64, false>);
+  return launch(kernel, dim3(grid), sv::kWeighThreads, 0, stream, p);
+}
+
+long long spec_cache_evict_workspace(const spec_cache_evict_args* a) {
+  const int rc = check_evict(a, false);
+  if (rc != SPEC_OK) return rc;
+  return (long long)evict_space(a).bytes;
+}
+
+int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* device_status) {
+  int rc = check_evict(a, true);
+  if (rc != SPEC_OK) return rc;
+  const int sms = sm_count();
+  if (!sms) return SPEC_ERR_UNSUPPORTED;
+  const EvictSpace ws = evict_space(a);
+  if (a->B > 0 && (!a->workspace || a->workspace_bytes < ws.bytes)) return SPEC_ERR_CAPACITY;
+  if (!aligned(a->workspace, 256)) return SPEC_ERR_INVALID_ARG;
+  unsigned* status = status_word(device_status);
+  if (!status) return SPEC_ERR_CUDA;
+  sv::EvictParams p;
+  std::memset(&p, 0, sizeof p);
+  p.rq = requests(a->B, 0, a->width, a->page_size, a->table_stride, a->num_pages, a->block_table,
+                  a->lens, nullptr, status);
+  p.kv_heads = a->kv_heads, p.dim = a->dim, p.first = a->first, p.recent = a->recent;
+  p.k = (char*)a->k_pages;
+  p.k_page = a->kp_page * 2, p.k_token = a->kp_token * 2, p.k_head = a->kp_head * 2;
+  p.v = (char*)a->v_pages;
+  p.v_page = a->vp_page * 2, p.v_token = a->vp_token * 2, p.v_head = a->vp_head * 2;
+  p.weights = a->weights;
+  p.w_page = a->w_page, p.w_head = a->w_head;
+  p.budget = a->budget;
+  p.free_pages = a->free_pages;
+  p.free_count = a->free_count;
+  p.lens_out = a->lens_out;
+  p.free_count_out = a->free_count_out;
+  p.begin = (int*)a->workspace;
+  p.from = (int*)((char*)a->workspace + ws.from);
+  p.by_page = ws.by_page;
+  p.slices = (a->dim * 2 + 63) / 64;
+  // up to 40000 weights (160 KB) in shared memory
+  const long long most = (long long)a->width * a->page_size;
+  p.held = most < 40000 ? (int)most : 40000;
+  static std::atomic<unsigned long long> ready;
+  rc = allow(sv::k_evict_pick, 40000 * 4, ready);
+  if (rc != SPEC_OK) return rc;
+  const long long rows = (long long)a->B * a->kv_heads;
+  const long long warps = rows * (2 * p.slices + 1);
+  const unsigned grid = blocks(rows > 0 ? rows : 1);
+  const unsigned moves = blocks((warps + sv::kMoveThreads / 32 - 1) / (sv::kMoveThreads / 32));
+  if (!grid || (rows > 0 && !moves)) return SPEC_ERR_UNSUPPORTED;
+  rc = launch(sv::k_evict_pick, dim3(grid), sv::kPickThreads, p.held * 4, stream, p);
+  if (rc != SPEC_OK || rows == 0) return rc;
+  return launch(sv::k_evict_move, dim3(moves), sv::kMoveThreads, 0, stream, p);
+}
+
+}  // extern "C"
