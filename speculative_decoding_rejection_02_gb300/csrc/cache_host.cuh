@@ -1,6 +1,7 @@
 // What the host sides of the paged cache's calls share: the device's size, the status word,
-// the launch.
+// the launch, tensor maps.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -62,5 +63,39 @@ int launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, void* stre
 }
 
 inline bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// A map of [x3][x2][x1][dim] 16-bit elements (strides in elements, not looked
+// at for an extent of 1) for boxes of 64 elements x box1 x 1 x box3 in rows of
+// 128 bytes, swizzled; elements past an extent read as zeros.
+inline bool tensor_map(CUtensorMap* map, int dtype, const void* base, int dim, long long x1,
+                long long s1, long long x2, long long s2, long long x3, long long s3,
+                unsigned box1, unsigned box3) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return (Encode)fn;
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)x1, (cuuint64_t)x2, (cuuint64_t)x3};
+  const cuuint64_t least = ((cuuint64_t)dim * 2 + 15) / 16 * 16;
+  const cuuint64_t strides[3] = {x1 > 1 ? (cuuint64_t)s1 * 2 : least,
+                                 x2 > 1 ? (cuuint64_t)s2 * 2 : least,
+                                 x3 > 1 ? (cuuint64_t)s3 * 2 : least};
+  const cuuint32_t box[4] = {64, box1, 1, box3}, ones[4] = {1, 1, 1, 1};
+  return encode(map, dtype == SPEC_CACHE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                4, const_cast<void*>(base), dims, strides, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace sv

@@ -2,99 +2,438 @@
 //
 //   w_j = (old ? decay w_j : 0) + sum over columns 2^(c q . k_j - lse log2(e)),  c = scale log2(e)
 //
-// where a column is a new token and one of its query heads on the kv head. A key's sum needs no
-// other key, so a warp takes 16 keys, has them in registers as operands, and goes over the
-// columns, 8 at a time; the 16 sums are fp32, in an order that does not depend on the call's
-// other requests. A lane loads 16 bytes, 8 channels, of a row: the order of the channels in the
-// products' sums is free, so they are taken as they come.
+// where a column is a new token and one of its query heads on the kv head. With the keys as rows,
 //
-// Bound by HBM (the keys, once) for few columns, by the columns' reloads from L2 for many.
+//   S^T = K Q^T     tcgen05, 128 keys x up to 128 columns, K and Q in shared memory, S in TMEM
+//   w += row sums   one thread per key: it reads its row of S, and its sum never leaves it
+//
+// so a sum needs no other thread and no other key, and there is nothing to join; sums are fp32.
+// A pair of key tiles goes over the request's column tiles together, so that a tile of Q is loaded
+// for 256 keys: with 128 the loads alone would take what an SM gets from L2. Each of the two
+// groups of four warps has one of the key tiles, and two places in TMEM, one of which is filled
+// while it works on the other.
+//
+// The pairs of all requests and kv heads stand in one list, in which a pair counts by its column
+// tiles (three at least: what its loads take), cut into equal parts, one for each block (one block
+// per SM). Every role of a block walks over the part by itself.
+//
+// Warps: 0-3 and 4-7 the sums, 8 loads K (TMA, through the block table), 9 loads Q and the lse,
+// 10 issues the products.
+//
+// Bound by HBM (the keys, once) for few columns, by the exponentials and the products, which take
+// about as long, for many.
 #pragma once
+#include <cuda.h>
+
 #include "sparse_common.cuh"
+#include "tcgen05.cuh"
 
 namespace sv {
 
-constexpr int kWeighThreads = 128;
+constexpr int kWeighThreads = 352, kWeighScan = 128;
+constexpr int kWeighTile = 128;
+constexpr int kWeighRing = 12;      // stages at most
+constexpr int kWeighSmem = 200 * 1024, kWeighStages = 192 * 1024;
+constexpr int kWeighLeast = 3;      // what a pair counts at least, in column tiles
+constexpr long long kWeighPatience = 2000000000;  // clocks that a wait may take
 
 struct WeighParams {
+  CUtensorMap q_map, k_map;
   Requests rq;
   int heads, kv_heads, G, dim;
-  const char* q;
-  long long q_token, q_head;  // bytes
-  const char* k;
-  long long k_page, k_token, k_head;
   const float* lse;
   float* weights;
   long long w_page, w_head;  // elements
   float c, decay;
-  int spread;  // blocks of a request and a kv head
+  int bf16;
+  int tile_tokens;          // new tokens of a column tile
+  int blocks;               // of 64 channels
+  int k_stages, q_stages;   // of blocks * 16 KB
 };
 
-template <int DP, bool BF16>
-__global__ void __launch_bounds__(kWeighThreads) k_cache_weigh(const WeighParams p) {
-  constexpr int kChunks = DP / 32;
+struct WeighShared {
+  uint64_t k_full[kWeighRing], k_empty[kWeighRing], q_full[kWeighRing], q_empty[kWeighRing];
+  uint64_t s_full[2][2], s_free[2][2], drain;
+  alignas(16) float shift[kWeighRing][kWeighTile];  // of a column tile: -lse log2(e)
+  long long sums[kWeighScan / 32];
+  long long at, begin, end;  // of the request that the part starts in, and of the part
+  int first;
+  uint32_t tmem;
+  int stop;
+};
+static_assert(sizeof(WeighShared) <= kWeighSmem - kWeighStages, "shared memory beside the tiles");
+
+__device__ __forceinline__ bool weigh_wait(WeighShared& sh, const WeighParams& p, uint64_t* bar,
+                                           uint32_t parity) {
+  if (!mbar_poll(bar, parity & 1)) {
+    const long long from = clock64();
+    for (;;) {
+      if (mbar_poll(bar, parity & 1)) break;
+      if (*(volatile int*)&sh.stop || clock64() - from > kWeighPatience) {
+        *(volatile int*)&sh.stop = 1;
+        atomicOr(p.rq.status, SPEC_STATUS_TIMEOUT);
+        break;
+      }
+    }
+  }
+  return __all_sync(~0u, !*(volatile int*)&sh.stop);
+}
+
+// The wait for what is in flight when a warp ends, 20 ms at most.
+__device__ __forceinline__ void weigh_land(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 1024; ++i)
+    if (mbar_try(bar, parity & 1)) break;
+}
+
+// Pairs of key tiles of a request and kv head, and what each counts.
+struct WeighUnit {
+  int lo, hi, len, old, pairs, tiles, cost;
+  __device__ __forceinline__ WeighUnit() {}
+  __device__ __forceinline__ WeighUnit(const WeighParams& p, int b) {
+    lo = p.rq.cu_q[b];
+    hi = p.rq.cu_q[b + 1];
+    len = p.rq.kv_lens[b];
+    const bool bad = lo < 0 || hi < lo || hi > p.rq.T || len < 0 ||
+                     len > ((long long)p.rq.width << p.rq.page_shift) || len > 0x7fff0000;
+    if (bad) {
+      atomicOr(p.rq.status, SPEC_CACHE_BAD_LENGTHS);
+      lo = hi = len = 0;
+    }
+    old = len - (hi - lo);
+    tiles = (hi - lo + p.tile_tokens - 1) / p.tile_tokens;  // of columns
+    pairs = tiles ? (len + 2 * kWeighTile - 1) / (2 * kWeighTile) : 0;
+    cost = max(tiles, kWeighLeast);
+  }
+};
+
+// A block's walk over its part of the list: pairs whose place is in [begin, end).
+struct WeighWalk {
+  WeighUnit u;
+  int b, head, pair;
+  bool fresh;           // the unit's first pair here
+  long long at, end;    // place of the pair, and the end of the part
+  __device__ __forceinline__ bool start(const WeighParams& p, const WeighShared& sh) {
+    b = sh.first;
+    at = sh.at;
+    end = sh.end;
+    if (b < 0) return false;
+    u = WeighUnit(p, b);
+    const long long skip = (sh.begin - at + u.cost - 1) / u.cost;
+    at += skip * u.cost;
+    head = u.pairs ? (int)(skip / u.pairs) : p.kv_heads;
+    pair = u.pairs ? (int)(skip - (long long)head * u.pairs) : 0;
+    fresh = true;
+    return settle(p);
+  }
+  __device__ __forceinline__ bool settle(const WeighParams& p) {
+    while (head >= p.kv_heads) {
+      if (at >= end || ++b >= p.rq.B) return false;
+      u = WeighUnit(p, b);
+      head = u.pairs ? 0 : p.kv_heads;
+      pair = 0;
+    }
+    return at < end;
+  }
+  __device__ __forceinline__ bool next(const WeighParams& p) {
+    at += u.cost;
+    fresh = false;
+    if (++pair == u.pairs) {
+      pair = 0;
+      ++head;
+      fresh = true;
+    }
+    return settle(p);
+  }
+  // Whether the pair after this one, if it is in the part, is another unit's or there is none.
+  __device__ __forceinline__ bool ends_unit() const {
+    return pair + 1 == u.pairs || at + u.cost >= end;
+  }
+  // The first column tile that sees a key of the pair.
+  __device__ __forceinline__ int first_tile(const WeighParams& p) const {
+    return max(pair * 2 * kWeighTile - u.old, 0) / p.tile_tokens;
+  }
+  __device__ __forceinline__ bool has(int g) const {
+    return (pair * 2 + g) * kWeighTile < u.len;
+  }
+};
+
+__global__ void __launch_bounds__(kWeighThreads, 1)
+    k_cache_weigh(const __grid_constant__ WeighParams p, const int run) {
+  extern __shared__ __align__(1024) char smem[];
+  WeighShared& sh = *reinterpret_cast<WeighShared*>(smem + kWeighStages);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int stage_bytes = p.blocks * kWeighTile * 128;
+  char* q_smem = smem + p.k_stages * stage_bytes;
+  if (warp == 8) {
+    if (lane < kWeighRing) {
+      mbar_init(&sh.k_full[lane], 1);
+      mbar_init(&sh.k_empty[lane], 1);
+      mbar_init(&sh.q_full[lane], 1);
+      mbar_init(&sh.q_empty[lane], 8);
+    }
+    if (lane < 4) {
+      mbar_init(&sh.s_full[lane >> 1][lane & 1], 1);
+      mbar_init(&sh.s_free[lane >> 1][lane & 1], 4);
+    }
+    if (lane == 0) {
+      mbar_init(&sh.drain, 1);
+      sh.stop = 0;
+      sh.first = -1;
+      prefetch_map(&p.q_map);
+      prefetch_map(&p.k_map);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 10) tmem_alloc(&sh.tmem, 512);
   pdl_trigger();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x = lane >> 2, c = lane & 3;
-  const int part = blockIdx.x % p.spread, unit = blockIdx.x / p.spread;
-  const int b = unit / p.kv_heads, head = unit - b * p.kv_heads;
-  int lo, hi;
-  const int len = p.rq.request(b, lo, hi);
-  if (hi == lo) return;
-  const int old = len - (hi - lo);  // position of the first new token
-  const int columns = (hi - lo) * p.G;  // (at most T * heads)
-  const char* q = p.q + (long long)lo * p.q_token + (long long)head * p.G * p.q_head + 16 * c;
-  const float* lse = p.lse + (long long)lo * p.heads + head * p.G;
-  const int step = p.spread * (kWeighThreads / 32) * 16;
-#pragma unroll 1
-  for (long long j0 = (part * (kWeighThreads / 32) + warp) * 16; j0 < len; j0 += step) {
-    const int key[2] = {(int)j0 + x, (int)j0 + x + 8};
-    uint4 a[2][kChunks];
-    float* w[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int page = key[r] < len ? p.rq.page(b, key[r] >> p.rq.page_shift) : -1;
-      const int at = key[r] & ((1 << p.rq.page_shift) - 1);
-      const char* src = p.k + page * p.k_page + at * p.k_token + head * p.k_head + 16 * c;
-      w[r] = page < 0 ? nullptr : p.weights + page * p.w_page + head * p.w_head + at;
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i)
-        a[r][i] = page >= 0 && 32 * i + 8 * c < p.dim ? *(const uint4*)(src + 64 * i)
-                                                      : make_uint4(0, 0, 0, 0);
+  // ---- this block's part of the list
+  if (tid < kWeighScan) {
+    const int r0 = (int)min((long long)tid * run, (long long)p.rq.B), r1 = min(r0 + run, p.rq.B);
+    auto places = [&](int r) {
+      const WeighUnit u(p, r);
+      return (long long)u.pairs * u.cost * p.kv_heads;
+    };
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) mine += places(r);
+    long long upto = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += x;
     }
-    float sum[2] = {0.f, 0.f};
-    // the first column that sees a key here
-    const int from = j0 > old ? (int)min((j0 - old) * p.G, (long long)columns) & ~7 : 0;
-#pragma unroll 1
-    for (int col0 = from; col0 < columns; col0 += 8) {
-      const int mine = col0 + x, tok = mine / p.G;
-      const char* src = q + (long long)tok * p.q_token + (long long)(mine - tok * p.G) * p.q_head;
-      float d[4] = {};
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const uint4 v = mine < columns && 32 * i + 8 * c < p.dim ? *(const uint4*)(src + 64 * i)
-                                                                 : make_uint4(0, 0, 0, 0);
-        mma_16816<BF16>(d, a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y, v.x, v.y);
-        mma_16816<BF16>(d, a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w, v.z, v.w);
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int col = col0 + 2 * c + y, tok = col / p.G;
-        if (col >= columns) continue;
-        const float z = lse[(long long)tok * p.heads + col - tok * p.G];
-        const float shift = z == -INFINITY ? INFINITY : z * 1.4426950408889634f;
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (key[r] <= old + tok) sum[r] += ex2(d[2 * r + y] * p.c - shift);
-      }
+    if (lane == 31) sh.sums[warp] = upto;
+    named_sync(1, kWeighScan);
+    long long before = upto - mine, total = 0;
+    for (int w = 0; w < kWeighScan / 32; ++w) {
+      if (w < warp) before += sh.sums[w];
+      total += sh.sums[w];
     }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      sum[r] += __shfl_xor_sync(~0u, sum[r], 1);
-      sum[r] += __shfl_xor_sync(~0u, sum[r], 2);
-      if (c == 0 && w[r])
-        *w[r] = sum[r] + (key[r] < old && p.decay != 0.f ? p.decay * *w[r] : 0.f);
+    const long long begin = total / gridDim.x * blockIdx.x +
+                            min((long long)blockIdx.x, total % gridDim.x);
+    const long long end = begin + total / gridDim.x + (blockIdx.x < total % gridDim.x);
+    if (before <= begin && begin < before + mine) {
+      int r = r0;
+      if (run > 1)
+        for (;; ++r) {
+          const long long n = places(r);
+          if (begin < before + n || r + 1 >= r1) break;
+          before += n;
+        }
+      sh.first = r;
+      sh.at = before;
+      sh.begin = begin;
+      sh.end = end;
     }
+  }
+  __syncthreads();
+  WeighWalk walk;
+  if (walk.start(p, sh)) {
+    if (warp == 8) {
+      // ---- K: the pair's tiles, page by page
+      const int page = 1 << p.rq.page_shift, box = min(page, kWeighTile);
+      const int boxes = kWeighTile / box;
+      unsigned issued = 0;
+      bool ok = true;
+      do {
+        const int* table = p.rq.table + walk.b * p.rq.table_stride;
+        for (int g = 0; ok && g < 2 && walk.has(g); ++g) {
+          const int j = (walk.pair * 2 + g) * kWeighTile + lane * box;
+          int number = -1;
+          if (lane < boxes && j < walk.u.len) {
+            number = table[j >> p.rq.page_shift];
+            if (number < 0 || number >= p.rq.num_pages) {
+              atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
+              number = -1;
+            }
+          }
+          const int count = __popc(__ballot_sync(~0u, number >= 0));
+          const unsigned at = issued % p.k_stages;
+          ok = weigh_wait(sh, p, &sh.k_empty[at], issued / p.k_stages + 1);
+          if (!ok) break;
+          if (lane == 0)
+            mbar_arrive_expect_tx(&sh.k_full[at], count * p.blocks * box * 128);
+          __syncwarp();
+          if (number >= 0)
+            for (int x = 0; x < p.blocks; ++x)
+              tma_load_4d(smem + at * stage_bytes + x * kWeighTile * 128 + lane * box * 128,
+                          &p.k_map, 64 * x, j & (page - 1), walk.head, number, &sh.k_full[at]);
+          __syncwarp();
+          ++issued;
+        }
+      } while (ok && walk.next(p));
+      for (unsigned r = issued > p.k_stages ? issued - p.k_stages : 0; r < issued; ++r)
+        weigh_land(&sh.k_full[r % p.k_stages], r / p.k_stages);
+    } else if (warp == 9) {
+      // ---- Q and the columns' -lse log2(e): of every pair's column tiles, or once for a unit
+      // that has only one
+      unsigned issued = 0;
+      bool ok = true;
+      do {
+        if (walk.u.tiles == 1 && !walk.fresh) continue;
+        const float* lse = p.lse + (long long)walk.u.lo * p.heads + walk.head * p.G;
+        const int columns = (walk.u.hi - walk.u.lo) * p.G;
+        float z[4];
+        auto look = [&](int t) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int col = lane + 32 * y;  // of the tile
+            const int tok = col / p.G, all = t * p.tile_tokens * p.G + col;
+            z[y] = tok < p.tile_tokens && all < columns
+                       ? lse[(long long)(t * p.tile_tokens + tok) * p.heads + col - tok * p.G]
+                       : -INFINITY;
+          }
+        };
+        const int t0 = walk.first_tile(p);
+        look(t0);
+        for (int t = t0; t < walk.u.tiles; ++t) {
+          const unsigned at = issued % p.q_stages;
+          ok = weigh_wait(sh, p, &sh.q_empty[at], issued / p.q_stages + 1);
+          if (!ok) break;
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            sh.shift[at][lane + 32 * y] =
+                z[y] == -INFINITY ? -INFINITY : z[y] * -1.4426950408889634f;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.q_full[at], p.blocks * p.tile_tokens * p.G * 128);
+            for (int x = 0; x < p.blocks; ++x)
+              tma_load_4d(q_smem + at * stage_bytes + x * kWeighTile * 128, &p.q_map, 64 * x, 0,
+                          walk.head, walk.u.lo + t * p.tile_tokens, &sh.q_full[at]);
+          }
+          __syncwarp();
+          ++issued;
+          if (t + 1 < walk.u.tiles) look(t + 1);
+        }
+      } while (ok && walk.next(p));
+      for (unsigned r = issued > p.q_stages ? issued - p.q_stages : 0; r < issued; ++r)
+        weigh_land(&sh.q_full[r % p.q_stages], r / p.q_stages);
+    } else if (warp == 10) {
+      // ---- products
+      const bool one = elect_one();
+      const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
+      const uint64_t k0 = mma_desc(smem_addr(smem), 16), q0 = mma_desc(smem_addr(q_smem), 16);
+      const int steps = (p.dim + 15) / 16;
+      unsigned k_count = 0, q_count = 0, s_count[2] = {0, 0};
+      bool ok = true;
+      do {
+        const int tiles = 1 + walk.has(1);
+        const bool single = walk.u.tiles == 1;
+        for (int t = walk.first_tile(p); ok && t < walk.u.tiles; ++t) {
+          const unsigned qa = q_count % p.q_stages;
+          ok = weigh_wait(sh, p, &sh.q_full[qa], q_count / p.q_stages);
+          const int columns = min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
+          const uint32_t kind = mma_kind(p.bf16, false, kWeighTile, (columns + 15) / 16 * 16);
+          for (int g = 0; ok && g < tiles; ++g) {
+            const unsigned ka = (k_count + g) % p.k_stages, s = s_count[g] & 1;
+            ok = weigh_wait(sh, p, &sh.k_full[ka], (k_count + g) / p.k_stages) &&
+                 weigh_wait(sh, p, &sh.s_free[g][s], s_count[g] / 2 + 1);
+            if (!ok) break;
+            tmem_fence_after();
+            const uint64_t kd = k0 + ka * (stage_bytes / 16), qd = q0 + qa * (stage_bytes / 16);
+            for (int x = 0; x < steps; ++x) {
+              const unsigned y = ((x / 4) * (kWeighTile * 128) + (x % 4) * 32) / 16;
+              mma_ss(tmem + g * 256 + s * 128, kd + y, qd + y, kind, x > 0, one);
+            }
+            mma_commit(&sh.s_full[g][s], one);
+            ++s_count[g];
+          }
+          if (!single) ++q_count;
+        }
+        if (single && walk.ends_unit()) ++q_count;
+        k_count += tiles;
+      } while (ok && walk.next(p));
+      mma_commit(&sh.drain, one);
+      weigh_land(&sh.drain, 0);
+    } else if (warp < 8) {
+      // ---- sums
+      const int g = warp >> 2, row = tid & (kWeighTile - 1);
+      const uint32_t tmem = sh.tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 256;
+      const unsigned long long c2 = f2_pack(p.c, p.c);
+      unsigned q_count = 0, k_count = 0, s_count = 0;
+      bool ok = true;
+      do {
+        const int tiles = 1 + walk.has(1);
+        const bool mine = g < tiles, single = walk.u.tiles == 1, last = walk.ends_unit();
+        const int key = (walk.pair * 2 + g) * kWeighTile + row;
+        float* w = nullptr;
+        float before = 0.f;
+        if (mine && key < walk.u.len) {
+          const int number = p.rq.table[walk.b * p.rq.table_stride + (key >> p.rq.page_shift)];
+          if (number >= 0 && number < p.rq.num_pages)
+            w = p.weights + number * p.w_page + walk.head * p.w_head +
+                (key & ((1 << p.rq.page_shift) - 1));
+          if (w && key < walk.u.old && p.decay != 0.f) before = *w * p.decay;
+        }
+        unsigned long long sum2[2] = {0, 0};
+        float rest = 0.f;
+        for (int t = walk.first_tile(p); ok && t < walk.u.tiles; ++t) {
+          const unsigned qa = q_count % p.q_stages;
+          ok = weigh_wait(sh, p, &sh.q_full[qa], q_count / p.q_stages);
+          if (!ok) break;
+          if (mine) {
+            const unsigned s = s_count & 1;
+            ok = weigh_wait(sh, p, &sh.s_full[g][s], s_count / 2);
+            if (!ok) break;
+            ++s_count;
+            tmem_fence_after();
+            // columns [from, columns) of the tile see the key
+            const int columns =
+                min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
+            const long long ahead = (long long)key - walk.u.old - t * p.tile_tokens;
+            const int from = ahead > 0 ? (int)min(ahead * p.G, (long long)kWeighTile) : 0;
+            const float* shift = sh.shift[qa];
+            for (int k = 0; k < columns; k += 32) {
+              float x[32];
+              tmem_ld32(tmem + s * 128 + k, x);
+              tmem_wait_ld(x);
+              if (__all_sync(~0u, from <= k) && k + 32 <= columns) {
+#pragma unroll
+                for (int y = 0; y < 32; y += 4) {
+                  const ulonglong2 z = *(const ulonglong2*)(shift + k + y);
+                  float a, b;
+                  f2_unpack(f2_fma(f2_pack(x[y], x[y + 1]), c2, z.x), a, b);
+                  sum2[0] = f2_add(sum2[0], f2_pack(ex2(a), ex2(b)));
+                  f2_unpack(f2_fma(f2_pack(x[y + 2], x[y + 3]), c2, z.y), a, b);
+                  sum2[1] = f2_add(sum2[1], f2_pack(ex2(a), ex2(b)));
+                }
+              } else {
+#pragma unroll
+                for (int y = 0; y < 32; ++y) {
+                  const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
+                  if (k + y >= from && k + y < columns) rest += e;
+                }
+              }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.s_free[g][s]);
+          }
+          __syncwarp();
+          if (lane == 0 && (!single || last)) mbar_arrive(&sh.q_empty[qa]);
+          if (!single) ++q_count;
+        }
+        if (!ok) break;
+        if (single && last) ++q_count;
+        if (mine && (warp & 3) == 0 && lane == 0)
+          mbar_arrive(&sh.k_empty[(k_count + g) % p.k_stages]);
+        k_count += tiles;
+        if (w) {
+          float a, b;
+          f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
+          *w = before + (rest + (a + b));
+        }
+      } while (walk.next(p));
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 10) {
+    tmem_fence_after();
+    tmem_free(sh.tmem, 512);
   }
 }
 

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   constexpr float kBias = sel_bias<BF16>();
   constexpr int kLanes = DP / 8;        // lanes that copy a row's 16-byte pieces
   constexpr int kRows = 32 / kLanes;    // rows of one copy instruction
-  extern __shared__ __align__(128) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   __shared__ GroupShared<kSelThreads> sh;
   __shared__ int sums[kSelWarps], listed;
   pdl_trigger();

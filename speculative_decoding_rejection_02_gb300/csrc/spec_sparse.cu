@@ -23,6 +23,7 @@ using sv::launch;
 using sv::launch_cluster;
 using sv::sm_count;
 using sv::status_word;
+using sv::tensor_map;
 
 struct Axis {
   long long extent, stride;  // elements
@@ -471,29 +472,34 @@ int spec_cache_weigh(const spec_cache_weigh_args* a, void* stream, unsigned* dev
   unsigned* status = status_word(device_status);
   if (!status) return SPEC_ERR_CUDA;
   sv::WeighParams p;
+  std::memset(&p, 0, sizeof p);
   p.rq = requests(a->B, a->num_tokens, a->width, a->page_size, a->table_stride, a->num_pages,
                   a->block_table, a->kv_lens, a->cu_q, status);
   p.heads = a->heads, p.kv_heads = a->kv_heads, p.G = a->heads / a->kv_heads, p.dim = a->dim;
-  p.q = (const char*)a->q;
-  p.q_token = a->q_token * 2, p.q_head = a->q_head * 2;
-  p.k = (const char*)a->k_pages;
-  p.k_page = a->kp_page * 2, p.k_token = a->kp_token * 2, p.k_head = a->kp_head * 2;
   p.lse = a->lse;
   p.weights = a->weights;
   p.w_page = a->w_page, p.w_head = a->w_head;
   p.c = a->scale * kLog2e;
   p.decay = a->decay;
-  const long long units = (long long)a->B * a->kv_heads;
-  const long long tiles = ((long long)a->width * a->page_size + 63) / 64;
-  const long long waves = 32ll * sms / units + 1;
-  p.spread = (int)(tiles < waves ? tiles : waves);
-  const unsigned grid = blocks(units * p.spread);
-  if (!grid) return SPEC_ERR_UNSUPPORTED;
-  const bool bf16 = a->dtype == SPEC_CACHE_BF16;
-  auto kernel = a->dim > 64
-                    ? (bf16 ? sv::k_cache_weigh<128, true> : sv::k_cache_weigh<128, false>)
-                    : (bf16 ? sv::k_cache_weigh<64, true> : sv::k_cache_weigh<64, false>);
-  return launch(kernel, dim3(grid), sv::kWeighThreads, 0, stream, p);
+  p.bf16 = a->dtype == SPEC_CACHE_BF16;
+  p.tile_tokens = sv::kWeighTile / p.G < a->max_q ? sv::kWeighTile / p.G : a->max_q;
+  p.blocks = a->dim > 64 ? 2 : 1;
+  // Q of one column tile stays, and all other stages hold keys; of several, they come again for
+  // every pair of key tiles
+  const int stages = sv::kWeighStages / (p.blocks * sv::kWeighTile * 128);
+  p.q_stages = a->max_q <= p.tile_tokens ? 1 : stages / 2;
+  p.k_stages = stages - p.q_stages;
+  const int box = a->page_size < sv::kWeighTile ? a->page_size : sv::kWeighTile;
+  if (!tensor_map(&p.q_map, a->dtype, a->q, a->dim, p.G, a->q_head, a->kv_heads, a->q_head * p.G,
+                  a->num_tokens, a->q_token, p.G, p.tile_tokens) ||
+      !tensor_map(&p.k_map, a->dtype, a->k_pages, a->dim, a->page_size, a->kp_token, a->kv_heads,
+                  a->kp_head, a->num_pages, a->kp_page, box, 1))
+    return SPEC_ERR_CUDA;
+  static std::atomic<unsigned long long> ready;
+  const int ok = allow(sv::k_cache_weigh, sv::kWeighSmem, ready);
+  if (ok != SPEC_OK) return ok;
+  const int run = a->B > sv::kWeighScan ? (a->B + sv::kWeighScan - 1) / sv::kWeighScan : 1;
+  return launch(sv::k_cache_weigh, dim3(sms), sv::kWeighThreads, sv::kWeighSmem, stream, p, run);
 }
 
 long long spec_cache_evict_workspace(const spec_cache_evict_args* a) {
