@@ -9,16 +9,21 @@
 //
 // so a sum needs no other thread and no other key, and there is nothing to join; sums are fp32.
 // A pair of key tiles goes over the request's column tiles together, so that a tile of Q is loaded
-// for 256 keys: with 128 the loads alone would take what an SM gets from L2. Each of the two
-// groups of four warps has one of the key tiles, and two places in TMEM, one of which is filled
-// while it works on the other.
+// for 256 keys: with 128 the loads alone would take what an SM gets from L2. Each key tile has two
+// groups of four warps with a place in TMEM each, which take its column tiles in turns; at the end
+// of the pair one passes its sums to the other. (One group with both places leaves the tensor
+// cores and the exponentials idle for two thirds of the time: two warps for each scheduler do not
+// cover the latency of what they do.)
 //
 // The pairs of all requests and kv heads stand in one list, in which a pair counts by its column
 // tiles (three at least: what its loads take), cut into equal parts, one for each block (one block
 // per SM). Every role of a block walks over the part by itself.
 //
-// Warps: 0-3 and 4-7 the sums, 8 loads K (TMA, through the block table), 9 loads Q and the lse,
-// 10 issues the products.
+// Warps: 0-7 and 8-15 the sums of the pair's two tiles, 16 loads K (TMA, through the block table),
+// 17 loads Q and the lse, 18 and 19 issue the products of the one and the other tile. (With one
+// issuer for both two chunks of 2048 take 540 us: it is the issue of a product that takes its
+// time, not the product.) The two tiles' chains go ahead of one another, so each has its own
+// stages of K.
 //
 // Bound by HBM (the keys, once) for few columns, by the exponentials and the products, which take
 // about as long, for many.
@@ -30,10 +35,11 @@
 
 namespace sv {
 
-constexpr int kWeighThreads = 352, kWeighScan = 128;
+constexpr int kWeighSums = 16, kWeighThreads = (kWeighSums + 4) * 32, kWeighScan = 128;
 constexpr int kWeighTile = 128;
 constexpr int kWeighRing = 12;      // stages at most
-constexpr int kWeighSmem = 200 * 1024, kWeighStages = 192 * 1024;
+constexpr int kWeighSmem = 204 * 1024, kWeighStages = 192 * 1024;
+constexpr int kWeighShifts = 8;     // column tiles whose lse are ahead
 constexpr int kWeighLeast = 3;      // what a pair counts at least, in column tiles
 constexpr long long kWeighPatience = 2000000000;  // clocks that a wait may take
 
@@ -48,13 +54,17 @@ struct WeighParams {
   int bf16;
   int tile_tokens;          // new tokens of a column tile
   int blocks;               // of 64 channels
-  int k_stages, q_stages;   // of blocks * 16 KB
+  int k_stages, q_stages;   // of blocks * 16 KB; of K for each of a pair's two tiles
 };
 
 struct WeighShared {
   uint64_t k_full[kWeighRing], k_empty[kWeighRing], q_full[kWeighRing], q_empty[kWeighRing];
-  uint64_t s_full[2][2], s_free[2][2], drain;
-  alignas(16) float shift[kWeighRing][kWeighTile];  // of a column tile: -lse log2(e)
+  uint64_t s_full[2][2], s_free[2][2], joined[2], drain[2];
+  uint64_t l_full[kWeighShifts], l_empty[kWeighShifts];
+  alignas(16) float shift[kWeighShifts][kWeighTile];  // of a column tile: -lse log2(e)
+  // Sums on their way from one group of a tile to the other, of two pairs in turn.
+  float part[2][2][kWeighTile];
+  int pages[kWeighRing][16];  // of a tile of keys; -1: none
   long long sums[kWeighScan / 32];
   long long at, begin, end;  // of the request that the part starts in, and of the part
   int first;
@@ -63,20 +73,22 @@ struct WeighShared {
 };
 static_assert(sizeof(WeighShared) <= kWeighSmem - kWeighStages, "shared memory beside the tiles");
 
+// A bounded wait of a whole warp (about a second), with one answer for all its lanes; once one
+// has run out every later one that would wait returns at once.
 __device__ __forceinline__ bool weigh_wait(WeighShared& sh, const WeighParams& p, uint64_t* bar,
                                            uint32_t parity) {
-  if (!mbar_poll(bar, parity & 1)) {
+  bool there = mbar_poll(bar, parity & 1);
+  if (__builtin_expect(!there, 0)) {
     const long long from = clock64();
-    for (;;) {
-      if (mbar_poll(bar, parity & 1)) break;
-      if (*(volatile int*)&sh.stop || clock64() - from > kWeighPatience) {
-        *(volatile int*)&sh.stop = 1;
-        atomicOr(p.rq.status, SPEC_STATUS_TIMEOUT);
-        break;
-      }
+    do {
+      there = mbar_poll(bar, parity & 1);
+    } while (!there && !*(volatile int*)&sh.stop && clock64() - from < kWeighPatience);
+    if (!there) {
+      *(volatile int*)&sh.stop = 1;
+      atomicOr(p.rq.status, SPEC_STATUS_TIMEOUT);
     }
   }
-  return __all_sync(~0u, !*(volatile int*)&sh.stop);
+  return __all_sync(~0u, there);
 }
 
 // The wait for what is in flight when a warp ends, 20 ms at most.
@@ -164,20 +176,27 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   WeighShared& sh = *reinterpret_cast<WeighShared*>(smem + kWeighStages);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int stage_bytes = p.blocks * kWeighTile * 128;
-  char* q_smem = smem + p.k_stages * stage_bytes;
-  if (warp == 8) {
+  char* q_smem = smem + 2 * p.k_stages * stage_bytes;
+  if (warp == kWeighSums) {
     if (lane < kWeighRing) {
       mbar_init(&sh.k_full[lane], 1);
-      mbar_init(&sh.k_empty[lane], 1);
+      mbar_init(&sh.k_empty[lane], 4);
       mbar_init(&sh.q_full[lane], 1);
-      mbar_init(&sh.q_empty[lane], 8);
+      mbar_init(&sh.q_empty[lane], 2);
+    }
+    if (lane < kWeighShifts) {
+      mbar_init(&sh.l_full[lane], 1);
+      mbar_init(&sh.l_empty[lane], kWeighSums);
     }
     if (lane < 4) {
       mbar_init(&sh.s_full[lane >> 1][lane & 1], 1);
       mbar_init(&sh.s_free[lane >> 1][lane & 1], 4);
     }
+    if (lane < 2) {
+      mbar_init(&sh.joined[lane], 8);
+      mbar_init(&sh.drain[lane], 1);
+    }
     if (lane == 0) {
-      mbar_init(&sh.drain, 1);
       sh.stop = 0;
       sh.first = -1;
       prefetch_map(&p.q_map);
@@ -185,7 +204,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     }
     fence_mbar_init();
   }
-  if (warp == 10) tmem_alloc(&sh.tmem, 512);
+  if (warp == kWeighSums + 2) tmem_alloc(&sh.tmem, 512);
   pdl_trigger();
   tmem_fence_before();
   __syncthreads();
@@ -232,72 +251,76 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   __syncthreads();
   WeighWalk walk;
   if (walk.start(p, sh)) {
-    if (warp == 8) {
+    if (warp == kWeighSums) {
       // ---- K: the pair's tiles, page by page
       const int page = 1 << p.rq.page_shift, box = min(page, kWeighTile);
       const int boxes = kWeighTile / box;
-      unsigned issued = 0;
+      unsigned issued[2] = {0, 0};
       bool ok = true;
+      // the number of the page that the lane loads of a tile; -1: none
+      auto look = [&](int g) {
+        const int j = (walk.pair * 2 + g) * kWeighTile + lane * box;
+        if (lane >= boxes || j >= walk.u.len) return -1;
+        return p.rq.table[walk.b * p.rq.table_stride + (j >> p.rq.page_shift)];
+      };
       do {
-        const int* table = p.rq.table + walk.b * p.rq.table_stride;
-        for (int g = 0; ok && g < 2 && walk.has(g); ++g) {
+        int number[2] = {look(0), look(1)};
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (!ok || !walk.has(g)) break;
           const int j = (walk.pair * 2 + g) * kWeighTile + lane * box;
-          int number = -1;
-          if (lane < boxes && j < walk.u.len) {
-            number = table[j >> p.rq.page_shift];
-            if (number < 0 || number >= p.rq.num_pages) {
-              atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
-              number = -1;
-            }
+          if (lane < boxes && j < walk.u.len && (number[g] < 0 || number[g] >= p.rq.num_pages)) {
+            atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
+            number[g] = -1;
           }
-          const int count = __popc(__ballot_sync(~0u, number >= 0));
-          const unsigned at = issued % p.k_stages;
-          ok = weigh_wait(sh, p, &sh.k_empty[at], issued / p.k_stages + 1);
+          const int count = __popc(__ballot_sync(~0u, number[g] >= 0));
+          const unsigned at = g * p.k_stages + issued[g] % p.k_stages;
+          ok = weigh_wait(sh, p, &sh.k_empty[at], issued[g] / p.k_stages + 1);
           if (!ok) break;
+          if (lane < boxes) sh.pages[at][lane] = number[g];
+          __syncwarp();
           if (lane == 0)
             mbar_arrive_expect_tx(&sh.k_full[at], count * p.blocks * box * 128);
           __syncwarp();
-          if (number >= 0)
+          if (number[g] >= 0)
             for (int x = 0; x < p.blocks; ++x)
               tma_load_4d(smem + at * stage_bytes + x * kWeighTile * 128 + lane * box * 128,
-                          &p.k_map, 64 * x, j & (page - 1), walk.head, number, &sh.k_full[at]);
+                          &p.k_map, 64 * x, j & (page - 1), walk.head, number[g],
+                          &sh.k_full[at]);
           __syncwarp();
-          ++issued;
+          ++issued[g];
         }
       } while (ok && walk.next(p));
-      for (unsigned r = issued > p.k_stages ? issued - p.k_stages : 0; r < issued; ++r)
-        weigh_land(&sh.k_full[r % p.k_stages], r / p.k_stages);
-    } else if (warp == 9) {
-      // ---- Q and the columns' -lse log2(e): of every pair's column tiles, or once for a unit
-      // that has only one
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        for (unsigned r = issued[g] > p.k_stages ? issued[g] - p.k_stages : 0; r < issued[g]; ++r)
+          weigh_land(&sh.k_full[g * p.k_stages + r % p.k_stages], r / p.k_stages);
+    } else if (warp == kWeighSums + 1) {
+      // ---- Q and its columns' -lse log2(e) (loaded two tiles ahead) of every pair's column
+      // tiles, or once for a unit that has only one
+      int tok[4], from[4];  // of the lane's columns of a tile: token, place of the lse
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        tok[y] = (lane + 32 * y) / p.G;
+        from[y] = tok[y] * p.heads + lane + 32 * y - tok[y] * p.G;
+      }
       unsigned issued = 0;
       bool ok = true;
       do {
         if (walk.u.tiles == 1 && !walk.fresh) continue;
         const float* lse = p.lse + (long long)walk.u.lo * p.heads + walk.head * p.G;
-        const int columns = (walk.u.hi - walk.u.lo) * p.G;
-        float z[4];
-        auto look = [&](int t) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int col = lane + 32 * y;  // of the tile
-            const int tok = col / p.G, all = t * p.tile_tokens * p.G + col;
-            z[y] = tok < p.tile_tokens && all < columns
-                       ? lse[(long long)(t * p.tile_tokens + tok) * p.heads + col - tok * p.G]
-                       : -INFINITY;
-          }
-        };
-        const int t0 = walk.first_tile(p);
-        look(t0);
-        for (int t = t0; t < walk.u.tiles; ++t) {
-          const unsigned at = issued % p.q_stages;
-          ok = weigh_wait(sh, p, &sh.q_empty[at], issued / p.q_stages + 1);
-          if (!ok) break;
+        const int tokens = walk.u.hi - walk.u.lo, t0 = walk.first_tile(p);
+        float z[2][4];
+        auto look = [&](int t, float* z) {
+          const int first = t * p.tile_tokens, n = min(p.tile_tokens, tokens - first);
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            sh.shift[at][lane + 32 * y] =
-                z[y] == -INFINITY ? -INFINITY : z[y] * -1.4426950408889634f;
-          __syncwarp();
+            z[y] = tok[y] < n ? lse[(long long)first * p.heads + from[y]] : -INFINITY;
+        };
+        auto put = [&](int t, float* z) {
+          const unsigned at = issued % p.q_stages, la = issued % kWeighShifts;
+          ok = weigh_wait(sh, p, &sh.q_empty[at], issued / p.q_stages + 1);
+          if (!ok) return;
           if (lane == 0) {
             mbar_arrive_expect_tx(&sh.q_full[at], p.blocks * p.tile_tokens * p.G * 128);
             for (int x = 0; x < p.blocks; ++x)
@@ -306,89 +329,119 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
           }
           __syncwarp();
           ++issued;
-          if (t + 1 < walk.u.tiles) look(t + 1);
+          ok = weigh_wait(sh, p, &sh.l_empty[la], (issued - 1) / kWeighShifts + 1);
+          if (!ok) return;
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            sh.shift[la][lane + 32 * y] =
+                z[y] == -INFINITY ? -INFINITY : z[y] * -1.4426950408889634f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.l_full[la]);
+          look(t + 2, z);
+        };
+        look(t0, z[0]);
+        look(t0 + 1, z[1]);
+        for (int t = t0; ok && t < walk.u.tiles; t += 2) {
+          put(t, z[0]);
+          if (ok && t + 1 < walk.u.tiles) put(t + 1, z[1]);
         }
       } while (ok && walk.next(p));
       for (unsigned r = issued > p.q_stages ? issued - p.q_stages : 0; r < issued; ++r)
         weigh_land(&sh.q_full[r % p.q_stages], r / p.q_stages);
-    } else if (warp == 10) {
-      // ---- products
+    } else if (warp == kWeighSums + 2 || warp == kWeighSums + 3) {
+      // ---- products of the pair's one or other tile
+      const int g = warp - kWeighSums - 2;
       const bool one = elect_one();
-      const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0);
+      const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0) + g * 256;
       const uint64_t k0 = mma_desc(smem_addr(smem), 16), q0 = mma_desc(smem_addr(q_smem), 16);
       const int steps = (p.dim + 15) / 16;
-      unsigned k_count = 0, q_count = 0, s_count[2] = {0, 0};
+      unsigned k_count = 0, q_count = 0, s_count = 0;
       bool ok = true;
       do {
-        const int tiles = 1 + walk.has(1);
-        const bool single = walk.u.tiles == 1;
-        for (int t = walk.first_tile(p); ok && t < walk.u.tiles; ++t) {
-          const unsigned qa = q_count % p.q_stages;
-          ok = weigh_wait(sh, p, &sh.q_full[qa], q_count / p.q_stages);
-          const int columns = min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
-          const uint32_t kind = mma_kind(p.bf16, false, kWeighTile, (columns + 15) / 16 * 16);
-          for (int g = 0; ok && g < tiles; ++g) {
-            const unsigned ka = (k_count + g) % p.k_stages, s = s_count[g] & 1;
-            ok = weigh_wait(sh, p, &sh.k_full[ka], (k_count + g) / p.k_stages) &&
-                 weigh_wait(sh, p, &sh.s_free[g][s], s_count[g] / 2 + 1);
-            if (!ok) break;
-            tmem_fence_after();
-            const uint64_t kd = k0 + ka * (stage_bytes / 16), qd = q0 + qa * (stage_bytes / 16);
-            for (int x = 0; x < steps; ++x) {
-              const unsigned y = ((x / 4) * (kWeighTile * 128) + (x % 4) * 32) / 16;
-              mma_ss(tmem + g * 256 + s * 128, kd + y, qd + y, kind, x > 0, one);
-            }
-            mma_commit(&sh.s_full[g][s], one);
-            ++s_count[g];
-          }
-          if (!single) ++q_count;
-        }
-        if (single && walk.ends_unit()) ++q_count;
-        k_count += tiles;
-      } while (ok && walk.next(p));
-      mma_commit(&sh.drain, one);
-      weigh_land(&sh.drain, 0);
-    } else if (warp < 8) {
-      // ---- sums
-      const int g = warp >> 2, row = tid & (kWeighTile - 1);
-      const uint32_t tmem = sh.tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 256;
-      const unsigned long long c2 = f2_pack(p.c, p.c);
-      unsigned q_count = 0, k_count = 0, s_count = 0;
-      bool ok = true;
-      do {
-        const int tiles = 1 + walk.has(1);
-        const bool mine = g < tiles, single = walk.u.tiles == 1, last = walk.ends_unit();
-        const int key = (walk.pair * 2 + g) * kWeighTile + row;
-        float* w = nullptr;
-        float before = 0.f;
-        if (mine && key < walk.u.len) {
-          const int number = p.rq.table[walk.b * p.rq.table_stride + (key >> p.rq.page_shift)];
-          if (number >= 0 && number < p.rq.num_pages)
-            w = p.weights + number * p.w_page + walk.head * p.w_head +
-                (key & ((1 << p.rq.page_shift) - 1));
-          if (w && key < walk.u.old && p.decay != 0.f) before = *w * p.decay;
-        }
-        unsigned long long sum2[2] = {0, 0};
-        float rest = 0.f;
+        const bool mine = walk.has(g), single = walk.u.tiles == 1, last = walk.ends_unit();
+        const unsigned ka = g * p.k_stages + k_count % p.k_stages;
+        const uint64_t kd = k0 + ka * (stage_bytes / 16);
+        if (mine) ok = weigh_wait(sh, p, &sh.k_full[ka], k_count / p.k_stages);
         for (int t = walk.first_tile(p); ok && t < walk.u.tiles; ++t) {
           const unsigned qa = q_count % p.q_stages;
           ok = weigh_wait(sh, p, &sh.q_full[qa], q_count / p.q_stages);
           if (!ok) break;
           if (mine) {
-            const unsigned s = s_count & 1;
-            ok = weigh_wait(sh, p, &sh.s_full[g][s], s_count / 2);
+            const int columns =
+                min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
+            const uint32_t kind =
+                mma_kind(p.bf16, false, kWeighTile, (columns + 15) / 16 * 16);
+            const uint32_t s = s_count & 1;
+            ok = weigh_wait(sh, p, &sh.s_free[g][s], s_count / 2 + 1);
             if (!ok) break;
-            ++s_count;
             tmem_fence_after();
+            const uint64_t qd = q0 + qa * (stage_bytes / 16);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const unsigned y = ((x / 4) * (kWeighTile * 128) + (x % 4) * 32) / 16;
+              if (x < steps) mma_ss(tmem + s * 128, kd + y, qd + y, kind, x > 0, one);
+            }
+            mma_commit(&sh.s_full[g][s], one);
+            ++s_count;
+          }
+          if (!single || last) {
+            mma_commit(&sh.q_empty[qa], one);
+            ++q_count;
+          }
+        }
+        k_count += mine;
+      } while (ok && walk.next(p));
+      mma_commit(&sh.drain[g], one);
+      weigh_land(&sh.drain[g], 0);
+    } else if (warp < kWeighSums) {
+      // ---- sums
+      const int g = warp >> 3, turn = warp >> 2 & 1, row = tid & (kWeighTile - 1);
+      const uint32_t tmem =
+          sh.tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * 256 + turn * 128;
+      const int box_shift = min(p.rq.page_shift, 7);
+      const unsigned long long c2 = f2_pack(p.c, p.c);
+      unsigned l_count = 0, k_count = 0, s_count = 0, joins = 0;
+      bool ok = true;
+      do {
+        const int t0 = walk.first_tile(p), n = walk.u.tiles - t0;
+        const bool mine = walk.has(g), single = walk.u.tiles == 1, last = walk.ends_unit();
+        const int key = (walk.pair * 2 + g) * kWeighTile + row;
+        float* w = nullptr;
+        float before = 0.f;
+        unsigned long long sum2[2] = {0, 0};
+        float rest = 0.f;
+        for (int t = t0; ok && t < walk.u.tiles; ++t) {
+          const unsigned la = l_count % kWeighShifts;
+          ok = weigh_wait(sh, p, &sh.l_full[la], l_count / kWeighShifts);
+          if (!ok) break;
+          if (mine && (s_count & 1) == turn) {
+            ok = weigh_wait(sh, p, &sh.s_full[g][turn], s_count / 2);
+            if (!ok) break;
+            tmem_fence_after();
+            if (t + 1 == walk.u.tiles) {  // the pair's last: this group writes the weights
+              const unsigned ka = g * p.k_stages + k_count % p.k_stages;
+              ok = weigh_wait(sh, p, &sh.k_full[ka], k_count / p.k_stages);  // (it has landed)
+              if (!ok) break;
+              const int number = sh.pages[ka][row >> box_shift];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.k_empty[ka]);
+              __syncwarp();
+              if (number >= 0 && key < walk.u.len)
+                w = p.weights + number * p.w_page + walk.head * p.w_head +
+                    (key & ((1 << p.rq.page_shift) - 1));
+              if (w && key < walk.u.old && p.decay != 0.f) before = *w;
+              __syncwarp();
+            }
             // columns [from, columns) of the tile see the key
             const int columns =
                 min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
             const long long ahead = (long long)key - walk.u.old - t * p.tile_tokens;
             const int from = ahead > 0 ? (int)min(ahead * p.G, (long long)kWeighTile) : 0;
-            const float* shift = sh.shift[qa];
+            const float* shift = sh.shift[la];
+#pragma unroll 1
             for (int k = 0; k < columns; k += 32) {
               float x[32];
-              tmem_ld32(tmem + s * 128 + k, x);
+              tmem_ld32(tmem + k, x);
               tmem_wait_ld(x);
               if (__all_sync(~0u, from <= k) && k + 32 <= columns) {
 #pragma unroll
@@ -410,28 +463,41 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             }
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_free[g][s]);
+            if (lane == 0) mbar_arrive(&sh.s_free[g][turn]);
           }
+          s_count += mine;
           __syncwarp();
-          if (lane == 0 && (!single || last)) mbar_arrive(&sh.q_empty[qa]);
-          if (!single) ++q_count;
+          if (!single || last) {
+            if (lane == 0) mbar_arrive(&sh.l_empty[la]);
+            ++l_count;
+          }
         }
         if (!ok) break;
-        if (single && last) ++q_count;
-        if (mine && (warp & 3) == 0 && lane == 0)
-          mbar_arrive(&sh.k_empty[(k_count + g) % p.k_stages]);
-        k_count += tiles;
-        if (w) {
-          float a, b;
-          f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
-          *w = before + (rest + (a + b));
+        k_count += mine;
+        float a, b;
+        f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
+        a = rest + (a + b);
+        if (mine && n > 1) {
+          // The other group's part: all eight warps meet, and meet again before `part` is
+          // written anew.
+          const bool writes = (s_count - 1 & 1) == turn;
+          float* part = sh.part[g][joins & 1] + row;
+          if (!writes) *part = a;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.joined[g]);
+          __syncwarp();
+          ok = weigh_wait(sh, p, &sh.joined[g], joins);
+          if (!ok) break;
+          if (writes) a += *part;
+          ++joins;
         }
+        if (w) *w = before * p.decay + a;
       } while (walk.next(p));
     }
   }
   tmem_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == kWeighSums + 2) {
     tmem_fence_after();
     tmem_free(sh.tmem, 512);
   }

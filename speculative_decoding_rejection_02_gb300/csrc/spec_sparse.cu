@@ -484,11 +484,11 @@ int spec_cache_weigh(const spec_cache_weigh_args* a, void* stream, unsigned* dev
   p.bf16 = a->dtype == SPEC_CACHE_BF16;
   p.tile_tokens = sv::kWeighTile / p.G < a->max_q ? sv::kWeighTile / p.G : a->max_q;
   p.blocks = a->dim > 64 ? 2 : 1;
-  // Q of one column tile stays, and all other stages hold keys; of several, they come again for
-  // every pair of key tiles
+  // Q of one column tile stays for a unit, and most stages hold keys; of several, they come again
+  // for every pair of key tiles. (A wait for keys is rare then: a pair goes over all columns.)
   const int stages = sv::kWeighStages / (p.blocks * sv::kWeighTile * 128);
-  p.q_stages = a->max_q <= p.tile_tokens ? 1 : stages / 2;
-  p.k_stages = stages - p.q_stages;
+  p.q_stages = a->max_q <= p.tile_tokens ? 2 : 4;
+  p.k_stages = (stages - p.q_stages) / 2;
   const int box = a->page_size < sv::kWeighTile ? a->page_size : sv::kWeighTile;
   if (!tensor_map(&p.q_map, a->dtype, a->q, a->dim, p.G, a->q_head, a->kv_heads, a->q_head * p.G,
                   a->num_tokens, a->q_token, p.G, p.tile_tokens) ||
