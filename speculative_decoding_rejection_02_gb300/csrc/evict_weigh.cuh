@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         const int key = (walk.pair * 2 + g) * kWeighTile + row;
         float* w = nullptr;
         float before = 0.f;
-        unsigned long long sum2[2] = {0, 0};
+        unsigned long long sum2[4] = {0, 0, 0, 0};
         float rest = 0.f;
         for (int t = t0; ok && t < walk.u.tiles; ++t) {
           const unsigned la = l_count % kWeighShifts;
@@ -441,17 +441,19 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
 #pragma unroll 1
             for (int k = 0; k < columns; k += 32) {
               float x[32];
+              ulonglong2 z[8];
               tmem_ld32(tmem + k, x);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) z[y] = *(const ulonglong2*)(shift + k + 4 * y);
               tmem_wait_ld(x);
               if (__all_sync(~0u, from <= k) && k + 32 <= columns) {
 #pragma unroll
-                for (int y = 0; y < 32; y += 4) {
-                  const ulonglong2 z = *(const ulonglong2*)(shift + k + y);
-                  float a, b;
-                  f2_unpack(f2_fma(f2_pack(x[y], x[y + 1]), c2, z.x), a, b);
-                  sum2[0] = f2_add(sum2[0], f2_pack(ex2(a), ex2(b)));
-                  f2_unpack(f2_fma(f2_pack(x[y + 2], x[y + 3]), c2, z.y), a, b);
-                  sum2[1] = f2_add(sum2[1], f2_pack(ex2(a), ex2(b)));
+                for (int y = 0; y < 8; ++y) {
+                  float a, b, c, d;
+                  f2_unpack(f2_fma(f2_pack(x[4 * y], x[4 * y + 1]), c2, z[y].x), a, b);
+                  f2_unpack(f2_fma(f2_pack(x[4 * y + 2], x[4 * y + 3]), c2, z[y].y), c, d);
+                  sum2[2 * (y & 1)] = f2_add(sum2[2 * (y & 1)], f2_pack(ex2(a), ex2(b)));
+                  sum2[2 * (y & 1) + 1] = f2_add(sum2[2 * (y & 1) + 1], f2_pack(ex2(c), ex2(d)));
                 }
               } else {
 #pragma unroll
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         if (!ok) break;
         k_count += mine;
         float a, b;
-        f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
+        f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, b);
         a = rest + (a + b);
         if (mine && n > 1) {
           // The other group's part: all eight warps meet, and meet again before `part` is
