@@ -1,21 +1,21 @@
 // Eviction: which tokens stay, and the closing of the gaps (spec_cache_evict).
 //
-// k_evict_pick, one block for a request and kv head: the heaviest free tokens by the largest
-// weights' cut (pick_cut) and one pass over all tokens in order (pick_words), which writes for
-// each kept token that moves where it comes from. The same blocks do the requests' bookkeeping:
+// k_evict_pick, one block for a request and kv head: the kept tokens are those of the largest
+// keys (pick_items, pick_any), the ones that always stay among them; for each that moves it is
+// written down where it comes from. The same blocks do the requests' bookkeeping:
 // every block adds up all requests' pages that go, so each finds for itself whether the call can
 // be done at all and where its request's pages come on the stack.
 //
 // k_evict_move: keys, values and weights to their new places. Tokens only move down and keep
-// their order, so a warp that takes 64 bytes of the channels may go upwards in batches: it has
-// read a batch before it writes one, and what it overwrites is never a later batch's source.
+// their order, so a request and head go upwards in batches: all of a batch is read, in registers,
+// before any of it is written, and what is overwritten is never a later batch's source. One block
+// for a request and head, or a cluster of up to eight where there are few. Bound by HBM.
 #pragma once
 #include "sparse_common.cuh"
 
 namespace sv {
 
-constexpr int kPickThreads = 512;
-constexpr int kMoveThreads = 128;
+constexpr int kMoveThreads = 256;
 
 struct EvictParams {
   Requests rq;  // kv_lens: lens; no cu_q
@@ -31,11 +31,12 @@ struct EvictParams {
   const int* free_count;
   int* lens_out;
   int* free_count_out;
-  int held;      // weights that fit the dynamic shared memory
+  int held;      // weights that fit the dynamic shared memory (any length)
+  int vec;       // weights of 8 tokens on 16-byte boundaries
   int by_page;   // whether `from` goes by pages of the pool, or by columns of the table
   int* begin;    // [B][kv_heads] the first kept token that moves; none: 0x7fffffff
   int* from;     // where kept tokens come from, in pages [kv_heads][page_size]
-  int slices;    // 64-byte pieces of a key
+  int cluster;   // blocks of a request and kv head that move its tokens
 
   __device__ __forceinline__ int kept(int len, int budget) const {
     return (int)min((long long)len, max((long long)budget, (long long)first + recent));
@@ -56,11 +57,12 @@ struct EvictParams {
   }
 };
 
-__global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictParams p) {
-  extern __shared__ uint32_t held[];
-  __shared__ PickShared<kPickThreads> sh;
+// ITEMS: tokens of a thread (8 at a time, which one page holds), or 0 for requests of any length.
+template <int NT, int ITEMS>
+__global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
+  __shared__ PickShared<NT> sh;
   __shared__ int begin;
-  __shared__ long long sums[kPickThreads / 32], befores[kPickThreads / 32];
+  __shared__ long long sums[NT / 32], befores[NT / 32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictParams p
   // ---- all requests' pages that go, and those of the requests before this one
   long long gone = 0, before = 0;
   bool bad = false;
-  for (int r = tid; r < p.rq.B; r += kPickThreads) {
+  for (int r = tid; r < p.rq.B; r += NT) {
     const int len = p.rq.kv_lens[r], budget = p.budget[r];
     bad |= len < 0 || len > most || len > 0x7fff0000 || budget < 0;
     const int n = p.pages(len) - p.pages(p.kept(len, budget));
@@ -84,7 +86,7 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictParams p
   if (tid == 0) begin = 0x7fffffff;
   bad = __syncthreads_or(bad);
   gone = before = 0;
-  for (int w = 0; w < kPickThreads / 32; ++w) gone += sums[w], before += befores[w];
+  for (int w = 0; w < NT / 32; ++w) gone += sums[w], before += befores[w];
   const int free_now = *p.free_count;
   bad |= free_now < 0 || free_now + gone > p.rq.num_pages;
   if (blockIdx.x == 0 && tid == 0) {
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictParams p
     if (tid == 0) p.lens_out[b] = kept;
     if (!bad) {
       const int c0 = p.pages(kept), n = p.pages(len) - c0;
-      for (int i = tid; i < n; i += kPickThreads)
+      for (int i = tid; i < n; i += NT)
         p.free_pages[free_now + before + i] = p.rq.table[b * p.rq.table_stride + c0 + i];
     }
   }
@@ -106,37 +108,62 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictParams p
     return;
   }
   // ---- the kept tokens
-  auto weight = [&](int j) {
-    const int page = p.rq.page(b, j >> p.rq.page_shift);
-    return page < 0 ? 0.f
-                    : p.weights[page * p.w_page + head * p.w_head +
-                                (j & ((1 << p.rq.page_shift) - 1))];
-  };
-  const int m = len - p.first - p.recent, k = kept - p.first - p.recent;
-  const bool fits = m <= p.held;
-  if (fits && k > 0)
-    for (int j = tid; j < m; j += kPickThreads) held[j] = order_key(weight(p.first + j));
-  __syncthreads();
-  auto key = [&](int j) { return fits ? held[j] : order_key(weight(p.first + j)); };
-  uint32_t cut = 0xffffffffu;
-  int equals = 0;
-  if (k > 0) equals = pick_cut<kPickThreads>(key, m, k, sh, cut);
-  auto kind = [&](int j) {
-    if (j < p.first || j >= len - p.recent) return 2;
-    if (k == 0) return 0;
-    const uint32_t x = key(j - p.first);
-    return x > cut ? 2 : x == cut ? 1 : 0;
-  };
+  const int in_page = (1 << p.rq.page_shift) - 1;
+  auto always = [&](int j) { return j < p.first || j >= len - p.recent; };
   int mine = 0x7fffffff;
-  pick_words<kPickThreads>(kind, len, equals, sh, [&](int w, uint32_t taken, int at) {
-    for (; taken; taken &= taken - 1, ++at) {
-      const int j = 32 * w + __ffs(taken) - 1;
-      if (j == at) continue;
-      mine = min(mine, at);
-      int* to = p.from_at(b, head, at);
-      if (to) *to = j;
+  auto moves = [&](int j, int at) {  // token j becomes token `at`
+    if (j == at) return;
+    mine = min(mine, at);
+    int* to = p.from_at(b, head, at);
+    if (to) *to = j;
+  };
+  if constexpr (ITEMS > 0) {
+    uint32_t keys[ITEMS];
+    const int j0 = tid * ITEMS;
+#pragma unroll
+    for (int i = 0; i < ITEMS; i += 8) {
+      float w[8] = {};
+      const int page = j0 + i < len ? p.rq.page(b, (j0 + i) >> p.rq.page_shift) : -1;
+      if (page >= 0) {
+        const float* src = p.weights + page * p.w_page + head * p.w_head + ((j0 + i) & in_page);
+        if (p.vec) {
+          const float4 x = *(const float4*)src, y = *(const float4*)(src + 4);
+          w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+          w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+        } else {
+#pragma unroll
+          for (int y = 0; y < 8; ++y) w[y] = src[y];
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const int j = j0 + i + y;
+        keys[i + y] = j >= len ? 0u : always(j) ? kAlways : order_key(w[y]);
+      }
     }
-  });
+    int at;
+    if (kept > 0)
+      for (uint32_t taken = pick_items<NT, ITEMS>(keys, kept, sh, at); taken; taken &= taken - 1)
+        moves(j0 + __ffs(taken) - 1, at++);
+  } else {
+    extern __shared__ __align__(1024) char smem[];
+    uint32_t* held = (uint32_t*)smem;
+    auto look = [&](int j) {
+      if (always(j)) return kAlways;
+      const int page = p.rq.page(b, j >> p.rq.page_shift);
+      return order_key(
+          page < 0 ? 0.f : p.weights[page * p.w_page + head * p.w_head + (j & in_page)]);
+    };
+    const int fits = min(len, p.held);
+#pragma unroll 4
+    for (int j = tid; j < fits; j += NT) held[j] = look(j);
+    __syncthreads();
+    auto key = [&](int j) { return j < fits ? held[j] : look(j); };
+    if (kept > 0)
+      pick_any<NT>(key, len, kept, sh, [&](int w, uint32_t taken, int at) {
+        for (; taken; taken &= taken - 1, ++at) moves(32 * w + __ffs(taken) - 1, at);
+      });
+  }
   mine = __reduce_min_sync(~0u, mine);
   if (lane == 0) atomicMin(&begin, mine);
   __syncthreads();
@@ -144,67 +171,89 @@ __global__ void __launch_bounds__(kPickThreads) k_evict_pick(const EvictParams p
 }
 
 __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const EvictParams p) {
+  constexpr int kWarps = kMoveThreads / 32;
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long task = blockIdx.x * (kMoveThreads / 32ll) + (threadIdx.x >> 5);
-  const int tasks = 2 * p.slices + 1;
-  const long long row = task / tasks;
-  const int slice = (int)(task - row * tasks);
-  if (row >= (long long)p.rq.B * p.kv_heads) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = p.cluster > 1 ? blockIdx.x % p.cluster : 0;
+  const long long row = blockIdx.x / p.cluster;
   const int b = (int)(row / p.kv_heads), head = (int)(row - (long long)b * p.kv_heads);
   const int begin = p.begin[row], kept = p.lens_out[b];
-  if (begin >= kept) return;
+  if (begin >= kept) return;  // (the whole cluster)
   const int len = p.rq.kv_lens[b], mask = (1 << p.rq.page_shift) - 1;
-  // where kept token i comes from; -1 where that cannot be
-  auto source = [&](int i) {
-    const int* at = i < kept ? p.from_at(b, head, i) : nullptr;
-    const int j = at ? *at : -1;
-    return j > i && j < len ? j : -1;
-  };
-  if (slice == 2 * p.slices) {
-    for (int i0 = begin; i0 < kept; i0 += 128) {
-      float got[4];
-      float* to[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + 32 * u + lane, j = source(i);
-        const int src = j < 0 ? -1 : p.rq.page(b, j >> p.rq.page_shift);
-        const int dst = j < 0 ? -1 : p.rq.page(b, i >> p.rq.page_shift);
-        to[u] = src < 0 || dst < 0
-                    ? nullptr
-                    : p.weights + dst * p.w_page + head * p.w_head + (i & mask);
-        if (to[u]) got[u] = p.weights[src * p.w_page + head * p.w_head + (j & mask)];
-      }
-      __syncwarp();
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (to[u]) *to[u] = got[u];
-      __syncwarp();
-    }
-    return;
-  }
-  const bool is_v = slice >= p.slices;
-  const int piece = (is_v ? slice - p.slices : slice) * 4 + (lane & 3);
+  // A warp's lanes take the 16-byte pieces of a token's keys and values, of up to four tokens at
+  // a time; eight times as many are a batch, and a lane keeps what one of those needs.
+  const int pieces = p.dim / 8, at_once = min(32 / (2 * pieces), 4);
+  const int sub = lane / (2 * pieces), piece = lane - sub * 2 * pieces;
+  const bool is_v = piece >= pieces, there = sub < at_once;
+  const int per_warp = 8 * at_once, per_batch = p.cluster * kWarps * per_warp;
   const long long s_page = is_v ? p.v_page : p.k_page, s_token = is_v ? p.v_token : p.k_token;
-  char* base = (is_v ? p.v + head * p.v_head : p.k + head * p.k_head) + piece * 16;
-  const bool there = piece * 8 < p.dim;
-  for (int i0 = begin; i0 < kept; i0 += 64) {
-    uint4 got[8];
-    char* to[8];
+  char* base = is_v ? p.v + head * p.v_head + (piece - pieces) * 16
+                    : p.k + head * p.k_head + piece * 16;
+  struct Token {
+    int src, src_page, dst_page;  // pages < 0: does not move
+  };
+  const long long first = (long long)begin + (rank * kWarps + warp) * per_warp;
+  auto look = [&](long long batch) {
+    const long long i = first + batch * per_batch + lane;
+    Token t = {0, -1, -1};
+    if (lane >= per_warp || i >= kept) return t;
+    const int* at = p.from_at(b, head, (int)i);
+    t.src = at ? *at : -1;
+    if (t.src <= i || t.src >= len) return t;
+    t.src_page = p.rq.page(b, t.src >> p.rq.page_shift);
+    t.dst_page = t.src_page < 0 ? -1 : p.rq.page(b, (int)i >> p.rq.page_shift);
+    return t;
+  };
+  auto load = [&](const Token& t, uint4* got, float& w) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int i = i0 + 8 * u + (lane >> 2), j = there ? source(i) : -1;
-      const int src = j < 0 ? -1 : p.rq.page(b, j >> p.rq.page_shift);
-      const int dst = j < 0 ? -1 : p.rq.page(b, i >> p.rq.page_shift);
-      to[u] = src < 0 || dst < 0 ? nullptr : base + dst * s_page + (i & mask) * s_token;
-      if (to[u]) got[u] = *(const uint4*)(base + src * s_page + (j & mask) * s_token);
+      const int from = there ? u * at_once + sub : 0;
+      const int src = __shfl_sync(~0u, t.src, from), page = __shfl_sync(~0u, t.src_page, from);
+      const bool moves = __shfl_sync(~0u, t.dst_page, from) >= 0 && there;
+      if (moves) got[u] = *(const uint4*)(base + page * s_page + (src & mask) * s_token);
     }
-    __syncwarp();
+    if (t.dst_page >= 0) w = p.weights[t.src_page * p.w_page + head * p.w_head + (t.src & mask)];
+  };
+  auto store = [&](const Token& t, long long batch, const uint4* got, float w) {
+    const long long i0 = first + batch * per_batch;
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (to[u]) *(uint4*)to[u] = got[u];
-    __syncwarp();
+    for (int u = 0; u < 8; ++u) {
+      const int from = there ? u * at_once + sub : 0;
+      const int page = __shfl_sync(~0u, t.dst_page, from);
+      if (page >= 0 && there)
+        *(uint4*)(base + page * s_page + ((int)(i0 + from) & mask) * s_token) = got[u];
+    }
+    if (t.dst_page >= 0)
+      p.weights[t.dst_page * p.w_page + head * p.w_head + ((int)(i0 + lane) & mask)] = w;
+  };
+  auto meet = [&] {
+    if (p.cluster > 1)
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                   ::: "memory");
+    else
+      __syncthreads();
+  };
+  // Everything of a batch is read before any of it is written; the next batch's reads, which no
+  // write of this one can hit, are under way by then.
+  const long long batches = ((long long)kept - begin + per_batch - 1) / per_batch;
+  Token now = look(0), then = look(1);
+  uint4 got[2][8];
+  float w[2];
+  load(now, got[0], w[0]);
+#pragma unroll 1
+  for (long long k = 0; k < batches; k += 2) {
+    Token more = look(k + 2);
+    load(then, got[1], w[1]);
+    meet();
+    store(now, k, got[0], w[0]);
+    if (k + 1 >= batches) break;
+    now = more;
+    more = look(k + 3);
+    load(now, got[0], w[0]);
+    meet();
+    store(then, k + 1, got[1], w[1]);
+    then = more;
   }
 }
 

@@ -181,7 +181,8 @@ __device__ __forceinline__ float2 unpack_pair(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// ---- the k largest of many values, of equal ones the first
+// ---- the k largest of many values, of equal ones the first: no result depends on the order of
+// the threads
 
 // Whole numbers in the order of the values: NaN as +inf, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -190,14 +191,18 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 
+// Items that are taken whatever the others: their key, which no value has.
+constexpr uint32_t kAlways = 0xffffffffu;
+
 template <int NT>
 struct PickShared {
-  int hist[2048];
-  int sums[NT / 32], sums2[NT / 32];
-  int bin, rest;
+  alignas(16) int hist[2048];
+  int sums[2][NT / 32];
+  int bin, rest, count;
 };
 
-// Sum of v over the threads before this one, and over all.
+// Sum of v over the threads before this one, and over all. By the whole block; `sums` is free
+// again after the block's next barrier.
 template <int NT>
 __device__ __forceinline__ int block_before(int v, int* sums, int& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -208,59 +213,107 @@ __device__ __forceinline__ int block_before(int v, int* sums, int& all) {
   }
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  int before = upto - v;
-  all = 0;
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
+  int w = lane < NT / 32 ? sums[lane] : 0;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(~0u, w, d);
+    if (lane >= d) w += x;
   }
-  __syncthreads();
-  return before;
+  all = __shfl_sync(~0u, w, 31);
+  const int before = __shfl_sync(~0u, w, max(warp - 1, 0));
+  return (warp ? before : 0) + upto - v;
 }
 
-// With keys key(0) .. key(m - 1) and 0 < k < m: the key `cut` of which fewer than k keys are
-// greater and at least k greater or equal; returns how many of those equal to it are among the
-// k largest. Three histograms of 11, 11 and 10 bits. By the whole block.
+// The cut of the k largest of all keys, 0 < k: fewer than k keys are above it, and with the first
+// `equals` keys that are equal to it there are k. `count(add)` calls add(key) for each of the
+// thread's keys. Histograms of 11, 11 and 10 bits, of which one is left out when all that the one
+// before it left open is taken. By the whole block.
 template <int NT, typename F>
-__device__ __forceinline__ int pick_cut(F key, int m, int k, PickShared<NT>& sh, uint32_t& cut) {
-  constexpr int kRun = 2048 / NT;  // bins of a thread, from the top
+__device__ __forceinline__ uint32_t pick_cut(F count, int k, PickShared<NT>& sh, int& equals) {
+  constexpr int kRun = 2048 / NT;  // bins of a thread, the first thread's the highest
+  const int low = 2048 - (threadIdx.x + 1) * kRun;
   uint32_t prefix = 0, mask = 0;
+  for (int i = threadIdx.x; i < 2048; i += NT) sh.hist[i] = 0;
+  __syncthreads();
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
+  for (int pass = 0;; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-    for (int i = threadIdx.x; i < 2048; i += NT) sh.hist[i] = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < m; j += NT) {
-      const uint32_t x = key(j);
+    count([&](uint32_t x) {
       if ((x & mask) == prefix) atomicAdd(&sh.hist[x >> shift & (bins - 1)], 1);
-    }
+    });
     __syncthreads();
-    int mine = 0, all;
-    const int top = 2047 - threadIdx.x * kRun;
-    for (int i = 0; i < kRun; ++i) mine += sh.hist[top - i];
-    const int before = block_before<NT>(mine, sh.sums, all);
+    int h[kRun], mine = 0, all;
+#pragma unroll
+    for (int i = 0; i < kRun; i += 2) {
+      const int2 v = *(const int2*)&sh.hist[low + i];
+      *(int2*)&sh.hist[low + i] = make_int2(0, 0);
+      h[i] = v.x, h[i + 1] = v.y;
+      mine += v.x + v.y;
+    }
+    const int before = block_before<NT>(mine, sh.sums[0], all);
     if (before < k && k <= before + mine) {
-      int left = k - before, i = 0;
-      while (left > sh.hist[top - i]) left -= sh.hist[top - i++];
-      sh.bin = top - i;
-      sh.rest = left;
+      int left = k - before;
+#pragma unroll
+      for (int i = kRun - 1; i >= 0; --i) {
+        if (left > 0 && left <= h[i]) sh.bin = low + i, sh.rest = left, sh.count = h[i];
+        left -= h[i];
+      }
     }
     __syncthreads();
     prefix |= (uint32_t)sh.bin << shift;
     mask |= (uint32_t)(bins - 1) << shift;
     k = sh.rest;
+    if (sh.count == k) {  // all of this bin
+      equals = 0;
+      return prefix - 1;  // (prefix > 0, or all keys there are would be taken)
+    }
+    if (pass == 2) break;
     __syncthreads();
   }
-  cut = prefix;
-  return k;
+  equals = k;
+  return prefix;
 }
 
-// Goes over items 0 .. n - 1 in words of 32: kind(j) says whether item j is taken (2), one of
-// equals (1), of which the first `equals` are taken, or not (0). put(w, taken, before) gets word
-// w's bits of taken items and the number of items taken before it. By the whole block.
+// Of the thread's ITEMS keys (items ITEMS * thread .. of the block's) those among the k largest,
+// of equal ones the first, as bits; `before`: how many items are taken before the thread's.
+// Fewer than k items may be there: others have key 0, and k keys are greater. By the whole block.
+template <int NT, int ITEMS>
+__device__ __forceinline__ uint32_t pick_items(const uint32_t* keys, int k, PickShared<NT>& sh,
+                                               int& before) {
+  int equals, all;
+  const uint32_t cut = pick_cut<NT>(
+      [&](auto add) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) add(keys[i]);
+      },
+      k, sh, equals);
+  uint32_t taken = 0, ties = 0;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    taken |= (uint32_t)(keys[i] > cut) << i;
+    ties |= (uint32_t)(keys[i] == cut) << i;
+  }
+  if (equals > 0) {
+    const int at = block_before<NT>(__popc(ties), sh.sums[1], all);
+    for (int x = __popc(ties); x > 0 && at + x > equals; --x) ties &= ~(1u << (31 - __clz(ties)));
+    taken |= ties;
+    __syncthreads();
+  }
+  before = block_before<NT>(__popc(taken), sh.sums[0], all);
+  return taken;
+}
+
+// The same for any number n of items, with key(j) looked at again for every histogram: put(w,
+// taken, before) gets the bits of items 32 w .. that are taken and how many are before them.
 template <int NT, typename K, typename P>
-__device__ __forceinline__ void pick_words(K kind, int n, int equals, PickShared<NT>& sh, P put) {
+__device__ __forceinline__ void pick_any(K key, int n, int k, PickShared<NT>& sh, P put) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int equals, all;
+  const uint32_t cut = pick_cut<NT>(
+      [&](auto add) {
+#pragma unroll 4
+        for (int j = threadIdx.x; j < n; j += NT) add(key(j));
+      },
+      k, sh, equals);
   int ties_before = 0, taken_before = 0;
 #pragma unroll 1
   for (int base = 0; base < n; base += NT * 32) {
@@ -269,19 +322,19 @@ __device__ __forceinline__ void pick_words(K kind, int n, int equals, PickShared
     for (int i = 0; i < 32; ++i) {
       const int j0 = base + (warp * 32 + i) * 32;
       if (j0 >= n) break;
-      const int x = j0 + lane < n ? kind(j0 + lane) : 0;
-      const uint32_t a = __ballot_sync(~0u, x == 2), b = __ballot_sync(~0u, x == 1);
+      const uint32_t x = j0 + lane < n ? key(j0 + lane) : 0;
+      const uint32_t a = __ballot_sync(~0u, j0 + lane < n && x > cut);
+      const uint32_t b = __ballot_sync(~0u, j0 + lane < n && x == cut);
       if (lane == i) sure = a, ties = b;
     }
-    int all;
-    const int before = ties_before + block_before<NT>(__popc(ties), sh.sums, all);
+    __syncthreads();
+    const int at = ties_before + block_before<NT>(__popc(ties), sh.sums[1], all);
     ties_before += all;
-    for (int x = __popc(ties); x > 0 && before + x > equals; --x)
-      ties &= ~(1u << (31 - __clz(ties)));
+    for (int x = __popc(ties); x > 0 && at + x > equals; --x) ties &= ~(1u << (31 - __clz(ties)));
     const uint32_t taken = sure | ties;
-    const int at = taken_before + block_before<NT>(__popc(taken), sh.sums2, all);
+    const int before = taken_before + block_before<NT>(__popc(taken), sh.sums[0], all);
     taken_before += all;
-    put(base / 32 + (int)threadIdx.x, taken, at);
+    put(base / 32 + (int)threadIdx.x, taken, before);
   }
 }
 

@@ -137,6 +137,7 @@ int allow(K kernel, int smem, std::atomic<unsigned long long>& ready) {
   return SPEC_OK;
 }
 
+constexpr int kMostHeld = 48 * 1024;  // keys of a row that is looked at from shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 
 int check_bounds(const spec_cache_bounds_args* a) {
@@ -399,11 +400,24 @@ int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* d
   p.scores = a->scores;
   p.s_token = a->s_token, p.s_head = a->s_head;
   p.out = a->selected;
-  // up to 9216 scores (36 KB) in shared memory, which leaves an SM six blocks
-  p.held = a->width < 9216 ? a->width : 9216;
+  p.vec = aligned(a->scores, 16) && a->s_token % 4 == 0 && a->s_head % 4 == 0;
   const unsigned grid = blocks((long long)a->num_tokens * a->kv_heads);
   if (!grid) return SPEC_ERR_UNSUPPORTED;
-  return launch(sv::k_cache_select, dim3(grid), sv::kSelectThreads, p.held * 4, stream, p);
+  // rows in registers up to 16384 columns, in as few threads as 8 columns each take (16 from 8192)
+  p.held = 0;
+  if (a->width <= 2048)
+    return launch(sv::k_cache_select<256, 8>, dim3(grid), 256, 0, stream, p);
+  if (a->width <= 4096)
+    return launch(sv::k_cache_select<512, 8>, dim3(grid), 512, 0, stream, p);
+  if (a->width <= 8192)
+    return launch(sv::k_cache_select<1024, 8>, dim3(grid), 1024, 0, stream, p);
+  if (a->width <= 16384)
+    return launch(sv::k_cache_select<1024, 16>, dim3(grid), 1024, 0, stream, p);
+  p.held = a->width < kMostHeld ? a->width : kMostHeld;
+  static std::atomic<unsigned long long> ready;
+  const int ok = allow(sv::k_cache_select<1024, 0>, kMostHeld * 4, ready);
+  if (ok != SPEC_OK) return ok;
+  return launch(sv::k_cache_select<1024, 0>, dim3(grid), 1024, p.held * 4, stream, p);
 }
 
 int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* stream,
@@ -537,21 +551,28 @@ int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* dev
   p.begin = (int*)a->workspace;
   p.from = (int*)((char*)a->workspace + ws.from);
   p.by_page = ws.by_page;
-  p.slices = (a->dim * 2 + 63) / 64;
-  // up to 40000 weights (160 KB) in shared memory
-  const long long most = (long long)a->width * a->page_size;
-  p.held = most < 40000 ? (int)most : 40000;
-  static std::atomic<unsigned long long> ready;
-  rc = allow(sv::k_evict_pick, 40000 * 4, ready);
-  if (rc != SPEC_OK) return rc;
+  p.vec = aligned(a->weights, 16) && a->w_page % 4 == 0 && a->w_head % 4 == 0;
   const long long rows = (long long)a->B * a->kv_heads;
-  const long long warps = rows * (2 * p.slices + 1);
-  const unsigned grid = blocks(rows > 0 ? rows : 1);
-  const unsigned moves = blocks((warps + sv::kMoveThreads / 32 - 1) / (sv::kMoveThreads / 32));
+  // clusters where one block for each request and head leaves SMs idle
+  p.cluster = 1;
+  while (p.cluster < 8 && rows * p.cluster < sms) p.cluster *= 2;
+  const unsigned grid = blocks(rows > 0 ? rows : 1), moves = blocks(rows * p.cluster);
   if (!grid || (rows > 0 && !moves)) return SPEC_ERR_UNSUPPORTED;
-  rc = launch(sv::k_evict_pick, dim3(grid), sv::kPickThreads, p.held * 4, stream, p);
+  // weights in registers up to 16384 tokens, as in spec_cache_select
+  const long long most = (long long)a->width * a->page_size;
+  if (most <= 4096) {
+    rc = launch(sv::k_evict_pick<512, 8>, dim3(grid), 512, 0, stream, p);
+  } else if (most <= 16384) {
+    rc = launch(sv::k_evict_pick<1024, 16>, dim3(grid), 1024, 0, stream, p);
+  } else {
+    p.held = most < kMostHeld ? (int)most : kMostHeld;
+    static std::atomic<unsigned long long> ready;
+    rc = allow(sv::k_evict_pick<1024, 0>, kMostHeld * 4, ready);
+    if (rc != SPEC_OK) return rc;
+    rc = launch(sv::k_evict_pick<1024, 0>, dim3(grid), 1024, p.held * 4, stream, p);
+  }
   if (rc != SPEC_OK || rows == 0) return rc;
-  return launch(sv::k_evict_move, dim3(moves), sv::kMoveThreads, 0, stream, p);
+  return launch_cluster(sv::k_evict_move, p.cluster, dim3(moves), sv::kMoveThreads, 0, stream, p);
 }
 
 }  // extern "C"
