@@ -275,7 +275,7 @@ __device__ __forceinline__ uint32_t pick_cut(F count, int k, PickShared<NT>& sh,
 
 // Of the thread's ITEMS keys (items ITEMS * thread .. of the block's) those among the k largest,
 // of equal ones the first, as bits; `before`: how many items are taken before the thread's.
-// Fewer than k items may be there: others have key 0, and k keys are greater. By the whole block.
+// Items that are not there have key 0; k are. By the whole block.
 template <int NT, int ITEMS>
 __device__ __forceinline__ uint32_t pick_items(const uint32_t* keys, int k, PickShared<NT>& sh,
                                                int& before) {
@@ -283,7 +283,8 @@ __device__ __forceinline__ uint32_t pick_items(const uint32_t* keys, int k, Pick
   const uint32_t cut = pick_cut<NT>(
       [&](auto add) {
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) add(keys[i]);
+        for (int i = 0; i < ITEMS; ++i)
+          if (keys[i]) add(keys[i]);
       },
       k, sh, equals);
   uint32_t taken = 0, ties = 0;

@@ -405,8 +405,8 @@ int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* d
   if (!grid) return SPEC_ERR_UNSUPPORTED;
   // rows in registers up to 16384 columns, in as few threads as 8 columns each take (16 from 8192)
   p.held = 0;
-  if (a->width <= 2048)
-    return launch(sv::k_cache_select<256, 8>, dim3(grid), 256, 0, stream, p);
+  if (a->width <= sv::kShortColumns)
+    return launch(sv::k_cache_select_short, dim3(grid), sv::kShortThreads, 0, stream, p);
   if (a->width <= 4096)
     return launch(sv::k_cache_select<512, 8>, dim3(grid), 512, 0, stream, p);
   if (a->width <= 8192)
