@@ -63,9 +63,9 @@ struct SelCfg {
   static_assert((kSelWarps + 1) * kCols * (kPitch + 2) * 4 <= kRing, "partial results in the ring");
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const char* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16 : 0)
+// 16 bytes to shared memory: `bytes` (0 or 16) from src, zeros for the others.
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     k_attend_selected(const __grid_constant__ SelectedParams p) {
   using Cfg = SelCfg<DP, N8>;
   constexpr float kBias = sel_bias<BF16>();
+  constexpr float kNone = -3e38f;       // the maximum of no score: finite, so that P is 0
   constexpr int kLanes = DP / 8;        // lanes that copy a row's 16-byte pieces
   constexpr int kRows = 32 / kLanes;    // rows of one copy instruction
   extern __shared__ __align__(1024) char smem[];
@@ -152,6 +153,8 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     const int heads = min(p.unit_heads, p.G - split * p.unit_heads);
     const int columns = g.tokens * heads;
     const int steps = (p.dim + 15) / 16, pieces = p.dim / 8;
+    const float factor = fabsf(p.c);
+    const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;
     // Q as operands, from memory: two channels of one column at a time
     for (int i = tid; i < N8 * (DP / 16) * 32; i += kSelThreads) {
       const int n8 = i / ((DP / 16) * 32), step = i / 32 % (DP / 16);
@@ -161,17 +164,18 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         const int tok = column / heads;
         const char* src = p.q + (long long)(g.token + tok) * p.q_token +
                           (long long)(head0 + column - tok * heads) * p.q_head + ch * 2;
-        if (ch < p.dim) v.x = *(const uint32_t*)src;
-        if (ch + 8 < p.dim) v.y = *(const uint32_t*)(src + 16);
+        // (a negative factor of the scores is Q's sign)
+        if (ch < p.dim) v.x = *(const uint32_t*)src ^ flip;
+        if (ch + 8 < p.dim) v.y = *(const uint32_t*)(src + 16) ^ flip;
       }
       q_frag[i] = v;
     }
-    // the token of each of the lane's columns, 8 for none, four bits each
-    uint32_t token_of = 0;
+    // the tokens of the lane's columns, a byte with one bit for each (none: no such column)
+    uint32_t token_of[(2 * N8 + 3) / 4] = {};
 #pragma unroll
     for (int y = 0; y < 2 * N8; ++y) {
       const int column = (y >> 1) * 8 + 2 * c + (y & 1);
-      token_of |= (column < columns ? (uint32_t)(column / heads) : 8u) << (4 * y);
+      if (column < columns) token_of[y / 4] |= 1u << (column / heads + 8 * (y & 3));
     }
     const uint32_t everyone = (1u << g.tokens) - 1;
     const int last = g.pos + g.tokens - 1;                       // the last token's position
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     float m[N8][2], l[N8][2], o[DP / 16][N8][4];
 #pragma unroll
     for (int n = 0; n < N8; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = kNone;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int y = 0; y < DP / 16; ++y) o[y][n][0] = o[y][n][1] = o[y][n][2] = o[y][n][3] = 0.f;
@@ -199,6 +203,17 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       }
       return col < visible && ((long long)col << shift) <= g.pos + k ? col : -1;
     };
+    // the lane's place in a copy of rows: 16 bytes of a key
+    const int piece = lane & (kLanes - 1), lane_row = lane / kLanes;
+    const bool copies = piece < pieces;
+    const char* k_lane = p.k + kv_head * p.k_head + lane_row * p.k_token + piece * 16;
+    const char* v_lane = p.v + kv_head * p.v_head + lane_row * p.v_token + piece * 16;
+    uint32_t lane_dst[8 / kRows];
+#pragma unroll
+    for (int y = 0; y < 8 / kRows; ++y) {
+      const int r = y * kRows + lane_row;
+      lane_dst[y] = r * (DP * 2) + ((piece ^ r) & 7) * 16 + (piece & 8) * 16;
+    }
     const bool one = g.tokens == 1;
     // One token's list is taken in parts of what the block lists at a time; of several tokens
     // the host made sure that all their pages fit.
@@ -251,41 +266,39 @@ __global__ void __launch_bounds__(kSelThreads, 2)
           *(uint4*)(ring + 16 * i) = make_uint4(0, 0, 0, 0);
         __syncwarp();
       }
-      const int tiles = (int)(((long long)n * page_size + 15) / 16);
+      const int tiles = (n * page_size + 15) / 16;
       const int from = rank * kSelWarps + warp, step = p.cluster * kSelWarps;
       uint32_t seen_by = 0;  // of key lane % 16 of the tiles in flight: bits of tokens, the
                              // youngest tile's lowest
       auto issue = [&](int tile, int stage) {
         uint32_t mine = 0;
         if (tile < tiles) {
+          // the lane's key (lanes 16 and up have those of 0 to 15 again), and who sees it
+          const int key = 16 * tile + (lane & 15), e = key >> shift;
+          int page = -1;
+          if (e < n) {
+            page = list.page[e];
+            const int ahead = (int)(((long long)list.col[e] << shift) +
+                                    (key & (page_size - 1)) - g.pos);
+            if (page >= 0 && ahead < kSelTokens)
+              mine = list.mask[e] & (everyone << max(ahead, 0));
+          }
+          const uint32_t seen = __ballot_sync(~0u, mine != 0) >> (lane / kLanes);
           const uint32_t dst = ring_at + stage * 2 * Cfg::kTile;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // 8 keys of one page
-            const long long key = 16ll * tile + 8 * half;
-            const int e = (int)(key >> shift), off = (int)key & (page_size - 1);
-            int page = -1, col = 0;
-            uint32_t mask = 0;
-            if (e < n) page = list.page[e], col = list.col[e], mask = list.mask[e];
-            if (page < 0) mask = 0;
-            const int ahead = (int)(((long long)col << shift) + off - g.pos);
-            // the tokens that see key r of the 8
-            auto see = [&](int r) {
-              const int z = ahead + r;
-              return z <= 0 ? mask : z >= kSelTokens ? 0u : mask & (everyone << z);
-            };
-            if ((lane >> 3 & 1) == half) mine = see(lane & 7);
-            const char* ks = p.k + page * p.k_page + off * p.k_token + kv_head * p.k_head;
-            const char* vs = p.v + page * p.v_page + off * p.v_token + kv_head * p.v_head;
-            const int piece = lane & (kLanes - 1);
-            if (piece < pieces) {
+            const long long at = max(__shfl_sync(~0u, page, 8 * half), 0);
+            const int off = (16 * tile + 8 * half) & (page_size - 1);
+            const char* ks = k_lane + at * p.k_page + off * p.k_token;
+            const char* vs = v_lane + at * p.v_page + off * p.v_token;
+            if (copies) {
 #pragma unroll
               for (int y = 0; y < 8 / kRows; ++y) {
-                const int r = y * kRows + lane / kLanes;
-                const bool there = see(r) != 0;
-                const uint32_t to = dst + (8 * half + r) * (DP * 2) + ((piece ^ r) & 7) * 16 +
-                                    (piece & 8) * 16;
-                copy16(to, there ? ks + r * p.k_token + piece * 16 : p.k, there);
-                copy16(to + Cfg::kTile, there ? vs + r * p.v_token + piece * 16 : p.v, there);
+                const uint32_t bytes = seen >> (8 * half + y * kRows) << 4 & 16;
+                copy16(dst + lane_dst[y] + 8 * half * (DP * 2), ks, bytes);
+                copy16(dst + lane_dst[y] + 8 * half * (DP * 2) + Cfg::kTile, vs, bytes);
+                ks += kRows * p.k_token;
+                vs += kRows * p.v_token;
               }
             }
           }
@@ -319,26 +332,22 @@ __global__ void __launch_bounds__(kSelThreads, 2)
             mma_16816<BF16>(s[n8], a[0], a[1], a[2], a[3], b.x, b.y);
           }
         }
-#pragma unroll
-        for (int n8 = 0; n8 < N8; ++n8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) s[n8][y] *= p.c;
         if (!__all_sync(~0u, seen == everyone)) {
-          const uint32_t k0 = __shfl_sync(~0u, seen, x), k1 = __shfl_sync(~0u, seen, x + 8);
+          const uint32_t k0 = __shfl_sync(~0u, seen, x) * 0x01010101u;
+          const uint32_t k1 = __shfl_sync(~0u, seen, x + 8) * 0x01010101u;
 #pragma unroll
-          for (int n8 = 0; n8 < N8; ++n8)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t bit = token_of >> (4 * (2 * n8 + y)) & 15;
-              if (!(k0 >> bit & 1)) s[n8][y] = -INFINITY;
-              if (!(k1 >> bit & 1)) s[n8][y + 2] = -INFINITY;
-            }
+          for (int y = 0; y < 2 * N8; ++y) {
+            const uint32_t bits = token_of[y / 4] & 255u << (8 * (y & 3));
+            if (!(k0 & bits)) s[y >> 1][y & 1] = -INFINITY;
+            if (!(k1 & bits)) s[y >> 1][(y & 1) + 2] = -INFINITY;
+          }
         }
         bool grown = false;
 #pragma unroll
         for (int n8 = 0; n8 < N8; ++n8)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) grown |= fmaxf(s[n8][y], s[n8][y + 2]) > m[n8][y] + 8.f;
+          for (int y = 0; y < 2; ++y)
+            grown |= fmaf(fmaxf(s[n8][y], s[n8][y + 2]), factor, -m[n8][y]) > 8.f;
         if (__any_sync(~0u, grown)) {
 #pragma unroll
           for (int n8 = 0; n8 < N8; ++n8)
@@ -346,8 +355,8 @@ __global__ void __launch_bounds__(kSelThreads, 2)
             for (int y = 0; y < 2; ++y) {
               float top = fmaxf(s[n8][y], s[n8][y + 2]);
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-              top = fmaxf(top, m[n8][y]);
-              const float keep = m[n8][y] == -INFINITY ? 0.f : ex2(m[n8][y] - top);
+              top = top == -INFINITY ? m[n8][y] : fmaxf(top * factor, m[n8][y]);
+              const float keep = m[n8][y] == kNone ? 0.f : ex2(m[n8][y] - top);
               m[n8][y] = top;
               l[n8][y] *= keep;
 #pragma unroll
@@ -359,9 +368,8 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         for (int n8 = 0; n8 < N8; ++n8) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float base = kBias - (m[n8][y] == -INFINITY ? 0.f : m[n8][y]);
-            s[n8][y] = ex2(s[n8][y] + base);
-            s[n8][y + 2] = ex2(s[n8][y + 2] + base);
+            s[n8][y] = ex2(fmaf(s[n8][y], factor, kBias - m[n8][y]));
+            s[n8][y + 2] = ex2(fmaf(s[n8][y + 2], factor, kBias - m[n8][y]));
             l[n8][y] += s[n8][y] + s[n8][y + 2];
           }
           b[n8][0] = transposed(pack_pair<BF16>(s[n8][0], s[n8][1]));
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
         const int column = n8 * 8 + 2 * c + y;
         if (x == 0) {
-          part_m[warp * Cfg::kCols + column] = m[n8][y];
+          part_m[warp * Cfg::kCols + column] = m[n8][y] == kNone ? -INFINITY : m[n8][y];
           part_l[warp * Cfg::kCols + column] = sum;
         }
         float* to = part_o + (warp * Cfg::kCols + column) * Cfg::kPitch + x;
