@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
       for (uint32_t taken = pick_items<NT, ITEMS>(keys, kept, sh, at); taken; taken &= taken - 1)
         moves(j0 + __ffs(taken) - 1, at++);
   } else {
-    extern __shared__ __align__(1024) char smem[];
+    extern __shared__ __align__(128) char smem[];
     uint32_t* held = (uint32_t*)smem;
     auto look = [&](int j) {
       if (always(j)) return kAlways;

@@ -172,7 +172,8 @@ struct WeighWalk {
 
 __global__ void __launch_bounds__(kWeighThreads, 1)
     k_cache_weigh(const __grid_constant__ WeighParams p, const int run) {
-  extern __shared__ __align__(1024) char smem[];
+  extern __shared__ __align__(1024) char weigh_smem[];
+  char* smem = weigh_smem;
   WeighShared& sh = *reinterpret_cast<WeighShared*>(smem + kWeighStages);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int stage_bytes = p.blocks * kWeighTile * 128;

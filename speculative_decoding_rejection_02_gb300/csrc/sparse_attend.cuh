@@ -28,8 +28,7 @@
 namespace sv {
 
 constexpr int kSelWarps = 4, kSelThreads = 32 * kSelWarps;
-constexpr int kSelStages = 3;
-constexpr int kSelList = 768;    // pages that a block lists at a time
+constexpr int kSelList = 640;    // pages that a block lists at a time
 constexpr int kSelTokens = 8;    // bits of a page's byte
 
 struct SelectedParams {
@@ -54,12 +53,17 @@ struct SelectedParams {
 
 template <int DP, int N8>
 struct SelCfg {
+  // Two tiles of each warp and three blocks on an SM, or three and two where the registers do not
+  // allow three blocks: twelve warps hide latency better than eight with more tiles in flight (183
+  // us in place of 171).
+  static constexpr int kStages = N8 <= 2 ? 2 : 3, kBlocks = N8 <= 2 ? 3 : 2;
   static constexpr int kTile = 16 * DP * 2;                       // bytes of 16 keys
-  static constexpr int kRing = kSelWarps * kSelStages * 2 * kTile;
+  static constexpr int kRing = kSelWarps * kStages * 2 * kTile;
   static constexpr int kQ = N8 * (DP / 16) * 256;                 // [n8][step][lane] 8 bytes
   static constexpr int kCols = 8 * N8;
   static constexpr int kPitch = DP + 4;                           // floats of a column's partial O
   static constexpr int kSmem = kRing + kQ + kSelList * 9;
+  static_assert(kBlocks * (kSmem + 2048) <= 228 * 1024, "blocks of an SM");
   static_assert((kSelWarps + 1) * kCols * (kPitch + 2) * 4 <= kRing, "partial results in the ring");
 };
 
@@ -120,14 +124,14 @@ struct SelList {
 };
 
 template <int DP, int N8, bool BF16>
-__global__ void __launch_bounds__(kSelThreads, 2)
+__global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8>::kBlocks)
     k_attend_selected(const __grid_constant__ SelectedParams p) {
   using Cfg = SelCfg<DP, N8>;
   constexpr float kBias = sel_bias<BF16>();
   constexpr float kNone = -3e38f;       // the maximum of no score: finite, so that P is 0
   constexpr int kLanes = DP / 8;        // lanes that copy a row's 16-byte pieces
   constexpr int kRows = 32 / kLanes;    // rows of one copy instruction
-  extern __shared__ __align__(1024) char smem[];
+  extern __shared__ __align__(128) char smem[];
   __shared__ GroupShared<kSelThreads> sh;
   __shared__ int sums[kSelWarps], listed;
   pdl_trigger();
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   unit /= p.kv_heads;
   const TokenGroup g = find_group<kSelThreads>(p.rq, unit, p.per, sh);
   if (g.b >= 0) {
-    char* ring = smem + warp * kSelStages * 2 * Cfg::kTile;
+    char* ring = smem + warp * Cfg::kStages * 2 * Cfg::kTile;
     const uint32_t ring_at = smem_addr(ring);
     uint2* q_frag = (uint2*)(smem + Cfg::kRing);
     SelList list;
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       __syncthreads();
       const int n = listed;
       if (p.dim % 16) {  // channels that the products take beside those that there are
-        for (int i = lane; i < 2 * kSelStages * Cfg::kTile / 16; i += 32)
+        for (int i = lane; i < 2 * Cfg::kStages * Cfg::kTile / 16; i += 32)
           *(uint4*)(ring + 16 * i) = make_uint4(0, 0, 0, 0);
         __syncwarp();
       }
@@ -307,16 +311,16 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         copy_commit();
       };
 #pragma unroll
-      for (int i = 0; i < kSelStages - 1; ++i) issue(from + i * step, i);
+      for (int i = 0; i < Cfg::kStages - 1; ++i) issue(from + i * step, i);
       int stage = 0;
 #pragma unroll 1
       for (int tile = from; tile < tiles; tile += step) {
-        copy_wait<kSelStages - 2>();
+        copy_wait<Cfg::kStages - 2>();
         __syncwarp();
-        issue(tile + (kSelStages - 1) * step, stage == 0 ? kSelStages - 1 : stage - 1);
-        const uint32_t seen = seen_by >> (8 * (kSelStages - 1)) & 255;
+        issue(tile + (Cfg::kStages - 1) * step, stage == 0 ? Cfg::kStages - 1 : stage - 1);
+        const uint32_t seen = seen_by >> (8 * (Cfg::kStages - 1)) & 255;
         const uint32_t k_at = ring_at + stage * 2 * Cfg::kTile, v_at = k_at + Cfg::kTile;
-        stage = stage == kSelStages - 1 ? 0 : stage + 1;
+        stage = stage == Cfg::kStages - 1 ? 0 : stage + 1;
         float s[N8][4];
 #pragma unroll
         for (int n8 = 0; n8 < N8; ++n8) s[n8][0] = s[n8][1] = s[n8][2] = s[n8][3] = 0.f;

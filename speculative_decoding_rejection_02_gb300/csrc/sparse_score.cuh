@@ -55,7 +55,7 @@ __device__ __forceinline__ void split3(float x, float* part) {
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kScoreThreads) k_cache_score(const ScoreParams p) {
   using Cfg = ScoreCfg<DP>;
-  extern __shared__ __align__(1024) char smem[];
+  extern __shared__ __align__(128) char smem[];
   __shared__ GroupShared<kScoreThreads> sh;
   __shared__ float unscale[kScoreGroups * kScoreGroup];
   pdl_trigger();

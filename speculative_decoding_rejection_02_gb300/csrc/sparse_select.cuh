@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(NT) k_cache_select(const SelectParams p) {
     for (uint32_t taken = pick_items<NT, ITEMS>(keys, p.count, sh, at); taken; taken &= taken - 1)
       out[at++] = c0 + __ffs(taken) - 1;
   } else {
-    extern __shared__ __align__(1024) char smem[];
+    extern __shared__ __align__(128) char smem[];
     uint32_t* held = (uint32_t*)smem;
     auto look = [&](int c) { return always(c) ? kAlways : order_key(row[c]); };
     const int fits = min(n, p.held);

@@ -451,8 +451,8 @@ int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* s
   // a kv head's query heads in units of 32 at most, and as many tokens of a request (if there may
   // be several) as 16 columns, the block's list and the bytes over its ring take. With 32 columns
   // a page is loaded for more tokens, but the block has half as much to hide latency with: 64
-  // requests of 2-8 tokens over 128 pages of 16, four heads on a kv head, 212 us in place of 183;
-  // with 8 columns 202 us.
+  // requests of 2-8 tokens over 128 pages of 16, four heads on a kv head, 212 us in place of 183
+  // (with eight warps on an SM); with 8 columns 202 us.
   p.unit_heads = p.G < 32 ? p.G : 32;
   p.splits = (p.G + p.unit_heads - 1) / p.unit_heads;
   p.per = 1;
@@ -468,7 +468,7 @@ int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* s
   // clusters of blocks where the units leave SMs idle, as long as each warp keeps two tiles
   const long long tiles = (long long)a->count * a->page_size / 16;
   p.cluster = 1;
-  while (p.cluster < 8 && units * p.cluster < 2ll * sms &&
+  while (p.cluster < 8 && units * p.cluster < 3ll * sms &&
          tiles >= 4ll * p.cluster * sv::kSelWarps)
     p.cluster *= 2;
   const unsigned grid = blocks(units * p.cluster);
