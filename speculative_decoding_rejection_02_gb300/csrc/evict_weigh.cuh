@@ -131,9 +131,9 @@ struct WeighWalk {
     end = sh.end;
     if (b < 0) return false;
     u = WeighUnit(p, b);
-    const long long skip = (sh.begin - at + u.cost - 1) / u.cost;
+    const long long skip = quotient(sh.begin - at + u.cost - 1, u.cost);
     at += skip * u.cost;
-    head = u.pairs ? (int)(skip / u.pairs) : p.kv_heads;
+    head = u.pairs ? (int)quotient(skip, u.pairs) : p.kv_heads;
     pair = u.pairs ? (int)(skip - (long long)head * u.pairs) : 0;
     fresh = true;
     return settle(p);
@@ -232,9 +232,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       if (w < warp) before += sh.sums[w];
       total += sh.sums[w];
     }
-    const long long begin = total / gridDim.x * blockIdx.x +
-                            min((long long)blockIdx.x, total % gridDim.x);
-    const long long end = begin + total / gridDim.x + (blockIdx.x < total % gridDim.x);
+    const long long each = quotient(total, gridDim.x), more = total - each * gridDim.x;
+    const long long begin = each * blockIdx.x + min((long long)blockIdx.x, more);
+    const long long end = begin + each + ((long long)blockIdx.x < more);
     if (before <= begin && begin < before + mine) {
       int r = r0;
       if (run > 1)

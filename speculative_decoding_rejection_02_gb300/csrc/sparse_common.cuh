@@ -12,6 +12,11 @@
 
 namespace sv {
 
+// a / b of numbers that are not negative; most fit 32 bits, whose division is much shorter.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 struct Requests {
   int B, T, width, page_shift;
   long long table_stride, num_pages;

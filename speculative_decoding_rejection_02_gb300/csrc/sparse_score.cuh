@@ -13,6 +13,11 @@
 // registers (a warp has 16 pages, 8 KB at dim 128, in flight). A lane loads 16 bytes, 8 channels,
 // of a row: the order of the channels in the sums is free, so they go into the products as they
 // come, and [N, P] lies in shared memory in the same order.
+//
+// Work is one list of 16 columns for each group of tokens and kv head, cut into equal parts, one for
+// each block: what a block has to do before its first product (find its part, split [N, P]) takes
+// longer than some tens of columns. (A grid over groups, heads and thirds of the columns: 64
+// requests of 2-8 tokens over 1000-30000, 55 us in place of XX.)
 #pragma once
 #include "sparse_common.cuh"
 
@@ -20,7 +25,8 @@ namespace sv {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreGroup = 8;    // tokens of a product
-constexpr int kScoreGroups = 4;   // of those in a block, at most
+constexpr int kScoreGroups = 4;   // of those in a group of tokens, at most
+constexpr int kScoreBlocks = 4;   // of an SM
 
 struct ScoreParams {
   Requests rq;
@@ -31,8 +37,7 @@ struct ScoreParams {
   long long b_page, b_head, b_side;
   float* scores;
   long long s_token, s_head;
-  int per;     // tokens of a block
-  int spread;  // blocks of a group of tokens and a head
+  int per;  // tokens of a group
 };
 
 template <int DP>
@@ -52,93 +57,192 @@ __device__ __forceinline__ void split3(float x, float* part) {
   }
 }
 
+// What a request is in the list that the blocks divide: for each kv head and group of tokens
+// `reals` places of 16 columns that some token may see, then `fills` places of 128 that none does.
+struct ScoreUnits {
+  int lo, hi, len, groups, reals, fills;
+  __device__ __forceinline__ ScoreUnits() {}
+  __device__ __forceinline__ ScoreUnits(const ScoreParams& p, int b) {
+    len = p.rq.request(b, lo, hi);
+    groups = (hi - lo + p.per - 1) / p.per;
+    const long long held = ((long long)len + (1 << p.rq.page_shift) - 1) >> p.rq.page_shift;
+    reals = (int)((held + 15) / 16);
+    fills = ((int)(((long long)p.rq.width + 15) / 16) - reals + 7) / 8;
+  }
+  __device__ __forceinline__ long long places(const ScoreParams& p) const {
+    return (long long)groups * (reals + fills) * p.kv_heads;
+  }
+};
+
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(kScoreThreads) k_cache_score(const ScoreParams p) {
+__global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
+    k_cache_score(const ScoreParams p, const int run) {
   using Cfg = ScoreCfg<DP>;
+  constexpr int kWarps = kScoreThreads / 32;
   extern __shared__ __align__(128) char smem[];
-  __shared__ GroupShared<kScoreThreads> sh;
   __shared__ float unscale[kScoreGroups * kScoreGroup];
+  __shared__ long long sums[kWarps], sh_at, sh_begin, sh_end;
+  __shared__ int pads[kWarps], gap[kWarps], sh_first;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, x = lane >> 2, c = lane & 3;
-  const int part = blockIdx.x % p.spread;
-  const long long unit = blockIdx.x / p.spread / p.kv_heads;
-  const int head = (int)(blockIdx.x / p.spread - unit * p.kv_heads);
-  const TokenGroup g = find_group<kScoreThreads>(p.rq, unit, p.per, sh);
-  if (g.b >= 0) {
-    // [N, P] of 8 tokens: a thread takes 8 channels of a token (DP / 8 <= 16 pieces)
-    const int groups = (g.tokens + kScoreGroup - 1) / kScoreGroup;
-    for (int i = tid; i < groups * kScoreGroup * 16; i += kScoreThreads) {
-      const int tok = i >> 4, piece = i & 15;
-      float up[8], down[8], top = 0.f;
-#pragma unroll
-      for (int y = 0; y < 8; ++y) up[y] = down[y] = 0.f;
-      if (tok < g.tokens && piece * 8 < p.dim) {
-        const char* src = p.q + (long long)(g.token + tok) * p.q_token +
-                          (long long)head * p.G * p.q_head + piece * 16;
-        for (int h = 0; h < p.G; ++h) {
-          const uint4 v = *(const uint4*)(src + h * p.q_head);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float2 f = unpack_pair<BF16>(w[y]);
-            // (not fmaxf, which would take 0 in place of NaN)
-            up[2 * y] += f.x < 0.f ? 0.f : f.x;
-            up[2 * y + 1] += f.y < 0.f ? 0.f : f.y;
-            down[2 * y] += f.x > 0.f ? 0.f : f.x;
-            down[2 * y + 1] += f.y > 0.f ? 0.f : f.y;
-          }
+  // ---- this block's part of the list
+  TokenGroup idle = {};
+  {
+    const int r0 = (int)min((long long)tid * run, (long long)p.rq.B), r1 = min(r0 + run, p.rq.B);
+    long long mine = 0;
+    int pad = 0, gaps = 0;
+    for (int r = r0; r < r1; ++r) {
+      const ScoreUnits u(p, r);
+      mine += u.places(p);
+      pad = max(pad, u.hi);
+      gaps |= u.lo < 0 || (r == 0 && u.lo > 0);
+    }
+    long long upto = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(~0u, upto, d);
+      if (lane >= d) upto += y;
+    }
+    pad = __reduce_max_sync(~0u, pad);
+    gaps = __any_sync(~0u, gaps);
+    if (lane == 31) sums[warp] = upto;
+    if (lane == 0) pads[warp] = pad, gap[warp] = gaps;
+    if (tid == 0) sh_first = -1;
+    __syncthreads();
+    long long before = upto - mine, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+      idle.pad = max(idle.pad, pads[w]);
+      idle.gaps |= gap[w];
+    }
+    const long long each = quotient(total, gridDim.x), more = total - each * gridDim.x;
+    const long long begin = each * blockIdx.x + min((long long)blockIdx.x, more);
+    if (before <= begin && begin < before + mine) {
+      int r = r0;
+      if (run > 1)
+        for (;; ++r) {
+          const long long n = ScoreUnits(p, r).places(p);
+          if (begin < before + n || r + 1 >= r1) break;
+          before += n;
         }
-#pragma unroll
-        for (int y = 0; y < 8; ++y) top = fmaxf(top, fmaxf(up[y], -down[y]));
-      }
-      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      // 2^14 <= top * scale < 2^15; the least values need no more than 2^100
-      int e = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
-      e = min(max(e, -100), 100);
-      const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
-      if (piece == 0) unscale[tok] = __uint_as_float((uint32_t)(127 - e) << 23);
-      if (piece * 8 < DP) {
-        char* dst = smem + (tok >> 3) * Cfg::kGroupBytes + (piece >> 2) * 3 * 512 +
-                    ((tok & 7) * 4 + (piece & 3)) * 16;
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          uint32_t w[3][4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float a[3], b[3];
-            split3<BF16>((side ? up : down)[2 * y] * scale, a);
-            split3<BF16>((side ? up : down)[2 * y + 1] * scale, b);
-#pragma unroll
-            for (int z = 0; z < 3; ++z) w[z][y] = pack_pair<BF16>(a[z], b[z]);
-          }
-#pragma unroll
-          for (int z = 0; z < 3; ++z)
-            *(uint4*)(dst + side * (Cfg::kChunks / 2) * 3 * 512 + z * 512) =
-                make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]);
-        }
-      }
+      sh_first = r;
+      sh_at = before;
+      sh_begin = begin;
+      sh_end = begin + each + ((long long)blockIdx.x < more);
     }
     __syncthreads();
-    const int last = g.pos + g.tokens - 1;  // position of the last token
-    const int seen = last < 0 ? 0 : (last >> p.rq.page_shift) + 1;  // columns
-    const char* base = p.bounds + head * p.b_head + 16 * c;
-    const bool there[4] = {8 * c < p.dim, 32 + 8 * c < p.dim, 64 + 8 * c < p.dim,
-                           96 + 8 * c < p.dim};
-    float* row = p.scores + (long long)g.token * p.s_token + head * p.s_head;
-    const int step = p.spread * (kScoreThreads / 32) * 16;
+  }
+  int b = sh_first;
+  if (b >= 0) {
+    // walk: place `at` of request b, up to the end of the part
+    long long left = sh_end - sh_begin, at = sh_begin - sh_at;
 #pragma unroll 1
-    for (long long col0 = ((long long)part * (kScoreThreads / 32) + warp) * 16; col0 < p.rq.width;
-         col0 += step) {
-      const int col[2] = {(int)col0 + x, (int)col0 + x + 8};
-      bool live[2];
-      uint4 a[2][Cfg::kChunks];
-      if (col0 < seen) {
+    while (left > 0) {
+      const ScoreUnits u(p, b);
+      const long long all = u.places(p);
+      if (at >= all) {  // (the next request; the part does not end behind the last)
+        at -= all;
+        if (++b >= p.rq.B) break;
+        continue;
+      }
+      const int per_unit = u.reals + u.fills;
+      const long long unit = quotient(at, per_unit);
+      const int from = (int)(at - unit * per_unit);
+      const int to = (int)min((long long)per_unit, from + left);
+      const int head = (int)quotient(unit, u.groups), first = (int)(unit - (long long)head * u.groups) * p.per;
+      const int tokens = min(p.per, u.hi - u.lo - first), token = u.lo + first;
+      const int pos = u.len ? u.len - (u.hi - u.lo) + first : -(1 << 30);
+      left -= to - from;
+      at += to - from;
+      float* row = p.scores + (long long)token * p.s_token + head * p.s_head;
+      // columns that nobody sees
+      for (int i = max(from - u.reals, 0) + warp; i < to - u.reals; i += kWarps)
+        for (int t = 0; t < tokens; ++t)
+          for (int col = u.reals * 16 + i * 128 + lane;
+               col < min((long long)p.rq.width, u.reals * 16ll + (i + 1) * 128ll); col += 32)
+            row[t * p.s_token + col] = -INFINITY;
+      if (from >= u.reals) continue;
+      const int columns = (int)(((long long)u.len + (1 << p.rq.page_shift) - 1) >> p.rq.page_shift);
+      // the page numbers of the lane's columns x and x + 8 of a place, which are looked up one
+      // place ahead; -1: none
+      auto look = [&](int i, int* page) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int page = col[r] < seen ? p.rq.page(g.b, col[r]) : -1;
-          live[r] = page >= 0;
-          const char* src = base + page * p.b_page;
+          const int col = 16 * i + x + 8 * r;
+          page[r] = i < u.reals && col < columns ? p.rq.table[b * p.rq.table_stride + col] : -1;
+        }
+      };
+      int next[2];
+      look(from + warp, next);
+      __syncthreads();  // (the unit before has been done with)
+      // [N, P] of 8 tokens: a thread takes 8 channels of a token (DP / 8 <= 16 pieces)
+      const int groups = (tokens + kScoreGroup - 1) / kScoreGroup;
+      for (int i = tid; i < groups * kScoreGroup * 16; i += kScoreThreads) {
+        const int tok = i >> 4, piece = i & 15;
+        float up[8], down[8], top = 0.f;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) up[y] = down[y] = 0.f;
+        if (tok < tokens && piece * 8 < p.dim) {
+          const char* src = p.q + (long long)(token + tok) * p.q_token +
+                            (long long)head * p.G * p.q_head + piece * 16;
+          for (int h = 0; h < p.G; ++h) {
+            const uint4 v = *(const uint4*)(src + h * p.q_head);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 f = unpack_pair<BF16>(w[y]);
+              // (not fmaxf, which would take 0 in place of NaN)
+              up[2 * y] += f.x < 0.f ? 0.f : f.x;
+              up[2 * y + 1] += f.y < 0.f ? 0.f : f.y;
+              down[2 * y] += f.x > 0.f ? 0.f : f.x;
+              down[2 * y + 1] += f.y > 0.f ? 0.f : f.y;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y) top = fmaxf(top, fmaxf(up[y], -down[y]));
+        }
+        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        // 2^14 <= top * scale < 2^15; the least values need no more than 2^100
+        int e = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
+        e = min(max(e, -100), 100);
+        const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
+        if (piece == 0) unscale[tok] = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (piece * 8 < DP) {
+          char* dst = smem + (tok >> 3) * Cfg::kGroupBytes + (piece >> 2) * 3 * 512 +
+                      ((tok & 7) * 4 + (piece & 3)) * 16;
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            uint32_t w[3][4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              float a[3], b[3];
+              split3<BF16>((side ? up : down)[2 * y] * scale, a);
+              split3<BF16>((side ? up : down)[2 * y + 1] * scale, b);
+#pragma unroll
+              for (int z = 0; z < 3; ++z) w[z][y] = pack_pair<BF16>(a[z], b[z]);
+            }
+#pragma unroll
+            for (int z = 0; z < 3; ++z)
+              *(uint4*)(dst + side * (Cfg::kChunks / 2) * 3 * 512 + z * 512) =
+                  make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]);
+          }
+        }
+      }
+      __syncthreads();
+      const char* base = p.bounds + head * p.b_head + 16 * c;
+      const bool there[4] = {8 * c < p.dim, 32 + 8 * c < p.dim, 64 + 8 * c < p.dim,
+                             96 + 8 * c < p.dim};
+#pragma unroll 1
+      for (int i = from + warp; i < min(to, u.reals); i += kWarps) {
+        const int col[2] = {16 * i + x, 16 * i + x + 8};
+        bool live[2];
+        uint4 a[2][Cfg::kChunks];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          live[r] = next[r] >= 0 && next[r] < p.rq.num_pages;
+          if (col[r] < columns && !live[r]) atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
+          const char* src = base + next[r] * p.b_page;
 #pragma unroll
           for (int i = 0; i < Cfg::kChunks; ++i) {
             const int k = i % (Cfg::kChunks / 2);
@@ -147,15 +251,11 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_score(const ScoreParams
                           : make_uint4(0, 0, 0, 0);
           }
         }
-      } else {
-        live[0] = live[1] = false;
-      }
+        look(i + kWarps, next);
 #pragma unroll 1
-      for (int gr = 0; gr < groups; ++gr) {
-        float d[3][4] = {};  // sums of the three parts, the first parts' of lo apart
-        if (col0 < seen) {
+        for (int gr = 0; gr < groups; ++gr) {
+          float d[3][4] = {}, d0[4] = {};  // sums of the three parts, the first parts' of lo apart
           const char* frag = smem + gr * Cfg::kGroupBytes + lane * 16;
-          float d0[4] = {};
 #pragma unroll
           for (int i = 0; i < Cfg::kChunks; ++i) {
 #pragma unroll
@@ -167,20 +267,18 @@ __global__ void __launch_bounds__(kScoreThreads) k_cache_score(const ScoreParams
             }
           }
 #pragma unroll
-          for (int y = 0; y < 4; ++y) d[0][y] = d[0][y] + d0[y] + (d[1][y] + d[2][y]);
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int tok = gr * kScoreGroup + 2 * c + (y & 1), r = y >> 1;
-          if (tok >= g.tokens || col[r] >= p.rq.width) continue;
-          const bool visible =
-              live[r] && ((long long)col[r] << p.rq.page_shift) <= g.pos + tok;
-          row[tok * p.s_token + col[r]] = visible ? d[0][y] * unscale[tok] : -INFINITY;
+          for (int y = 0; y < 4; ++y) {
+            const int tok = gr * kScoreGroup + 2 * c + (y & 1), r = y >> 1;
+            if (tok >= tokens || col[r] >= p.rq.width) continue;
+            const bool visible = live[r] && ((long long)col[r] << p.rq.page_shift) <= pos + tok;
+            row[tok * p.s_token + col[r]] =
+                visible ? (d[0][y] + d0[y] + (d[1][y] + d[2][y])) * unscale[tok] : -INFINITY;
+          }
         }
       }
     }
   }
-  for_idle_rows<kScoreThreads>(p.rq, g, [&](int t) {
+  for_idle_rows<kScoreThreads>(p.rq, idle, [&](int t) {
     for (int h = 0; h < p.kv_heads; ++h)
       for (int j = tid; j < p.rq.width; j += kScoreThreads)
         p.scores[t * p.s_token + h * p.s_head + j] = -INFINITY;

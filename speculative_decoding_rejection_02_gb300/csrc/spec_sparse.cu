@@ -294,14 +294,15 @@ EvictSpace evict_space(const spec_cache_evict_args* a) {
 }
 
 template <int DP, bool BF16>
-int score(const sv::ScoreParams& p, unsigned grid, void* stream) {
+int score(const sv::ScoreParams& p, int sms, void* stream) {
   static std::atomic<unsigned long long> ready;
   using Cfg = sv::ScoreCfg<DP>;
   const int rc = allow(sv::k_cache_score<DP, BF16>, sv::kScoreGroups * Cfg::kGroupBytes, ready);
   if (rc != SPEC_OK) return rc;
   const int groups = (p.per + sv::kScoreGroup - 1) / sv::kScoreGroup;
-  return launch(sv::k_cache_score<DP, BF16>, dim3(grid), sv::kScoreThreads,
-                groups * Cfg::kGroupBytes, stream, p);
+  const int run = (p.rq.B + sv::kScoreThreads - 1) / sv::kScoreThreads;
+  return launch(sv::k_cache_score<DP, BF16>, dim3(sms * sv::kScoreBlocks), sv::kScoreThreads,
+                groups * Cfg::kGroupBytes, stream, p, run);
 }
 
 template <int DP, int N8, bool BF16>
@@ -373,17 +374,10 @@ int spec_cache_score(const spec_cache_score_args* a, void* stream, unsigned* dev
   p.s_token = a->s_token, p.s_head = a->s_head;
   const int most = sv::kScoreGroup * sv::kScoreGroups;
   p.per = a->max_q < most ? a->max_q : most;
-  long long units = groups(a->num_tokens, a->B, p.per) * a->kv_heads;
-  if (units < 1) units = 1;  // (no requests: rows are filled all the same)
-  // some waves of blocks, for ragged batches, of no fewer than 64 columns each
-  const long long columns = ((long long)a->width + 63) / 64, waves = 16ll * sms / units + 1;
-  p.spread = (int)(columns < waves ? columns : waves);
-  const unsigned grid = blocks(units * p.spread);
-  if (!grid) return SPEC_ERR_UNSUPPORTED;
   const bool bf16 = a->dtype == SPEC_CACHE_BF16;
   if (a->dim > 64)
-    return bf16 ? score<128, true>(p, grid, stream) : score<128, false>(p, grid, stream);
-  return bf16 ? score<64, true>(p, grid, stream) : score<64, false>(p, grid, stream);
+    return bf16 ? score<128, true>(p, sms, stream) : score<128, false>(p, sms, stream);
+  return bf16 ? score<64, true>(p, sms, stream) : score<64, false>(p, sms, stream);
 }
 
 int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* device_status) {
