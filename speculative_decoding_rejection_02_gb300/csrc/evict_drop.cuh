@@ -117,30 +117,30 @@ __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
     int* to = p.from_at(b, head, at);
     if (to) *to = j;
   };
+  // the keys of tokens j .. j + 7, which are in one page
+  auto look8 = [&](int j, uint32_t* keys) {
+    float w[8] = {};
+    const int page = j < len ? p.rq.page(b, j >> p.rq.page_shift) : -1;
+    if (page >= 0) {
+      const float* src = p.weights + page * p.w_page + head * p.w_head + (j & in_page);
+      if (p.vec) {
+        const float4 x = *(const float4*)src, y = *(const float4*)(src + 4);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+      } else {
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y] = src[y];
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 8; ++y)
+      keys[y] = j + y >= len ? 0u : always(j + y) ? kAlways : order_key(w[y]);
+  };
   if constexpr (ITEMS > 0) {
     uint32_t keys[ITEMS];
     const int j0 = tid * ITEMS;
 #pragma unroll
-    for (int i = 0; i < ITEMS; i += 8) {
-      float w[8] = {};
-      const int page = j0 + i < len ? p.rq.page(b, (j0 + i) >> p.rq.page_shift) : -1;
-      if (page >= 0) {
-        const float* src = p.weights + page * p.w_page + head * p.w_head + ((j0 + i) & in_page);
-        if (p.vec) {
-          const float4 x = *(const float4*)src, y = *(const float4*)(src + 4);
-          w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-          w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-        } else {
-#pragma unroll
-          for (int y = 0; y < 8; ++y) w[y] = src[y];
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const int j = j0 + i + y;
-        keys[i + y] = j >= len ? 0u : always(j) ? kAlways : order_key(w[y]);
-      }
-    }
+    for (int i = 0; i < ITEMS; i += 8) look8(j0 + i, keys + i);
     int at;
     if (kept > 0)
       for (uint32_t taken = pick_items<NT, ITEMS>(keys, kept, sh, at); taken; taken &= taken - 1)
@@ -156,7 +156,12 @@ __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
     };
     const int fits = min(len, p.held);
 #pragma unroll 4
-    for (int j = tid; j < fits; j += NT) held[j] = look(j);
+    for (int j = 8 * tid; j < fits; j += 8 * NT) {  // (room for a multiple of 8)
+      uint32_t x[8];
+      look8(j, x);
+      *(uint4*)(held + j) = make_uint4(x[0], x[1], x[2], x[3]);
+      *(uint4*)(held + j + 4) = make_uint4(x[4], x[5], x[6], x[7]);
+    }
     __syncthreads();
     auto key = [&](int j) { return j < fits ? held[j] : look(j); };
     if (kept > 0)

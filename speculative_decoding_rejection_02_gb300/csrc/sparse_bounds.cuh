@@ -1,15 +1,17 @@
 // The channels' extremes of each page's keys (spec_cache_bounds).
 //
 // lo_d = min over the page's held tokens of k_d, hi_d = max: packed 16-bit comparisons, exact.
-// Bound by HBM: a page's keys read once, 4 dim bytes written for each of its heads. A block takes
-// one page at a time, a thread 8 channels of one head over all its tokens, eight of them loaded
-// before the first is used.
+// Bound by HBM: a page's keys read once, 4 dim bytes written for each of its heads. A block is
+// one warp, which takes 512 bytes of each of a page's tokens at a time (785 pages of 64 tokens of 8
+// heads: 18.8 us; 25.5 with larger blocks, of which some SMs have one more than the others), a
+// thread 8 channels of one head over all its tokens, sixteen of them
+// loaded before the first is used.
 #pragma once
 #include "sparse_common.cuh"
 
 namespace sv {
 
-constexpr int kBoundsThreads = 128;
+constexpr int kBoundsThreads = 32, kBoundsAtOnce = 16;  // tokens in flight
 
 struct BoundsParams {
   Requests rq;  // cu_q: NULL for all pages
@@ -18,6 +20,7 @@ struct BoundsParams {
   char* out;
   long long o_page, o_head, o_side;
   int pieces, row_pieces;  // 16-byte pieces of a head's row, and of a token's
+  int chunks;              // of kBoundsThreads pieces of a token's row
   int spread;              // blocks of a request
 };
 
@@ -54,24 +57,26 @@ __global__ void __launch_bounds__(kBoundsThreads) k_cache_bounds(const BoundsPar
     len = p.rq.length(b);
   }
   const int columns = (int)(((long long)len + page_size - 1) >> p.rq.page_shift);
+  const long long works = (long long)(columns - from) * p.chunks;
 #pragma unroll 1
-  for (int c = from + x; c < columns; c += p.spread) {
+  for (long long w = x; w < works; w += p.spread) {
+    const int c = from + (int)quotient(w, p.chunks);
+    const int i = (int)(w - (long long)(c - from) * p.chunks) * kBoundsThreads + threadIdx.x;
     const int page = p.rq.page(b, c);
     if (page < 0) continue;
     const int n = min(page_size, len - (c << p.rq.page_shift));
-#pragma unroll 1
-    for (int i = threadIdx.x; i < p.row_pieces; i += kBoundsThreads) {
+    if (i < p.row_pieces) {
       const int head = i / p.pieces, piece = i - head * p.pieces;
       const char* src = p.k + page * p.k_page + head * p.k_head + piece * 16;
       uint4 low = *(const uint4*)src, high = low;
 #pragma unroll 1
-      for (int t = 0; t < n; t += 8) {
-        uint4 v[8];
+      for (int t = 0; t < n; t += kBoundsAtOnce) {
+        uint4 v[kBoundsAtOnce];
 #pragma unroll
-        for (int y = 0; y < 8; ++y)  // (the last token again past the end)
+        for (int y = 0; y < kBoundsAtOnce; ++y)  // (the last token again past the end)
           v[y] = *(const uint4*)(src + min(t + y, n - 1) * p.k_token);
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
+        for (int y = 0; y < kBoundsAtOnce; ++y) {
           extreme8<BF16, false>(low, v[y]);
           extreme8<BF16, true>(high, v[y]);
         }

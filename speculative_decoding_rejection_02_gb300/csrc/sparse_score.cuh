@@ -27,6 +27,7 @@ constexpr int kScoreThreads = 128;
 constexpr int kScoreGroup = 8;    // tokens of a product
 constexpr int kScoreGroups = 4;   // of those in a group of tokens, at most
 constexpr int kScoreBlocks = 4;   // of an SM
+constexpr int kScorePart = 4;     // places of a block at least: one for each warp
 
 struct ScoreParams {
   Requests rq;
@@ -116,8 +117,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
       idle.pad = max(idle.pad, pads[w]);
       idle.gaps |= gap[w];
     }
-    const long long each = quotient(total, gridDim.x), more = total - each * gridDim.x;
-    const long long begin = each * blockIdx.x + min((long long)blockIdx.x, more);
+    const long long each = max(quotient(total + gridDim.x - 1, gridDim.x), (long long)kScorePart);
+    const long long begin = each * blockIdx.x;
     if (before <= begin && begin < before + mine) {
       int r = r0;
       if (run > 1)
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
       sh_first = r;
       sh_at = before;
       sh_begin = begin;
-      sh_end = begin + each + ((long long)blockIdx.x < more);
+      sh_end = min(begin + each, total);
     }
     __syncthreads();
   }
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
   if (b >= 0) {
     // walk: place `at` of request b, up to the end of the part
     long long left = sh_end - sh_begin, at = sh_begin - sh_at;
+    bool begins = true;
 #pragma unroll 1
     while (left > 0) {
       const ScoreUnits u(p, b);
@@ -148,7 +150,12 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
       }
       const int per_unit = u.reals + u.fills;
       const long long unit = quotient(at, per_unit);
-      const int from = (int)(at - unit * per_unit);
+      int from = (int)(at - unit * per_unit);
+      // A part that ends within the first places of a unit leaves them to the next part, which
+      // begins with them: one start of a unit less, in the block that takes longest.
+      if (begins && from > 0 && from < kScorePart) at -= from, left += from, from = 0;
+      if (!begins && from == 0 && left < kScorePart && left < per_unit) break;
+      begins = false;
       const int to = (int)min((long long)per_unit, from + left);
       const int head = (int)quotient(unit, u.groups), first = (int)(unit - (long long)head * u.groups) * p.per;
       const int tokens = min(p.per, u.hi - u.lo - first), token = u.lo + first;

@@ -342,11 +342,13 @@ int spec_cache_bounds(const spec_cache_bounds_args* a, void* stream, unsigned* d
   p.o_page = a->b_page * 2, p.o_head = a->b_head * 2, p.o_side = a->b_side * 2;
   p.pieces = a->dim / 8;
   p.row_pieces = p.pieces * a->kv_heads;
-  // a block for each page that there may be, up to some waves of blocks
+  p.chunks = (p.row_pieces + sv::kBoundsThreads - 1) / sv::kBoundsThreads;
+  // a block for each piece of work that there may be, up to some waves of blocks
   long long spread = a->cu_q ? ((long long)a->max_q + a->page_size - 2) / a->page_size + 1
                              : a->width;
   if (spread > a->width) spread = a->width;
-  const long long most = 64ll * sms / a->B + 1;
+  spread *= p.chunks;
+  const long long most = 128ll * sms / a->B + 1;
   p.spread = (int)(spread < most ? spread : most);
   const unsigned grid = blocks((long long)a->B * p.spread);
   if (!grid) return SPEC_ERR_UNSUPPORTED;
