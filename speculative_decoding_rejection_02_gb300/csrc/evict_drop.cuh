@@ -11,6 +11,8 @@
 // before any of it is written, and what is overwritten is never a later batch's source. One block
 // for a request and head, or a cluster of up to eight where there are few. Bound by HBM.
 #pragma once
+#include <type_traits>
+
 #include "sparse_common.cuh"
 
 namespace sv {
@@ -36,7 +38,8 @@ struct EvictParams {
   int by_page;   // whether `from` goes by pages of the pool, or by columns of the table
   int* begin;    // [B][kv_heads] the first kept token that moves; none: 0x7fffffff
   int* from;     // where kept tokens come from, in pages [kv_heads][page_size]
-  int cluster;   // blocks of a request and kv head that move its tokens
+  int ranks;     // blocks of a request and kv head that pick its tokens
+  int cluster;   // ... that move its tokens
 
   __device__ __forceinline__ int kept(int len, int budget) const {
     return (int)min((long long)len, max((long long)budget, (long long)first + recent));
@@ -58,15 +61,18 @@ struct EvictParams {
 };
 
 // ITEMS: tokens of a thread (8 at a time, which one page holds), or 0 for requests of any length.
-template <int NT, int ITEMS>
+// CLUSTER: p.ranks blocks for a request and kv head.
+template <int NT, int ITEMS, bool CLUSTER>
 __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
-  __shared__ PickShared<NT> sh;
+  __shared__ std::conditional_t<CLUSTER, ClusterPick<NT>, PickShared<NT>> sh;
   __shared__ int begin;
   __shared__ long long sums[NT / 32], befores[NT / 32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / p.kv_heads, head = blockIdx.x - b * p.kv_heads;
+  const int rank = CLUSTER ? blockIdx.x % p.ranks : 0;
+  const int row = CLUSTER ? blockIdx.x / p.ranks : blockIdx.x;
+  const int b = row / p.kv_heads, head = row - b * p.kv_heads;
   const long long most = (long long)p.rq.width << p.rq.page_shift;
   // ---- all requests' pages that go, and those of the requests before this one
   long long gone = 0, before = 0;
@@ -95,7 +101,7 @@ __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
   }
   if (b >= p.rq.B) return;  // (a call without requests)
   const int len = p.rq.kv_lens[b], kept = bad ? len : p.kept(len, p.budget[b]);
-  if (head == 0) {
+  if (head == 0 && rank == 0) {
     if (tid == 0) p.lens_out[b] = kept;
     if (!bad) {
       const int c0 = p.pages(kept), n = p.pages(len) - c0;
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
     }
   }
   if (kept == len) {
-    if (tid == 0) p.begin[blockIdx.x] = begin;
+    if (tid == 0 && rank == 0) p.begin[row] = begin;
     return;
   }
   // ---- the kept tokens
@@ -138,13 +144,18 @@ __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
   };
   if constexpr (ITEMS > 0) {
     uint32_t keys[ITEMS];
-    const int j0 = tid * ITEMS;
+    const int j0 = (rank * NT + tid) * ITEMS;
 #pragma unroll
     for (int i = 0; i < ITEMS; i += 8) look8(j0 + i, keys + i);
-    int at;
-    if (kept > 0)
-      for (uint32_t taken = pick_items<NT, ITEMS>(keys, kept, sh, at); taken; taken &= taken - 1)
-        moves(j0 + __ffs(taken) - 1, at++);
+    int at = 0;
+    uint32_t taken = 0;
+    if (kept > 0) {
+      if constexpr (CLUSTER)
+        taken = pick_items_cluster<NT, ITEMS>(keys, kept, sh, p.ranks, rank, at);
+      else
+        taken = pick_items<NT, ITEMS>(keys, kept, sh, at);
+    }
+    for (; taken; taken &= taken - 1) moves(j0 + __ffs(taken) - 1, at++);
   } else {
     extern __shared__ __align__(128) char smem[];
     uint32_t* held = (uint32_t*)smem;
@@ -172,7 +183,18 @@ __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
   mine = __reduce_min_sync(~0u, mine);
   if (lane == 0) atomicMin(&begin, mine);
   __syncthreads();
-  if (tid == 0) p.begin[blockIdx.x] = begin;
+  if constexpr (CLUSTER) {  // the least of all blocks
+    if (tid == 0) sh.counts[1].y = begin;
+    cluster_sync();
+    if (tid == 0 && rank == 0) {
+      mine = begin;
+      for (int r = 1; r < p.ranks; ++r) mine = min(mine, cluster_load(&sh.counts[1], r).y);
+      p.begin[row] = mine;
+    }
+    cluster_sync();
+  } else {
+    if (tid == 0) p.begin[row] = begin;
+  }
 }
 
 __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const EvictParams p) {

@@ -186,6 +186,31 @@ __device__ __forceinline__ float2 unpack_pair(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// ---- clusters of blocks
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// The float or integers at the same place of another block's shared memory.
+__device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ int2 cluster_load(const int2* p, uint32_t rank) {
+  uint32_t at;
+  int2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
 // ---- the k largest of many values, of equal ones the first: no result depends on the order of
 // the threads
 
@@ -305,6 +330,125 @@ __device__ __forceinline__ uint32_t pick_items(const uint32_t* keys, int k, Pick
     __syncthreads();
   }
   before = block_before<NT>(__popc(taken), sh.sums[0], all);
+  return taken;
+}
+
+__device__ __forceinline__ int cluster_load(const int* p, uint32_t rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// pick_items by a cluster of `ranks` blocks (a power of two), of which each has the next run of
+// items. Other blocks' shared memory is far, so only one warp of each looks at their histograms:
+// at the sums of 64 bins, then at the 64 bins that have the cut. By the whole cluster.
+template <int NT>
+struct ClusterPick {
+  static_assert(NT == 1024, "a warp for each 64 bins");
+  PickShared<NT> own;
+  alignas(16) int hist[2][2048];
+  int coarse[2][32];
+  int2 counts[2];  // (ties, -) and (taken, the first item that the caller looks for)
+};
+template <int NT, int ITEMS>
+__device__ __forceinline__ uint32_t pick_items_cluster(const uint32_t* keys, int k,
+                                                       ClusterPick<NT>& sh, int ranks, int rank,
+                                                       int& before) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t prefix = 0, mask = 0, cut = 0;
+  int equals = 0, all;
+  for (int i = threadIdx.x; i < 4096; i += NT) sh.hist[0][i] = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    int* hist = sh.hist[pass & 1];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if (keys[i] && (keys[i] & mask) == prefix) atomicAdd(&hist[keys[i] >> shift & (bins - 1)], 1);
+    __syncthreads();
+    const int2 mine = ((const int2*)hist)[32 * warp + lane];
+    const int sum = __reduce_add_sync(~0u, mine.x + mine.y);
+    if (lane == 0) sh.coarse[pass & 1][warp] = sum;
+    cluster_sync();
+    // the other one is free for the next pass: all blocks have read it before they came here
+    ((int2*)sh.hist[~pass & 1])[threadIdx.x] = make_int2(0, 0);
+    if (warp == 0) {
+      // lane l has the l-th highest group, then the l-th highest pair of bins
+      auto upto = [&](int v) {
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(~0u, v, d);
+          if (lane >= d) v += y;
+        }
+        return v;
+      };
+      int v[8], n = 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)  // (from ranks on the same ones again)
+        v[r] = cluster_load(&sh.coarse[pass & 1][31 - lane], r & (ranks - 1));
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < ranks) n += v[r];
+      int sums = upto(n);
+      int who = __ffs(__ballot_sync(~0u, k <= sums)) - 1;
+      int left = k - __shfl_sync(~0u, sums - n, who);
+      const int pair = 32 * (31 - who) + 31 - lane;
+      int2 w[8];
+      int low = 0, high = 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) w[r] = cluster_load((const int2*)hist + pair, r & (ranks - 1));
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < ranks) low += w[r].x, high += w[r].y;
+      sums = upto(low + high);
+      who = __ffs(__ballot_sync(~0u, left <= sums)) - 1;
+      if (lane == who) {
+        left -= sums - low - high;
+        const bool upper = left <= high;
+        sh.own.bin = 2 * pair + upper;
+        sh.own.rest = upper ? left : left - high;
+        sh.own.count = upper ? high : low;
+      }
+    }
+    __syncthreads();
+    prefix |= (uint32_t)sh.own.bin << shift;
+    mask |= (uint32_t)(bins - 1) << shift;
+    k = sh.own.rest;
+    cut = prefix;
+    equals = k;
+    if (sh.own.count == k) {
+      cut = prefix - 1;
+      equals = 0;
+      break;
+    }
+    if (pass == 2) break;
+    __syncthreads();
+  }
+  uint32_t taken = 0, ties = 0;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    taken |= (uint32_t)(keys[i] > cut) << i;
+    ties |= (uint32_t)(keys[i] == cut) << i;
+  }
+  auto other_ranks = [&](int which) {  // the sum of the ranks before this one
+    cluster_sync();
+    int sum = 0;
+    for (int r = 0; r < rank; ++r) sum += cluster_load(&sh.counts[which], r).x;
+    return sum;
+  };
+  if (equals > 0) {
+    int at = block_before<NT>(__popc(ties), sh.own.sums[1], all);
+    if (threadIdx.x == 0) sh.counts[0].x = all;
+    at += other_ranks(0);
+    for (int x = __popc(ties); x > 0 && at + x > equals; --x) ties &= ~(1u << (31 - __clz(ties)));
+    taken |= ties;
+  }
+  before = block_before<NT>(__popc(taken), sh.own.sums[0], all);
+  if (threadIdx.x == 0) sh.counts[1].x = all;
+  before += other_ranks(1);
+  cluster_sync();  // (the last reads of others' shared memory)
   return taken;
 }
 

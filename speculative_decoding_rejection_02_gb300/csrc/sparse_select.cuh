@@ -4,11 +4,14 @@
 // all scores'. The k-th largest is found by histograms of its bits, and of equal ones the lowest
 // columns are taken. One block for a row (token, kv head): of four warps up to 2048 columns
 // (k_cache_select_short), else with a run of ITEMS columns in each thread's registers (pick_items;
-// with scores from a model two of the three histograms decide) up to 16384 columns. Longer rows are read again from shared memory, and what does not fit there
+// with scores from a model two of the three histograms decide) up to 16384 columns, or by a cluster of blocks where the rows
+// leave SMs idle. Longer rows are read again from shared memory, and what does not fit there
 // from L2.
 //
 // Bound by the chain of a row: request, scores, histograms, the places.
 #pragma once
+#include <type_traits>
+
 #include "sparse_common.cuh"
 
 namespace sv {
@@ -20,6 +23,7 @@ struct SelectParams {
   long long s_token, s_head;
   int vec;      // rows on 16-byte boundaries
   int* out;
+  int ranks;    // blocks of a row
   int held;     // scores that fit the dynamic shared memory (any length)
 };
 
@@ -277,27 +281,30 @@ __global__ void __launch_bounds__(kShortThreads, 8) k_cache_select_short(const S
   }
 }
 
-// ITEMS: columns of a thread, or 0 for rows of any length.
-template <int NT, int ITEMS>
+// ITEMS: columns of a thread, or 0 for rows of any length. CLUSTER: p.ranks blocks for a row.
+template <int NT, int ITEMS, bool CLUSTER>
 __global__ void __launch_bounds__(NT) k_cache_select(const SelectParams p) {
-  __shared__ PickShared<NT> sh;
+  __shared__ std::conditional_t<CLUSTER, ClusterPick<NT>, PickShared<NT>> sh;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
-  const long long t = blockIdx.x / p.kv_heads;
-  const int head = (int)(blockIdx.x - t * p.kv_heads);
-  int* out = p.out + blockIdx.x * (long long)p.count;
+  const int rank = CLUSTER ? blockIdx.x % p.ranks : 0;
+  const long long at_row = CLUSTER ? blockIdx.x / p.ranks : blockIdx.x;
+  const long long t = at_row / p.kv_heads;
+  const int head = (int)(at_row - t * p.kv_heads);
+  int* out = p.out + at_row * p.count;
   select_check<NT>(p);
   const int n = select_visible(p, t);
   if (n <= p.count) {
-    for (int i = tid; i < p.count; i += NT) out[i] = i < n ? i : -1;
+    for (int i = tid + rank * NT; i < p.count; i += (CLUSTER ? p.ranks : 1) * NT)
+      out[i] = i < n ? i : -1;
     return;
   }
   const float* row = p.scores + t * p.s_token + head * p.s_head;
   auto always = [&](int c) { return c < p.first || c >= n - p.recent; };
   if constexpr (ITEMS > 0) {
     uint32_t keys[ITEMS];
-    const int c0 = tid * ITEMS;
+    const int c0 = (rank * NT + tid) * ITEMS;
 #pragma unroll
     for (int i = 0; i < ITEMS; i += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -316,8 +323,12 @@ __global__ void __launch_bounds__(NT) k_cache_select(const SelectParams p) {
     for (int i = 0; i < ITEMS; ++i)
       keys[i] = c0 + i >= n ? 0u : always(c0 + i) ? kAlways : keys[i];
     int at;
-    for (uint32_t taken = pick_items<NT, ITEMS>(keys, p.count, sh, at); taken; taken &= taken - 1)
-      out[at++] = c0 + __ffs(taken) - 1;
+    uint32_t taken;
+    if constexpr (CLUSTER)
+      taken = pick_items_cluster<NT, ITEMS>(keys, p.count, sh, p.ranks, rank, at);
+    else
+      taken = pick_items<NT, ITEMS>(keys, p.count, sh, at);
+    for (; taken; taken &= taken - 1) out[at++] = c0 + __ffs(taken) - 1;
   } else {
     extern __shared__ __align__(128) char smem[];
     uint32_t* held = (uint32_t*)smem;

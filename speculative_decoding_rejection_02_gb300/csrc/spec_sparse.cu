@@ -138,6 +138,16 @@ int allow(K kernel, int smem, std::atomic<unsigned long long>& ready) {
 }
 
 constexpr int kMostHeld = 48 * 1024;  // keys of a row that is looked at from shared memory
+// Blocks of a cluster that pick from a row of n items together, up to 8; 1: a block alone. A row that
+// fits one block's registers (16384 items) is as fast there (40 rows of 12500: 12.7 us alone, 13.0
+// with two blocks each), longer ones are faster in a cluster as long as that has an SM for each
+// block (12 rows of 20000-33000: 30.6 us alone, 19.3 with eight).
+int pick_ranks(long long rows, long long n, int sms) {
+  int ranks = 1;
+  while (ranks < 8 && rows * ranks * 2 <= sms) ranks *= 2;
+  return n > 16384 && n <= 16384ll * ranks ? ranks : 1;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 int check_bounds(const spec_cache_bounds_args* a) {
@@ -287,7 +297,9 @@ struct EvictSpace {
 EvictSpace evict_space(const spec_cache_evict_args* a) {
   EvictSpace s;
   const long long columns = (long long)a->B * a->width;
-  s.by_page = a->num_pages < columns;
+  // (by columns it takes no look at the table to find a place; a table much wider than what the
+  // requests can hold is not worth that)
+  s.by_page = columns > 4ll * a->num_pages;
   s.from = ((size_t)a->B * a->kv_heads * 4 + 255) / 256 * 256;
   s.bytes = s.from + (size_t)(s.by_page ? a->num_pages : columns) * a->kv_heads * a->page_size * 4;
   return s;
@@ -385,7 +397,8 @@ int spec_cache_score(const spec_cache_score_args* a, void* stream, unsigned* dev
 int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* device_status) {
   const int rc = check_select(a);
   if (rc != SPEC_OK) return rc;
-  if (!sm_count()) return SPEC_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (!sms) return SPEC_ERR_UNSUPPORTED;
   if (a->num_tokens == 0) return SPEC_OK;
   unsigned* status = status_word(device_status);
   if (!status) return SPEC_ERR_CUDA;
@@ -403,17 +416,27 @@ int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* d
   p.held = 0;
   if (a->width <= sv::kShortColumns)
     return launch(sv::k_cache_select_short, dim3(grid), sv::kShortThreads, 0, stream, p);
+  const long long rows = (long long)a->num_tokens * a->kv_heads;
+  p.ranks = pick_ranks(rows, a->width, sms);
+  if (p.ranks > 1) {
+    const unsigned wide = blocks(rows * p.ranks);
+    return a->width <= p.ranks * 8192
+               ? launch_cluster(sv::k_cache_select<1024, 8, true>, p.ranks, dim3(wide), 1024, 0,
+                                stream, p)
+               : launch_cluster(sv::k_cache_select<1024, 16, true>, p.ranks, dim3(wide), 1024, 0,
+                                stream, p);
+  }
   if (a->width <= 4096)
-    return launch(sv::k_cache_select<512, 8>, dim3(grid), 512, 0, stream, p);
+    return launch(sv::k_cache_select<512, 8, false>, dim3(grid), 512, 0, stream, p);
   if (a->width <= 8192)
-    return launch(sv::k_cache_select<1024, 8>, dim3(grid), 1024, 0, stream, p);
+    return launch(sv::k_cache_select<1024, 8, false>, dim3(grid), 1024, 0, stream, p);
   if (a->width <= 16384)
-    return launch(sv::k_cache_select<1024, 16>, dim3(grid), 1024, 0, stream, p);
+    return launch(sv::k_cache_select<1024, 16, false>, dim3(grid), 1024, 0, stream, p);
   p.held = a->width < kMostHeld ? a->width : kMostHeld;
   static std::atomic<unsigned long long> ready;
-  const int ok = allow(sv::k_cache_select<1024, 0>, kMostHeld * 4, ready);
+  const int ok = allow(sv::k_cache_select<1024, 0, false>, kMostHeld * 4, ready);
   if (ok != SPEC_OK) return ok;
-  return launch(sv::k_cache_select<1024, 0>, dim3(grid), 1024, p.held * 4, stream, p);
+  return launch(sv::k_cache_select<1024, 0, false>, dim3(grid), 1024, p.held * 4, stream, p);
 }
 
 int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* stream,
@@ -559,18 +582,25 @@ int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* dev
   while (p.cluster < 8 && rows * p.cluster < sms) p.cluster *= 2;
   const unsigned grid = blocks(rows > 0 ? rows : 1), moves = blocks(rows * p.cluster);
   if (!grid || (rows > 0 && !moves)) return SPEC_ERR_UNSUPPORTED;
-  // weights in registers up to 16384 tokens, as in spec_cache_select
+  // weights in registers as in spec_cache_select
   const long long most = (long long)a->width * a->page_size;
-  if (most <= 4096) {
-    rc = launch(sv::k_evict_pick<512, 8>, dim3(grid), 512, 0, stream, p);
+  p.ranks = rows > 0 ? pick_ranks(rows, most, sms) : 1;
+  if (p.ranks > 1) {
+    const unsigned wide = blocks(rows * p.ranks);
+    rc = most <= p.ranks * 8192
+             ? launch_cluster(sv::k_evict_pick<1024, 8, true>, p.ranks, dim3(wide), 1024, 0, stream, p)
+             : launch_cluster(sv::k_evict_pick<1024, 16, true>, p.ranks, dim3(wide), 1024, 0, stream,
+                              p);
+  } else if (most <= 4096) {
+    rc = launch(sv::k_evict_pick<512, 8, false>, dim3(grid), 512, 0, stream, p);
   } else if (most <= 16384) {
-    rc = launch(sv::k_evict_pick<1024, 16>, dim3(grid), 1024, 0, stream, p);
+    rc = launch(sv::k_evict_pick<1024, 16, false>, dim3(grid), 1024, 0, stream, p);
   } else {
     p.held = most < kMostHeld ? (int)most : kMostHeld;
     static std::atomic<unsigned long long> ready;
-    rc = allow(sv::k_evict_pick<1024, 0>, kMostHeld * 4, ready);
+    rc = allow(sv::k_evict_pick<1024, 0, false>, kMostHeld * 4, ready);
     if (rc != SPEC_OK) return rc;
-    rc = launch(sv::k_evict_pick<1024, 0>, dim3(grid), 1024, p.held * 4, stream, p);
+    rc = launch(sv::k_evict_pick<1024, 0, false>, dim3(grid), 1024, p.held * 4, stream, p);
   }
   if (rc != SPEC_OK || rows == 0) return rc;
   return launch_cluster(sv::k_evict_move, p.cluster, dim3(moves), sv::kMoveThreads, 0, stream, p);

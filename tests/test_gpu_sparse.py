@@ -330,3 +330,49 @@ def test_evict(dtype, layout, lens, budget, first, recent, page, kv_heads, dim, 
     assert f.tolist() == want[4] and int(r.free_count) == want[5]
     assert torch.equal(t.cpu(), table)
     assert same(w, want[2]) and same(k, want[0]) and same(v, want[1])
+
+
+@pytest.mark.parametrize("lens,budget,first,recent,page,kv_heads", [
+    ([20000, 9000], [3000, 8999], 5, 100, 16, 2),      # clusters of blocks
+    ([70000], [100], 0, 0, 64, 1), ([140000], [139000], 3, 9, 32, 1),  # longer than registers
+    ([5000] * 20, [4097] * 20, 0, 1, 16, 8)])           # a block for each of many
+@pytest.mark.parametrize("values", ["random", "few"])
+def test_evict_long(lens, budget, first, recent, page, kv_heads, values):
+    g = torch.Generator().manual_seed(14)
+    kp, vp, table, _, _ = cache_ref.cache(lens, page, kv_heads, 8, BF, g)
+    weights = torch.rand((kp.shape[0], kv_heads, page), generator=g)
+    if values == "few":
+        weights = (weights * 5).floor()
+    free = [-9] * kp.shape[0]
+    want = ref.evict(kp, vp, weights, table, lens, budget, free, 0, first, recent)
+    k, v, w, f = kp.to(DEV), vp.to(DEV), weights.to(DEV), ints(free)
+    status = status_word()
+    r = sv.cache_evict(k, v, w, table.to(DEV), ints(lens), ints(budget), f, ints([0]), first=first,
+                       recent=recent, status=status)
+    assert int(status) == 0
+    assert r.lens.tolist() == want[3] and f.tolist() == want[4]
+    assert same(w, want[2]) and same(k, want[0]) and same(v, want[1])
+
+
+@pytest.mark.parametrize("rows,columns,count", [
+    (1, 5000, 77), (30, 9000, 500), (200, 3000, 64), (200, 6000, 5999), (160, 12000, 250),
+    (3, 60000, 1000), (100, 20000, 19000), (1, 140000, 3)])
+@pytest.mark.parametrize("values", ["random", "few", "spikes"])
+def test_select_long(rows, columns, count, values):
+    g = torch.Generator().manual_seed(15)
+    x = torch.randn((rows, 1, columns), generator=g)
+    if values == "few":
+        x = (x * 2).round()
+    if values == "spikes":  # nearly all in one place, a few orders of magnitude away
+        x = torch.where(torch.rand(x.shape, generator=g) < 0.01, x * 1e30, x * 1e-30)
+    lens = [columns * 8 - 8 * (r % 7) for r in range(rows)]
+    got = sv.cache_select(x.to(DEV), ints(lens), starts([1] * rows), page_size=8, count=count,
+                          first=2, recent=1)
+    for r in range(rows):
+        n = lens[r] // 8
+        score = x[r, 0, 2:n - 1].double()
+        best = torch.sort(score, descending=True, stable=True).indices[: count - 3] + 2
+        want = torch.full((count,), -1)  # past the last where fewer are visible
+        chosen = torch.cat([torch.tensor([0, 1, n - 1]), best]).sort().values
+        want[: len(chosen)] = chosen
+        assert torch.equal(got[r, 0].cpu().long(), want), r
