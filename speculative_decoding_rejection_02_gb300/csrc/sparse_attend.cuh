@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8>::kBlocks)
     auto entry = [&](int k, int i) {
       const int* row = lists + k * next_list;
       const int col = row[i], before = i > 0 ? row[i - 1] : -1;
-      if (col < 0) return -1;
+      if (col < 0 || g.len == 0) return -1;
       if ((i > 0 && (before < 0 || before >= col)) ||
           ((long long)col << shift) >= g.len) {
         atomicOr(p.rq.status, SPEC_CACHE_BAD_SELECTION);

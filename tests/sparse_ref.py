@@ -149,15 +149,15 @@ def evict(kp, vp, weights, table, lens, budget, free, count, first, recent):
             count += 1
         if n == m:
             continue
+        j = torch.arange(n)
+        where, off = torch.tensor(row)[j // page].long(), j % page
         for h in range(K):
-            w = [float(weights[row[j // page], h, j % page]) for j in range(n)]
-            w = [math.inf if math.isnan(x) else x for x in w]
-            always = [j for j in range(n) if j < first or j >= n - recent]
-            rest = sorted((j for j in range(first, n - recent)), key=lambda j: -w[j])
-            stay = sorted(always + rest[: m - len(always)])
-            for i, j in enumerate(stay):
-                a, b = (row[i // page], i % page), (row[j // page], j % page)
-                out_k[a[0], a[1], h] = kp[b[0], b[1], h]
-                out_v[a[0], a[1], h] = vp[b[0], b[1], h]
-                out_w[a[0], h, a[1]] = weights[b[0], h, b[1]]
+            w = weights[where, h, off].double()
+            w = torch.where(w.isnan(), math.inf, w)
+            always = (j < first) | (j >= n - recent)
+            rest = torch.sort(w[first: n - recent], descending=True, stable=True).indices + first
+            stay = torch.cat([j[always], rest[: m - int(always.sum())]]).sort().values
+            out_k[where[:m], off[:m], h] = kp[where[stay], off[stay], h]
+            out_v[where[:m], off[:m], h] = vp[where[stay], off[stay], h]
+            out_w[where[:m], h, off[:m]] = weights[where[stay], h, off[stay]]
     return out_k, out_v, out_w, kept, free, count
