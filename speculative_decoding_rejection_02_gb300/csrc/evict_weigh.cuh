@@ -351,7 +351,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         weigh_land(&sh.q_full[r % p.q_stages], r / p.q_stages);
     } else if (warp == kWeighSums + 2 || warp == kWeighSums + 3) {
       // ---- products of the pair's one or other tile
-      const int g = warp - kWeighSums - 2;
+      const int g = __shfl_sync(~0u, warp - kWeighSums - 2, 0);
+      // (shuffles tell the compiler that a value is the same in all lanes, so that descriptors are
+      // made in uniform registers, where the products take them from)
       const bool one = elect_one();
       const uint32_t tmem = __shfl_sync(~0u, sh.tmem, 0) + g * 256;
       const uint64_t k0 = mma_desc(smem_addr(smem), 16), q0 = mma_desc(smem_addr(q_smem), 16);
@@ -360,19 +362,20 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       bool ok = true;
       do {
         const bool mine = walk.has(g), single = walk.u.tiles == 1, last = walk.ends_unit();
-        const unsigned ka = g * p.k_stages + k_count % p.k_stages;
+        const unsigned ka = __shfl_sync(~0u, g * p.k_stages + k_count % p.k_stages, 0);
         const uint64_t kd = k0 + ka * (stage_bytes / 16);
         if (mine) ok = weigh_wait(sh, p, &sh.k_full[ka], k_count / p.k_stages);
         for (int t = walk.first_tile(p); ok && t < walk.u.tiles; ++t) {
-          const unsigned qa = q_count % p.q_stages;
+          const unsigned qa = __shfl_sync(~0u, q_count % p.q_stages, 0);
           ok = weigh_wait(sh, p, &sh.q_full[qa], q_count / p.q_stages);
           if (!ok) break;
           if (mine) {
             const int columns =
-                min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
+                __shfl_sync(~0u, min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens), 0) *
+                p.G;
             const uint32_t kind =
                 mma_kind(p.bf16, false, kWeighTile, (columns + 15) / 16 * 16);
-            const uint32_t s = s_count & 1;
+            const uint32_t s = __shfl_sync(~0u, s_count & 1, 0);
             ok = weigh_wait(sh, p, &sh.s_free[g][s], s_count / 2 + 1);
             if (!ok) break;
             tmem_fence_after();
