@@ -412,6 +412,11 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         const int key = (walk.pair * 2 + g) * kWeighTile + row;
         float* w = nullptr;
         float before = 0.f;
+        // column tiles [all_from, whole) have `full` columns, all of which see all keys: code that
+        // looks at each column's place takes 387 us for two chunks of 2048, not 344
+        const int over = max((walk.pair * 2 + g + 1) * kWeighTile - 1 - walk.u.old, 0);
+        const int all_from = (over + p.tile_tokens - 1) / p.tile_tokens;
+        const int whole = (walk.u.hi - walk.u.lo) / p.tile_tokens, full = p.tile_tokens * p.G;
         unsigned long long sum2[4] = {0, 0, 0, 0};
         float rest = 0.f;
         for (int t = t0; ok && t < walk.u.tiles; ++t) {
@@ -436,30 +441,54 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
               if (w && key < walk.u.old && p.decay != 0.f) before = *w;
               __syncwarp();
             }
-            // columns [from, columns) of the tile see the key
-            const int columns =
-                min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
-            const long long ahead = (long long)key - walk.u.old - t * p.tile_tokens;
-            const int from = ahead > 0 ? (int)min(ahead * p.G, (long long)kWeighTile) : 0;
             const float* shift = sh.shift[la];
-#pragma unroll 1
-            for (int k = 0; k < columns; k += 32) {
+            // 32 columns from k on, which all keys see
+            auto add = [&](int k) {
               float x[32];
-              ulonglong2 z[8];
               tmem_ld32(tmem + k, x);
+              ulonglong2 z[8];
 #pragma unroll
               for (int y = 0; y < 8; ++y) z[y] = *(const ulonglong2*)(shift + k + 4 * y);
               tmem_wait_ld(x);
-              if (__all_sync(~0u, from <= k) && k + 32 <= columns) {
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                  float a, b, c, d;
-                  f2_unpack(f2_fma(f2_pack(x[4 * y], x[4 * y + 1]), c2, z[y].x), a, b);
-                  f2_unpack(f2_fma(f2_pack(x[4 * y + 2], x[4 * y + 3]), c2, z[y].y), c, d);
-                  sum2[2 * (y & 1)] = f2_add(sum2[2 * (y & 1)], f2_pack(ex2(a), ex2(b)));
-                  sum2[2 * (y & 1) + 1] = f2_add(sum2[2 * (y & 1) + 1], f2_pack(ex2(c), ex2(d)));
-                }
-              } else {
+              for (int y = 0; y < 8; ++y) {
+                float a, b, c, d;
+                f2_unpack(f2_fma(f2_pack(x[4 * y], x[4 * y + 1]), c2, z[y].x), a, b);
+                f2_unpack(f2_fma(f2_pack(x[4 * y + 2], x[4 * y + 3]), c2, z[y].y), c, d);
+                sum2[2 * (y & 1)] = f2_add(sum2[2 * (y & 1)], f2_pack(ex2(a), ex2(b)));
+                sum2[2 * (y & 1) + 1] = f2_add(sum2[2 * (y & 1) + 1], f2_pack(ex2(c), ex2(d)));
+              }
+            };
+            // the same, of which only the first n are columns
+            auto add_some = [&](int k, int n) {
+              float x[32];
+              tmem_ld32(tmem + k, x);
+              tmem_wait_ld(x);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) {
+                const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
+                if (y < n) rest += e;
+              }
+            };
+            if (t >= all_from && t < whole && full == kWeighTile) {
+#pragma unroll
+              for (int k = 0; k < kWeighTile; k += 32) add(k);
+            } else if (t >= all_from && t < whole) {
+              int k = 0;
+#pragma unroll 1
+              for (; k + 32 <= full; k += 32) add(k);
+              if (k < full) add_some(k, full - k);
+            } else {
+              // columns [from, columns) of the tile see the key
+              const int columns =
+                  min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
+              const long long ahead = (long long)key - walk.u.old - t * p.tile_tokens;
+              const int from = ahead > 0 ? (int)min(ahead * p.G, (long long)kWeighTile) : 0;
+#pragma unroll 1
+              for (int k = 0; k < columns; k += 32) {
+                float x[32];
+                tmem_ld32(tmem + k, x);
+                tmem_wait_ld(x);
 #pragma unroll
                 for (int y = 0; y < 32; ++y) {
                   const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
