@@ -51,12 +51,12 @@ struct SelectedParams {
   int cluster;    // blocks of a unit
 };
 
-template <int DP, int N8>
+template <int DP, int N8, bool DEEP>
 struct SelCfg {
   // Two tiles of each warp and three blocks on an SM, or three and two where the registers do not
-  // allow three blocks: twelve warps hide latency better than eight with more tiles in flight (183
-  // us in place of 171).
-  static constexpr int kStages = N8 <= 2 ? 2 : 3, kBlocks = N8 <= 2 ? 3 : 2;
+  // allow three blocks: twelve warps hide latency better than eight with more tiles in flight (171
+  // us in place of 183). DEEP: five tiles, for calls that leave most of the SMs idle.
+  static constexpr int kStages = DEEP ? 5 : N8 <= 2 ? 2 : 3, kBlocks = DEEP ? 1 : N8 <= 2 ? 3 : 2;
   static constexpr int kTile = 16 * DP * 2;                       // bytes of 16 keys
   static constexpr int kRing = kSelWarps * kStages * 2 * kTile;
   static constexpr int kQ = N8 * (DP / 16) * 256;                 // [n8][step][lane] 8 bytes
@@ -111,10 +111,10 @@ struct SelList {
   unsigned char* mask;
 };
 
-template <int DP, int N8, bool BF16>
-__global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8>::kBlocks)
+template <int DP, int N8, bool DEEP, bool BF16>
+__global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
     k_attend_selected(const __grid_constant__ SelectedParams p) {
-  using Cfg = SelCfg<DP, N8>;
+  using Cfg = SelCfg<DP, N8, DEEP>;
   constexpr float kBias = sel_bias<BF16>();
   constexpr float kNone = -3e38f;       // the maximum of no score: finite, so that P is 0
   constexpr int kLanes = DP / 8;        // lanes that copy a row's 16-byte pieces
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8>::kBlocks)
       }
       const int tiles = (n * page_size + 15) / 16;
       const int from = rank * kSelWarps + warp, step = p.cluster * kSelWarps;
-      uint32_t seen_by = 0;  // of key lane % 16 of the tiles in flight: bits of tokens, the
+      unsigned long long seen_by = 0;  // of key lane % 16 of the tiles in flight: bits of tokens, the
                              // youngest tile's lowest
       auto issue = [&](int tile, int stage) {
         uint32_t mine = 0;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8>::kBlocks)
         copy_wait<Cfg::kStages - 2>();
         __syncwarp();
         issue(tile + (Cfg::kStages - 1) * step, stage == 0 ? Cfg::kStages - 1 : stage - 1);
-        const uint32_t seen = seen_by >> (8 * (Cfg::kStages - 1)) & 255;
+        const uint32_t seen = (uint32_t)(seen_by >> (8 * (Cfg::kStages - 1))) & 255;
         const uint32_t k_at = ring_at + stage * 2 * Cfg::kTile, v_at = k_at + Cfg::kTile;
         stage = stage == Cfg::kStages - 1 ? 0 : stage + 1;
         float s[N8][4];

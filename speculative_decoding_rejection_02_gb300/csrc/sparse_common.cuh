@@ -26,8 +26,8 @@ struct Requests {
   unsigned* status;
 
   // The length of request b; 0 with a status bit if it cannot be.
-  __device__ __forceinline__ int length(int b) const {
-    const int len = kv_lens[b];
+  __device__ __forceinline__ int length(int b) const { return checked(kv_lens[b]); }
+  __device__ __forceinline__ int checked(int len) const {
     if (len >= 0 && len <= ((long long)width << page_shift) && len <= 0x7fff0000) return len;
     atomicOr(status, SPEC_CACHE_BAD_LENGTHS);
     return 0;
@@ -75,10 +75,11 @@ __device__ __forceinline__ TokenGroup find_group(const Requests& p, long long un
   const int run = (p.B + NT - 1) / NT, r0 = min((long long)tid * run, (long long)p.B);
   const int r1 = min(r0 + run, p.B);
   long long mine = 0;
-  int pad = 0, gaps = 0, lo = 0, hi = 0;
+  int pad = 0, gaps = 0, lo = 0, hi = 0, len = 0;
   auto groups_of = [&](int r) {
     lo = p.cu_q[r];
     hi = p.cu_q[r + 1];
+    len = p.kv_lens[r];
     if (lo < 0 || hi < lo || hi > p.T) {
       atomicOr(p.status, SPEC_CACHE_BAD_LENGTHS);
       lo = hi = -1;
@@ -113,7 +114,8 @@ __device__ __forceinline__ TokenGroup find_group(const Requests& p, long long un
         if (unit < at + n || r + 1 >= r1) break;
         at += n;
       }
-    const int skip = (int)(unit - at) * per, len = p.length(r);
+    const int skip = (int)(unit - at) * per;
+    len = p.checked(len);
     TokenGroup g;
     g.b = r;
     g.token = lo + skip;

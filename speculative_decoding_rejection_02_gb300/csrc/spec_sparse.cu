@@ -317,20 +317,24 @@ int score(const sv::ScoreParams& p, int sms, void* stream) {
                 groups * Cfg::kGroupBytes, stream, p, run);
 }
 
-template <int DP, int N8, bool BF16>
+template <int DP, int N8, bool DEEP, bool BF16>
 int selected(const sv::SelectedParams& p, unsigned grid, void* stream) {
   static std::atomic<unsigned long long> ready;
-  constexpr int smem = sv::SelCfg<DP, N8>::kSmem;
-  const int rc = allow(sv::k_attend_selected<DP, N8, BF16>, smem, ready);
+  constexpr int smem = sv::SelCfg<DP, N8, DEEP>::kSmem;
+  const int rc = allow(sv::k_attend_selected<DP, N8, DEEP, BF16>, smem, ready);
   if (rc != SPEC_OK) return rc;
-  return launch_cluster(sv::k_attend_selected<DP, N8, BF16>, p.cluster, dim3(grid),
+  return launch_cluster(sv::k_attend_selected<DP, N8, DEEP, BF16>, p.cluster, dim3(grid),
                         sv::kSelThreads, smem, stream, p);
 }
 template <int DP, bool BF16>
-int selected(const sv::SelectedParams& p, int columns, unsigned grid, void* stream) {
-  if (columns <= 8) return selected<DP, 1, BF16>(p, grid, stream);
-  if (columns <= 16) return selected<DP, 2, BF16>(p, grid, stream);
-  return selected<DP, 4, BF16>(p, grid, stream);
+int selected(const sv::SelectedParams& p, int columns, int sms, unsigned grid, void* stream) {
+  // more tiles in flight where there is a block for each SM at most (one token over 64 pages of
+  // 32: 10.1 us in place of 11.4)
+  if (columns <= 8)
+    return (int)grid <= sms ? selected<DP, 1, true, BF16>(p, grid, stream)
+                            : selected<DP, 1, false, BF16>(p, grid, stream);
+  if (columns <= 16) return selected<DP, 2, false, BF16>(p, grid, stream);
+  return selected<DP, 4, false, BF16>(p, grid, stream);
 }
 
 }  // namespace
@@ -475,7 +479,7 @@ int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* s
   p.unit_heads = p.G < 32 ? p.G : 32;
   p.splits = (p.G + p.unit_heads - 1) / p.unit_heads;
   p.per = 1;
-  const int ring = a->dim > 64 ? sv::SelCfg<128, 1>::kRing : sv::SelCfg<64, 1>::kRing;
+  const int ring = a->dim > 64 ? sv::SelCfg<128, 1, false>::kRing : sv::SelCfg<64, 1, false>::kRing;
   if (a->num_tokens > a->B && a->width <= ring) {
     p.per = 16 / p.unit_heads;
     if (p.per > sv::kSelTokens) p.per = sv::kSelTokens;
@@ -495,10 +499,10 @@ int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* s
   const int columns = p.per * p.unit_heads;
   const bool bf16 = a->dtype == SPEC_CACHE_BF16;
   if (a->dim > 64)
-    return bf16 ? selected<128, true>(p, columns, grid, stream)
-                : selected<128, false>(p, columns, grid, stream);
-  return bf16 ? selected<64, true>(p, columns, grid, stream)
-              : selected<64, false>(p, columns, grid, stream);
+    return bf16 ? selected<128, true>(p, columns, sms, grid, stream)
+                : selected<128, false>(p, columns, sms, grid, stream);
+  return bf16 ? selected<64, true>(p, columns, sms, grid, stream)
+              : selected<64, false>(p, columns, sms, grid, stream);
 }
 
 int spec_cache_weigh(const spec_cache_weigh_args* a, void* stream, unsigned* device_status) {
