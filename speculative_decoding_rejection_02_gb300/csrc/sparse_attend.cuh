@@ -27,7 +27,6 @@
 
 namespace sv {
 
-constexpr int kSelWarps = 4, kSelThreads = 32 * kSelWarps;
 constexpr int kSelList = 640;    // pages that a block lists at a time
 constexpr int kSelTokens = 8;    // bits of a page's byte
 
@@ -53,18 +52,20 @@ struct SelectedParams {
 
 template <int DP, int N8, bool DEEP>
 struct SelCfg {
-  // Two tiles of each warp and three blocks on an SM, or three and two where the registers do not
-  // allow three blocks: twelve warps hide latency better than eight with more tiles in flight (171
-  // us in place of 183). DEEP: five tiles, for calls that leave most of the SMs idle.
-  static constexpr int kStages = DEEP ? 5 : N8 <= 2 ? 2 : 3, kBlocks = DEEP ? 1 : N8 <= 2 ? 3 : 2;
+  // Four warps with two tiles each and three blocks on an SM, or three tiles and two blocks where
+  // the registers do not allow three: twelve warps hide latency better than eight with more tiles
+  // in flight (171 us in place of 183). DEEP: eight warps with three tiles each, for calls that
+  // leave most of the SMs idle.
+  static constexpr int kWarps = DEEP ? 8 : 4, kThreads = 32 * kWarps;
+  static constexpr int kStages = !DEEP && N8 <= 2 ? 2 : 3, kBlocks = DEEP ? 1 : N8 <= 2 ? 3 : 2;
   static constexpr int kTile = 16 * DP * 2;                       // bytes of 16 keys
-  static constexpr int kRing = kSelWarps * kStages * 2 * kTile;
+  static constexpr int kRing = kWarps * kStages * 2 * kTile;
   static constexpr int kQ = N8 * (DP / 16) * 256;                 // [n8][step][lane] 8 bytes
   static constexpr int kCols = 8 * N8;
   static constexpr int kPitch = DP + 4;                           // floats of a column's partial O
   static constexpr int kSmem = kRing + kQ + kSelList * 9;
   static_assert(kBlocks * (kSmem + 2048) <= 228 * 1024, "blocks of an SM");
-  static_assert((kSelWarps + 1) * kCols * (kPitch + 2) * 4 <= kRing, "partial results in the ring");
+  static_assert((kWarps + 1) * kCols * (kPitch + 2) * 4 <= kRing, "partial results in the ring");
 };
 
 // 16 bytes to shared memory: `bytes` (0 or 16) from src, zeros for the others.
@@ -112,16 +113,17 @@ struct SelList {
 };
 
 template <int DP, int N8, bool DEEP, bool BF16>
-__global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
+__global__ void __launch_bounds__(SelCfg<DP, N8, DEEP>::kThreads, SelCfg<DP, N8, DEEP>::kBlocks)
     k_attend_selected(const __grid_constant__ SelectedParams p) {
   using Cfg = SelCfg<DP, N8, DEEP>;
+  constexpr int kWarps = Cfg::kWarps, kThreads = Cfg::kThreads;
   constexpr float kBias = sel_bias<BF16>();
   constexpr float kNone = -3e38f;       // the maximum of no score: finite, so that P is 0
   constexpr int kLanes = DP / 8;        // lanes that copy a row's 16-byte pieces
   constexpr int kRows = 32 / kLanes;    // rows of one copy instruction
   extern __shared__ __align__(128) char smem[];
-  __shared__ GroupShared<kSelThreads> sh;
-  __shared__ int sums[kSelWarps], listed;
+  __shared__ GroupShared<kThreads> sh;
+  __shared__ int sums[kWarps], listed;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, x = lane >> 2, c = lane & 3;
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
   unit /= p.splits;
   const int kv_head = (int)(unit % p.kv_heads);
   unit /= p.kv_heads;
-  const TokenGroup g = find_group<kSelThreads>(p.rq, unit, p.per, sh);
+  const TokenGroup g = find_group<kThreads>(p.rq, unit, p.per, sh);
   if (g.b >= 0) {
     char* ring = smem + warp * Cfg::kStages * 2 * Cfg::kTile;
     const uint32_t ring_at = smem_addr(ring);
@@ -147,21 +149,6 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
     const int steps = (p.dim + 15) / 16, pieces = p.dim / 8;
     const float factor = fabsf(p.c);
     const uint32_t flip = p.c < 0.f ? 0x80008000u : 0u;
-    // Q as operands, from memory: two channels of one column at a time
-    for (int i = tid; i < N8 * (DP / 16) * 32; i += kSelThreads) {
-      const int n8 = i / ((DP / 16) * 32), step = i / 32 % (DP / 16);
-      const int column = n8 * 8 + (i >> 2 & 7), ch = step * 16 + 2 * (i & 3);
-      uint2 v = make_uint2(0, 0);
-      if (column < columns) {
-        const int tok = column / heads;
-        const char* src = p.q + (long long)(g.token + tok) * p.q_token +
-                          (long long)(head0 + column - tok * heads) * p.q_head + ch * 2;
-        // (a negative factor of the scores is Q's sign)
-        if (ch < p.dim) v.x = *(const uint32_t*)src ^ flip;
-        if (ch + 8 < p.dim) v.y = *(const uint32_t*)(src + 16) ^ flip;
-      }
-      q_frag[i] = v;
-    }
     // the tokens of the lane's columns, a byte with one bit for each (none: no such column)
     uint32_t token_of[(2 * N8 + 3) / 4] = {};
 #pragma unroll
@@ -207,6 +194,29 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
       lane_dst[y] = r * (DP * 2) + ((piece ^ r) & 7) * 16 + (piece & 8) * 16;
     }
     const bool one = g.tokens == 1;
+    // The start of the list, Q and the pages' numbers, each on its way while the others are
+    // waited for. Q as operands: two channels of one column at a time.
+    const int entry0 = one && tid < min(kSelList, p.count) ? entry(0, tid) : -1;
+    constexpr int kQs = (N8 * (DP / 16) * 32 + kThreads - 1) / kThreads;
+    uint2 qs[kQs];
+#pragma unroll
+    for (int y = 0; y < kQs; ++y) {
+      const int i = tid + y * kThreads, n8 = i / ((DP / 16) * 32), step = i / 32 % (DP / 16);
+      const int column = n8 * 8 + (i >> 2 & 7), ch = step * 16 + 2 * (i & 3);
+      qs[y] = make_uint2(0, 0);
+      if (n8 < N8 && column < columns) {
+        const int tok = column / heads;
+        const char* src = p.q + (long long)(g.token + tok) * p.q_token +
+                          (long long)(head0 + column - tok * heads) * p.q_head + ch * 2;
+        if (ch < p.dim) qs[y].x = *(const uint32_t*)src;
+        if (ch + 8 < p.dim) qs[y].y = *(const uint32_t*)(src + 16);
+      }
+    }
+    const int page0 = entry0 >= 0 ? p.rq.table[g.b * p.rq.table_stride + entry0] : -1;
+#pragma unroll
+    for (int y = 0; y < kQs; ++y)  // (a negative factor of the scores is Q's sign)
+      if (tid + y * kThreads < N8 * (DP / 16) * 32)
+        q_frag[tid + y * kThreads] = make_uint2(qs[y].x ^ flip, qs[y].y ^ flip);
     // One token's list is taken in parts of what the block lists at a time; of several tokens
     // the host made sure that all their pages fit.
     for (int part = 0; part < (one ? p.count : 1); part += kSelList) {
@@ -215,10 +225,16 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
       __syncthreads();
       if (one) {
         int top = 0;
-        for (int i = tid; i < kSelList && part + i < p.count; i += kSelThreads) {
-          const int col = entry(0, part + i);
+        for (int i = tid; i < kSelList && part + i < p.count; i += kThreads) {
+          const bool known = part + i < kThreads;
+          const int col = known ? entry0 : entry(0, part + i);
+          int page = known ? page0 : col >= 0 ? p.rq.table[g.b * p.rq.table_stride + col] : -1;
+          if (col >= 0 && (page < 0 || page >= p.rq.num_pages)) {
+            atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
+            page = -1;
+          }
           list.col[i] = col;
-          list.page[i] = col >= 0 ? p.rq.page(g.b, col) : -1;
+          list.page[i] = page;
           list.mask[i] = col >= 0;
           if (col >= 0) top = i + 1;
         }
@@ -227,10 +243,10 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
       } else {
         // a byte for each visible column, over the ring; then the bytes that are not 0 in order
         uint32_t* bytes = (uint32_t*)smem;
-        const int words = (visible + 3) / 4, run = (words + kSelThreads - 1) / kSelThreads;
-        for (int i = tid; i < words; i += kSelThreads) bytes[i] = 0;
+        const int words = (visible + 3) / 4, run = (words + kThreads - 1) / kThreads;
+        for (int i = tid; i < words; i += kThreads) bytes[i] = 0;
         __syncthreads();
-        for (int i = tid; i < g.tokens * p.count; i += kSelThreads) {
+        for (int i = tid; i < g.tokens * p.count; i += kThreads) {
           const int k = i / p.count, col = entry(k, i - k * p.count);
           if (col >= 0) atomicOr(&bytes[col >> 2], 1u << (8 * (col & 3) + k));
         }
@@ -239,7 +255,7 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
         int n = 0;
         for (int i = w0; i < w1; ++i) n += __popc(__vcmpgtu4(bytes[i], 0)) / 8;
         int all;
-        int at = block_before<kSelThreads>(n, sums, all);
+        int at = block_before<kThreads>(n, sums, all);
         for (int i = w0; i < w1; ++i)
           for (uint32_t w = bytes[i], y = 0; w; w >>= 8, ++y)
             if (w & 255) {
@@ -248,7 +264,7 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
               ++at;
             }
         __syncthreads();
-        for (int i = tid; i < all; i += kSelThreads) list.page[i] = p.rq.page(g.b, list.col[i]);
+        for (int i = tid; i < all; i += kThreads) list.page[i] = p.rq.page(g.b, list.col[i]);
         if (tid == 0) listed = all;
       }
       __syncthreads();
@@ -259,7 +275,7 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
         __syncwarp();
       }
       const int tiles = (n * page_size + 15) / 16;
-      const int from = rank * kSelWarps + warp, step = p.cluster * kSelWarps;
+      const int from = rank * kWarps + warp, step = p.cluster * kWarps;
       unsigned long long seen_by = 0;  // of key lane % 16 of the tiles in flight: bits of tokens, the
                              // youngest tile's lowest
       auto issue = [&](int tile, int stage) {
@@ -383,11 +399,11 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
     // ---- join: the block's warps
     __syncthreads();
     float* part_o = (float*)smem;                                     // [warp][column][pitch]
-    float* all_o = part_o + kSelWarps * Cfg::kCols * Cfg::kPitch;     // the block's
+    float* all_o = part_o + kWarps * Cfg::kCols * Cfg::kPitch;     // the block's
     float* part_m = all_o + Cfg::kCols * Cfg::kPitch;                 // [warp + 1][column]
-    float* part_l = part_m + (kSelWarps + 1) * Cfg::kCols;
-    float* all_m = part_m + kSelWarps * Cfg::kCols;
-    float* all_l = part_l + kSelWarps * Cfg::kCols;
+    float* part_l = part_m + (kWarps + 1) * Cfg::kCols;
+    float* all_m = part_m + kWarps * Cfg::kCols;
+    float* all_l = part_l + kWarps * Cfg::kCols;
 #pragma unroll
     for (int n8 = 0; n8 < N8; ++n8)
 #pragma unroll
@@ -419,13 +435,13 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
         p.lse[t * p.heads + head] =
             sum == 0.f ? -INFINITY : (top + log2f(sum) - kBias) * 0.69314718055994531f;
     };
-    for (int i = tid; i < columns * pairs; i += kSelThreads) {
+    for (int i = tid; i < columns * pairs; i += kThreads) {
       const int column = i / pairs, d = i - column * pairs;
       float top = -INFINITY, sum = 0.f, a = 0.f, b = 0.f;
 #pragma unroll
-      for (int w = 0; w < kSelWarps; ++w) top = fmaxf(top, part_m[w * Cfg::kCols + column]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * Cfg::kCols + column]);
 #pragma unroll
-      for (int w = 0; w < kSelWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float f = weight_of(part_m[w * Cfg::kCols + column], top);
         const float2 y =
             *(const float2*)(part_o + (w * Cfg::kCols + column) * Cfg::kPitch + 2 * d);
@@ -443,28 +459,39 @@ __global__ void __launch_bounds__(kSelThreads, SelCfg<DP, N8, DEEP>::kBlocks)
     // ---- the cluster's blocks, each a part of the results
     if (p.cluster > 1) {
       cluster_sync();
-      for (int i = tid + rank * kSelThreads; i < columns * pairs; i += p.cluster * kSelThreads) {
+      for (int i = tid + rank * kThreads; i < columns * pairs; i += p.cluster * kThreads) {
         const int column = i / pairs, d = i - column * pairs;
-        float top = -INFINITY, sum = 0.f, a = 0.f, b = 0.f;
-        for (int w = 0; w < p.cluster; ++w) top = fmaxf(top, cluster_load(all_m + column, w));
-        for (int w = 0; w < p.cluster; ++w) {
-          const float f = weight_of(cluster_load(all_m + column, w), top);
-          sum += f * cluster_load(all_l + column, w);
-          a += f * cluster_load(all_o + column * Cfg::kPitch + 2 * d, w);
-          b += f * cluster_load(all_o + column * Cfg::kPitch + 2 * d + 1, w);
+        float m[8], l[8], top = -INFINITY, sum = 0.f, a = 0.f, b = 0.f;
+        float2 o[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {  // (the cluster is a power of two: others are read again)
+          const int from = w & (p.cluster - 1);
+          m[w] = cluster_load(all_m + column, from);
+          l[w] = cluster_load(all_l + column, from);
+          o[w] = cluster_load((const float2*)(all_o + column * Cfg::kPitch + 2 * d), from);
+        }
+#pragma unroll
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, m[w]);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          if (w >= p.cluster) break;
+          const float f = weight_of(m[w], top);
+          sum += f * l[w];
+          a += f * o[w].x;
+          b += f * o[w].y;
         }
         put(column, d, a, b, top, sum);
       }
       cluster_sync();
     }
   }
-  for_idle_rows<kSelThreads>(p.rq, g, [&](int t) {
+  for_idle_rows<kThreads>(p.rq, g, [&](int t) {
     const int pieces = p.dim / 8;
-    for (int i = tid; i < p.heads * pieces; i += kSelThreads)
+    for (int i = tid; i < p.heads * pieces; i += kThreads)
       *(uint4*)(p.out + t * p.out_token + (i / pieces) * p.out_head + (i % pieces) * 16) =
           make_uint4(0, 0, 0, 0);
     if (p.lse)
-      for (int i = tid; i < p.heads; i += kSelThreads) p.lse[(long long)t * p.heads + i] = -INFINITY;
+      for (int i = tid; i < p.heads; i += kThreads) p.lse[(long long)t * p.heads + i] = -INFINITY;
   });
 }
 

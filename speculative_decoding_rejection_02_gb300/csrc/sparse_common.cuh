@@ -202,6 +202,16 @@ __device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
+__device__ __forceinline__ float2 cluster_load(const float2* p, uint32_t rank) {
+  uint32_t at;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(at)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ int2 cluster_load(const int2* p, uint32_t rank) {
   uint32_t at;
   int2 v;
