@@ -170,10 +170,9 @@ __global__ void __launch_bounds__(SelCfg<DP, N8, DEEP>::kThreads, SelCfg<DP, N8,
 #pragma unroll
       for (int y = 0; y < DP / 16; ++y) o[y][n][0] = o[y][n][1] = o[y][n][2] = o[y][n][3] = 0.f;
     }
-    // Entry i of token k's list as a visible column, or -1. (Broken lists are told of once.)
-    auto entry = [&](int k, int i) {
-      const int* row = lists + k * next_list;
-      const int col = row[i], before = i > 0 ? row[i - 1] : -1;
+    // Entry i of token k's list, which follows `before`, as a visible column, or -1. (Broken lists
+    // are told of once.)
+    auto checked = [&](int k, int i, int col, int before) {
       if (col < 0 || g.len == 0) return -1;
       if ((i > 0 && (before < 0 || before >= col)) ||
           ((long long)col << shift) >= g.len) {
@@ -194,9 +193,19 @@ __global__ void __launch_bounds__(SelCfg<DP, N8, DEEP>::kThreads, SelCfg<DP, N8,
       lane_dst[y] = r * (DP * 2) + ((piece ^ r) & 7) * 16 + (piece & 8) * 16;
     }
     const bool one = g.tokens == 1;
-    // The start of the list, Q and the pages' numbers, each on its way while the others are
-    // waited for. Q as operands: two channels of one column at a time.
-    const int entry0 = one && tid < min(kSelList, p.count) ? entry(0, tid) : -1;
+    // The lists (of one token's the start), Q and a first page's number, each on its way while
+    // the others are waited for. Q as operands: two channels of one column at a time.
+    constexpr int kEntries = (kSelList + kThreads - 1) / kThreads;
+    int entries[kEntries], befores[kEntries];
+#pragma unroll
+    for (int y = 0; y < kEntries; ++y) {
+      const int i = tid + y * kThreads;
+      const bool there = i < kSelList && i < g.tokens * p.count;
+      const int k = one ? 0 : i / p.count, at = i - k * p.count;
+      const int* row = lists + k * next_list + at;
+      entries[y] = there ? row[0] : -1;
+      befores[y] = there && at > 0 ? row[-1] : -1;
+    }
     constexpr int kQs = (N8 * (DP / 16) * 32 + kThreads - 1) / kThreads;
     uint2 qs[kQs];
 #pragma unroll
@@ -212,7 +221,12 @@ __global__ void __launch_bounds__(SelCfg<DP, N8, DEEP>::kThreads, SelCfg<DP, N8,
         if (ch + 8 < p.dim) qs[y].y = *(const uint32_t*)(src + 16);
       }
     }
-    const int page0 = entry0 >= 0 ? p.rq.table[g.b * p.rq.table_stride + entry0] : -1;
+#pragma unroll
+    for (int y = 0; y < kEntries; ++y) {
+      const int i = tid + y * kThreads, k = one ? 0 : i / p.count;
+      entries[y] = checked(k, i - k * p.count, entries[y], befores[y]);
+    }
+    const int page0 = one && entries[0] >= 0 ? p.rq.table[g.b * p.rq.table_stride + entries[0]] : -1;
 #pragma unroll
     for (int y = 0; y < kQs; ++y)  // (a negative factor of the scores is Q's sign)
       if (tid + y * kThreads < N8 * (DP / 16) * 32)
@@ -225,10 +239,16 @@ __global__ void __launch_bounds__(SelCfg<DP, N8, DEEP>::kThreads, SelCfg<DP, N8,
       __syncthreads();
       if (one) {
         int top = 0;
-        for (int i = tid; i < kSelList && part + i < p.count; i += kThreads) {
-          const bool known = part + i < kThreads;
-          const int col = known ? entry0 : entry(0, part + i);
-          int page = known ? page0 : col >= 0 ? p.rq.table[g.b * p.rq.table_stride + col] : -1;
+#pragma unroll
+        for (int y = 0; y < kEntries; ++y) {
+          const int i = tid + y * kThreads;
+          if (i >= kSelList || part + i >= p.count) break;
+          int col = entries[y];
+          if (part > 0)
+            col = checked(0, part + i, lists[part + i], lists[part + i - 1]);
+          int page = part == 0 && y == 0 ? page0
+                     : col >= 0          ? p.rq.table[g.b * p.rq.table_stride + col]
+                                         : -1;
           if (col >= 0 && (page < 0 || page >= p.rq.num_pages)) {
             atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
             page = -1;
@@ -246,8 +266,9 @@ __global__ void __launch_bounds__(SelCfg<DP, N8, DEEP>::kThreads, SelCfg<DP, N8,
         const int words = (visible + 3) / 4, run = (words + kThreads - 1) / kThreads;
         for (int i = tid; i < words; i += kThreads) bytes[i] = 0;
         __syncthreads();
-        for (int i = tid; i < g.tokens * p.count; i += kThreads) {
-          const int k = i / p.count, col = entry(k, i - k * p.count);
+#pragma unroll
+        for (int y = 0; y < kEntries; ++y) {
+          const int col = entries[y], k = (tid + y * kThreads) / p.count;
           if (col >= 0) atomicOr(&bytes[col >> 2], 1u << (8 * (col & 3) + k));
         }
         __syncthreads();
