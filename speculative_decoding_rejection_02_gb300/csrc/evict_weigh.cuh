@@ -253,45 +253,53 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   WeighWalk walk;
   if (walk.start(p, sh)) {
     if (warp == kWeighSums) {
-      // ---- K: the pair's tiles, page by page
+      // ---- K, page by page: the first 16 lanes load the pair's one tile, the others the other
       const int page = 1 << p.rq.page_shift, box = min(page, kWeighTile);
-      const int boxes = kWeighTile / box;
+      const int boxes = kWeighTile / box, g = lane >> 4, part = lane & 15;
+      const uint32_t half = 0xffffu << (lane & 16);
       unsigned issued[2] = {0, 0};
       bool ok = true;
-      // the number of the page that the lane loads of a tile; -1: none
-      auto look = [&](int g) {
-        const int j = (walk.pair * 2 + g) * kWeighTile + lane * box;
-        if (lane >= boxes || j >= walk.u.len) return -1;
+      // the number of the page that the lane loads; -1: none. Looked up a pair ahead.
+      auto place = [&](const WeighWalk& walk) {
+        return (walk.pair * 2 + g) * kWeighTile + part * box;
+      };
+      auto look = [&](const WeighWalk& walk) {
+        const int j = place(walk);
+        if (part >= boxes || j >= walk.u.len) return -1;
         return p.rq.table[walk.b * p.rq.table_stride + (j >> p.rq.page_shift)];
       };
-      do {
-        int number[2] = {look(0), look(1)};
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (!ok || !walk.has(g)) break;
-          const int j = (walk.pair * 2 + g) * kWeighTile + lane * box;
-          if (lane < boxes && j < walk.u.len && (number[g] < 0 || number[g] >= p.rq.num_pages)) {
-            atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
-            number[g] = -1;
-          }
-          const int count = __popc(__ballot_sync(~0u, number[g] >= 0));
-          const unsigned at = g * p.k_stages + issued[g] % p.k_stages;
-          ok = weigh_wait(sh, p, &sh.k_empty[at], issued[g] / p.k_stages + 1);
-          if (!ok) break;
-          if (lane < boxes) sh.pages[at][lane] = number[g];
-          __syncwarp();
-          if (lane == 0)
-            mbar_arrive_expect_tx(&sh.k_full[at], count * p.blocks * box * 128);
-          __syncwarp();
-          if (number[g] >= 0)
-            for (int x = 0; x < p.blocks; ++x)
-              tma_load_4d(smem + at * stage_bytes + x * kWeighTile * 128 + lane * box * 128,
-                          &p.k_map, 64 * x, j & (page - 1), walk.head, number[g],
-                          &sh.k_full[at]);
-          __syncwarp();
-          ++issued[g];
+      int next = look(walk);
+      for (bool more = true; more;) {
+        int number = next;
+        WeighWalk ahead = walk;
+        more = ahead.next(p);
+        if (more) next = look(ahead);
+        const int j = place(walk);
+        if (part < boxes && j < walk.u.len && (number < 0 || number >= p.rq.num_pages)) {
+          atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
+          number = -1;
         }
-      } while (ok && walk.next(p));
+        const bool both = walk.has(1);
+        const unsigned at0 = issued[0] % p.k_stages, at1 = p.k_stages + issued[1] % p.k_stages;
+        ok = weigh_wait(sh, p, &sh.k_empty[at0], issued[0] / p.k_stages + 1) &&
+             (!both || weigh_wait(sh, p, &sh.k_empty[at1], issued[1] / p.k_stages + 1));
+        if (!ok) break;
+        const unsigned at = g ? at1 : at0;
+        const uint32_t live = __ballot_sync(~0u, number >= 0);
+        if (g == 0 || both) sh.pages[at][part] = number;
+        __syncwarp();
+        if (part == 0 && (g == 0 || both))
+          mbar_arrive_expect_tx(&sh.k_full[at], __popc(live & half) * p.blocks * box * 128);
+        __syncwarp();
+        if (number >= 0)
+          for (int x = 0; x < p.blocks; ++x)
+            tma_load_4d(smem + at * stage_bytes + x * kWeighTile * 128 + part * box * 128, &p.k_map,
+                        64 * x, j & (page - 1), walk.head, number, &sh.k_full[at]);
+        __syncwarp();
+        ++issued[0];
+        issued[1] += both;
+        walk = ahead;
+      }
 #pragma unroll
       for (int g = 0; g < 2; ++g)
         for (unsigned r = issued[g] > p.k_stages ? issued[g] - p.k_stages : 0; r < issued[g]; ++r)
@@ -412,11 +420,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         const int key = (walk.pair * 2 + g) * kWeighTile + row;
         float* w = nullptr;
         float before = 0.f;
-        // column tiles [all_from, whole) have `full` columns, all of which see all keys: code that
-        // looks at each column's place takes 387 us for two chunks of 2048, not 344
+        // from column tile all_from on all columns see all keys: code that looks at each column's
+        // place takes 387 us for two chunks of 2048, not 347
         const int over = max((walk.pair * 2 + g + 1) * kWeighTile - 1 - walk.u.old, 0);
         const int all_from = (over + p.tile_tokens - 1) / p.tile_tokens;
-        const int whole = (walk.u.hi - walk.u.lo) / p.tile_tokens, full = p.tile_tokens * p.G;
         unsigned long long sum2[4] = {0, 0, 0, 0};
         float rest = 0.f;
         for (int t = t0; ok && t < walk.u.tiles; ++t) {
@@ -459,29 +466,33 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 sum2[2 * (y & 1) + 1] = f2_add(sum2[2 * (y & 1) + 1], f2_pack(ex2(c), ex2(d)));
               }
             };
-            // the same, of which only the first n are columns
+            // the same, of which only the first n are columns (others may hold anything)
             auto add_some = [&](int k, int n) {
               float x[32];
               tmem_ld32(tmem + k, x);
               tmem_wait_ld(x);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) {
-                const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
-                if (y < n) rest += e;
+              for (int y = 0; y < 32; y += 4) {
+                if (y >= n) break;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  const float e = ex2(fmaf(x[y + z], p.c, shift[k + y + z]));
+                  if (y + z < n) rest += e;
+                }
               }
             };
-            if (t >= all_from && t < whole && full == kWeighTile) {
+            const int columns =
+                min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
+            if (t >= all_from && columns == kWeighTile) {
 #pragma unroll
               for (int k = 0; k < kWeighTile; k += 32) add(k);
-            } else if (t >= all_from && t < whole) {
+            } else if (t >= all_from) {
               int k = 0;
 #pragma unroll 1
-              for (; k + 32 <= full; k += 32) add(k);
-              if (k < full) add_some(k, full - k);
+              for (; k + 32 <= columns; k += 32) add(k);
+              if (k < columns) add_some(k, columns - k);
             } else {
               // columns [from, columns) of the tile see the key
-              const int columns =
-                  min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
               const long long ahead = (long long)key - walk.u.old - t * p.tile_tokens;
               const int from = ahead > 0 ? (int)min(ahead * p.G, (long long)kWeighTile) : 0;
 #pragma unroll 1

@@ -14,10 +14,10 @@
 // of a row: the order of the channels in the sums is free, so they go into the products as they
 // come, and [N, P] lies in shared memory in the same order.
 //
-// Work is one list of 16 columns for each group of tokens and kv head, cut into equal parts, one for
-// each block: what a block has to do before its first product (find its part, split [N, P]) takes
-// longer than some tens of columns. (A grid over groups, heads and thirds of the columns: 64
-// requests of 2-8 tokens over 1000-30000, 55 us in place of XX.)
+// Work is one list of 16 columns for each group of tokens and kv head, with the start of a group
+// counted in, cut into equal parts, one for each block: what a block has to do before its first
+// product (find its part, split [N, P]) takes longer than some tens of columns. (A grid over groups,
+// heads and thirds of the columns: 64 requests of 2-8 tokens over 1000-30000, 55 us in place of 35.)
 #pragma once
 #include "sparse_common.cuh"
 
@@ -28,6 +28,7 @@ constexpr int kScoreGroup = 8;    // tokens of a product
 constexpr int kScoreGroups = 4;   // of those in a group of tokens, at most
 constexpr int kScoreBlocks = 4;   // of an SM
 constexpr int kScorePart = 4;     // places of a block at least: one for each warp
+constexpr int kScoreStart = 4;    // what the start of a unit counts: splitting [N, P]
 
 struct ScoreParams {
   Requests rq;
@@ -59,7 +60,8 @@ __device__ __forceinline__ void split3(float x, float* part) {
 }
 
 // What a request is in the list that the blocks divide: for each kv head and group of tokens
-// `reals` places of 16 columns that some token may see, then `fills` places of 128 that none does.
+// kScoreStart places for the start, `reals` of 16 columns that some token may see, then `fills` of
+// 128 that none does.
 struct ScoreUnits {
   int lo, hi, len, groups, reals, fills;
   __device__ __forceinline__ ScoreUnits() {}
@@ -71,7 +73,7 @@ struct ScoreUnits {
     fills = ((int)(((long long)p.rq.width + 15) / 16) - reals + 7) / 8;
   }
   __device__ __forceinline__ long long places(const ScoreParams& p) const {
-    return (long long)groups * (reals + fills) * p.kv_heads;
+    return (long long)groups * (kScoreStart + reals + fills) * p.kv_heads;
   }
 };
 
@@ -138,7 +140,6 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
   if (b >= 0) {
     // walk: place `at` of request b, up to the end of the part
     long long left = sh_end - sh_begin, at = sh_begin - sh_at;
-    bool begins = true;
 #pragma unroll 1
     while (left > 0) {
       const ScoreUnits u(p, b);
@@ -148,20 +149,18 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
         if (++b >= p.rq.B) break;
         continue;
       }
-      const int per_unit = u.reals + u.fills;
+      const int per_unit = kScoreStart + u.reals + u.fills;
       const long long unit = quotient(at, per_unit);
-      int from = (int)(at - unit * per_unit);
-      // A part that ends within the first places of a unit leaves them to the next part, which
-      // begins with them: one start of a unit less, in the block that takes longest.
-      if (begins && from > 0 && from < kScorePart) at -= from, left += from, from = 0;
-      if (!begins && from == 0 && left < kScorePart && left < per_unit) break;
-      begins = false;
-      const int to = (int)min((long long)per_unit, from + left);
-      const int head = (int)quotient(unit, u.groups), first = (int)(unit - (long long)head * u.groups) * p.per;
+      const int place = (int)(at - unit * per_unit);
+      const int end = (int)min((long long)per_unit, place + left);
+      left -= end - place;
+      at += end - place;
+      const int from = max(place - kScoreStart, 0), to = end - kScoreStart;
+      if (to <= 0) continue;  // (the next part begins with the unit)
+      const int head = (int)quotient(unit, u.groups);
+      const int first = (int)(unit - (long long)head * u.groups) * p.per;
       const int tokens = min(p.per, u.hi - u.lo - first), token = u.lo + first;
       const int pos = u.len ? u.len - (u.hi - u.lo) + first : -(1 << 30);
-      left -= to - from;
-      at += to - from;
       float* row = p.scores + (long long)token * p.s_token + head * p.s_head;
       // columns that nobody sees
       for (int i = max(from - u.reals, 0) + warp; i < to - u.reals; i += kWarps)

@@ -489,7 +489,7 @@ int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* s
   long long units = groups(a->num_tokens, a->B, p.per) * a->kv_heads * p.splits;
   if (units < 1) units = 1;
   // clusters of blocks where the units leave SMs idle, as long as each warp keeps two tiles
-  const long long tiles = (long long)a->count * a->page_size / 16;
+  const long long tiles = (long long)(a->count < a->width ? a->count : a->width) * a->page_size / 16;
   p.cluster = 1;
   while (p.cluster < 8 && units * p.cluster < 3ll * sms &&
          tiles >= 16ll * p.cluster)
