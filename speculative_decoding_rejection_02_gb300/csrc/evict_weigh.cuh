@@ -20,10 +20,11 @@
 // per SM). Every role of a block walks over the part by itself.
 //
 // Warps: 0-7 and 8-15 the sums of the pair's two tiles, 16 loads K (TMA, through the block table),
-// 17 loads Q and the lse, 18 and 19 issue the products of the one and the other tile. (With one
-// issuer for both two chunks of 2048 take 540 us: it is the issue of a product that takes its
-// time, not the product.) The two tiles' chains go ahead of one another, so each has its own
-// stages of K.
+// 17 loads Q and the lse, and where those come once for many pairs half of K (with small pages it is
+// the issue of the loads that takes the time), 18 and 19 issue the products of the one and the other
+// tile. (With one issuer for both two chunks of 2048 take 540 us: it is the issue of a product that
+// takes its time, not the product.) The two tiles' chains go ahead of one another, so each has its
+// own stages of K.
 //
 // Bound by HBM (the keys, once) for few columns, by the exponentials and the products, which take
 // about as long, for many.
@@ -55,6 +56,7 @@ struct WeighParams {
   int tile_tokens;          // new tokens of a column tile
   int blocks;               // of 64 channels
   int k_stages, q_stages;   // of blocks * 16 KB; of K for each of a pair's two tiles
+  int shared_loads;         // the warp that loads Q loads half of K
 };
 
 struct WeighShared {
@@ -170,6 +172,75 @@ struct WeighWalk {
   }
 };
 
+// One warp's loads of K, page by page, of one tile of each pair or of both: the first 16 lanes load
+// the one, the others the other. Pages are looked up a pair ahead.
+struct WeighKeys {
+  int tiles;  // bits: which of a pair's tiles
+  int page, box, g, part;
+  bool on;
+  unsigned issued[2] = {0, 0};
+  int next;
+  __device__ __forceinline__ WeighKeys(const WeighParams& p, const WeighWalk& walk, int tiles)
+      : tiles(tiles) {
+    const int lane = threadIdx.x & 31;
+    page = 1 << p.rq.page_shift;
+    box = min(page, kWeighTile);  // tokens of one load
+    g = lane >> 4;
+    part = lane & 15;
+    on = part < kWeighTile / box && (tiles >> g & 1);
+    next = look(p, walk);
+  }
+  __device__ __forceinline__ int place(const WeighWalk& walk) const {
+    return (walk.pair * 2 + g) * kWeighTile + part * box;
+  }
+  // The number of the page that the lane loads; -1: none.
+  __device__ __forceinline__ int look(const WeighParams& p, const WeighWalk& walk) const {
+    const int j = place(walk);
+    if (!on || j >= walk.u.len) return -1;
+    return p.rq.table[walk.b * p.rq.table_stride + (j >> p.rq.page_shift)];
+  }
+  // The pair's loads; `ahead` is the next one, if there is `more`.
+  __device__ __forceinline__ bool load(WeighShared& sh, const WeighParams& p, char* smem,
+                                       int stage_bytes, const WeighWalk& walk,
+                                       const WeighWalk& ahead, bool more) {
+    int number = next;
+    if (more) next = look(p, ahead);
+    const int j = place(walk);
+    if (on && j < walk.u.len && (number < 0 || number >= p.rq.num_pages)) {
+      atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
+      number = -1;
+    }
+    const int now = tiles & (walk.has(1) ? 3 : 1);
+    const unsigned at0 = issued[0] % p.k_stages, at1 = p.k_stages + issued[1] % p.k_stages;
+    if ((now & 1) && !weigh_wait(sh, p, &sh.k_empty[at0], issued[0] / p.k_stages + 1))
+      return false;
+    if ((now & 2) && !weigh_wait(sh, p, &sh.k_empty[at1], issued[1] / p.k_stages + 1))
+      return false;
+    const unsigned at = g ? at1 : at0;
+    const uint32_t live = __ballot_sync(~0u, number >= 0) & 0xffffu << 16 * g;
+    if (now >> g & 1) sh.pages[at][part] = number;
+    __syncwarp();
+    if (part == 0 && (now >> g & 1))
+      mbar_arrive_expect_tx(&sh.k_full[at], __popc(live) * p.blocks * box * 128);
+    __syncwarp();
+    if (number >= 0)
+      for (int x = 0; x < p.blocks; ++x)
+        tma_load_4d(smem + at * stage_bytes + x * kWeighTile * 128 + part * box * 128, &p.k_map,
+                    64 * x, j & (page - 1), walk.head, number, &sh.k_full[at]);
+    __syncwarp();
+    issued[0] += now & 1;
+    issued[1] += now >> 1;
+    return true;
+  }
+  // Lets the last loads land.
+  __device__ __forceinline__ void land(WeighShared& sh, const WeighParams& p) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      for (unsigned r = issued[t] > p.k_stages ? issued[t] - p.k_stages : 0; r < issued[t]; ++r)
+        weigh_land(&sh.k_full[t * p.k_stages + r % p.k_stages], r / p.k_stages);
+  }
+};
+
 __global__ void __launch_bounds__(kWeighThreads, 1)
     k_cache_weigh(const __grid_constant__ WeighParams p, const int run) {
   extern __shared__ __align__(1024) char weigh_smem[];
@@ -253,57 +324,15 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
   WeighWalk walk;
   if (walk.start(p, sh)) {
     if (warp == kWeighSums) {
-      // ---- K, page by page: the first 16 lanes load the pair's one tile, the others the other
-      const int page = 1 << p.rq.page_shift, box = min(page, kWeighTile);
-      const int boxes = kWeighTile / box, g = lane >> 4, part = lane & 15;
-      const uint32_t half = 0xffffu << (lane & 16);
-      unsigned issued[2] = {0, 0};
-      bool ok = true;
-      // the number of the page that the lane loads; -1: none. Looked up a pair ahead.
-      auto place = [&](const WeighWalk& walk) {
-        return (walk.pair * 2 + g) * kWeighTile + part * box;
-      };
-      auto look = [&](const WeighWalk& walk) {
-        const int j = place(walk);
-        if (part >= boxes || j >= walk.u.len) return -1;
-        return p.rq.table[walk.b * p.rq.table_stride + (j >> p.rq.page_shift)];
-      };
-      int next = look(walk);
+      // ---- K, or of it the pairs' first tiles
+      WeighKeys keys(p, walk, p.shared_loads ? 1 : 3);
       for (bool more = true; more;) {
-        int number = next;
         WeighWalk ahead = walk;
         more = ahead.next(p);
-        if (more) next = look(ahead);
-        const int j = place(walk);
-        if (part < boxes && j < walk.u.len && (number < 0 || number >= p.rq.num_pages)) {
-          atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
-          number = -1;
-        }
-        const bool both = walk.has(1);
-        const unsigned at0 = issued[0] % p.k_stages, at1 = p.k_stages + issued[1] % p.k_stages;
-        ok = weigh_wait(sh, p, &sh.k_empty[at0], issued[0] / p.k_stages + 1) &&
-             (!both || weigh_wait(sh, p, &sh.k_empty[at1], issued[1] / p.k_stages + 1));
-        if (!ok) break;
-        const unsigned at = g ? at1 : at0;
-        const uint32_t live = __ballot_sync(~0u, number >= 0);
-        if (g == 0 || both) sh.pages[at][part] = number;
-        __syncwarp();
-        if (part == 0 && (g == 0 || both))
-          mbar_arrive_expect_tx(&sh.k_full[at], __popc(live & half) * p.blocks * box * 128);
-        __syncwarp();
-        if (number >= 0)
-          for (int x = 0; x < p.blocks; ++x)
-            tma_load_4d(smem + at * stage_bytes + x * kWeighTile * 128 + part * box * 128, &p.k_map,
-                        64 * x, j & (page - 1), walk.head, number, &sh.k_full[at]);
-        __syncwarp();
-        ++issued[0];
-        issued[1] += both;
+        if (!keys.load(sh, p, smem, stage_bytes, walk, ahead, more)) break;
         walk = ahead;
       }
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        for (unsigned r = issued[g] > p.k_stages ? issued[g] - p.k_stages : 0; r < issued[g]; ++r)
-          weigh_land(&sh.k_full[g * p.k_stages + r % p.k_stages], r / p.k_stages);
+      keys.land(sh, p);
     } else if (warp == kWeighSums + 1) {
       // ---- Q and its columns' -lse log2(e) (loaded two tiles ahead) of every pair's column
       // tiles, or once for a unit that has only one
@@ -313,12 +342,16 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         tok[y] = (lane + 32 * y) / p.G;
         from[y] = tok[y] * p.heads + lane + 32 * y - tok[y] * p.G;
       }
+      WeighKeys keys(p, walk, p.shared_loads ? 2 : 0);
       unsigned issued = 0;
       bool ok = true;
-      do {
-        if (walk.u.tiles == 1 && !walk.fresh) continue;
-        const float* lse = p.lse + (long long)walk.u.lo * p.heads + walk.head * p.G;
-        const int tokens = walk.u.hi - walk.u.lo, t0 = walk.first_tile(p);
+      for (bool more = true; ok && more;) {
+        const WeighWalk now = walk;
+        more = walk.next(p);
+        if (p.shared_loads && !keys.load(sh, p, smem, stage_bytes, now, walk, more)) break;
+        if (now.u.tiles == 1 && !now.fresh) continue;
+        const float* lse = p.lse + (long long)now.u.lo * p.heads + now.head * p.G;
+        const int tokens = now.u.hi - now.u.lo, t0 = now.first_tile(p);
         float z[2][4];
         auto look = [&](int t, float* z) {
           const int first = t * p.tile_tokens, n = min(p.tile_tokens, tokens - first);
@@ -334,7 +367,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             mbar_arrive_expect_tx(&sh.q_full[at], p.blocks * p.tile_tokens * p.G * 128);
             for (int x = 0; x < p.blocks; ++x)
               tma_load_4d(q_smem + at * stage_bytes + x * kWeighTile * 128, &p.q_map, 64 * x, 0,
-                          walk.head, walk.u.lo + t * p.tile_tokens, &sh.q_full[at]);
+                          now.head, now.u.lo + t * p.tile_tokens, &sh.q_full[at]);
           }
           __syncwarp();
           ++issued;
@@ -350,11 +383,12 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         };
         look(t0, z[0]);
         look(t0 + 1, z[1]);
-        for (int t = t0; ok && t < walk.u.tiles; t += 2) {
+        for (int t = t0; ok && t < now.u.tiles; t += 2) {
           put(t, z[0]);
-          if (ok && t + 1 < walk.u.tiles) put(t + 1, z[1]);
+          if (ok && t + 1 < now.u.tiles) put(t + 1, z[1]);
         }
-      } while (ok && walk.next(p));
+      }
+      keys.land(sh, p);
       for (unsigned r = issued > p.q_stages ? issued - p.q_stages : 0; r < issued; ++r)
         weigh_land(&sh.q_full[r % p.q_stages], r / p.q_stages);
     } else if (warp == kWeighSums + 2 || warp == kWeighSums + 3) {

@@ -529,7 +529,8 @@ int spec_cache_weigh(const spec_cache_weigh_args* a, void* stream, unsigned* dev
   // Q of one column tile stays for a unit, and most stages hold keys; of several, they come again
   // for every pair of key tiles. (A wait for keys is rare then: a pair goes over all columns.)
   const int stages = sv::kWeighStages / (p.blocks * sv::kWeighTile * 128);
-  p.q_stages = a->max_q <= p.tile_tokens ? 2 : 4;
+  p.shared_loads = a->max_q <= p.tile_tokens;
+  p.q_stages = p.shared_loads ? 2 : 4;
   p.k_stages = (stages - p.q_stages) / 2;
   const int box = a->page_size < sv::kWeighTile ? a->page_size : sv::kWeighTile;
   if (!tensor_map(&p.q_map, a->dtype, a->q, a->dim, p.G, a->q_head, a->kv_heads, a->q_head * p.G,
