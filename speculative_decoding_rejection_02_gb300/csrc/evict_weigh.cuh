@@ -454,10 +454,12 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         const int key = (walk.pair * 2 + g) * kWeighTile + row;
         float* w = nullptr;
         float before = 0.f;
-        // from column tile all_from on all columns see all keys: code that looks at each column's
-        // place takes 387 us for two chunks of 2048, not 347
+        // From column tile all_from on all columns see all keys, and up to `whole` there are `full`
+        // columns: code that looks at each column's place takes 387 us for two chunks of 2048, not
+        // 350.
         const int over = max((walk.pair * 2 + g + 1) * kWeighTile - 1 - walk.u.old, 0);
         const int all_from = (over + p.tile_tokens - 1) / p.tile_tokens;
+        const int whole = (walk.u.hi - walk.u.lo) / p.tile_tokens, full = p.tile_tokens * p.G;
         unsigned long long sum2[4] = {0, 0, 0, 0};
         float rest = 0.f;
         for (int t = t0; ok && t < walk.u.tiles; ++t) {
@@ -506,18 +508,14 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
               tmem_ld32(tmem + k, x);
               tmem_wait_ld(x);
 #pragma unroll
-              for (int y = 0; y < 32; y += 4) {
-                if (y >= n) break;
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  const float e = ex2(fmaf(x[y + z], p.c, shift[k + y + z]));
-                  if (y + z < n) rest += e;
-                }
+              for (int y = 0; y < 32; ++y) {
+                const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
+                if (y < n) rest += e;
               }
             };
             const int columns =
                 min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
-            if (t >= all_from && columns == kWeighTile) {
+            if (t >= all_from && t < whole && full == kWeighTile) {
 #pragma unroll
               for (int k = 0; k < kWeighTile; k += 32) add(k);
             } else if (t >= all_from) {
