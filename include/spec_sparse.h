@@ -29,8 +29,8 @@
  * -inf (scores), -1 (columns) or 0 (outputs). A request whose length cannot be sees nothing;
  * offsets that cannot be (negative, falling, past the last row) make the outputs of the call
  * meaningless. Both set SPEC_CACHE_BAD_LENGTHS.
- * Page sizes are powers of two from 8 to 2^20, dim is a multiple of 8 up to 128 and a kv head has up
- * to 128 query heads (SPEC_ERR_UNSUPPORTED). Addresses and strides (of more than one element)
+ * Page sizes are powers of two from 8 to 2^20, dim is a multiple of 8 up to 128 and a kv head has
+ * up to 128 query heads (SPEC_ERR_UNSUPPORTED). Addresses and strides (of more than one element)
  * of 16-bit arrays are multiples of 16 bytes. What a call writes overlaps none of its other
  * arguments. Results are the same to the bit in every call with the same arguments.
  */

@@ -256,8 +256,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const EvictParams p
   };
   auto meet = [&] {
     if (p.cluster > 1)
-      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-                   ::: "memory");
+      cluster_sync();
     else
       __syncthreads();
   };

@@ -11,20 +11,21 @@
 // A pair of key tiles goes over the request's column tiles together, so that a tile of Q is loaded
 // for 256 keys: with 128 the loads alone would take what an SM gets from L2. Each key tile has two
 // groups of four warps with a place in TMEM each, which take its column tiles in turns; at the end
-// of the pair one passes its sums to the other. (One group with both places leaves the tensor
-// cores and the exponentials idle for two thirds of the time: two warps for each scheduler do not
-// cover the latency of what they do.)
+// of the pair one passes its sums to the other. (One group with both places: 421 us for two chunks
+// of 2048 over 11000-14000 where two groups took 391: two warps for each scheduler do not cover the
+// latency of what they do.)
 //
 // The pairs of all requests and kv heads stand in one list, in which a pair counts by its column
 // tiles (three at least: what its loads take), cut into equal parts, one for each block (one block
 // per SM). Every role of a block walks over the part by itself.
 //
 // Warps: 0-7 and 8-15 the sums of the pair's two tiles, 16 loads K (TMA, through the block table),
-// 17 loads Q and the lse, and where those come once for many pairs half of K (with small pages it is
-// the issue of the loads that takes the time), 18 and 19 issue the products of the one and the other
-// tile. (With one issuer for both two chunks of 2048 take 540 us: it is the issue of a product that
-// takes its time, not the product.) The two tiles' chains go ahead of one another, so each has its
-// own stages of K.
+// 17 loads Q and the lse, and where those come once for many pairs half of K (with small pages it
+// is the issue of the loads that takes the time: 49 single tokens over 38000 in pages of 8 or 16
+// 607 us in place of 668), 18 and 19 issue the products of the one and the other tile. (A
+// second issuer took two chunks of 2048 over 11000-14000 from 540 us to 409: it is the issue of a
+// product that takes its time, not the product.) The two tiles' chains go ahead of one another, so
+// each has its own stages of K.
 //
 // Bound by HBM (the keys, once) for few columns, by the exponentials and the products, which take
 // about as long, for many.

@@ -73,7 +73,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const char* src, uint32_t b
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -226,7 +228,8 @@ __global__ void __launch_bounds__(SelCfg<DP, N8, DEEP>::kThreads, SelCfg<DP, N8,
       const int i = tid + y * kThreads, k = one ? 0 : i / p.count;
       entries[y] = checked(k, i - k * p.count, entries[y], befores[y]);
     }
-    const int page0 = one && entries[0] >= 0 ? p.rq.table[g.b * p.rq.table_stride + entries[0]] : -1;
+    const int* table = p.rq.table + g.b * p.rq.table_stride;
+    const int page0 = one && entries[0] >= 0 ? table[entries[0]] : -1;
 #pragma unroll
     for (int y = 0; y < kQs; ++y)  // (a negative factor of the scores is Q's sign)
       if (tid + y * kThreads < N8 * (DP / 16) * 32)
@@ -297,8 +300,8 @@ __global__ void __launch_bounds__(SelCfg<DP, N8, DEEP>::kThreads, SelCfg<DP, N8,
       }
       const int tiles = (n * page_size + 15) / 16;
       const int from = rank * kWarps + warp, step = p.cluster * kWarps;
-      unsigned long long seen_by = 0;  // of key lane % 16 of the tiles in flight: bits of tokens, the
-                             // youngest tile's lowest
+      // of key lane % 16 of the tiles in flight: bits of tokens, the youngest tile's lowest
+      unsigned long long seen_by = 0;
       auto issue = [&](int tile, int stage) {
         uint32_t mine = 0;
         if (tile < tiles) {

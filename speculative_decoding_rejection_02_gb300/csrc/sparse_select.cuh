@@ -2,11 +2,11 @@
 //
 // Scores become whole numbers of the same order; columns that are always selected have one above
 // all scores'. The k-th largest is found by histograms of its bits, and of equal ones the lowest
-// columns are taken. One block for a row (token, kv head): of four warps up to 2048 columns
-// (k_cache_select_short), else with a run of ITEMS columns in each thread's registers (pick_items;
-// with scores from a model two of the three histograms decide) up to 16384 columns, or by a cluster of blocks where the rows
-// leave SMs idle. Longer rows are read again from shared memory, and what does not fit there
-// from L2.
+// columns are taken. One block for a row (token, kv head): with 16 columns in each thread's
+// registers up to 4096 columns (k_cache_select_short), else with ITEMS (pick_items; with scores
+// from a model two of the three histograms decide) up to 16384. Longer rows are picked from by a
+// cluster of blocks where there are few, else by a block that reads them again from shared memory,
+// and what does not fit there from L2.
 //
 // Bound by the chain of a row: request, scores, histograms, the places.
 #pragma once
@@ -55,35 +55,36 @@ __device__ __forceinline__ void select_check(const SelectParams& p) {
   }
 }
 
-constexpr int kShortThreads = 128, kShortColumns = 2048;
+constexpr int kShortWords = 4;  // of 128 columns for each warp: 16 columns a thread
 constexpr int kShortList = 32;  // candidates that are compared with one another
 
-// Rows of up to kShortColumns columns: four warps for each, a run of columns in the registers of
-// each warp, and one histogram of 256 bins. The bins divide the values between the least and the
-// largest score evenly, so that the bin of the k-th largest as a rule holds a few, which are
-// compared with one another; else it is divided again, by the bits of the values' keys, which takes
-// four rounds at most. (pick_items on 2560 rows of some 500 columns takes 21 us: with bins by the
-// first bits most scores of a row are in a few bins, whose counts come one after the other.)
-// Instructions are what bounds it, so scores stay floats (NaN as +inf), and only words of columns
-// with one that is always selected, or past the last, look at each column's place.
-__global__ void __launch_bounds__(kShortThreads, 8) k_cache_select_short(const SelectParams p) {
-  constexpr int kWarps = kShortThreads / 32, kWords = kShortColumns / 128 / kWarps;
+// Rows of up to 16 NT columns: a run of columns in the registers of each warp, and one histogram of
+// 256 bins. The bins divide the values between the least and the largest score evenly, so that the
+// bin of the k-th largest as a rule holds a few, which are compared with one another; else it is
+// divided again, by the bits of the values' keys, which takes four rounds at most. 2560 rows of
+// some 500 columns: 13 us, 21 with pick_items (with bins by the first bits most scores of a row
+// are in a few bins, whose counts come one after the other), 15 to 21 with a warp for a row at
+// other sizes. Instructions are what bounds it, so scores stay floats (NaN as +inf), and only words
+// of columns with one that is always selected, or past the last, look at each column's place.
+template <int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_cache_select_short(const SelectParams p) {
+  constexpr int kWarps = NT / 32, kWords = kShortWords, kAllTies = 0x7fffffff;
   __shared__ __align__(16) int hist[2][256];
   __shared__ float list[kShortList], low_of[2][kWarps], high_of[2][kWarps];
   __shared__ int listed, taken_of[kWarps], ties_of[kWarps];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  select_check<kShortThreads>(p);
+  select_check<NT>(p);
   const long long t = blockIdx.x / p.kv_heads;
   const int head = (int)(blockIdx.x - t * p.kv_heads);
   int* out = p.out + blockIdx.x * (long long)p.count;
   const int n = select_visible(p, t);
   if (n <= p.count) {
-    for (int i = tid; i < p.count; i += kShortThreads) out[i] = i < n ? i : -1;
+    for (int i = tid; i < p.count; i += NT) out[i] = i < n ? i : -1;
     return;
   }
-  ((int4*)hist)[tid] = make_int4(0, 0, 0, 0);
+  for (int i = tid; i < 128; i += NT) ((int4*)hist)[i] = make_int4(0, 0, 0, 0);
   if (tid == 0) listed = 0;
   const float* row = p.scores + t * p.s_token + head * p.s_head;
   // ---- the warp's words of 128 columns; a lane has four adjacent ones of each
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kShortThreads, 8) k_cache_select_short(const S
     if (there == k || least == most) {  // all of them, or the first of them
       cut = least;
       equals = k;
-      if (there == k) equals = kShortColumns;
+      if (there == k) equals = kAllTies;
       break;
     }
     if (there <= kShortList) {
@@ -221,11 +222,11 @@ __global__ void __launch_bounds__(kShortThreads, 8) k_cache_select_short(const S
       const int who = __ffs(it) - 1;
       cut = __shfl_sync(~0u, y, who);
       equals = k - __shfl_sync(~0u, above, who);
-      if (equals == __shfl_sync(~0u, same, who)) equals = kShortColumns;
+      if (equals == __shfl_sync(~0u, same, who)) equals = kAllTies;
       break;
     }
     linear = false;
-    bins[tid] = bins[tid + 128] = 0;  // (the next round has the other one)
+    for (int i = tid; i < 256; i += NT) bins[i] = 0;  // (the next round has the other one)
   }
   // ---- the places of what is taken
   uint32_t taken = 0, ties = 0;
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kShortThreads, 8) k_cache_select_short(const S
     all = __shfl_sync(~0u, upto, 31);
     return upto - mine;
   };
-  if (equals == kShortColumns) {
+  if (equals == kAllTies) {
     taken |= ties;
   } else if (equals > 0) {  // (in all threads or none)
     const int mine = __reduce_add_sync(~0u, __popc(ties));

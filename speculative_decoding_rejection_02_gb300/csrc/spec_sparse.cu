@@ -138,10 +138,10 @@ int allow(K kernel, int smem, std::atomic<unsigned long long>& ready) {
 }
 
 constexpr int kMostHeld = 48 * 1024;  // keys of a row that is looked at from shared memory
-// Blocks of a cluster that pick from a row of n items together, up to 8; 1: a block alone. A row that
-// fits one block's registers (16384 items) is as fast there (40 rows of 12500: 12.7 us alone, 13.0
-// with two blocks each), longer ones are faster in a cluster as long as that has an SM for each
-// block (12 rows of 20000-33000: 30.6 us alone, 19.3 with eight).
+// Blocks of a cluster that pick from a row of n items together, up to 8; 1: a block alone. A row
+// that fits one block's registers (16384 items) is as fast there (40 rows of 12500: 12.7 us alone,
+// 13.0 with two blocks each), longer ones are faster in a cluster as long as that has an SM for
+// each block (12 rows of 20000-33000: 30.6 us alone, 19.3 with eight).
 int pick_ranks(long long rows, long long n, int sms) {
   int ranks = 1;
   while (ranks < 8 && rows * ranks * 2 <= sms) ranks *= 2;
@@ -416,10 +416,18 @@ int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* d
   p.vec = aligned(a->scores, 16) && a->s_token % 4 == 0 && a->s_head % 4 == 0;
   const unsigned grid = blocks((long long)a->num_tokens * a->kv_heads);
   if (!grid) return SPEC_ERR_UNSUPPORTED;
-  // rows in registers up to 16384 columns, in as few threads as 8 columns each take (16 from 8192)
+  // Rows of up to 4096 columns in as few threads as 16 columns each take (12000 rows of some 500
+  // columns 44 us, with 128 threads for each 59), up to 16384 in 1024 threads, and longer ones
+  // where the row is read again for each histogram.
   p.held = 0;
-  if (a->width <= sv::kShortColumns)
-    return launch(sv::k_cache_select_short, dim3(grid), sv::kShortThreads, 0, stream, p);
+  if (a->width <= 512)
+    return launch(sv::k_cache_select_short<32>, dim3(grid), 32, 0, stream, p);
+  if (a->width <= 1024)
+    return launch(sv::k_cache_select_short<64>, dim3(grid), 64, 0, stream, p);
+  if (a->width <= 2048)
+    return launch(sv::k_cache_select_short<128>, dim3(grid), 128, 0, stream, p);
+  if (a->width <= 4096)
+    return launch(sv::k_cache_select_short<256>, dim3(grid), 256, 0, stream, p);
   const long long rows = (long long)a->num_tokens * a->kv_heads;
   p.ranks = pick_ranks(rows, a->width, sms);
   if (p.ranks > 1) {
@@ -430,8 +438,6 @@ int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* d
                : launch_cluster(sv::k_cache_select<1024, 16, true>, p.ranks, dim3(wide), 1024, 0,
                                 stream, p);
   }
-  if (a->width <= 4096)
-    return launch(sv::k_cache_select<512, 8, false>, dim3(grid), 512, 0, stream, p);
   if (a->width <= 8192)
     return launch(sv::k_cache_select<1024, 8, false>, dim3(grid), 1024, 0, stream, p);
   if (a->width <= 16384)
@@ -471,17 +477,20 @@ int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* s
   // a factor of 0 still leaves masked scores at -inf
   p.c = a->scale * kLog2e;
   if (std::fabs(p.c) < 1.1754944e-38f) p.c = 1.1754944e-38f;
-  // a kv head's query heads in units of 32 at most, and as many tokens of a request (if there may
-  // be several) as 16 columns, the block's list and the bytes over its ring take. With 32 columns
-  // a page is loaded for more tokens, but the block has half as much to hide latency with: 64
-  // requests of 2-8 tokens over 128 pages of 16, four heads on a kv head, 212 us in place of 183
-  // (with eight warps on an SM); with 8 columns 202 us.
+  // A kv head's query heads in units of 32 at most, and as many tokens of a request (if there may
+  // be several) as 16 columns, the block's list and the bytes over its ring take; as 32 columns
+  // where requests have eight tokens or more on average and long lists. With 32 columns a page is
+  // loaded for more tokens, but the SM has fewer warps to hide latency with: 64 requests of 2-8
+  // tokens over 128 pages of 16, four heads on a kv head, 212 us in place of 183 (with 8 columns
+  // 202), 9 of 19-26 over 19 of 16 with seven heads 61 in place of 44; but 28 of 11-18 over 43 of
+  // 64, four heads, 136 in place of 158.
   p.unit_heads = p.G < 32 ? p.G : 32;
   p.splits = (p.G + p.unit_heads - 1) / p.unit_heads;
   p.per = 1;
   const int ring = a->dim > 64 ? sv::SelCfg<128, 1, false>::kRing : sv::SelCfg<64, 1, false>::kRing;
   if (a->num_tokens > a->B && a->width <= ring) {
-    p.per = 16 / p.unit_heads;
+    const bool many = a->num_tokens >= 8ll * a->B && (long long)a->count * a->page_size >= 1024;
+    p.per = (many ? 32 : 16) / p.unit_heads;
     if (p.per > sv::kSelTokens) p.per = sv::kSelTokens;
     if (p.per > sv::kSelList / a->count) p.per = sv::kSelList / a->count;
     if (p.per < 1) p.per = 1;
@@ -489,10 +498,10 @@ int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* s
   long long units = groups(a->num_tokens, a->B, p.per) * a->kv_heads * p.splits;
   if (units < 1) units = 1;
   // clusters of blocks where the units leave SMs idle, as long as each warp keeps two tiles
-  const long long tiles = (long long)(a->count < a->width ? a->count : a->width) * a->page_size / 16;
+  const int listed = a->count < a->width ? a->count : a->width;
+  const long long tiles = (long long)listed * a->page_size / 16;
   p.cluster = 1;
-  while (p.cluster < 8 && units * p.cluster < 3ll * sms &&
-         tiles >= 16ll * p.cluster)
+  while (p.cluster < 8 && units * p.cluster < 3ll * sms && tiles >= 16ll * p.cluster)
     p.cluster *= 2;
   const unsigned grid = blocks(units * p.cluster);
   if (!grid) return SPEC_ERR_UNSUPPORTED;
@@ -587,15 +596,19 @@ int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* dev
   while (p.cluster < 8 && rows * p.cluster < sms) p.cluster *= 2;
   const unsigned grid = blocks(rows > 0 ? rows : 1), moves = blocks(rows * p.cluster);
   if (!grid || (rows > 0 && !moves)) return SPEC_ERR_UNSUPPORTED;
-  // weights in registers as in spec_cache_select
+  // Weights in registers up to 16384 tokens, where few rows are split over clusters; longer
+  // requests' in shared memory, as far as they fit, and looked at again for each histogram.
   const long long most = (long long)a->width * a->page_size;
   p.ranks = rows > 0 ? pick_ranks(rows, most, sms) : 1;
   if (p.ranks > 1) {
     const unsigned wide = blocks(rows * p.ranks);
     rc = most <= p.ranks * 8192
-             ? launch_cluster(sv::k_evict_pick<1024, 8, true>, p.ranks, dim3(wide), 1024, 0, stream, p)
-             : launch_cluster(sv::k_evict_pick<1024, 16, true>, p.ranks, dim3(wide), 1024, 0, stream,
-                              p);
+             ? launch_cluster(sv::k_evict_pick<1024, 8, true>, p.ranks, dim3(wide), 1024, 0,
+                              stream, p)
+             : launch_cluster(sv::k_evict_pick<1024, 16, true>, p.ranks, dim3(wide), 1024, 0,
+                              stream, p);
+  } else if (most <= 1024) {
+    rc = launch(sv::k_evict_pick<128, 8, false>, dim3(grid), 128, 0, stream, p);
   } else if (most <= 4096) {
     rc = launch(sv::k_evict_pick<512, 8, false>, dim3(grid), 512, 0, stream, p);
   } else if (most <= 16384) {
