@@ -55,231 +55,44 @@ __device__ __forceinline__ void select_check(const SelectParams& p) {
   }
 }
 
-constexpr int kShortWords = 4;  // of 128 columns for each warp: 16 columns a thread
-constexpr int kShortList = 32;  // candidates that are compared with one another
-
-// Rows of up to 16 NT columns: a run of columns in the registers of each warp, and one histogram of
-// 256 bins. The bins divide the values between the least and the largest score evenly, so that the
-// bin of the k-th largest as a rule holds a few, which are compared with one another; else it is
-// divided again, by the bits of the values' keys, which takes four rounds at most. 2560 rows of
-// some 500 columns: 13 us, 21 with pick_items (with bins by the first bits most scores of a row
-// are in a few bins, whose counts come one after the other), 15 to 21 with a warp for a row at
-// other sizes. Instructions are what bounds it, so scores stay floats (NaN as +inf), and only words
-// of columns with one that is always selected, or past the last, look at each column's place.
+// Rows of up to 16 NT columns, which the registers hold (pick_short).
 template <int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) k_cache_select_short(const SelectParams p) {
-  constexpr int kWarps = NT / 32, kWords = kShortWords, kAllTies = 0x7fffffff;
-  __shared__ __align__(16) int hist[2][256];
-  __shared__ float list[kShortList], low_of[2][kWarps], high_of[2][kWarps];
-  __shared__ int listed, taken_of[kWarps], ties_of[kWarps];
+__global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
+    k_cache_select_short(const SelectParams p) {
+  __shared__ ShortPick<NT> sh;
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   select_check<NT>(p);
   const long long t = blockIdx.x / p.kv_heads;
   const int head = (int)(blockIdx.x - t * p.kv_heads);
   int* out = p.out + blockIdx.x * (long long)p.count;
   const int n = select_visible(p, t);
   if (n <= p.count) {
-    for (int i = tid; i < p.count; i += NT) out[i] = i < n ? i : -1;
+    for (int i = threadIdx.x; i < p.count; i += NT) out[i] = i < n ? i : -1;
     return;
   }
-  for (int i = tid; i < 128; i += NT) ((int4*)hist)[i] = make_int4(0, 0, 0, 0);
-  if (tid == 0) listed = 0;
-  const float* row = p.scores + t * p.s_token + head * p.s_head;
-  // ---- the warp's words of 128 columns; a lane has four adjacent ones of each
-  const int words = (n + 127) / 128, run = (words + kWarps - 1) / kWarps;
-  const int c0 = 128 * run * warp + 4 * lane, busy = max(min(run, words - run * warp), 0);
-  float v[kWords][4];
+  sh.clear();
+  const float* scores = p.scores + t * p.s_token + head * p.s_head;
+  const ShortRow<NT> row(n);
+  float v[kShortWords][4];
 #pragma unroll
-  for (int w = 0; w < kWords; ++w) {
-    const int c = c0 + 128 * w;
+  for (int w = 0; w < kShortWords; ++w) {
+    const int c = row.c0 + 128 * w;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (w < busy) {
+    if (w < row.busy) {
       if (p.vec && c + 3 < n) {
-        x = *(const float4*)(row + c);
+        x = *(const float4*)(scores + c);
       } else {
-        if (c < n) x.x = row[c];
-        if (c + 1 < n) x.y = row[c + 1];
-        if (c + 2 < n) x.z = row[c + 2];
-        if (c + 3 < n) x.w = row[c + 3];
+        if (c < n) x.x = scores[c];
+        if (c + 1 < n) x.y = scores[c + 1];
+        if (c + 2 < n) x.z = scores[c + 2];
+        if (c + 3 < n) x.w = scores[c + 3];
       }
     }
     v[w][0] = x.x, v[w][1] = x.y, v[w][2] = x.z, v[w][3] = x.w;
   }
-  // bits of the columns that scores decide, and of those that are always selected
-  uint32_t free = 0, always = 0;
-  float least = INFINITY, most = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kWords; ++w) {
-    if (w >= busy) break;
-    const int first = c0 - 4 * lane + 128 * w;
-    uint32_t mine = 15;
-    if (first < p.first || first + 128 > n - p.recent) {
-      mine = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + 128 * w + i;
-        const bool decides = c >= p.first && c < n - p.recent;
-        mine |= (uint32_t)decides << i;
-        always |= (uint32_t)(c < n && !decides) << (4 * w + i);
-      }
-    }
-    free |= mine << (4 * w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (v[w][i] != v[w][i]) v[w][i] = INFINITY;
-      if (mine >> i & 1) least = fminf(least, v[w][i]), most = fmaxf(most, v[w][i]);
-    }
-  }
-  auto spread = [&](int turn) {  // least and most of all warps
-    for (int d = 1; d < 32; d <<= 1) {
-      least = fminf(least, __shfl_xor_sync(~0u, least, d));
-      most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
-    }
-    if (lane == 0) low_of[turn][warp] = least, high_of[turn][warp] = most;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      least = fminf(least, low_of[turn][w]);
-      most = fmaxf(most, high_of[turn][w]);
-    }
-  };
-  spread(0);
-  // ---- the cut: values above it are taken, and the first `equals` of those equal to it
-  float cut = INFINITY;
-  int k = p.count - p.first - p.recent, equals = 0;
-  const float scale = 254.9f / (most - least);
-  bool linear = least > -INFINITY && scale > 0.f && scale < INFINITY;
-#pragma unroll 1
-  for (int turn = 0; k > 0; turn ^= 1) {
-    const float low = least, high = most;
-    const uint32_t low_key = order_key(low);
-    const int shift = max(24 - __clz(order_key(high) - low_key), 0);
-    auto bin_of = [&](float x) {  // from 0 to 255, never falls where x rises
-      if (linear) return __float_as_int(fmaf(x - low, scale, 8388608.f)) & 255;
-      return (int)((order_key(x) - low_key) >> shift);
-    };
-    int* bins = hist[turn];
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-      if (w >= busy) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (free >> (4 * w + i) & 1 && v[w][i] >= low && v[w][i] <= high)
-          atomicAdd(&bins[bin_of(v[w][i])], 1);
-    }
-    __syncthreads();
-    // each warp for itself: the lane's bins, the first lane's the highest
-    const int first = 256 - 8 * (lane + 1);
-    const int4 a = *(const int4*)&bins[first], b = *(const int4*)&bins[first + 4];
-    const int h[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    int upto = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
-    const int mine = upto;
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(~0u, upto, d);
-      if (lane >= d) upto += y;
-    }
-    const int who = __ffs(__ballot_sync(~0u, k <= upto)) - 1;
-    int left = k - (upto - mine), bin = 0, rest = 0, there = 0;
-#pragma unroll
-    for (int i = 7; i >= 0; --i) {
-      if (left > 0 && left <= h[i]) bin = first + i, rest = left, there = h[i];
-      left -= h[i];
-    }
-    bin = __shfl_sync(~0u, bin, who);
-    k = __shfl_sync(~0u, rest, who);
-    there = __shfl_sync(~0u, there, who);
-    // the bin's values
-    least = INFINITY, most = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-      if (w >= busy) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (free >> (4 * w + i) & 1 && v[w][i] >= low && v[w][i] <= high &&
-            bin_of(v[w][i]) == bin) {
-          least = fminf(least, v[w][i]), most = fmaxf(most, v[w][i]);
-          if (there <= kShortList) list[atomicAdd(&listed, 1)] = v[w][i];
-        }
-    }
-    spread(turn ^ 1);
-    if (there == k || least == most) {  // all of them, or the first of them
-      cut = least;
-      equals = k;
-      if (there == k) equals = kAllTies;
-      break;
-    }
-    if (there <= kShortList) {
-      const float y = lane < there ? list[lane] : 0.f;
-      int above = 0, same = 0;
-      for (int i = 0; i < there; ++i) {
-        const float z = list[i];
-        above += z > y;
-        same += z == y;
-      }
-      const uint32_t it = __ballot_sync(~0u, lane < there && above < k && k <= above + same);
-      const int who = __ffs(it) - 1;
-      cut = __shfl_sync(~0u, y, who);
-      equals = k - __shfl_sync(~0u, above, who);
-      if (equals == __shfl_sync(~0u, same, who)) equals = kAllTies;
-      break;
-    }
-    linear = false;
-    for (int i = tid; i < 256; i += NT) bins[i] = 0;  // (the next round has the other one)
-  }
-  // ---- the places of what is taken
-  uint32_t taken = 0, ties = 0;
-#pragma unroll
-  for (int w = 0; w < kWords; ++w) {
-    if (w >= busy) break;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      taken |= (uint32_t)(v[w][i] > cut) << (4 * w + i);
-      ties |= (uint32_t)(v[w][i] == cut) << (4 * w + i);
-    }
-  }
-  taken = (taken & free) | always;
-  ties &= free;
-  auto before_in_word = [&](uint32_t bits, int w, int& all) {
-    const int mine = __popc(bits >> (4 * w) & 15);
-    int upto = mine;
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(~0u, upto, d);
-      if (lane >= d) upto += y;
-    }
-    all = __shfl_sync(~0u, upto, 31);
-    return upto - mine;
-  };
-  if (equals == kAllTies) {
-    taken |= ties;
-  } else if (equals > 0) {  // (in all threads or none)
-    const int mine = __reduce_add_sync(~0u, __popc(ties));
-    if (lane == 0) ties_of[warp] = mine;
-    __syncthreads();
-    int at = 0;
-    for (int w = 0; w < warp; ++w) at += ties_of[w];
-    for (int w = 0; w < busy; ++w) {
-      int all, before = at + before_in_word(ties, w, all);
-      at += all;
-      for (int i = 4 * w; i < 4 * w + 4; ++i)
-        if (ties >> i & 1) taken |= (uint32_t)(before++ < equals) << i;
-    }
-  }
-  const int mine = __reduce_add_sync(~0u, __popc(taken));
-  if (lane == 0) taken_of[warp] = mine;
-  __syncthreads();
-  int at = 0;
-  for (int w = 0; w < warp; ++w) at += taken_of[w];
-#pragma unroll
-  for (int w = 0; w < kWords; ++w) {
-    if (w >= busy) break;
-    int all, before = at + before_in_word(taken, w, all);
-    at += all;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (taken >> (4 * w + i) & 1) out[before++] = c0 + 128 * w + i;
-  }
+  pick_short<NT>(v, row, n, p.first, p.recent, p.count - p.first - p.recent, sh,
+                 [&](int c, int at) { out[at] = c; });
 }
 
 // ITEMS: columns of a thread, or 0 for rows of any length. CLUSTER: p.ranks blocks for a row.

@@ -607,10 +607,10 @@ int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* dev
                               stream, p)
              : launch_cluster(sv::k_evict_pick<1024, 16, true>, p.ranks, dim3(wide), 1024, 0,
                               stream, p);
-  } else if (most <= 1024) {
-    rc = launch(sv::k_evict_pick<128, 8, false>, dim3(grid), 128, 0, stream, p);
+  } else if (most <= 2048) {
+    rc = launch(sv::k_evict_pick_short<128>, dim3(grid), 128, 0, stream, p);
   } else if (most <= 4096) {
-    rc = launch(sv::k_evict_pick<512, 8, false>, dim3(grid), 512, 0, stream, p);
+    rc = launch(sv::k_evict_pick_short<256>, dim3(grid), 256, 0, stream, p);
   } else if (most <= 16384) {
     rc = launch(sv::k_evict_pick<1024, 16, false>, dim3(grid), 1024, 0, stream, p);
   } else {
