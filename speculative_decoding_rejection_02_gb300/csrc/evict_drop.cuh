@@ -1,8 +1,8 @@
 // Eviction: which tokens stay, and the closing of the gaps (spec_cache_evict).
 //
-// k_evict_pick, one block for a request and kv head, or a cluster: the kept tokens are those of the
-// largest weights (pick_short, pick_items, pick_any), the ones that always stay among them; for each
-// that moves it is written down where it comes from. The same blocks do the requests' bookkeeping:
+// k_evict_pick, one block for a request and kv head, or a cluster: the kept tokens are those of
+// the largest weights (pick_short, pick_items, pick_any), the ones that always stay among them; for
+// each that moves it is written down where it comes from. The same blocks do the bookkeeping:
 // every block adds up all requests' pages that go, so each finds for itself whether the call can
 // be done at all and where its request's pages come on the stack.
 //
@@ -68,8 +68,8 @@ struct EvictBooks {
 
 // A request's bookkeeping. True: tokens go, of which `kept` of `len` stay. By the whole block.
 template <int NT>
-__device__ __forceinline__ bool evict_books(const EvictParams& p, int row, int b, int head, int rank,
-                                            EvictBooks<NT>& sh, int& len, int& kept) {
+__device__ __forceinline__ bool evict_books(const EvictParams& p, int row, int b, int head,
+                                            int rank, EvictBooks<NT>& sh, int& len, int& kept) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long most = (long long)p.rq.width << p.rq.page_shift;
   // ---- all requests' pages that go, and those of the requests before this one
@@ -123,7 +123,8 @@ __device__ __forceinline__ void evict_note(const EvictParams& p, int b, int head
 }
 
 // Requests of up to 16 NT tokens, whose weights the registers hold (pick_short). 108 requests of
-// 138-173 tokens with 8 heads: both kernels 33 us with pick_items, 17.5 so; 64 of 1990-2500 98 and 90.
+// 138-173 tokens with 8 heads: both kernels 33 us with pick_items, 17.5 so; 64 of 1990-2500 98 and
+// 90.
 template <int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_evict_pick_short(const EvictParams p) {
   __shared__ ShortPick<NT> sh;

@@ -417,8 +417,10 @@ int spec_cache_select(const spec_cache_select_args* a, void* stream, unsigned* d
   const unsigned grid = blocks((long long)a->num_tokens * a->kv_heads);
   if (!grid) return SPEC_ERR_UNSUPPORTED;
   // Rows of up to 4096 columns in as few threads as 16 columns each take (12000 rows of some 500
-  // columns 44 us, with 128 threads for each 59), up to 16384 in 1024 threads, and longer ones
-  // where the row is read again for each histogram.
+  // columns 44 us, with 128 threads for each 59), longer ones with pick_items, up to 16384 columns
+  // in registers (4000 rows of 5000-6250 columns 96 us, 109 with pick_short, which has twice as
+  // many counts for each thread between its barriers), and beyond that looked at again for each
+  // histogram.
   p.held = 0;
   if (a->width <= 512)
     return launch(sv::k_cache_select_short<32>, dim3(grid), 32, 0, stream, p);
@@ -596,8 +598,10 @@ int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* dev
   while (p.cluster < 8 && rows * p.cluster < sms) p.cluster *= 2;
   const unsigned grid = blocks(rows > 0 ? rows : 1), moves = blocks(rows * p.cluster);
   if (!grid || (rows > 0 && !moves)) return SPEC_ERR_UNSUPPORTED;
-  // Weights in registers up to 16384 tokens, where few rows are split over clusters; longer
-  // requests' in shared memory, as far as they fit, and looked at again for each histogram.
+  // Weights in registers up to 16384 tokens, with pick_short up to 4096 as in spec_cache_select
+  // (16 requests of 12000-16000 with 8 heads 82 us, 96 with pick_short); longer requests' in
+  // clusters' registers where there are few, else in shared memory as far as they fit, and looked
+  // at again for each histogram.
   const long long most = (long long)a->width * a->page_size;
   p.ranks = rows > 0 ? pick_ranks(rows, most, sms) : 1;
   if (p.ranks > 1) {
