@@ -15,9 +15,11 @@
 // of 2048 over 11000-14000 where two groups took 391: two warps for each scheduler do not cover the
 // latency of what they do.)
 //
-// The pairs of all requests and kv heads stand in one list, in which a pair counts by its column
-// tiles (three at least: what its loads take), cut into equal parts, one for each block (one block
-// per SM). Every role of a block walks over the part by itself.
+// The pairs of all requests and kv heads stand in one list, in which a pair counts by the column
+// tiles that see it and three more for its start, cut into equal parts, one for each block (one
+// block per SM). Every role of a block walks over the part by itself. (Four prompts of 1000-1500
+// tokens 56 us; with all of the request's column tiles counted for every pair 72, and 82 with the
+// tiles of the diagonal looked at column by column.)
 //
 // Warps: 0-7 and 8-15 the sums of the pair's two tiles, 16 loads K (TMA, through the block table),
 // 17 loads Q and the lse, and where those come once for many pairs half of K (with small pages it
@@ -28,7 +30,9 @@
 // each has its own stages of K.
 //
 // Bound by HBM (the keys, once) for few columns, by the exponentials and the products, which take
-// about as long, for many.
+// about as long, for many: 64 requests of 2-8 tokens over 1000-30000 180 to 185 us (0.94 to 0.96 of
+// a copy's rate), two chunks of 2048 over 11000-14000 355 us (336 in runs of some milliseconds; 0.65
+// of a large library product's rate).
 #pragma once
 #include <cuda.h>
 
@@ -42,7 +46,7 @@ constexpr int kWeighTile = 128;
 constexpr int kWeighRing = 12;      // stages at most
 constexpr int kWeighSmem = 204 * 1024, kWeighStages = 192 * 1024;
 constexpr int kWeighShifts = 8;     // column tiles whose lse are ahead
-constexpr int kWeighLeast = 3;      // what a pair counts at least, in column tiles
+constexpr int kWeighStart = 3;      // what a pair counts beside its column tiles
 constexpr long long kWeighPatience = 2000000000;  // clocks that a wait may take
 
 struct WeighParams {
@@ -55,6 +59,7 @@ struct WeighParams {
   float c, decay;
   int bf16;
   int tile_tokens;          // new tokens of a column tile
+  int late_tiles;           // of those, how many fewer see a pair of keys than the one before
   int blocks;               // of 64 channels
   int k_stages, q_stages;   // of blocks * 16 KB; of K for each of a pair's two tiles
   int shared_loads;         // the warp that loads Q loads half of K
@@ -103,70 +108,100 @@ __device__ __forceinline__ void weigh_land(uint64_t* bar, uint32_t parity) {
 
 // Pairs of key tiles of a request and kv head, and what each counts.
 struct WeighUnit {
-  int lo, hi, len, old, pairs, tiles, cost;
+  int lo, tokens, len, pairs, tiles;  // (of column tiles)
   __device__ __forceinline__ WeighUnit() {}
   __device__ __forceinline__ WeighUnit(const WeighParams& p, int b) {
     lo = p.rq.cu_q[b];
-    hi = p.rq.cu_q[b + 1];
     len = p.rq.kv_lens[b];
+    const int hi = p.rq.cu_q[b + 1];
     const bool bad = lo < 0 || hi < lo || hi > p.rq.T || len < 0 ||
                      len > ((long long)p.rq.width << p.rq.page_shift) || len > 0x7fff0000;
+    tokens = hi - lo;
     if (bad) {
       atomicOr(p.rq.status, SPEC_CACHE_BAD_LENGTHS);
-      lo = hi = len = 0;
+      lo = tokens = len = 0;
     }
-    old = len - (hi - lo);
-    tiles = (hi - lo + p.tile_tokens - 1) / p.tile_tokens;  // of columns
+    tiles = (tokens + p.tile_tokens - 1) / p.tile_tokens;
     pairs = tiles ? (len + 2 * kWeighTile - 1) / (2 * kWeighTile) : 0;
-    cost = max(tiles, kWeighLeast);
+  }
+  __device__ __forceinline__ int old() const { return len - tokens; }
+  // Pairs before this one that column tiles do not see in full.
+  __device__ __forceinline__ int late(int pair) const {
+    return max(pair - max(old(), 0) / (2 * kWeighTile) - 1, 0);
+  }
+  // What the pairs before this one count: each its start, and the column tiles that see it.
+  __device__ __forceinline__ long long place(const WeighParams& p, int pair) const {
+    const long long m = late(pair);
+    return (long long)(kWeighStart + tiles) * pair - p.late_tiles * (m * (m - 1) / 2);
+  }
+  // The first pair at that place or after it (or the number of pairs).
+  __device__ __forceinline__ int find(const WeighParams& p, long long at) const {
+    const long long all = quotient(at + kWeighStart + tiles - 1, kWeighStart + tiles);
+    int a = (int)min(all, (long long)pairs), b = late(a) ? pairs : a;
+    while (a < b) {
+      const int c = (a + b) / 2;
+      if (place(p, c) < at)
+        a = c + 1;
+      else
+        b = c;
+    }
+    return a;
   }
 };
 
 // A block's walk over its part of the list: pairs whose place is in [begin, end).
 struct WeighWalk {
   WeighUnit u;
-  int b, head, pair;
-  bool fresh;           // the unit's first pair here
-  long long at, end;    // place of the pair, and the end of the part
+  int b, head, pair, stop;  // stop: where the unit's pairs or the part's end
+  bool fresh;               // the unit's first pair here
+  long long left;           // of the part from the next unit on
   __device__ __forceinline__ bool start(const WeighParams& p, const WeighShared& sh) {
     b = sh.first;
-    at = sh.at;
-    end = sh.end;
     if (b < 0) return false;
+    long long at = sh.at;
     u = WeighUnit(p, b);
-    const long long skip = quotient(sh.begin - at + u.cost - 1, u.cost);
-    at += skip * u.cost;
-    head = u.pairs ? (int)quotient(skip, u.pairs) : p.kv_heads;
-    pair = u.pairs ? (int)(skip - (long long)head * u.pairs) : 0;
-    fresh = true;
+    head = p.kv_heads;
+    pair = 0;
+    if (u.pairs) {
+      const long long all = u.place(p, u.pairs);
+      head = (int)quotient(sh.begin - at, all);
+      at += head * all;
+      pair = u.find(p, sh.begin - at);
+      if (pair == u.pairs) {
+        at += all;
+        pair = 0;
+        ++head;
+      }
+    }
+    left = sh.end - at;
     return settle(p);
   }
+  // To the next unit, and its pair.
   __device__ __forceinline__ bool settle(const WeighParams& p) {
     while (head >= p.kv_heads) {
-      if (at >= end || ++b >= p.rq.B) return false;
+      if (left <= 0 || ++b >= p.rq.B) return false;
       u = WeighUnit(p, b);
       head = u.pairs ? 0 : p.kv_heads;
-      pair = 0;
     }
-    return at < end;
+    const long long all = u.place(p, u.pairs);
+    stop = left >= all ? u.pairs : left > 0 ? u.find(p, left) : 0;
+    left -= all;
+    fresh = true;
+    return pair < stop;
   }
   __device__ __forceinline__ bool next(const WeighParams& p) {
-    at += u.cost;
     fresh = false;
-    if (++pair == u.pairs) {
-      pair = 0;
-      ++head;
-      fresh = true;
-    }
+    if (++pair < stop) return true;
+    if (stop < u.pairs) return false;
+    pair = 0;
+    ++head;
     return settle(p);
   }
   // Whether the pair after this one, if it is in the part, is another unit's or there is none.
-  __device__ __forceinline__ bool ends_unit() const {
-    return pair + 1 == u.pairs || at + u.cost >= end;
-  }
+  __device__ __forceinline__ bool ends_unit() const { return pair + 1 == stop; }
   // The first column tile that sees a key of the pair.
   __device__ __forceinline__ int first_tile(const WeighParams& p) const {
-    return max(pair * 2 * kWeighTile - u.old, 0) / p.tile_tokens;
+    return max(pair * 2 * kWeighTile - u.old(), 0) / p.tile_tokens;
   }
   __device__ __forceinline__ bool has(int g) const {
     return (pair * 2 + g) * kWeighTile < u.len;
@@ -288,7 +323,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     const int r0 = (int)min((long long)tid * run, (long long)p.rq.B), r1 = min(r0 + run, p.rq.B);
     auto places = [&](int r) {
       const WeighUnit u(p, r);
-      return (long long)u.pairs * u.cost * p.kv_heads;
+      return u.place(p, u.pairs) * p.kv_heads;
     };
     long long mine = 0;
     for (int r = r0; r < r1; ++r) mine += places(r);
@@ -352,7 +387,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         if (p.shared_loads && !keys.load(sh, p, smem, stage_bytes, now, walk, more)) break;
         if (now.u.tiles == 1 && !now.fresh) continue;
         const float* lse = p.lse + (long long)now.u.lo * p.heads + now.head * p.G;
-        const int tokens = now.u.hi - now.u.lo, t0 = now.first_tile(p);
+        const int tokens = now.u.tokens, t0 = now.first_tile(p);
         float z[2][4];
         auto look = [&](int t, float* z) {
           const int first = t * p.tile_tokens, n = min(p.tile_tokens, tokens - first);
@@ -414,7 +449,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
           if (!ok) break;
           if (mine) {
             const int columns =
-                __shfl_sync(~0u, min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens), 0) *
+                __shfl_sync(~0u, min(p.tile_tokens, walk.u.tokens - t * p.tile_tokens), 0) *
                 p.G;
             const uint32_t kind =
                 mma_kind(p.bf16, false, kWeighTile, (columns + 15) / 16 * 16);
@@ -450,17 +485,19 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
       unsigned l_count = 0, k_count = 0, s_count = 0, joins = 0;
       bool ok = true;
       do {
-        const int t0 = walk.first_tile(p), n = walk.u.tiles - t0;
+        const int t0 = walk.first_tile(p);
+        const bool several = walk.u.tiles - t0 > 1;
         const bool mine = walk.has(g), single = walk.u.tiles == 1, last = walk.ends_unit();
         const int key = (walk.pair * 2 + g) * kWeighTile + row;
         float* w = nullptr;
         float before = 0.f;
-        // From column tile all_from on all columns see all keys, and up to `whole` there are `full`
-        // columns: code that looks at each column's place takes 387 us for two chunks of 2048, not
-        // 350.
-        const int over = max((walk.pair * 2 + g + 1) * kWeighTile - 1 - walk.u.old, 0);
+        // From column tile all_from on all columns see all keys, and up to `whole` there are 128
+        // columns: with code that looked at each column's place two chunks of 2048 took 387 us, 350
+        // without.
+        const int over = max((walk.pair * 2 + g + 1) * kWeighTile - 1 - walk.u.old(), 0);
         const int all_from = (over + p.tile_tokens - 1) / p.tile_tokens;
-        const int whole = (walk.u.hi - walk.u.lo) / p.tile_tokens, full = p.tile_tokens * p.G;
+        const int whole =
+            p.tile_tokens * p.G == kWeighTile ? walk.u.tokens / p.tile_tokens : 0;
         unsigned long long sum2[4] = {0, 0, 0, 0};
         float rest = 0.f;
         for (int t = t0; ok && t < walk.u.tiles; ++t) {
@@ -482,7 +519,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
               if (number >= 0 && key < walk.u.len)
                 w = p.weights + number * p.w_page + walk.head * p.w_head +
                     (key & ((1 << p.rq.page_shift) - 1));
-              if (w && key < walk.u.old && p.decay != 0.f) before = *w;
+              if (w && key < walk.u.old() && p.decay != 0.f) before = *w;
               __syncwarp();
             }
             const float* shift = sh.shift[la];
@@ -503,40 +540,35 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 sum2[2 * (y & 1) + 1] = f2_add(sum2[2 * (y & 1) + 1], f2_pack(ex2(c), ex2(d)));
               }
             };
-            // the same, of which only the first n are columns (others may hold anything)
-            auto add_some = [&](int k, int n) {
-              float x[32];
+            // the same, of which the key sees those whose bits are set (others may hold anything)
+            auto add_some = [&](int k, uint32_t seen) {
+              float x[32], sum[4] = {};
               tmem_ld32(tmem + k, x);
               tmem_wait_ld(x);
 #pragma unroll
               for (int y = 0; y < 32; ++y) {
                 const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
-                if (y < n) rest += e;
+                sum[y & 3] += seen >> y & 1 ? e : 0.f;
               }
+              rest += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             };
-            const int columns =
-                min(p.tile_tokens, walk.u.hi - walk.u.lo - t * p.tile_tokens) * p.G;
-            if (t >= all_from && t < whole && full == kWeighTile) {
-#pragma unroll
-              for (int k = 0; k < kWeighTile; k += 32) add(k);
-            } else if (t >= all_from) {
-              int k = 0;
+            if (t >= all_from && t < whole) {
 #pragma unroll 1
-              for (; k + 32 <= columns; k += 32) add(k);
-              if (k < columns) add_some(k, columns - k);
+              for (int k = 0; k < kWeighTile; k += 32) add(k);
             } else {
-              // columns [from, columns) of the tile see the key
-              const long long ahead = (long long)key - walk.u.old - t * p.tile_tokens;
-              const int from = ahead > 0 ? (int)min(ahead * p.G, (long long)kWeighTile) : 0;
+              // the key sees the columns [from, columns) of the tile
+              const int columns =
+                  min(p.tile_tokens, walk.u.tokens - t * p.tile_tokens) * p.G;
+              const int ahead = key - walk.u.old() - t * p.tile_tokens;
+              const int from = min(max(ahead, 0), kWeighTile) * p.G;
 #pragma unroll 1
               for (int k = 0; k < columns; k += 32) {
-                float x[32];
-                tmem_ld32(tmem + k, x);
-                tmem_wait_ld(x);
-#pragma unroll
-                for (int y = 0; y < 32; ++y) {
-                  const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
-                  if (k + y >= from && k + y < columns) rest += e;
+                if (__all_sync(~0u, from >= k + 32)) continue;
+                if (__all_sync(~0u, from <= k) && k + 32 <= columns) {
+                  add(k);
+                } else {
+                  const uint32_t past = columns - k >= 32 ? 0u : ~0u << (columns - k);
+                  add_some(k, from - k >= 32 ? 0u : ~0u << max(from - k, 0) & ~past);
                 }
               }
             }
@@ -556,7 +588,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         float a, b;
         f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), a, b);
         a = rest + (a + b);
-        if (mine && n > 1) {
+        if (mine && several) {
           // The other group's part: all eight warps meet, and meet again before `part` is
           // written anew.
           const bool writes = (s_count - 1 & 1) == turn;

@@ -536,6 +536,7 @@ int spec_cache_weigh(const spec_cache_weigh_args* a, void* stream, unsigned* dev
   p.decay = a->decay;
   p.bf16 = a->dtype == SPEC_CACHE_BF16;
   p.tile_tokens = sv::kWeighTile / p.G < a->max_q ? sv::kWeighTile / p.G : a->max_q;
+  p.late_tiles = 2 * sv::kWeighTile / p.tile_tokens;
   p.blocks = a->dim > 64 ? 2 : 1;
   // Q of one column tile stays for a unit, and most stages hold keys; of several, they come again
   // for every pair of key tiles. (A wait for keys is rare then: a pair goes over all columns.)
