@@ -30,9 +30,9 @@
 // each has its own stages of K.
 //
 // Bound by HBM (the keys, once) for few columns, by the exponentials and the products, which take
-// about as long, for many: 64 requests of 2-8 tokens over 1000-30000 180 to 185 us (0.94 to 0.96 of
-// a copy's rate), two chunks of 2048 over 11000-14000 355 us (336 in runs of some milliseconds; 0.65
-// of a large library product's rate).
+// about as long, for many: 64 requests of 2-8 tokens over 1000-30000 180 to 185 us (0.94 to 0.96
+// of a copy's rate), two chunks of 2048 over 11000-14000 355 us (336 in runs of some milliseconds;
+// 0.65 of a large library product's rate).
 #pragma once
 #include <cuda.h>
 
