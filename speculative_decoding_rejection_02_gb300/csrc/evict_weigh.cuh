@@ -18,8 +18,8 @@
 // The pairs of all requests and kv heads stand in one list, in which a pair counts by the column
 // tiles that see it and three more for its start, cut into equal parts, one for each block (one
 // block per SM). Every role of a block walks over the part by itself. (Four prompts of 1000-1500
-// tokens 56 us; with all of the request's column tiles counted for every pair 72, and 82 with the
-// tiles of the diagonal looked at column by column.)
+// tokens 55 us; 82 with all of the request's column tiles counted for every pair and the tiles of
+// the diagonal looked at column by column.)
 //
 // Warps: 0-7 and 8-15 the sums of the pair's two tiles, 16 loads K (TMA, through the block table),
 // 17 loads Q and the lse, and where those come once for many pairs half of K (with small pages it
@@ -30,9 +30,9 @@
 // each has its own stages of K.
 //
 // Bound by HBM (the keys, once) for few columns, by the exponentials and the products, which take
-// about as long, for many: 64 requests of 2-8 tokens over 1000-30000 180 to 185 us (0.94 to 0.96
-// of a copy's rate), two chunks of 2048 over 11000-14000 355 us (336 in runs of some milliseconds;
-// 0.65 of a large library product's rate).
+// about as long, for many: 64 requests of 2-8 tokens over 1000-30000 186 us (0.93 of a copy's
+// rate), two chunks of 2048 over 11000-14000 351 us (326 in runs of some milliseconds; 0.66 of a
+// large library product's rate).
 #pragma once
 #include <cuda.h>
 
@@ -540,35 +540,44 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 sum2[2 * (y & 1) + 1] = f2_add(sum2[2 * (y & 1) + 1], f2_pack(ex2(c), ex2(d)));
               }
             };
-            // the same, of which the key sees those whose bits are set (others may hold anything)
-            auto add_some = [&](int k, uint32_t seen) {
-              float x[32], sum[4] = {};
+            // the same, of which only the first n are columns (others may hold anything)
+            auto add_some = [&](int k, int n) {
+              float x[32];
               tmem_ld32(tmem + k, x);
               tmem_wait_ld(x);
 #pragma unroll
               for (int y = 0; y < 32; ++y) {
                 const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
-                sum[y & 3] += seen >> y & 1 ? e : 0.f;
+                if (y < n) rest += e;
               }
-              rest += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             };
+            const int columns = min(p.tile_tokens, walk.u.tokens - t * p.tile_tokens) * p.G;
             if (t >= all_from && t < whole) {
-#pragma unroll 1
+#pragma unroll
               for (int k = 0; k < kWeighTile; k += 32) add(k);
+            } else if (t >= all_from) {
+              int k = 0;
+#pragma unroll 1
+              for (; k + 32 <= columns; k += 32) add(k);
+              if (k < columns) add_some(k, columns - k);
             } else {
-              // the key sees the columns [from, columns) of the tile
-              const int columns =
-                  min(p.tile_tokens, walk.u.tokens - t * p.tile_tokens) * p.G;
-              const int ahead = key - walk.u.old() - t * p.tile_tokens;
-              const int from = min(max(ahead, 0), kWeighTile) * p.G;
+              // columns [from, columns) of the tile see the key
+              const long long ahead = (long long)key - walk.u.old() - t * p.tile_tokens;
+              const int from = ahead > 0 ? (int)min(ahead * p.G, (long long)kWeighTile) : 0;
 #pragma unroll 1
               for (int k = 0; k < columns; k += 32) {
                 if (__all_sync(~0u, from >= k + 32)) continue;
                 if (__all_sync(~0u, from <= k) && k + 32 <= columns) {
                   add(k);
-                } else {
-                  const uint32_t past = columns - k >= 32 ? 0u : ~0u << (columns - k);
-                  add_some(k, from - k >= 32 ? 0u : ~0u << max(from - k, 0) & ~past);
+                  continue;
+                }
+                float x[32];
+                tmem_ld32(tmem + k, x);
+                tmem_wait_ld(x);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) {
+                  const float e = ex2(fmaf(x[y], p.c, shift[k + y]));
+                  if (k + y >= from && k + y < columns) rest += e;
                 }
               }
             }
