@@ -155,9 +155,9 @@ typedef struct {
 /*
  * spec_cache_attend_selected — spec_cache_attend where token t and the query heads of kv head h
  * see the tokens up to t's own in the columns selected[t][h] alone. A row that sees nothing gives
- * out = 0 and lse = -inf. Scores, softmax statistics and sums are fp32; the softmax weights are
- * rounded to the cache's type before they meet the values. Slots that no row sees do not reach
- * the outputs, whatever they hold; pages in no list are not read.
+ * out = 0 and lse = -inf. Scores, softmax statistics and sums are fp32; the softmax weights meet
+ * the values with 16 bits (bf16) or 22 bits (fp16). Slots that no row sees do not reach the
+ * outputs, whatever they hold; pages in no list are not read.
  */
 int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* stream,
                                unsigned* device_status);
