@@ -231,7 +231,9 @@ long long spec_cache_evict_workspace(const spec_cache_evict_args* a);
  * anew, and no window fits any more.
  * If a length or budget cannot be, or the stack would not hold the pages, SPEC_CACHE_BAD_LENGTHS
  * is set and nothing is changed (lens_out = lens, free_count_out = free_count). A page number
- * outside the pool sets SPEC_CACHE_BAD_PAGE; the request's tokens are not meaningful then.
+ * outside the pool sets SPEC_CACHE_BAD_PAGE; the request's tokens are not meaningful then. One that
+ * would be given back stays off the stack and does not count in free_count_out (entries of
+ * free_pages from there on are not meaningful then).
  * Requests must not share pages.
  */
 int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* device_status);

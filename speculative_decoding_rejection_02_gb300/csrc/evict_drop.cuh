@@ -4,7 +4,9 @@
 // the largest weights (pick_short, pick_items, pick_any), the ones that always stay among them; for
 // each that moves it is written down where it comes from. The same blocks do the bookkeeping:
 // every block adds up all requests' pages that go, so each finds for itself whether the call can
-// be done at all and where its request's pages come on the stack.
+// be done at all and where its request's pages come on the stack. Numbers there that are no pages
+// are found by the block that puts them on; where there are some the stack is written again
+// without them, by one more block of k_evict_move, before anything can take from it.
 //
 // k_evict_move: keys, values and weights to their new places. Tokens only move down and keep
 // their order, so a request and head go upwards in batches: all of a batch is read, in registers,
@@ -37,6 +39,7 @@ struct EvictParams {
   int vec;       // weights of 8 tokens on 16-byte boundaries
   int by_page;   // whether `from` goes by pages of the pool, or by columns of the table
   int* begin;    // [B][kv_heads] the first kept token that moves; none: 0x7fffffff
+  int* broken;   // [B] whether a column that is given back holds no page
   int* from;     // where kept tokens come from, in pages [kv_heads][page_size]
   int ranks;     // blocks of a request and kv head that pick its tokens
   int cluster;   // ... that move its tokens
@@ -101,11 +104,20 @@ __device__ __forceinline__ bool evict_books(const EvictParams& p, int row, int b
   len = p.rq.kv_lens[b];
   kept = bad ? len : p.kept(len, p.budget[b]);
   if (head == 0 && rank == 0) {
-    if (tid == 0) p.lens_out[b] = kept;
+    bool none = false;
     if (!bad) {
       const int c0 = p.pages(kept), n = p.pages(len) - c0;
-      for (int i = tid; i < n; i += NT)
-        p.free_pages[free_now + before + i] = p.rq.table[b * p.rq.table_stride + c0 + i];
+      for (int i = tid; i < n; i += NT) {
+        const int page = p.rq.table[b * p.rq.table_stride + c0 + i];
+        none |= page < 0 || page >= p.rq.num_pages;
+        p.free_pages[free_now + before + i] = page;
+      }
+    }
+    none = __syncthreads_or(none);
+    if (tid == 0) {
+      p.lens_out[b] = kept;
+      p.broken[b] = none;
+      if (none) atomicOr(p.rq.status, SPEC_CACHE_BAD_PAGE);
     }
   }
   if (kept < len) return true;
@@ -253,6 +265,28 @@ __global__ void __launch_bounds__(NT) k_evict_pick(const EvictParams p) {
   }
 }
 
+// The stack without the numbers that are no pages, if there are such. By a whole block; what a
+// broken table costs does not matter, so one warp goes through the requests in order.
+__device__ __forceinline__ void evict_restack(const EvictParams& p) {
+  bool any = false;
+  for (int b = threadIdx.x; b < p.rq.B; b += kMoveThreads) any |= p.broken[b] != 0;
+  if (!__syncthreads_or(any) || threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  int top = *p.free_count;
+  for (int b = 0; b < p.rq.B; ++b) {
+    const int end = p.pages(p.rq.kv_lens[b]);
+    for (int c = p.pages(p.lens_out[b]); c < end; c += 32) {
+      const int page = c + lane < end ? p.rq.table[b * p.rq.table_stride + c + lane] : -1;
+      const bool there = page >= 0 && page < p.rq.num_pages;
+      const uint32_t votes = __ballot_sync(~0u, there);
+      if (there) p.free_pages[top + __popc(votes & ((1u << lane) - 1))] = page;
+      top += __popc(votes);
+    }
+  }
+  if (lane == 0) *p.free_count_out = top;
+}
+
+// One row of blocks for each request and kv head, and one for the stack.
 __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const EvictParams p) {
   constexpr int kWarps = kMoveThreads / 32;
   pdl_trigger();
@@ -261,6 +295,10 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const EvictParams p
   const int rank = p.cluster > 1 ? blockIdx.x % p.cluster : 0;
   const long long row = blockIdx.x / p.cluster;
   const int b = (int)(row / p.kv_heads), head = (int)(row - (long long)b * p.kv_heads);
+  if (b == p.rq.B) {
+    if (rank == 0) evict_restack(p);
+    return;
+  }
   const int begin = p.begin[row], kept = p.lens_out[b];
   if (begin >= kept) return;  // (the whole cluster)
   const int len = p.rq.kv_lens[b], mask = (1 << p.rq.page_shift) - 1;

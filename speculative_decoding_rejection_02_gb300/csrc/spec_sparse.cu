@@ -288,11 +288,12 @@ int check_evict(const spec_cache_evict_args* a, bool pointers) {
   return SPEC_OK;
 }
 
-// Workspace of spec_cache_evict: where each request's and head's moves begin, then where the
-// moved tokens come from, for all pages of the pool or all columns of the table.
+// Workspace of spec_cache_evict: where each request's and head's moves begin, whether a request
+// gives back what is no page, then where the moved tokens come from, for all pages of the pool or
+// all columns of the table.
 struct EvictSpace {
   bool by_page;
-  size_t from, bytes;
+  size_t broken, from, bytes;
 };
 EvictSpace evict_space(const spec_cache_evict_args* a) {
   EvictSpace s;
@@ -300,7 +301,8 @@ EvictSpace evict_space(const spec_cache_evict_args* a) {
   // (by columns it takes no look at the table to find a place; a table much wider than what the
   // requests can hold is not worth that)
   s.by_page = columns > 4ll * a->num_pages;
-  s.from = ((size_t)a->B * a->kv_heads * 4 + 255) / 256 * 256;
+  s.broken = (size_t)a->B * a->kv_heads * 4;
+  s.from = (s.broken + (size_t)a->B * 4 + 255) / 256 * 256;
   s.bytes = s.from + (size_t)(s.by_page ? a->num_pages : columns) * a->kv_heads * a->page_size * 4;
   return s;
 }
@@ -590,6 +592,7 @@ int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* dev
   p.lens_out = a->lens_out;
   p.free_count_out = a->free_count_out;
   p.begin = (int*)a->workspace;
+  p.broken = (int*)((char*)a->workspace + ws.broken);
   p.from = (int*)((char*)a->workspace + ws.from);
   p.by_page = ws.by_page;
   p.vec = aligned(a->weights, 16) && a->w_page % 4 == 0 && a->w_head % 4 == 0;
@@ -597,8 +600,8 @@ int spec_cache_evict(const spec_cache_evict_args* a, void* stream, unsigned* dev
   // clusters where one block for each request and head leaves SMs idle
   p.cluster = 1;
   while (p.cluster < 8 && rows * p.cluster < sms) p.cluster *= 2;
-  const unsigned grid = blocks(rows > 0 ? rows : 1), moves = blocks(rows * p.cluster);
-  if (!grid || (rows > 0 && !moves)) return SPEC_ERR_UNSUPPORTED;
+  const unsigned grid = blocks(rows > 0 ? rows : 1), moves = blocks((rows + 1) * p.cluster);
+  if (!grid || !moves) return SPEC_ERR_UNSUPPORTED;
   // Weights in registers up to 16384 tokens, with pick_short up to 4096 as in spec_cache_select
   // (16 requests of 12000-16000 with 8 heads 82 us, 96 with pick_short); longer requests' in
   // clusters' registers where there are few, else in shared memory as far as they fit, and looked
