@@ -5,9 +5,10 @@
 //   P_d = sum_g max(q_gd, 0),  N_d = sum_g min(q_gd, 0),
 // so the heads of a group cost no more than one, and the scores are a product of the bounds
 // (pages x 2 dim, 16 bits) with [N, P] (2 dim x tokens, fp32). It runs on the warp's tensor
-// cores, 16 pages x 8 tokens at a time: P and N are scaled by a power of two, which is taken out
-// again at the end, and split into three 16-bit parts that together hold 24 bits or more (33 of
-// the largest in fp16), so the products are exact and the sums are fp32.
+// cores, 16 pages x 8 tokens at a time: P and N are scaled by powers of two for the types' ranges
+// (score_shift), which are taken out again at the end, and split into three 16-bit parts that
+// together hold 24 bits or more (33 of the largest in fp16), so the products are exact and the sums
+// are fp32.
 //
 // Bound by HBM: 4 dim bytes of bounds for each page and head, read once for up to 32 tokens, into
 // registers (a warp has 16 pages, 8 KB at dim 128, in flight). A lane loads 16 bytes, 8 channels,
@@ -58,6 +59,23 @@ __device__ __forceinline__ void split3(float x, float* part) {
     part[i] = y.x;
     x = isinf(y.x) ? 0.f : x - y.x;
   }
+}
+
+// P and N are sums over up to 128 heads; of values 2^-8 of q's they stay under 2^127 for any q that
+// is finite, and lose no bit (2^-149 holds the last one of 16-bit types' least values so).
+constexpr int kScoreDown = 8;
+constexpr float kScoreDownBy = 1.f / (1 << kScoreDown);
+
+// The power of two that a token's P and N are multiplied by then, the largest of which is in
+// [2^top, 2^(top + 1)), so that their parts are what the type holds. fp16 wants the largest in [2^14,
+// 2^15): with bounds under 2^16 no sum of theirs is past 2^40. bf16 has fp32's range, and bounds of
+// any size, so sums must not grow by it: nothing, but for top values under 2^-10, which go up to
+// there (a sum of 2 dim products with bounds under 2^128 stays under 2^128 then), so that the
+// parts of others a 2^-90th of them are still held.
+template <bool BF16>
+__device__ __forceinline__ int score_shift(int top) {
+  if (!BF16) return min(max(14 - top, -100), 100);
+  return top < -10 ? min(-10 - top, 100) : 0;
 }
 
 // What a request is in the list that the blocks divide: for each kv head and group of tokens
@@ -200,21 +218,20 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
             for (int y = 0; y < 4; ++y) {
               const float2 f = unpack_pair<BF16>(w[y]);
               // (not fmaxf, which would take 0 in place of NaN)
-              up[2 * y] += f.x < 0.f ? 0.f : f.x;
-              up[2 * y + 1] += f.y < 0.f ? 0.f : f.y;
-              down[2 * y] += f.x > 0.f ? 0.f : f.x;
-              down[2 * y + 1] += f.y > 0.f ? 0.f : f.y;
+              up[2 * y] = fmaf(f.x < 0.f ? 0.f : f.x, kScoreDownBy, up[2 * y]);
+              up[2 * y + 1] = fmaf(f.y < 0.f ? 0.f : f.y, kScoreDownBy, up[2 * y + 1]);
+              down[2 * y] = fmaf(f.x > 0.f ? 0.f : f.x, kScoreDownBy, down[2 * y]);
+              down[2 * y + 1] = fmaf(f.y > 0.f ? 0.f : f.y, kScoreDownBy, down[2 * y + 1]);
             }
           }
 #pragma unroll
           for (int y = 0; y < 8; ++y) top = fmaxf(top, fmaxf(up[y], -down[y]));
         }
         for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        // 2^14 <= top * scale < 2^15; the least values need no more than 2^100
-        int e = top > 0.f && top < INFINITY ? 14 - ilogbf(top) : 0;
-        e = min(max(e, -100), 100);
+        const int e = top > 0.f && top < INFINITY ? score_shift<BF16>(ilogbf(top)) : 0;
         const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
-        if (piece == 0) unscale[tok] = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (piece == 0)
+          unscale[tok] = __uint_as_float((uint32_t)(127 - e + kScoreDown) << 23);
         if (piece * 8 < DP) {
           char* dst = smem + (tok >> 3) * Cfg::kGroupBytes + (piece >> 2) * 3 * 512 +
                       ((tok & 7) * 4 + (piece & 3)) * 16;

@@ -40,3 +40,38 @@ def test_attend_selected_rounds_its_outputs_alone(shape, dtype):
     over = ((out - want).abs() - tol).max()
     assert over <= 0, float(over)
     assert not math.isnan(float(out.sum()))
+
+
+@pytest.mark.parametrize("q_size,b_size", [(1e-3, 1e35), (1e-30, 3e38), (1e-38, 3e38), (1.0, 1e35),
+                                           (1e28, 1e7), (1e30, 1e-30), (3e38, 1e-5), (1e-20, 1e-10)])
+@pytest.mark.parametrize("signs", ["mixed", "below", "above"])
+def test_score_of_bounds_of_any_size(q_size, b_size, signs):
+    """Scores that fp32 holds, of queries and finite bounds up to the type's largest (ref.score's
+    error bounds, which count roundings relative to the sums of absolute values)."""
+    g = torch.Generator().manual_seed(32)
+    q = (torch.randn((3, 8, 64), generator=g).clamp(-1, 1) * q_size).to(BF)
+    b = torch.randn((4, 2, 2, 64), generator=g).clamp(-1, 1)
+    if signs != "mixed":  # P . hi and N . lo of opposite signs or one
+        b = b.abs() * (1 if signs == "above" else -1)
+    b = (b.sort(2).values * b_size).to(BF)
+    assert torch.isfinite(b).all() and torch.isfinite(q).all()
+    want, tol = ref.score(q, [b], [3], [60], 16, 4)
+    got = sv.cache_score(q.to(DEV), b.to(DEV), ints([[0, 1, 2, 3]]), ints([60]), ints([0, 3]),
+                         page_size=16).double().cpu()
+    assert torch.isfinite(want).all() and want.abs().max() < 3e38
+    over = ((got - want).abs() - tol).max()
+    assert over <= 0, float(over)
+
+
+def test_score_of_channels_of_different_sizes():
+    """A channel of large queries and small bounds beside others the other way round."""
+    g = torch.Generator().manual_seed(33)
+    q, b = torch.randn((2, 4, 64), generator=g), torch.randn((3, 1, 2, 64), generator=g)
+    q[..., 1:] *= 1e-25
+    b[..., 0] *= 1e-30
+    b[..., 1:] *= 1e20
+    q, b = q.to(BF), b.sort(2).values.to(BF)
+    want, tol = ref.score(q, [b], [2], [48], 16, 3)
+    got = sv.cache_score(q.to(DEV), b.to(DEV), ints([[0, 1, 2]]), ints([48]), ints([0, 2]),
+                         page_size=16).double().cpu()
+    assert ((got - want).abs() <= tol).all()
