@@ -47,6 +47,10 @@ extern "C" {
                                             one that is not above the one before it; the row's
                                             outputs are not meaningful */
 
+/* flags of spec_cache_weigh, test only: waits run out after some 0.1 ms, and one that the call needs
+ * is never signalled, so that it ends with SPEC_STATUS_TIMEOUT */
+#define SPEC_CACHE_TEST_WAIT_TIMEOUT 0x1u
+
 typedef struct {
   int B;                     /* requests, >= 0 */
   int width;                 /* columns of block_table, >= 1 */
@@ -181,6 +185,7 @@ typedef struct {
   float* weights;            /* [num_pages, kv_heads, page_size] in/out, tokens adjacent */
   long long w_page, w_head;  /* elements */
   float scale, decay;        /* decay: finite */
+  unsigned flags;            /* 0, or SPEC_CACHE_TEST_WAIT_TIMEOUT */
 } spec_cache_weigh_args;
 
 /*
@@ -188,7 +193,8 @@ typedef struct {
  *   w_j = (j is no new token ? decay * w_j : 0) + sum e^(scale q . k_j - lse)
  * over the new tokens at j or after and the head's query heads. New tokens' slots are written
  * whatever they held, and so are all with decay = 0. A row whose lse is -inf gives nothing.
- * Products and sums are fp32. Requests must not share pages (either's weights may be lost).
+ * Products and sums are fp32. Requests must not share pages (either's weights may be lost). A call
+ * that sets SPEC_STATUS_TIMEOUT has updated some of the weights and others not.
  */
 int spec_cache_weigh(const spec_cache_weigh_args* a, void* stream, unsigned* device_status);
 

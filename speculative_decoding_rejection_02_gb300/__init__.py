@@ -340,8 +340,8 @@ _CACHE_NAMES = ("CACHE_BAD_LENGTHS", "CACHE_BAD_PAGE", "CACHE_BAD_SLOT", "CACHE_
                 "cache_attend", "cache_status", "cache_step")
 
 
-_SPARSE_NAMES = ("AttendSelectedArgs", "BoundsArgs", "CACHE_BAD_SELECTION", "CacheEvict",
-                 "EvictArgs", "ScoreArgs", "SelectArgs", "WeighArgs", "cache_attend_selected",
+_SPARSE_NAMES = ("AttendSelectedArgs", "BoundsArgs", "CACHE_BAD_SELECTION",
+                 "CACHE_TEST_WAIT_TIMEOUT", "CacheEvict", "EvictArgs", "ScoreArgs", "SelectArgs", "WeighArgs", "cache_attend_selected",
                  "cache_bounds", "cache_evict", "cache_score", "cache_select", "cache_weigh")
 
 

@@ -230,7 +230,7 @@ int check_selected(const spec_cache_attend_selected_args* a) {
 }
 
 int check_weigh(const spec_cache_weigh_args* a) {
-  if (!a) return SPEC_ERR_INVALID_ARG;
+  if (!a || a->flags & ~SPEC_CACHE_TEST_WAIT_TIMEOUT) return SPEC_ERR_INVALID_ARG;
   int rc = check_sizes(a->B, a->width, a->kv_heads, a->dim, a->page_size, a->num_pages, a->dtype);
   if (rc == SPEC_OK) rc = check_heads(a->heads, a->kv_heads, a->num_tokens, a->max_q);
   if (rc != SPEC_OK || a->num_tokens == 0 || a->B == 0) return rc;
@@ -337,6 +337,15 @@ int selected(const sv::SelectedParams& p, int columns, int sms, unsigned grid, v
                             : selected<DP, 1, false, BF16>(p, grid, stream);
   if (columns <= 16) return selected<DP, 2, false, BF16>(p, grid, stream);
   return selected<DP, 4, false, BF16>(p, grid, stream);
+}
+
+template <bool MUTE>
+int weigh(const sv::WeighParams& p, int sms, int run, void* stream) {
+  static std::atomic<unsigned long long> ready;
+  const int rc = allow(sv::k_cache_weigh<MUTE>, sv::kWeighSmem, ready);
+  if (rc != SPEC_OK) return rc;
+  return launch(sv::k_cache_weigh<MUTE>, dim3(sms), sv::kWeighThreads, sv::kWeighSmem, stream, p,
+                run);
 }
 
 }  // namespace
@@ -552,11 +561,9 @@ int spec_cache_weigh(const spec_cache_weigh_args* a, void* stream, unsigned* dev
       !tensor_map(&p.k_map, a->dtype, a->k_pages, a->dim, a->page_size, a->kp_token, a->kv_heads,
                   a->kp_head, a->num_pages, a->kp_page, box, 1))
     return SPEC_ERR_CUDA;
-  static std::atomic<unsigned long long> ready;
-  const int ok = allow(sv::k_cache_weigh, sv::kWeighSmem, ready);
-  if (ok != SPEC_OK) return ok;
   const int run = a->B > sv::kWeighScan ? (a->B + sv::kWeighScan - 1) / sv::kWeighScan : 1;
-  return launch(sv::k_cache_weigh, dim3(sms), sv::kWeighThreads, sv::kWeighSmem, stream, p, run);
+  return a->flags & SPEC_CACHE_TEST_WAIT_TIMEOUT ? weigh<true>(p, sms, run, stream)
+                                                 : weigh<false>(p, sms, run, stream);
 }
 
 long long spec_cache_evict_workspace(const spec_cache_evict_args* a) {

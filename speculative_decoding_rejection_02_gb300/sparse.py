@@ -28,6 +28,7 @@ import speculative_decoding_rejection_02_gb300 as _sv
 from .cache import _I, _L, _P, _native, _on
 
 CACHE_BAD_SELECTION = 0x1000
+CACHE_TEST_WAIT_TIMEOUT = 0x1  # WeighArgs.flags, test only: a wait runs out
 
 _F = C.c_float
 
@@ -73,7 +74,8 @@ class WeighArgs(C.Structure):
                 ("num_pages", _L), ("dtype", _I), ("q", _P), ("q_token", _L), ("q_head", _L),
                 ("k_pages", _P), ("kp_page", _L), ("kp_token", _L), ("kp_head", _L),
                 ("block_table", _P), ("kv_lens", _P), ("cu_q", _P), ("lse", _P),
-                ("weights", _P), ("w_page", _L), ("w_head", _L), ("scale", _F), ("decay", _F)]
+                ("weights", _P), ("w_page", _L), ("w_head", _L), ("scale", _F), ("decay", _F),
+                ("flags", C.c_uint)]
 
 
 class EvictArgs(C.Structure):
