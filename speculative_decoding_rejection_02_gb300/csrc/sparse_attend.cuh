@@ -21,7 +21,8 @@
 // Each warp has its own ring of tiles of 16 keys and values, filled by 16-byte asynchronous
 // copies, and its own softmax statistics, and waits for no other warp until the end: a block's
 // warps, then a cluster's blocks through each other's shared memory, join their parts. Slots that
-// no token sees are not loaded; zeros stand in their place.
+// no token sees are not loaded; zeros stand in their place. What one token of a unit sees meets the
+// others with P = 0, which keeps finite values out of their sums, but not infinities and NaN.
 //
 // Bound by HBM where the selections of a request's tokens agree, by the latency of the chain
 // (requests, list, pages, keys, join) in small calls.

@@ -147,7 +147,9 @@ def cache_attend_selected(q, k_pages, v_pages, block_table, kv_lens, cu_q, selec
                           out=None, return_lse=False, status=None, stream=None):
     """``cache_attend`` over the pages in ``selected`` (int32 [T, kv_heads, count]) alone: token t
     and the query heads of kv head h see the tokens up to t's own in columns ``selected[t, h]``,
-    which ascend and end with -1, as ``cache_select`` leaves them."""
+    which ascend and end with -1, as ``cache_select`` leaves them. A value that is not finite may
+    reach rows of its request and kv head that do not see it (as 0 times infinity); a key that is
+    not finite reaches only those that do."""
     if stream is not None:
         return _on(stream, cache_attend_selected, q, k_pages, v_pages, block_table, kv_lens, cu_q,
                    selected, scale=scale, out=out, return_lse=return_lse, status=status)
