@@ -238,6 +238,11 @@ long long spec_cache_evict_workspace(const spec_cache_evict_args* a);
  * entries stay. A kept token's position within its request changes, and differs from head to
  * head: the caller counts positions for rotary embeddings by itself, page bounds have to be found
  * anew, and no window fits any more.
+ * A spec_cache_step that drops rejected drafts drops a request's last slots, whatever stands there,
+ * and drafts, which few queries have looked at, are the first to go here. So where drafts await that
+ * drop, `recent` has to be at least the most new tokens that a request has had in the round; or
+ * the drop comes first, by a spec_cache_step with new_lens = 0. With less, older tokens are dropped
+ * in the drafts' place and rejected drafts stay, and no status bit tells of it.
  * If a length or budget cannot be, or the stack would not hold the pages, SPEC_CACHE_BAD_LENGTHS
  * is set and nothing is changed (lens_out = lens, free_count_out = free_count). A page number
  * outside the pool sets SPEC_CACHE_BAD_PAGE; the request's tokens are not meaningful then. One that

@@ -187,6 +187,11 @@ def cache_evict(k_pages, v_pages, weights, block_table, lens, budget, free_pages
 
     A kept token's place is no longer its position: the caller counts positions for rotary
     embeddings itself, and calls ``cache_bounds`` anew (without ``cu_q``) where it uses them.
+    Between a round's append and the ``cache_step`` that drops its rejected drafts, ``recent`` must
+    be at least the most new tokens of a request in the round: the step drops the last slots,
+    whatever stands there, and drafts weigh little, so they would go first. Or drop first, by a
+    ``cache_step`` whose ``new_lens`` are 0.
+
     If a length or budget cannot be, nothing changes and ``status`` gets CACHE_BAD_LENGTHS.
     """
     if stream is not None:
