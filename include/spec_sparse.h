@@ -195,7 +195,9 @@ typedef struct {
  * spec_cache_weigh — for every held token j of each request with new tokens, and each kv head,
  *   w_j = (j is no new token ? decay * w_j : 0) + sum e^(scale q . k_j - lse)
  * over the new tokens at j or after and the head's query heads. New tokens' slots are written
- * whatever they held, and so are all with decay = 0. A row whose lse is -inf gives nothing.
+ * whatever they held, and so are all with decay = 0. A row whose lse is -inf gives nothing (where
+ * its scores are finite): what drafts gave stays in the sums when they are rejected, so a caller
+ * who does not want that calls after the verification, with -inf in the rejected rows' lse.
  * Products and sums are fp32. Requests must not share pages (either's weights may be lost). A call
  * that sets SPEC_STATUS_TIMEOUT has updated some of the weights and others not.
  */

@@ -166,7 +166,15 @@ def cache_weigh(q, k_pages, block_table, kv_lens, cu_q, lse, weights, *, max_q=N
     every cached token: the sum over the new tokens that see it and the query heads of its kv head
     of e^(scale q . k - lse), with ``lse`` from ``cache_attend`` (without a window). Older sums are
     multiplied by ``decay`` first; the new tokens' own slots start from 0, whatever they held.
-    Requests without new tokens stay as they are. ``max_q`` as in ``cache_attend``."""
+    Requests without new tokens stay as they are. ``max_q`` as in ``cache_attend``.
+
+    Drafts give their weight like other tokens, and it stays when they are rejected. To leave it
+    out, call after the verification with the rejected rows' lse at -inf; for a round of the last
+    token and its drafts, with the row's number in its request::
+
+        rejected = row - cu_q[request] > num_accepted[request]
+        cache_weigh(..., lse.masked_fill(rejected[:, None], -math.inf), weights)
+    """
     if stream is not None:
         return _on(stream, cache_weigh, q, k_pages, block_table, kv_lens, cu_q, lse, weights,
                    max_q=max_q, scale=scale, decay=decay, status=status)
