@@ -33,6 +33,11 @@
  * up to 128 query heads (SPEC_ERR_UNSUPPORTED). Addresses and strides (of more than one element)
  * of 16-bit arrays are multiples of 16 bytes. What a call writes overlaps none of its other
  * arguments. Results are the same to the bit in every call with the same arguments.
+ * spec_cache_score writes, and spec_cache_select and spec_cache_evict choose their forms by, the
+ * width that they are given (columns of scores or block_table), not the requests' lengths: pass the
+ * columns that the longest request may have, as the first ones of a wider table (table_stride). 64
+ * requests of 2-8 tokens over 1000-30000 in pages of 16, 1876 columns against 8192: score 35 and
+ * 57 us, select 13 and 52. The other calls take the same time.
  */
 #ifndef SPEC_SPARSE_H
 #define SPEC_SPARSE_H

@@ -15,6 +15,11 @@ current one), errors in device data set bits of ``status`` or are kept for ``cac
 tensors that require a gradient are refused while gradients are enabled. Page sizes are powers of
 two from 8, dim is a multiple of 8 up to 128; addresses and strides of 16-bit tensors are multiples
 of 16 bytes; what a call writes may not overlap its other arguments.
+
+``cache_score``, ``cache_select`` and ``cache_evict`` take longer in tables that are wider than
+their requests need (scores of a round over up to 30000 tokens: 35 us with 1876 columns, 57 with
+8192; its selection 13 and 52): pass a view of the first columns, ``block_table[:, :n]``, as far
+as the longest request may reach.
 """
 from __future__ import annotations
 
