@@ -331,7 +331,7 @@ int selected(const sv::SelectedParams& p, unsigned grid, void* stream) {
 template <int DP, bool BF16>
 int selected(const sv::SelectedParams& p, int columns, int sms, unsigned grid, void* stream) {
   // more tiles in flight where there is a block for each SM at most (one token over 64 pages of
-  // 32: 8.9 us in place of 10.2)
+  // 32: 9.6 us in place of 11.5)
   if (columns <= 8)
     return (int)grid <= sms ? selected<DP, 1, true, BF16>(p, grid, stream)
                             : selected<DP, 1, false, BF16>(p, grid, stream);
@@ -491,19 +491,20 @@ int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* s
   p.c = a->scale * kLog2e;
   if (std::fabs(p.c) < 1.1754944e-38f) p.c = 1.1754944e-38f;
   // A kv head's query heads in units of 32 at most, and as many tokens of a request (if there may
-  // be several) as 16 columns, the block's list and the bytes over its ring take; as 32 columns
-  // where requests have eight tokens or more on average and long lists. With 32 columns a page is
-  // loaded for more tokens, but the SM has fewer warps to hide latency with: 64 requests of 2-8
-  // tokens over 128 pages of 16, four heads on a kv head, 212 us in place of 183 (with 8 columns
-  // 202), 9 of 19-26 over 19 of 16 with seven heads 61 in place of 44; but 28 of 11-18 over 43 of
-  // 64, four heads, 136 in place of 158.
+  // be several) as 16 columns, the block's list and the bytes over its ring take. With 8 columns 64
+  // requests of 2-8 tokens over 128 pages of 16, four heads on a kv head, take the same 176 us, 28
+  // of 11-18 over 43 of 64 182 in place of 177, 40 of 4-6 over 64 of 32, eight heads, 162 in place
+  // of 150. 32 columns load a page for more tokens, but leave the SM two thirds of the warps, and
+  // columns empty where a request's tokens do not fill them: the same three 256, 160 and 208 us. Of
+  // 45 calls of 8 tokens a request or more the best gained 14 % with 32 (18 of 8 over 60 of 16: 59
+  // us in place of 69), a third lost 20 to 100 % (20 of 9-10 over 64 of 32, eight heads: 122 in
+  // place of 80); the lengths that decide it are not known here.
   p.unit_heads = p.G < 32 ? p.G : 32;
   p.splits = (p.G + p.unit_heads - 1) / p.unit_heads;
   p.per = 1;
   const int ring = a->dim > 64 ? sv::SelCfg<128, 1, false>::kRing : sv::SelCfg<64, 1, false>::kRing;
   if (a->num_tokens > a->B && a->width <= ring) {
-    const bool many = a->num_tokens >= 8ll * a->B && (long long)a->count * a->page_size >= 1024;
-    p.per = (many ? 32 : 16) / p.unit_heads;
+    p.per = 16 / p.unit_heads;
     if (p.per > sv::kSelTokens) p.per = sv::kSelTokens;
     if (p.per > sv::kSelList / a->count) p.per = sv::kSelList / a->count;
     if (p.per < 1) p.per = 1;
