@@ -11,7 +11,8 @@
 // k_evict_move: keys, values and weights to their new places. Tokens only move down and keep
 // their order, so a request and head go upwards in batches: all of a batch is read, in registers,
 // before any of it is written, and what is overwritten is never a later batch's source. One block
-// for a request and head, or a cluster of up to eight where there are few. Bound by HBM.
+// for a request and head, or a cluster of up to eight where there are few. Bound by HBM: 64 requests
+// of 1990-2500 move 765 MB in 159 us, 0.72 of the rate of a copy.
 #pragma once
 #include <type_traits>
 
@@ -135,8 +136,8 @@ __device__ __forceinline__ void evict_note(const EvictParams& p, int b, int head
 }
 
 // Requests of up to 16 NT tokens, whose weights the registers hold (pick_short). 108 requests of
-// 138-173 tokens with 8 heads: both kernels 33 us with pick_items, 17.5 so; 64 of 1990-2500 98 and
-// 90.
+// 138-173 tokens with 8 heads: both kernels 17.3 us, 33 with pick_items in as many threads, 76 in the
+// 1024 of longer requests; 64 of 1990-2500, on three pools in turn, 187 and with those 1024 207.
 template <int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_evict_pick_short(const EvictParams p) {
   __shared__ ShortPick<NT> sh;

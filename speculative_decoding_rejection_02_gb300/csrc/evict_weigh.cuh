@@ -29,10 +29,10 @@
 // product that takes its time, not the product.) The two tiles' chains go ahead of one another, so
 // each has its own stages of K.
 //
-// Bound by HBM (the keys, once) for few columns, by the exponentials and the products, which take
-// about as long, for many: 64 requests of 2-8 tokens over 1000-30000 186 us (0.93 of a copy's
-// rate), two chunks of 2048 over 11000-14000 351 us (326 in runs of some milliseconds; 0.66 of a
-// large library product's rate).
+// Bound by HBM (the keys, once) for few columns, by the chain of products for many: 64 requests of
+// 2-8 tokens over 1000-30000 186 us (0.93 of a copy's rate), two chunks of 2048 over 11000-14000
+// 354 us (0.66 of a large library product's rate; 331 in runs of some milliseconds, of which 296 are
+// left with no exponential computed).
 #pragma once
 #include <cuda.h>
 

@@ -11,8 +11,8 @@
 //   O^T += V^T P     dim x columns, fp32. The products take 16-bit operands, so P goes in as two
 //                    parts of the cache's type, P rounded and what that left over: off by 2^-16
 //                    (bf16) or 2^-22 (fp16) of itself. With the first part alone the outputs are
-//                    off by 2.0e-3 to 2.3e-3 where 1.7e-3 are their own rounding (bf16), and the
-//                    call takes 6 % less (64 requests of 2-8 tokens: 166 us in place of 176)
+//                    off by 2.0e-3 to 2.3e-3 where 1.7e-3 are their own rounding (bf16), and
+//                    calls take 2 to 13 % less (64 requests of 2-8 tokens: 166 us in place of 176)
 //
 // With c = scale * log2(e). Keys as the rows leave no tensor-core row empty however few columns
 // there are; P^T gets from a product's layout of sums to that of an operand by a transposition of
