@@ -165,11 +165,11 @@ typedef struct {
  * spec_cache_attend_selected — spec_cache_attend where token t and the query heads of kv head h
  * see the tokens up to t's own in the columns selected[t][h] alone. A row that sees nothing gives
  * out = 0 and lse = -inf. Scores, softmax statistics and sums are fp32; the softmax weights meet
- * the values with 16 bits (bf16) or 22 bits (fp16). Slots that no row sees do not reach the
- * outputs, whatever they hold; pages in no list are not read. A value that a row sees and that is not
- * finite leaves its output not finite (NaN, for infinities too), and may do so to other rows of its
- * request and kv head in that channel, also to some whose lists do not have its page (they share a
- * product, where its weight is 0). A key that is not finite reaches only the rows that see it.
+ * the values with an error of 2^-15 (bf16) or 2^-21 (fp16) of themselves. Slots that no row sees do
+ * not reach the outputs, whatever they hold; pages in no list are not read. A value that some row
+ * sees and that is not finite may make other rows of its request and kv head NaN in its channel, also
+ * rows whose lists do not have its page (they share a product, where its weight is 0). A key that is
+ * not finite reaches only the rows that see it.
  */
 int spec_cache_attend_selected(const spec_cache_attend_selected_args* a, void* stream,
                                unsigned* device_status);

@@ -183,6 +183,15 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   return r;
 }
 template <bool BF16>
+__device__ __forceinline__ uint32_t pack_pair_down(float lo, float hi) {  // cut off, not rounded
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool BF16>
 __device__ __forceinline__ float2 unpack_pair(uint32_t v) {
   if (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
   return __half22float2(*reinterpret_cast<const __half2*>(&v));

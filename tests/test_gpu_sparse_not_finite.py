@@ -77,3 +77,23 @@ def test_one_token_alone_sees_its_own_list():
                                        sel[t:t + 1].to(DEV))
         bad = torch.isnan(out).flatten(1).any(1)
         assert bool(bad) == (t == TOKEN)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("tokens", [1, 4])
+def test_an_infinite_value_that_a_row_sees_stays_infinite(dtype, tokens):
+    """Keys of one direction, so that many weights are the same power of two, which the type holds
+    without a rest, and others that it does not hold."""
+    g = torch.Generator().manual_seed(62)
+    n, page, dim = 64, 16, 64
+    k = torch.ones((4, page, 1, dim), dtype=dtype)
+    k[1::2] *= torch.rand((2, page, 1, 1), generator=g).to(dtype)
+    v = torch.randn((4, page, 1, dim), generator=g).to(dtype)
+    v[0, 5, 0, 3], v[1, 6, 0, 7] = math.inf, -math.inf
+    q = torch.full((tokens, 2, dim), 0.25, dtype=dtype)
+    q[:, 1] = 0
+    sel = torch.arange(4, dtype=torch.int32).expand(tokens, 1, 4).contiguous()
+    out = sv.cache_attend_selected(q.to(DEV), k.to(DEV), v.to(DEV), ints([[0, 1, 2, 3]]), ints([n]),
+                                   ints([0, tokens]), sel.to(DEV))
+    assert (out[:, :, 3] == math.inf).all() and (out[:, :, 7] == -math.inf).all()
+    assert int(torch.isfinite(out).sum()) == tokens * 2 * (dim - 2)

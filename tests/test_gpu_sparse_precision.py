@@ -20,8 +20,9 @@ pytestmark = pytest.mark.gpu
     ([9, 12], [20, 90], 16, 16, 1, 128)])        # 32 columns a block
 def test_attend_selected_rounds_its_outputs_alone(shape, dtype):
     """Beside fp32's own errors (ref.attend's, without the rounding of the weights to the type) a
-    weight is off by u^2, since its second part is off by u of what the first left over, at most u
-    of it; and the output by its one rounding, u of it and of what it was off by already."""
+    weight is off by 2 u^2, since the first part, cut off, leaves less than 2 u of it, of which the
+    second is off by u, and by 2^-23, which is added; and the output by its one rounding, u of it and
+    of what it was off by already."""
     q_lens, kv_lens, page, heads, kv_heads, dim = shape
     g, q, kp, vp, table, ks, vs = inputs(shape, dtype, "token", 31)
     held = max(-(-n // page) for n in kv_lens)
@@ -33,7 +34,7 @@ def test_attend_selected_rounds_its_outputs_alone(shape, dtype):
     size = ref.attend(q, ks, [v.abs() for v in vs], q_lens, sel, page)[0]
     u = cache_ref.UNIT[dtype]
     tol = loose - 2 * u * size                   # fp32's errors
-    tol = tol + u * u * size
+    tol = tol + (2 * u * u + 2.0 ** -23) * size
     tol = tol + u * (want.abs() + tol) + 2.0 ** -25   # (and an output below fp16's least normal)
     out = sv.cache_attend_selected(q.to(DEV), kp.to(DEV), vp.to(DEV), table.to(DEV), ints(kv_lens),
                                    starts(q_lens), sel.to(DEV)).double().cpu()
