@@ -8,7 +8,9 @@
 // cores, 16 pages x 8 tokens at a time: P and N are scaled by powers of two for the types' ranges
 // (score_shift), which are taken out again at the end, and split into three 16-bit parts that
 // together hold 24 bits or more (33 of the largest in fp16), so the products are exact and the sums
-// are fp32.
+// are fp32. The tensor cores cut their sums off, where an addition rounds, so that the error of a
+// long chain grows with its length: the first parts' products are summed two instructions at a time
+// and added up in registers (off by 4e-8 to 1e-7 in place of 5e-8 to 4e-7, for 2 % of the time).
 //
 // Bound by HBM: 4 dim bytes of bounds for each page and head, read once for up to 32 tokens, into
 // registers (a warp has 16 pages, 8 KB at dim 128, in flight). A lane loads 16 bytes, 8 channels,
@@ -18,7 +20,7 @@
 // Work is one list of 16 columns for each group of tokens and kv head, with the start of a group
 // counted in, cut into equal parts, one for each block: what a block has to do before its first
 // product (find its part, split [N, P]) takes longer than some tens of columns. 64 requests of 2-8
-// tokens over 1000-30000, 16-bit bounds of 8 heads: 35 us, 22 at the rate of a copy; 55 with a grid
+// tokens over 1000-30000, 16-bit bounds of 8 heads: 36 us, 22 at the rate of a copy; 55 with a grid
 // over groups, heads and thirds of the columns.
 #pragma once
 #include "sparse_common.cuh"
@@ -278,16 +280,23 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
         look(i + kWarps, next);
 #pragma unroll 1
         for (int gr = 0; gr < groups; ++gr) {
-          float d[3][4] = {}, d0[4] = {};  // sums of the three parts, the first parts' of lo apart
+          float d[4] = {}, low[4] = {};  // sums with the first parts, and with the two others
           const char* frag = smem + gr * Cfg::kGroupBytes + lane * 16;
 #pragma unroll
           for (int i = 0; i < Cfg::kChunks; ++i) {
 #pragma unroll
             for (int z = 0; z < 3; ++z) {
               const uint4 b = *(const uint4*)(frag + (i * 3 + z) * 512);
-              float* to = z == 0 && i < Cfg::kChunks / 2 ? d0 : d[z];
-              mma_16816<BF16>(to, a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y, b.x, b.y);
-              mma_16816<BF16>(to, a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w, b.z, b.w);
+              if (z == 0) {
+                float now[4];
+                mma_16816_new<BF16>(now, a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y, b.x, b.y);
+                mma_16816<BF16>(now, a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w, b.z, b.w);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) d[y] += now[y];
+              } else {
+                mma_16816<BF16>(low, a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y, b.x, b.y);
+                mma_16816<BF16>(low, a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w, b.z, b.w);
+              }
             }
           }
 #pragma unroll
@@ -296,7 +305,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocks)
             if (tok >= tokens || col[r] >= p.rq.width) continue;
             const bool visible = live[r] && ((long long)col[r] << p.rq.page_shift) <= pos + tok;
             row[tok * p.s_token + col[r]] =
-                visible ? (d[0][y] + d0[y] + (d[1][y] + d[2][y])) * unscale[tok] : -INFINITY;
+                visible ? (d[y] + low[y]) * unscale[tok] : -INFINITY;
           }
         }
       }

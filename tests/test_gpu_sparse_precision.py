@@ -76,3 +76,23 @@ def test_score_of_channels_of_different_sizes():
     got = sv.cache_score(q.to(DEV), b.to(DEV), ints([[0, 1, 2]]), ints([48]), ints([0, 2]),
                          page_size=16).double().cpu()
     assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("kv_heads,G,dim", [(2, 1, 128), (2, 1, 64), (4, 3, 96), (1, 8, 128)])
+def test_score_sums_do_not_drift(dtype, kv_heads, G, dim):
+    """Scores whose terms are all positive, in the mean over many. Two instructions' sums are cut off
+    under 2^-23 of what they sum, half of that on average and the first one's half the pair: 0.75
+    2^-23 at most; the additions after it and those of P and N round, 2^-24 / sqrt(3) each in the
+    mean, of partial sums, in no direction: together under 2^-23."""
+    g = torch.Generator().manual_seed(34)
+    q = (torch.randn((40, kv_heads * G, dim), generator=g) * 1.5).to(dtype)
+    b = torch.randn((64, kv_heads, 2, dim), generator=g).abs() + 1.0
+    b[:, :, 0] *= -1.0
+    b = b.to(dtype)
+    want, _ = ref.score(q, [b], [40], [16 * 64], 16, 64)
+    got = sv.cache_score(q.to(DEV), b.to(DEV), ints([list(range(64))]), ints([16 * 64]),
+                         ints([0, 40]), page_size=16).double().cpu()
+    there = torch.isfinite(want)
+    off = (got[there] - want[there]) / want[there]
+    assert float(off.pow(2).mean().sqrt()) < 2.0 ** -23
