@@ -36,7 +36,7 @@
  * spec_cache_score writes, and spec_cache_select and spec_cache_evict choose their forms by, the
  * width that they are given (columns of scores or block_table), not the requests' lengths: pass the
  * columns that the longest request may have, as the first ones of a wider table (table_stride). 64
- * requests of 2-8 tokens over 1000-30000 in pages of 16, 1876 columns against 8192: score 35 and
+ * requests of 2-8 tokens over 1000-30000 in pages of 16, 1876 columns against 8192: score 36 and
  * 57 us, select 13 and 52. The other calls take the same time.
  */
 #ifndef SPEC_SPARSE_H

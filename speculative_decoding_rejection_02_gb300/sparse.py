@@ -17,7 +17,7 @@ two from 8, dim is a multiple of 8 up to 128; addresses and strides of 16-bit te
 of 16 bytes; what a call writes may not overlap its other arguments.
 
 ``cache_score``, ``cache_select`` and ``cache_evict`` take longer in tables that are wider than
-their requests need (scores of a round over up to 30000 tokens: 35 us with 1876 columns, 57 with
+their requests need (scores of a round over up to 30000 tokens: 36 us with 1876 columns, 57 with
 8192; its selection 13 and 52): pass a view of the first columns, ``block_table[:, :n]``, as far
 as the longest request may reach.
 """
